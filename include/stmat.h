@@ -608,6 +608,94 @@ st_status st_static_check(void *stream, uint32_t *flags);
  * Returns ST_E_DEVICE when any flag was set. */
 st_status st_plan_check(const st_plan_t *plan, void *stream, uint32_t *flags);
 
+/* ------------------------------------------------- operators on tensors */
+/* What a layer does with the tensors the library materializes: a norm vector
+ * (st_rms_norm), a weight kept in 16 bits or as stored in scaled FP8
+ * (st_linear), and the activation between two of them (st_gated_act).  The
+ * first and the last write 8-bit rows with scales, which st_linear takes
+ * beside a scaled-FP8 weight that st_plan kept with ST_KEEP.
+ *
+ * Conventions: matrices are row-major with unit stride inside a row; ld* is
+ * the number of elements between rows (at least the row's length; 0 for an
+ * input: the same row for all).  All pointers are device memory, aligned to
+ * their itemsize only (16-byte aligned pointers and row strides take the
+ * faster paths).  An output may be the very matrix of an input (same pointer,
+ * stride and itemsize: in place); any other overlap gives undefined values.
+ * Calls run on `stream` (a cudaStream_t; NULL is the legacy default stream)
+ * without host synchronization, workspace or allocation, can be captured in a
+ * CUDA graph, and give the same bits on every run.  Zero rows or columns:
+ * nothing is written.  Errors: ST_E_INVAL (sizes, strides, NULL), ST_E_DTYPE,
+ * ST_E_ALIGN, ST_E_CUDA (launch failure); nothing is queued then.  Values
+ * are computed in binary32 and rounded once (round to nearest even); NaN and
+ * infinities go through the formulas.
+ *
+ * 8-bit rows (y_dtype ST_F8_E4M3): code = e4m3(clamp(v / s, -448, 448)) for
+ * the value v, with either
+ *   scales  one binary32 per row, written: s = max(max |v| / 448, 2^-126),
+ *           NaN for a row with a NaN;
+ *   scale   one binary32 given by the caller (a checkpoint's input scale).
+ * The division is a multiplication by the correctly rounded 1 / s. */
+typedef enum st_act {
+  ST_ACT_NONE = 0,
+  ST_ACT_RELU = 1,      /* v < 0 ? 0 : v */
+  ST_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+  ST_ACT_GELU = 3,      /* v / 2 * (1 + erf(v / sqrt(2))) */
+  ST_ACT_GELU_TANH = 4  /* v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3))) */
+} st_act;
+
+/* Root-mean-square norm of each row, with the residual's addition:
+ *   h = x + residual;  y = h * weight / sqrt(mean(h^2) + eps). */
+typedef struct st_rms_norm_args {
+  int64_t rows, cols;
+  float eps;                        /* >= 0 */
+  st_dtype x_dtype;                 /* BF16, F16 or F32: x, residual and h */
+  st_dtype w_dtype;                 /* BF16, F16 or F32 */
+  st_dtype y_dtype;                 /* BF16, F16, F32 or F8_E4M3 */
+  const void *x;        int64_t ldx;
+  const void *residual; int64_t ldr; /* NULL: h = x */
+  const void *weight;               /* cols entries, or NULL: 1 */
+  void *h;              int64_t ldh; /* the new residual, or NULL: not kept */
+  void *y;              int64_t ldy;
+  const float *scale;               /* F8_E4M3: the given scale, or */
+  float *scales;                    /* rows entries, written */
+} st_rms_norm_args;
+st_status st_rms_norm(const st_rms_norm_args *args, void *stream);
+
+/* y = act(gate) * up, or act(gate) without `up`; both halves of one [rows,
+ * 2 cols] product are a gate and an up of stride 2 cols. */
+typedef struct st_gated_act_args {
+  int64_t rows, cols;
+  st_act act;
+  st_dtype x_dtype;                 /* BF16, F16 or F32: gate and up */
+  st_dtype y_dtype;                 /* BF16, F16, F32 or F8_E4M3 */
+  const void *gate;     int64_t ldg;
+  const void *up;       int64_t ldu; /* or NULL */
+  void *y;              int64_t ldy;
+  const float *scale;
+  float *scales;
+} st_gated_act_args;
+st_status st_gated_act(const st_gated_act_args *args, void *stream);
+
+/* Matrix product with a checkpoint's [n, k] weight:
+ *   y[i, j] = act(x_scale[i] * w_scale[j] * sum_l x[i, l] * weight[j, l] + bias[j]) + residual[i, j].
+ * x and weight are both BF16, both F16, or F8_E4M3 with F8_E4M3 or F8_E5M2;
+ * the sum is held in 32 bits.  k = 0: the sum is 0. */
+typedef struct st_linear_args {
+  int64_t m, n, k;
+  st_act act;
+  st_dtype x_dtype, w_dtype;
+  st_dtype y_dtype;                 /* BF16, F16 or F32: y and residual */
+  st_dtype bias_dtype;              /* BF16, F16 or F32 */
+  const void *x;        int64_t ldx;
+  const void *w;        int64_t ldw;
+  const float *x_scale; int64_t x_scale_count; /* NULL: 1; else 1 or m entries */
+  const float *w_scale; int64_t w_scale_count; /* NULL: 1; else 1 or n entries */
+  const void *bias;                 /* n entries, or NULL */
+  const void *residual; int64_t ldr; /* or NULL */
+  void *y;              int64_t ldy;
+} st_linear_args;
+st_status st_linear(const st_linear_args *args, void *stream);
+
 /* ----------------------------------------------------------------- misc */
 
 /* Message of the calling thread's last failure ("" if none). */

@@ -1,0 +1,134 @@
+// st_ops.cpp -- C entry points of the operators on materialized tensors:
+// argument checks; the kernels are in st_rowops.cu and st_linear.cu.
+#include <cstdint>
+
+#include "st_ops.h"
+
+using namespace stmat;
+
+namespace {
+
+constexpr int64_t kMaxRows = 0x7fffffff;  // one grid dimension
+constexpr int64_t kMaxCols = 0x7fffffff;
+
+bool is_float16or32(st_dtype d) { return d == ST_BF16 || d == ST_F16 || d == ST_F32; }
+
+// A [rows, cols] operand: NULL only when it may be absent; ld elements
+// between rows (0: one row for all, inputs only), rows inside 63 bits.
+st_status check_matrix(const char *op, const char *name, const void *p, int64_t ld, st_dtype dtype, int64_t rows,
+                       int64_t cols, bool input) {
+  if (!p) return set_error(ST_E_INVAL, "%s: %s is NULL", op, name);
+  const int64_t item = static_cast<int64_t>(st_dtype_size(dtype));
+  if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(item))
+    return set_error(ST_E_ALIGN, "%s: %s is not aligned to its %lld-byte items", op, name, (long long)item);
+  if (ld < cols && rows > 1 && !(input && ld == 0))
+    return set_error(ST_E_INVAL, "%s: %s has %lld elements between rows of %lld", op, name, (long long)ld,
+                     (long long)cols);
+  int64_t span = 0;
+  if (ld < 0 || __builtin_mul_overflow(ld, rows, &span) || __builtin_add_overflow(span, cols, &span) ||
+      __builtin_mul_overflow(span, item, &span))
+    return set_error(ST_E_INVAL, "%s: %s with %lld rows of stride %lld overflows 63 bits", op, name, (long long)rows,
+                     (long long)ld);
+  return ST_OK;
+}
+
+st_status check_vector(const char *op, const char *name, const void *p, st_dtype dtype) {
+  const size_t item = st_dtype_size(dtype);
+  if (reinterpret_cast<uintptr_t>(p) % item)
+    return set_error(ST_E_ALIGN, "%s: %s is not aligned to its %zu-byte items", op, name, item);
+  return ST_OK;
+}
+
+st_status check_sizes(const char *op, int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > kMaxRows || cols > kMaxCols)
+    return set_error(ST_E_INVAL, "%s: %lld x %lld is out of range (0 .. 2^31 - 1)", op, (long long)rows,
+                     (long long)cols);
+  return ST_OK;
+}
+
+// The output's dtype and, for 8 bits, exactly one of a given scale and an
+// array for the rows' scales.
+st_status check_output(const char *op, st_dtype y, const float *scale, const float *scales) {
+  if (!is_float16or32(y) && y != ST_F8_E4M3)
+    return set_error(ST_E_DTYPE, "%s: the output is BF16, F16, F32 or F8_E4M3, not %d", op, static_cast<int>(y));
+  if (y == ST_F8_E4M3 ? !scale == !scales : (scale || scales))
+    return set_error(ST_E_INVAL, "%s: an F8_E4M3 output takes either scale or scales, another output neither", op);
+  st_status s = check_vector(op, "scale", scale, ST_F32);
+  return s != ST_OK ? s : check_vector(op, "scales", scales, ST_F32);
+}
+
+#define ST_TRY(expr)                         \
+  do {                                       \
+    const st_status try_status = (expr);     \
+    if (try_status != ST_OK) return try_status; \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+st_status st_rms_norm(const st_rms_norm_args *a, void *stream) {
+  if (!a) return set_error(ST_E_INVAL, "st_rms_norm: NULL arguments");
+  const char *op = "st_rms_norm";
+  ST_TRY(check_sizes(op, a->rows, a->cols));
+  if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: x is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
+  if (a->weight && !is_float16or32(a->w_dtype))
+    return set_error(ST_E_DTYPE, "%s: weight is BF16, F16 or F32, not %d", op, (int)a->w_dtype);
+  if (!(a->eps >= 0.0f)) return set_error(ST_E_INVAL, "%s: eps %g is not a non-negative number", op, (double)a->eps);
+  if (a->h && !a->residual) return set_error(ST_E_INVAL, "%s: h without a residual", op);
+  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales));
+  if (a->rows == 0 || a->cols == 0) return ST_OK;
+  ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->rows, a->cols, true));
+  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->x_dtype, a->rows, a->cols, true));
+  if (a->weight) ST_TRY(check_vector(op, "weight", a->weight, a->w_dtype));
+  if (a->h) ST_TRY(check_matrix(op, "h", a->h, a->ldh, a->x_dtype, a->rows, a->cols, false));
+  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->rows, a->cols, false));
+  return launch_rms_norm(*a, stream);
+}
+
+st_status st_gated_act(const st_gated_act_args *a, void *stream) {
+  if (!a) return set_error(ST_E_INVAL, "st_gated_act: NULL arguments");
+  const char *op = "st_gated_act";
+  ST_TRY(check_sizes(op, a->rows, a->cols));
+  if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: gate is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
+  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
+  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales));
+  if (a->rows == 0 || a->cols == 0) return ST_OK;
+  ST_TRY(check_matrix(op, "gate", a->gate, a->ldg, a->x_dtype, a->rows, a->cols, true));
+  if (a->up) ST_TRY(check_matrix(op, "up", a->up, a->ldu, a->x_dtype, a->rows, a->cols, true));
+  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->rows, a->cols, false));
+  return launch_gated_act(*a, stream);
+}
+
+st_status st_linear(const st_linear_args *a, void *stream) {
+  if (!a) return set_error(ST_E_INVAL, "st_linear: NULL arguments");
+  const char *op = "st_linear";
+  ST_TRY(check_sizes(op, a->m, a->n));
+  ST_TRY(check_sizes(op, a->m, a->k));
+  const bool sixteen = (a->x_dtype == ST_BF16 || a->x_dtype == ST_F16) && a->w_dtype == a->x_dtype;
+  const bool eight = a->x_dtype == ST_F8_E4M3 && (a->w_dtype == ST_F8_E4M3 || a->w_dtype == ST_F8_E5M2);
+  if (!sixteen && !eight)
+    return set_error(ST_E_DTYPE, "%s: x and weight are both BF16, both F16, or F8_E4M3 with F8_E4M3 or F8_E5M2 (got %d, %d)",
+                     op, (int)a->x_dtype, (int)a->w_dtype);
+  if (!is_float16or32(a->y_dtype)) return set_error(ST_E_DTYPE, "%s: the output is BF16, F16 or F32, not %d", op, (int)a->y_dtype);
+  if (a->bias && !is_float16or32(a->bias_dtype))
+    return set_error(ST_E_DTYPE, "%s: bias is BF16, F16 or F32, not %d", op, (int)a->bias_dtype);
+  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
+  if (a->x_scale && a->x_scale_count != 1 && a->x_scale_count != a->m)
+    return set_error(ST_E_INVAL, "%s: %lld scales for x (1 or m = %lld)", op, (long long)a->x_scale_count, (long long)a->m);
+  if (a->w_scale && a->w_scale_count != 1 && a->w_scale_count != a->n)
+    return set_error(ST_E_INVAL, "%s: %lld scales for weight (1 or n = %lld)", op, (long long)a->w_scale_count, (long long)a->n);
+  ST_TRY(check_vector(op, "x_scale", a->x_scale, ST_F32));
+  ST_TRY(check_vector(op, "w_scale", a->w_scale, ST_F32));
+  if (a->m == 0 || a->n == 0) return ST_OK;
+  if (a->k > 0) {
+    ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->m, a->k, true));
+    ST_TRY(check_matrix(op, "weight", a->w, a->ldw, a->w_dtype, a->n, a->k, true));
+  }
+  if (a->bias) ST_TRY(check_vector(op, "bias", a->bias, a->bias_dtype));
+  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->y_dtype, a->m, a->n, true));
+  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->m, a->n, false));
+  return launch_linear(*a, stream);
+}
+
+}  // extern "C"

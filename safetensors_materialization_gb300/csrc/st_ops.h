@@ -1,0 +1,21 @@
+// st_ops.h -- the operators on materialized tensors (st_rms_norm,
+// st_gated_act, st_linear): checked arguments and kernel launches.  Not part
+// of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include "st_internal.h"
+
+namespace stmat {
+
+constexpr float kE4M3Max = 448.0f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the smallest scale, so that 1 / scale is finite
+
+// Checked by the C entry points: dtypes known, sizes in range, pointers
+// aligned to their itemsize, rows, cols > 0.
+st_status launch_rms_norm(const st_rms_norm_args &a, void *stream);
+st_status launch_gated_act(const st_gated_act_args &a, void *stream);
+st_status launch_linear(const st_linear_args &a, void *stream);
+
+}  // namespace stmat

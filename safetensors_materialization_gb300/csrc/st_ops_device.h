@@ -1,0 +1,110 @@
+// st_ops_device.h -- conversions, activations and vector accesses shared by
+// the operator kernels (st_rowops.cu, st_linear.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "st_ops.h"
+
+namespace stmat {
+
+// max(a, b), NaN if either is one (fmaxf drops a NaN): a row with a NaN gets
+// a NaN scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+// Two E4M3 codes, nearest even, clamped to +-448, NaN kept.
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Eight consecutive elements from a 16-byte aligned address.
+template <class T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const T *e = reinterpret_cast<const T *>(&u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
+  }
+}
+
+// V consecutive elements of an array whose dtype is known at run time (the
+// branch is the same for every thread).
+template <int V>
+__device__ __forceinline__ void load_any(const void *base, st_dtype dtype, int64_t at, float (&v)[V]) {
+  if constexpr (V == 8) {
+    if (dtype == ST_BF16) load8(static_cast<const __nv_bfloat16 *>(base) + at, v);
+    else if (dtype == ST_F16) load8(static_cast<const __half *>(base) + at, v);
+    else load8(static_cast<const float *>(base) + at, v);
+  } else {
+    static_assert(V == 1, "scalar or eight");
+    if (dtype == ST_BF16) v[0] = to_float(static_cast<const __nv_bfloat16 *>(base)[at]);
+    else if (dtype == ST_F16) v[0] = to_float(static_cast<const __half *>(base)[at]);
+    else v[0] = static_cast<const float *>(base)[at];
+  }
+}
+
+// V consecutive values rounded to the dtype (F8_E4M3: already divided by the scale).
+template <int V>
+__device__ __forceinline__ void store_any(void *base, st_dtype dtype, int64_t at, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    if (dtype == ST_F8_E4M3) {
+      uint2 u;
+      u.x = pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16;
+      u.y = pack_e4m3(v[4], v[5]) | pack_e4m3(v[6], v[7]) << 16;
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(base) + at) = u;
+    } else if (dtype == ST_BF16) {
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else if (dtype == ST_F16) {
+      *reinterpret_cast<uint4 *>(static_cast<__half *>(base) + at) =
+          make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+    } else {
+      float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
+      p[0] = make_float4(v[0], v[1], v[2], v[3]);
+      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+    if (dtype == ST_F8_E4M3) static_cast<uint8_t *>(base)[at] = static_cast<uint8_t>(pack_e4m3(v[0], 0.0f));
+    else if (dtype == ST_BF16) static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(v[0]);
+    else if (dtype == ST_F16) static_cast<__half *>(base)[at] = __float2half_rn(v[0]);
+    else static_cast<float *>(base)[at] = v[0];
+  }
+}
+
+__device__ __forceinline__ float activate(float v, st_act act) {
+  switch (act) {
+    case ST_ACT_RELU: return v < 0.0f ? 0.0f : v;
+    case ST_ACT_SILU: return v / (1.0f + expf(-v));
+    case ST_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
+    case ST_ACT_GELU_TANH: return 0.5f * v * (1.0f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
+    default: return v;
+  }
+}
+
+}  // namespace stmat

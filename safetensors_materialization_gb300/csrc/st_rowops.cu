@@ -1,0 +1,240 @@
+// st_rowops.cu -- row operators for GB300 (sm_103a): the root-mean-square
+// norm with the residual's addition, and the gated activation, each with an
+// output in 16 or 32 bits or in 8 bits with scales.
+//
+// Mathematics.  With h = x + r:
+//   y = h w rstd,  rstd = 1 / sqrt(sum(h^2) / cols + eps)
+// and for 8 bits the scale max|y| / 448.  rstd is one positive number per row
+// and rounding is monotone, so max|y| = max|h w| * rstd exactly as computed:
+// the row needs one pass and one joint reduction of (sum h^2, max |h w|), and
+// the values stay in registers until they are written.  The gated activation
+// z = act(g) u needs max|z| alone.
+//
+// Bound: HBM (norm, BF16 with residual to 8 bits: 7 bytes an element).
+#include <string>
+
+#include "st_ops_device.h"
+
+namespace stmat {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr int kRowsPerBlock = 8;  // rows of one warp each
+
+struct RowArgs {
+  const void *x, *r, *w;  // norm: x, residual, weight; gate: gate, up
+  void *h, *y;
+  const float *scale;
+  float *scales;
+  int64_t ldx, ldr, ldh, ldy;
+  int64_t rows;
+  int cols;
+  float eps;
+  st_act act;
+  st_dtype w_dtype, y_dtype;
+};
+
+struct Stat {
+  float sum, top;  // sum of squares (norm), largest magnitude
+};
+
+__device__ __forceinline__ Stat warp_stat(Stat s) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    s.sum += __shfl_xor_sync(~0u, s.sum, d);
+    s.top = max_nan(s.top, __shfl_xor_sync(~0u, s.top, d));
+  }
+  return s;
+}
+
+// The block's joint statistics, in a fixed order.
+__device__ __forceinline__ Stat block_stat(Stat s) {
+  __shared__ Stat part[kMaxThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  s = warp_stat(s);
+  if (lane == 0) part[warp] = s;
+  __syncthreads();
+  return warp_stat(lane < warps ? part[lane] : Stat{0.0f, 0.0f});
+}
+
+// What every value of the row is multiplied by before it is stored: rstd (1
+// for the gated activation), then 1 / scale (1 unless 8 bits).  Two factors,
+// since their product can leave binary32's range (a zero row: 1 / scale =
+// 2^126).
+struct Factor {
+  float rstd, inv;
+};
+
+// The row's factors from its statistics; writes the row's scale.
+template <bool kNorm>
+__device__ __forceinline__ Factor row_factor(const RowArgs &a, Stat s, int64_t row, bool first) {
+  Factor f{1.0f, 1.0f};
+  if (kNorm) f.rstd = rsqrtf(s.sum / static_cast<float>(a.cols) + a.eps);
+  if (a.y_dtype != ST_F8_E4M3) return f;
+  float scale;
+  if (a.scales) {
+    scale = max_nan(s.top * f.rstd / kE4M3Max, kMinScale);
+    if (first) a.scales[row] = scale;
+  } else {
+    scale = *a.scale;
+  }
+  f.inv = 1.0f / scale;
+  return f;
+}
+
+template <bool kNorm>
+__device__ __forceinline__ float scaled(float v, Factor f) {
+  return (kNorm ? v * f.rstd : v) * f.inv;
+}
+
+// Reads V elements of the row at column c and returns the values before the
+// row's factor (h w, or z), adding to the statistics and writing h.
+template <class T, int V, bool kNorm, bool kFirst>
+__device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c, float (&v)[V], Stat &s) {
+  const st_dtype dt = sizeof(T) == 4 ? ST_F32 : std::is_same<T, __half>::value ? ST_F16 : ST_BF16;
+  load_any<V>(a.x, dt, row * a.ldx + c, v);
+  float r[V];
+  if (a.r) load_any<V>(a.r, dt, row * a.ldr + c, r);
+  if constexpr (kNorm) {
+    if (a.r) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += r[i];
+      if (a.h && kFirst) store_any<V>(a.h, dt, row * a.ldh + c, v);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) s.sum = fmaf(v[i], v[i], s.sum);
+    if (a.w) {
+      load_any<V>(a.w, a.w_dtype, c, r);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= r[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = activate(v[i], a.act);
+    if (a.r) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= r[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) s.top = max_nan(s.top, fabsf(v[i]));
+}
+
+// One row in registers: a block (or, kWarpRow, a warp) per row, NV accesses
+// of V elements per thread.
+template <class T, int V, int NV, bool kNorm, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kMaxThreads) row_kernel(const RowArgs a) {
+  const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+  const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x;
+  if (kWarpRow && row >= a.rows) return;
+  float v[NV][V];
+  Stat s{0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + t) * V;
+    if (c < a.cols) row_values<T, V, kNorm, true>(a, row, c, v[i], s);
+  }
+  s = kWarpRow ? warp_stat(s) : block_stat(s);
+  const Factor f = row_factor<kNorm>(a, s, row, t == 0);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + t) * V;
+    if (c < a.cols) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] = scaled<kNorm>(v[i][j], f);
+      store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v[i]);
+    }
+  }
+}
+
+// A row too long for registers: the second pass reads the inputs again (each
+// thread its own elements, so in-place outputs are read before they are
+// written; h is written in the second pass).
+template <class T, bool kNorm>
+__global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) {
+  const int64_t row = blockIdx.x;
+  Stat s{0.0f, 0.0f}, unused{0.0f, 0.0f};
+  float v[1];
+  for (int64_t c = threadIdx.x; c < a.cols; c += kMaxThreads) row_values<T, 1, kNorm, false>(a, row, static_cast<int>(c), v, s);
+  s = block_stat(s);
+  const Factor f = row_factor<kNorm>(a, s, row, threadIdx.x == 0);
+  for (int64_t c = threadIdx.x; c < a.cols; c += kMaxThreads) {
+    row_values<T, 1, kNorm, true>(a, row, static_cast<int>(c), v, unused);
+    v[0] = scaled<kNorm>(v[0], f);
+    store_any<1>(a.y, a.y_dtype, row * a.ldy + c, v);
+  }
+}
+
+template <class T, int V, int NV, bool kNorm>
+void launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
+  if (threads == 32)
+    row_kernel<T, V, NV, kNorm, true><<<static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
+                                        32 * kRowsPerBlock, 0, st>>>(a);
+  else
+    row_kernel<T, V, NV, kNorm, false><<<static_cast<unsigned>(a.rows), threads, 0, st>>>(a);
+}
+
+template <class T, bool kNorm>
+void launch_typed(const RowArgs &a, bool vec, cudaStream_t st) {
+  const int64_t accesses = vec ? a.cols / 8 : a.cols;
+  auto threads = [&](int nv) { return static_cast<int>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
+  if (vec && accesses <= 4 * kMaxThreads) {
+    if (accesses <= 256) launch_rows<T, 8, 1, kNorm>(a, threads(1), st);
+    else if (accesses <= 512) launch_rows<T, 8, 2, kNorm>(a, threads(2), st);
+    else launch_rows<T, 8, 4, kNorm>(a, threads(4), st);
+  } else if (!vec && accesses <= 16 * kMaxThreads) {
+    if (accesses <= 4 * 256) launch_rows<T, 1, 4, kNorm>(a, threads(4), st);
+    else launch_rows<T, 1, 16, kNorm>(a, threads(16), st);
+  } else {
+    row_loop_kernel<T, kNorm><<<static_cast<unsigned>(a.rows), kMaxThreads, 0, st>>>(a);
+  }
+}
+
+template <bool kNorm>
+st_status launch(const RowArgs &a, st_dtype x_dtype, bool vec, void *stream, const char *op) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (x_dtype == ST_BF16) launch_typed<__nv_bfloat16, kNorm>(a, vec, st);
+  else if (x_dtype == ST_F16) launch_typed<__half, kNorm>(a, vec, st);
+  else launch_typed<float, kNorm>(a, vec, st);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess)
+    return set_error(ST_E_CUDA, "%s launch (%lld rows): %s: %s", op, (long long)a.rows, cudaGetErrorName(e),
+                     cudaGetErrorString(e));
+  return ST_OK;
+}
+
+// Whether vectors of eight elements of the matrix are aligned for one access
+// (16 bytes; 8 for an 8-bit matrix).
+bool vec_ok(const void *p, int64_t ld, st_dtype dtype) {
+  if (!p) return true;
+  const uint64_t item = dtype == ST_F8_E4M3 ? 1 : dtype == ST_F32 ? 4 : 2, need = item == 1 ? 8 : 16;
+  return reinterpret_cast<uintptr_t>(p) % need == 0 && (static_cast<uint64_t>(ld) * item) % need == 0;
+}
+
+}  // namespace
+
+st_status launch_rms_norm(const st_rms_norm_args &p, void *stream) {
+  RowArgs a{};
+  a.x = p.x; a.r = p.residual; a.w = p.weight; a.h = p.h; a.y = p.y;
+  a.ldx = p.ldx; a.ldr = p.ldr; a.ldh = p.ldh; a.ldy = p.ldy;
+  a.scale = p.scale; a.scales = p.scales;
+  a.rows = p.rows; a.cols = static_cast<int>(p.cols);
+  a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.w_dtype; a.y_dtype = p.y_dtype;
+  const bool vec = p.cols % 8 == 0 && vec_ok(p.x, p.ldx, p.x_dtype) && vec_ok(p.residual, p.ldr, p.x_dtype) &&
+                   vec_ok(p.weight, 0, p.w_dtype) && vec_ok(p.h, p.ldh, p.x_dtype) && vec_ok(p.y, p.ldy, p.y_dtype);
+  return launch<true>(a, p.x_dtype, vec, stream, "st_rms_norm");
+}
+
+st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
+  RowArgs a{};
+  a.x = p.gate; a.r = p.up; a.y = p.y;
+  a.ldx = p.ldg; a.ldr = p.ldu; a.ldy = p.ldy;
+  a.scale = p.scale; a.scales = p.scales;
+  a.rows = p.rows; a.cols = static_cast<int>(p.cols);
+  a.act = p.act; a.w_dtype = ST_F32; a.y_dtype = p.y_dtype;
+  const bool vec = p.cols % 8 == 0 && vec_ok(p.gate, p.ldg, p.x_dtype) && vec_ok(p.up, p.ldu, p.x_dtype) &&
+                   vec_ok(p.y, p.ldy, p.y_dtype);
+  return launch<false>(a, p.x_dtype, vec, stream, "st_gated_act");
+}
+
+}  // namespace stmat

@@ -35,7 +35,7 @@ EXPORTS = [
     "st_materialize_noalloc", "st_static_check", "st_index_open", "st_files_open", "st_files_close", "st_files_read",
     "st_load_files", "st_cache_create", "st_cache_free", "st_cache_get", "st_cache_release",
     "st_cache_stats", "st_cache_clear", "st_load_tensors", "st_host_affinity", "st_device_reads_pageable",
-    "st_files_prefetch",
+    "st_files_prefetch", "st_rms_norm", "st_gated_act", "st_linear",
     "st_last_error", "st_status_name", "st_dtype_size", "st_dtype_name", "st_version",
 ]
 
@@ -93,6 +93,32 @@ class PlanOptions(C.Structure):
                 ("blocks_per_sm", C.c_uint32), ("unit_bytes", C.c_uint64), ("kernel", C.c_uint32),
                 ("order", C.c_uint32)]
 
+
+class RmsNormArgs(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("eps", C.c_float), ("x_dtype", C.c_int),
+                ("w_dtype", C.c_int), ("y_dtype", C.c_int), ("x", C.c_void_p), ("ldx", C.c_int64),
+                ("residual", C.c_void_p), ("ldr", C.c_int64), ("weight", C.c_void_p), ("h", C.c_void_p),
+                ("ldh", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64), ("scale", C.c_void_p),
+                ("scales", C.c_void_p)]
+
+
+class GatedActArgs(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("act", C.c_int), ("x_dtype", C.c_int),
+                ("y_dtype", C.c_int), ("gate", C.c_void_p), ("ldg", C.c_int64), ("up", C.c_void_p),
+                ("ldu", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64), ("scale", C.c_void_p),
+                ("scales", C.c_void_p)]
+
+
+class LinearArgs(C.Structure):
+    _fields_ = [("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64), ("act", C.c_int), ("x_dtype", C.c_int),
+                ("w_dtype", C.c_int), ("y_dtype", C.c_int), ("bias_dtype", C.c_int), ("x", C.c_void_p),
+                ("ldx", C.c_int64), ("w", C.c_void_p), ("ldw", C.c_int64), ("x_scale", C.c_void_p),
+                ("x_scale_count", C.c_int64), ("w_scale", C.c_void_p), ("w_scale_count", C.c_int64),
+                ("bias", C.c_void_p), ("residual", C.c_void_p), ("ldr", C.c_int64), ("y", C.c_void_p),
+                ("ldy", C.c_int64)]
+
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _lib = None
 
@@ -152,6 +178,9 @@ def lib():
             "st_host_affinity": [I, C.c_int32, C.c_char_p, S],
             "st_device_reads_pageable": [I, C.POINTER(C.c_int32)],
             "st_files_prefetch": [P, U64, U64, U32],
+            "st_rms_norm": [C.POINTER(RmsNormArgs), P],
+            "st_gated_act": [C.POINTER(GatedActArgs), P],
+            "st_linear": [C.POINTER(LinearArgs), P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -822,3 +851,209 @@ class Outputs:
 
     def tensors(self):
         return {info["name"]: self.tensor(i) for i, info in enumerate(self.infos)}
+
+
+# ------------------------------------------- operators on materialized tensors
+
+_TORCH = None  # (torch, {torch dtype: st_dtype}, {output name: (torch dtype, st_dtype)})
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        names = ("BF16", "F16", "F32", "F8_E4M3", "F8_E5M2")
+        _TORCH = (torch, {torch_dtype(n): DTYPES.index(n) for n in names},
+                  {n: (torch_dtype(n), DTYPES.index(n)) for n in names})
+    return _TORCH
+
+
+def _invalid(msg):
+    return StmatError(1, msg)
+
+
+def _matrix(t, name):
+    """(address, elements between rows, rows, columns) of a tensor whose
+    leading dimensions are the rows (a vector: one row); no copy is made."""
+    if not t.is_cuda:
+        raise _invalid(f"{name} is not on the GPU")
+    d = t.dim()
+    if d == 2:
+        rows, cols = t.shape
+        ld, inner = t.stride()
+    elif d == 1:
+        rows, cols, ld, inner = 1, t.shape[0], t.shape[0], t.stride(0)
+    elif d == 0:
+        raise _invalid(f"{name} has no dimensions")
+    else:
+        cols, inner = t.shape[-1], t.stride(-1)
+        rows, ld = 1, None
+        for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if n == 1:
+                continue
+            if ld is None:
+                ld = s
+            elif s != ld * rows:
+                raise _invalid(f"{name}: strides {tuple(t.stride())} are not one stride between rows")
+            rows *= n
+        ld = cols if ld is None else ld
+    if inner != 1 and cols > 1:
+        raise _invalid(f"{name}: the last dimension has stride {inner}, not 1")
+    return t.data_ptr(), cols if rows <= 1 else ld, rows, cols
+
+
+def _vector(t, name, counts, dtypes, codes):
+    """(address, entries, st_dtype) of a contiguous vector of one of `counts`
+    entries."""
+    if not t.is_cuda:
+        raise _invalid(f"{name} is not on the GPU")
+    n = t.numel()
+    if n not in counts or not t.is_contiguous():
+        raise _invalid(f"{name}: a contiguous tensor of {' or '.join(map(str, counts))} entries is needed")
+    code = codes.get(t.dtype)
+    if code not in dtypes:
+        raise StmatError(6, f"{name}: {t.dtype} is not one of {', '.join(DTYPES[d] for d in dtypes)}")
+    return t.data_ptr(), n, code
+
+
+_FLOATS = (10, 9, 11)  # BF16, F16, F32
+_F32 = (11,)
+_E4M3 = 13
+
+
+def _dst(dst, like, dsts, codes):
+    if dst is None:
+        return like, codes.get(like, -1)
+    if dst not in dsts:
+        raise StmatError(6, f"dst {dst!r} is not one of {', '.join(dsts)}")
+    return dsts[dst]
+
+
+class _On:
+    """Runs a call on `stream` (None: torch's current stream): outputs are
+    allocated there, and inputs stay allocated until its work is done."""
+
+    __slots__ = ("ctx", "stream")
+
+    def __init__(self, torch, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        self.stream, self.ctx = stream, torch.cuda.stream(stream)
+
+    def run(self, fn, tensors):
+        with self.ctx:
+            got = fn()
+        for t in tensors:
+            if t is not None:
+                t.record_stream(self.stream)
+        return got
+
+
+def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stream=None):
+    """st_rms_norm on the rows of x (BF16, F16 or F32; leading dimensions are
+    rows): h = x + residual, y = h * weight / sqrt(mean(h^2) + eps).
+
+    dst: "BF16", "F16", "F32" or "F8_E4M3" (default: x's dtype).  F8_E4M3 with
+    scale None writes one scale per row; scale: a one-element F32 tensor to
+    use instead.  Returns (y, scales or None, h in x's dtype, or None without
+    a residual); y * scales[..., None] stands for the normed rows."""
+    torch, codes, dsts = _torch()
+    if stream is not None:
+        return _On(torch, stream).run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
+                                      (x, weight, residual, scale))
+    a = RmsNormArgs()
+    a.x, a.ldx, rows, cols = _matrix(x, "x")
+    a.rows, a.cols, a.eps, a.x_dtype = rows, cols, eps, codes.get(x.dtype, -1)
+    ydt, a.y_dtype = _dst(dst, x.dtype, dsts, codes)
+    if weight is not None:
+        a.weight, _, a.w_dtype = _vector(weight, "weight", (cols,), _FLOATS, codes)
+    h = scales = None
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, x: {tuple(x.shape)} {x.dtype}")
+        a.residual, a.ldr, _, _ = _matrix(residual, "residual")
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        a.h, a.ldh = h.data_ptr(), cols
+    y = torch.empty(x.shape, dtype=ydt, device=x.device)
+    a.y, a.ldy = y.data_ptr(), cols
+    if scale is not None:
+        a.scale = _vector(scale, "scale", (1,), _F32, codes)[0]
+    elif a.y_dtype == _E4M3:
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        a.scales = scales.data_ptr()
+    _check(lib().st_rms_norm(a, torch.cuda.current_stream().cuda_stream))
+    return y, scales, h
+
+
+def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
+    """st_gated_act: y = act(gate) * up (act(gate) without up) on rows of BF16,
+    F16 or F32; gate and up may be the halves of one product's columns.  act:
+    "none", "relu", "silu", "gelu" or "gelu_tanh"; dst and scale as for
+    rms_norm.  Returns (y, scales or None)."""
+    torch, codes, dsts = _torch()
+    if stream is not None:
+        return _On(torch, stream).run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
+    a = GatedActArgs()
+    a.gate, a.ldg, a.rows, a.cols = _matrix(gate, "gate")
+    a.act, a.x_dtype = ACTS.get(act, -1), codes.get(gate.dtype, -1)
+    ydt, a.y_dtype = _dst(dst, gate.dtype, dsts, codes)
+    if up is not None:
+        if up.shape != gate.shape or up.dtype != gate.dtype:
+            raise _invalid(f"up: {tuple(up.shape)} {up.dtype}, gate: {tuple(gate.shape)} {gate.dtype}")
+        a.up, a.ldu, _, _ = _matrix(up, "up")
+    y = torch.empty(gate.shape, dtype=ydt, device=gate.device)
+    a.y, a.ldy = y.data_ptr(), gate.shape[-1]
+    scales = None
+    if scale is not None:
+        a.scale = _vector(scale, "scale", (1,), _F32, codes)[0]
+    elif a.y_dtype == _E4M3:
+        scales = torch.empty(gate.shape[:-1], dtype=torch.float32, device=gate.device)
+        a.scales = scales.data_ptr()
+    _check(lib().st_gated_act(a, torch.cuda.current_stream().cuda_stream))
+    return y, scales
+
+
+def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residual=None, dst=None, out=None,
+           stream=None):
+    """st_linear: act(x_scale * w_scale * (x @ weight.T) + bias) + residual with
+    a checkpoint's [n, k] weight; leading dimensions of x are rows.
+
+    x and weight: both BF16, both F16, or F8_E4M3 rows (rms_norm and gated_act
+    with dst="F8_E4M3") with an F8_E4M3 or F8_E5M2 weight.  x_scale: F32, one
+    entry or one per row; w_scale: F32, one entry or one per row of weight.
+    dst: "BF16", "F16" or "F32" (default: x's dtype, BF16 for 8-bit x);
+    residual has y's shape and dtype.  out: the tensor to write (may be the
+    residual); by default a new one."""
+    torch, codes, dsts = _torch()
+    if stream is not None:
+        return _On(torch, stream).run(lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
+                                      (x, weight, x_scale, w_scale, bias, residual, out))
+    a = LinearArgs()
+    a.x, a.ldx, m, k = _matrix(x, "x")
+    a.w, a.ldw, n, wk = _matrix(weight, "weight")
+    if wk != k or weight.dim() != 2:
+        raise _invalid(f"x has rows of {k}, weight is {tuple(weight.shape)}")
+    a.m, a.n, a.k, a.act = m, n, k, ACTS.get(act, -1)
+    a.x_dtype, a.w_dtype = codes.get(x.dtype, -1), codes.get(weight.dtype, -1)
+    if x_scale is not None:
+        a.x_scale, a.x_scale_count, _ = _vector(x_scale, "x_scale", (1, m), _F32, codes)
+    if w_scale is not None:
+        a.w_scale, a.w_scale_count, _ = _vector(w_scale, "w_scale", (1, n), _F32, codes)
+    if bias is not None:
+        a.bias, _, a.bias_dtype = _vector(bias, "bias", (n,), _FLOATS, codes)
+    shape = x.shape[:-1] + (n,)
+    if out is None:
+        ydt, a.y_dtype = _dst(dst, torch.bfloat16 if a.x_dtype == _E4M3 else x.dtype, dsts, codes)
+        out = torch.empty(shape, dtype=ydt, device=x.device)
+        a.y, a.ldy = out.data_ptr(), n
+    else:
+        if out.shape != shape or (dst is not None and dsts.get(dst, (None,))[0] != out.dtype):
+            raise _invalid(f"out: {tuple(out.shape)} {out.dtype}, the product is {tuple(shape)} {dst or ''}")
+        a.y_dtype = codes.get(out.dtype, -1)
+        a.y, a.ldy, _, _ = _matrix(out, "out")
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != out.dtype:
+            raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, y: {tuple(shape)} {out.dtype}")
+        a.residual, a.ldr, _, _ = _matrix(residual, "residual")
+    _check(lib().st_linear(a, torch.cuda.current_stream().cuda_stream))
+    return out
