@@ -1,69 +1,442 @@
 // st_linear.cu -- the matrix product with a checkpoint's weight, its scales,
 // bias, activation and residual, for GB300 (sm_103a).
+//
+//   y[i, j] = act(x_scale[i] w_scale[j] sum_l x[i, l] w[j, l] + bias[j]) + residual[i, j]
+//
+// split_kernel: the weight's rows are the MMA's rows (128 a tile), the tokens
+// its columns, so that one token costs no more than the 16 columns of the
+// narrowest MMA, and the weight streams through shared memory at the rate of
+// HBM.  The sum's range is split over the CTAs of a cluster, which join their
+// binary32 partial sums through distributed shared memory in rank order (no
+// workspace, no atomics, the same bits on every run).
+//
+// Both operands are staged 128 bytes of k at a time in the 128-byte swizzled
+// layout the MMA reads, by TMA, or, where a matrix's address or row stride is
+// not a multiple of 16 bytes, by eight warps that realign it on the way.
+#include <cuda.h>
+
+#include <mutex>
+
 #include "st_ops_device.h"
 
 namespace stmat {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kTileN = 128;          // weight rows per tile: the MMA's M
+constexpr int kStageK = 128;         // bytes of k per stage: one swizzle row
+constexpr int kMaxStages = 12;
+constexpr int kMaxSplit = 8;         // portable cluster size
+constexpr int kEpilogueWarps = 4;    // one per 32 TMEM lanes
+constexpr int kMmaWarp = 4, kFirstProducer = 5, kCopyWarps = 8;
+constexpr uint32_t kWaitLimit = 1u << 22;
 
-__device__ __forceinline__ float element(const void *p, st_dtype dtype, int64_t at) {
-  switch (dtype) {
-    case ST_BF16: return to_float(static_cast<const __nv_bfloat16 *>(p)[at]);
-    case ST_F16: return to_float(static_cast<const __half *>(p)[at]);
-    case ST_F8_E4M3: return static_cast<float>(static_cast<const __nv_fp8_e4m3 *>(p)[at]);
-    case ST_F8_E5M2: return static_cast<float>(static_cast<const __nv_fp8_e5m2 *>(p)[at]);
-    default: return static_cast<const float *>(p)[at];
+// One operand of the product.
+struct Side {
+  const uint8_t *p;
+  int64_t pitch;   // bytes between rows
+  int64_t span;    // bytes from the first row's start to the last row's end
+  int64_t rows;
+};
+
+struct LinArgs {
+  Side w, x;
+  int64_t m, n, kbytes;
+  int k_blocks, splits, stages, m_tiles;
+  uint32_t idesc;
+  int eight;                         // 8-bit operands
+  st_act act;
+  st_dtype y_dtype, bias_dtype;
+  const float *x_scale, *w_scale;
+  int x_scale_step, w_scale_step;    // 0: one entry for all
+  const void *bias, *residual;
+  void *y;
+  int64_t ldr, ldy;
+  uint32_t *err;
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Bounded: false after kWaitLimit polls.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+  for (uint32_t it = 0; it < kWaitLimit; ++it) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ void tma_load(const CUtensorMap *map, void *dst, uint64_t *bar, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar)) : "memory");
+}
+// Shared-memory descriptor of a K-major tile in the 128-byte swizzle: rows of
+// 128 bytes, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t tile_desc(const void *p) {
+  return (static_cast<uint64_t>(smem_addr(p) >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int eight, uint32_t add) {
+  if (eight)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The binary32 at the same shared address in the cluster's CTA `rank`.
+__device__ __forceinline__ float peer_load(const float *p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Sixteen bytes of a matrix row from byte `at` of its `row_bytes` on, at any
+// alignment: zeros past the row's end.  Aligned 16-byte words are read where
+// both lie between the matrix's first and last byte.
+__device__ __forceinline__ uint4 row_chunk(const Side &s, int64_t row, int64_t at, int64_t row_bytes) {
+  uint4 out = make_uint4(0, 0, 0, 0);
+  if (row >= s.rows || at >= row_bytes) return out;
+  const uint8_t *p = s.p + row * s.pitch + at;
+  const uint32_t r = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+  const uint8_t *a = p - r;
+  const int64_t left = row_bytes - at;
+  if (left >= 16 && r == 0) return *reinterpret_cast<const uint4 *>(p);
+  if (left >= 16 && a >= s.p && a + 32 <= s.p + s.span) {
+    const uint4 lo = reinterpret_cast<const uint4 *>(a)[0], hi = reinterpret_cast<const uint4 *>(a)[1];
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t v[6], u[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = r & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) u[i] = r & 4 ? v[i + 1] : v[i];
+    const uint32_t sh = 8 * (r & 3);
+    return make_uint4(__funnelshift_r(u[0], u[1], sh), __funnelshift_r(u[1], u[2], sh), __funnelshift_r(u[2], u[3], sh),
+                      __funnelshift_r(u[3], u[4], sh));
+  }
+  uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < left) v[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// `rows` tile rows of a side into a swizzled stage, by kCopyWarps warps.
+template <int kRows>
+__device__ __forceinline__ void copy_tile(const Side &s, uint8_t *dst, int64_t row0, int64_t at, int64_t row_bytes, int t) {
+  constexpr int kChunks = kRows * 8, kBatch = 4, kThreads = kCopyWarps * 32;
+#pragma unroll 1
+  for (int c0 = t; c0 < kChunks; c0 += kThreads * kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int c = c0 + i * kThreads;
+      if (c < kChunks) v[i] = row_chunk(s, row0 + c / 8, at + (c % 8) * 16, row_bytes);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int c = c0 + i * kThreads, row = c / 8;
+      if (c < kChunks) *reinterpret_cast<uint4 *>(dst + row * 128 + (((c % 8) ^ (row & 7)) << 4)) = v[i];
+    }
   }
 }
 
-// One 64 x 64 tile of y per block, 4 x 4 of it per thread, binary32 FMAs.
-__global__ void __launch_bounds__(kThreads) linear_simple(const st_linear_args a) {
-  __shared__ float xs[kStep][kTile + 1], ws[kStep][kTile + 1];
-  const int64_t m0 = int64_t(blockIdx.y) * kTile, n0 = int64_t(blockIdx.x) * kTile;
-  const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.k; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-      const int r = i / kStep, c = i % kStep;
-      const bool kin = k0 + c < a.k;
-      xs[c][r] = kin && m0 + r < a.m ? element(a.x, a.x_dtype, (m0 + r) * a.ldx + k0 + c) : 0.0f;
-      ws[c][r] = kin && n0 + r < a.n ? element(a.w, a.w_dtype, (n0 + r) * a.ldw + k0 + c) : 0.0f;
+template <int BM, bool kTma>
+__global__ void __launch_bounds__((kFirstProducer + (kTma ? 1 : kCopyWarps)) * 32)
+split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+             const __grid_constant__ LinArgs a) {
+  constexpr int kStageBytes = (kTileN + BM) * kStageK;
+  constexpr int kCols = BM < 32 ? 32 : BM;  // TMEM columns
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x % a.splits;
+  const int64_t tile = blockIdx.x / a.splits;
+  const int64_t m0 = tile % a.m_tiles * BM, n0 = tile / a.m_tiles * kTileN;
+  const int first = static_cast<int>(int64_t(a.k_blocks) * rank / a.splits);
+  const int blocks = static_cast<int>(int64_t(a.k_blocks) * (rank + 1) / a.splits) - first;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      bar_init(&full[i], kTma ? 1 : kCopyWarps * 32);
+      bar_init(&empty[i], 1);
     }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kStep; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[c][tm + 16 * i], ws[c][tn + 16 * j], acc[i][j]);
-    __syncthreads();
+    bar_init(&done, 1);
+    failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + tm + 16 * i, n = n0 + tn + 16 * j;
-      if (m >= a.m || n >= a.n) continue;
-      float v = acc[i][j];
-      if (a.x_scale) v *= a.x_scale[a.x_scale_count == 1 ? 0 : m];
-      if (a.w_scale) v *= a.w_scale[a.w_scale_count == 1 ? 0 : n];
-      if (a.bias) v += element(a.bias, a.bias_dtype, n);
-      v = activate(v, a.act);
-      if (a.residual) v += element(a.residual, a.y_dtype, m * a.ldr + n);
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "r"(kCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+
+  if (warp >= kFirstProducer) {
+    if (kTma) {
+      if (lane == 0) {
+        int i = 0;
+        bool ok = true;
+        for (; i < blocks && ok; ++i) {
+          const int s = i % a.stages;
+          if (i >= a.stages && !bar_wait(&empty[s], (i / a.stages - 1) & 1)) { ok = false; break; }
+          uint8_t *stage = smem + s * kStageBytes;
+          bar_expect(&full[s], kStageBytes);
+          const int at = (first + i) * (a.eight ? kStageK : kStageK / 2);
+          tma_load(&wmap, stage, &full[s], at, static_cast<int32_t>(n0));
+          tma_load(&xmap, stage + kTileN * kStageK, &full[s], at, static_cast<int32_t>(m0));
+        }
+        if (!ok) {  // a wait gave up: the copies in flight land before the CTA ends
+          failed = 1;
+          for (int j = i < a.stages ? 0 : i - a.stages; j < i; ++j) bar_wait(&full[j % a.stages], (j / a.stages) & 1);
+        }
+      }
+    } else {
+      const int t = threadIdx.x - kFirstProducer * 32;
+      for (int i = 0; i < blocks; ++i) {
+        const int s = i % a.stages;
+        if (i >= a.stages && !bar_wait(&empty[s], (i / a.stages - 1) & 1)) { failed = 1; break; }
+        uint8_t *stage = smem + s * kStageBytes;
+        const int64_t at = int64_t(first + i) * kStageK;
+        copy_tile<kTileN>(a.w, stage, n0, at, a.kbytes, t);
+        copy_tile<BM>(a.x, stage + kTileN * kStageK, m0, at, a.kbytes, t);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        bar_arrive(&full[s]);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && blocks > 0) {
+      bool ok = true;
+      for (int i = 0; i < blocks && ok; ++i) {
+        const int s = i % a.stages;
+        if (!bar_wait(&full[s], (i / a.stages) & 1)) { ok = false; break; }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t wd = tile_desc(smem + s * kStageBytes), xd = tile_desc(smem + s * kStageBytes + kTileN * kStageK);
+#pragma unroll
+        for (int j = 0; j < kStageK / 32; ++j) mma(tmem, wd + 2 * j, xd + 2 * j, a.idesc, a.eight, i > 0 || j > 0);
+        mma_commit(&empty[s]);
+      }
+      if (!ok) failed = 1;
+      mma_commit(&done);
+    }
+  }
+  __syncwarp();
+
+  float *part = reinterpret_cast<float *>(smem);  // [BM][kTileN], over the stages
+  if (warp < kEpilogueWarps) {
+    if (blocks > 0) {
+      if (!bar_wait(&done, 0)) failed = 1;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+      for (int c = 0; c < BM; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * kTileN + threadIdx.x] = __uint_as_float(v[j]);
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    } else {
+      for (int c = 0; c < BM; ++c) part[c * kTileN + threadIdx.x] = 0.0f;
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  if (a.splits > 1) cluster_sync();
+  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
+
+  const int64_t n = n0 + threadIdx.x;
+  if (warp < kEpilogueWarps && n < a.n) {
+    const float ws = a.w_scale ? a.w_scale[n * a.w_scale_step] : 1.0f;
+    float b[1] = {0.0f};
+    if (a.bias) load_any<1>(a.bias, a.bias_dtype, n, b);
+    const int cols = static_cast<int>(a.m - m0 < BM ? a.m - m0 : BM);
+    for (int c = static_cast<int>(rank); c < cols; c += a.splits) {
+      const int64_t m = m0 + c;
+      float v = part[c * kTileN + threadIdx.x];
+      if (a.splits > 1) {
+        v = 0.0f;
+        for (int r = 0; r < a.splits; ++r) v += peer_load(&part[c * kTileN + threadIdx.x], r);
+      }
+      if (a.x_scale) v *= a.x_scale[m * a.x_scale_step];
+      v = activate(v * ws + b[0], a.act);
+      if (a.residual) {
+        float r[1];
+        load_any<1>(a.residual, a.y_dtype, m * a.ldr + n, r);
+        v += r[0];
+      }
       const float out[1] = {v};
       store_any<1>(a.y, a.y_dtype, m * a.ldy + n, out);
     }
+  }
+  if (a.splits > 1) cluster_sync();  // the partial sums stay until every CTA has read them
+}
+
+// ------------------------------------------------------------------- host
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+st_status encoder(EncodeFn *out) {
+  static std::mutex mu;
+  static EncodeFn fn = nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!fn) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess || found != cudaDriverEntryPointSuccess || !p)
+      return set_error(ST_E_CUDA, "st_linear: the driver has no cuTensorMapEncodeTiled (%s)", cudaGetErrorName(e));
+    fn = reinterpret_cast<EncodeFn>(p);
+  }
+  *out = fn;
+  return ST_OK;
+}
+
+// Whether TMA can read the matrix: address and row stride multiples of 16
+// bytes, the stride under 2^40.
+bool tma_ok(const Side &s) {
+  return reinterpret_cast<uintptr_t>(s.p) % 16 == 0 && (s.rows == 1 || (s.pitch > 0 && s.pitch % 16 == 0 && s.pitch < (int64_t(1) << 40)));
+}
+
+st_status encode(CUtensorMap *map, const Side &s, int64_t k, int item, int box_rows) {
+  EncodeFn fn = nullptr;
+  const st_status st = encoder(&fn);
+  if (st != ST_OK) return st;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(s.rows)};
+  const cuuint64_t stride[1] = {s.rows == 1 ? static_cast<cuuint64_t>((k * item + 15) / 16 * 16) : static_cast<cuuint64_t>(s.pitch)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kStageK / item), static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  const CUresult r = fn(map, item == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                        const_cast<uint8_t *>(s.p), dims, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(ST_E_CUDA, "st_linear: tensor map of %lld x %lld refused (%d)", (long long)s.rows, (long long)k, static_cast<int>(r));
+  return ST_OK;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+  return sms;
+}
+
+template <int BM, bool kTma>
+st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int64_t tiles, cudaStream_t st) {
+  constexpr int kStageBytes = (kTileN + BM) * kStageK;
+  // About half of the SM's shared memory, so that two CTAs share one, but at
+  // least three stages and room for the partial sums.
+  a.stages = 108 * 1024 / kStageBytes;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  if (a.stages < 3) a.stages = 3;
+  const int smem = a.stages * kStageBytes + 1024;
+  static_assert(BM * kTileN * 4 <= 3 * kStageBytes, "partial sums fit over the stages");
+  auto kernel = split_kernel<BM, kTma>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits));
+    cfg.blockDim = dim3((kFirstProducer + (kTma ? 1 : kCopyWarps)) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, a);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return set_error(ST_E_CUDA, "st_linear launch (%lld x %lld, %lld bytes of k): %s: %s", (long long)a.m, (long long)a.n,
+                     (long long)a.kbytes, cudaGetErrorName(e), cudaGetErrorString(e));
+  }
+  return ST_OK;
 }
 
 }  // namespace
 
-st_status launch_linear(const st_linear_args &a, void *stream) {
-  const dim3 grid(static_cast<unsigned>((a.n + kTile - 1) / kTile), static_cast<unsigned>((a.m + kTile - 1) / kTile));
-  linear_simple<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess)
-    return set_error(ST_E_CUDA, "st_linear launch (%lld x %lld x %lld): %s: %s", (long long)a.m, (long long)a.n,
-                     (long long)a.k, cudaGetErrorName(e), cudaGetErrorString(e));
-  return ST_OK;
+st_status launch_linear(const st_linear_args &p, void *stream) {
+  const int item = p.x_dtype == ST_BF16 || p.x_dtype == ST_F16 ? 2 : 1;
+  LinArgs a{};
+  a.m = p.m; a.n = p.n; a.kbytes = p.k * item;
+  a.eight = item == 1;
+  a.act = p.act; a.y_dtype = p.y_dtype; a.bias_dtype = p.bias_dtype;
+  a.x_scale = p.x_scale; a.w_scale = p.w_scale;
+  a.x_scale_step = p.x_scale_count > 1; a.w_scale_step = p.w_scale_count > 1;
+  a.bias = p.bias; a.residual = p.residual; a.y = p.y;
+  a.ldr = p.ldr; a.ldy = p.ldy;
+  auto side = [&](const void *ptr, int64_t ld, int64_t rows) {
+    return Side{static_cast<const uint8_t *>(ptr), ld * item, ld * item * (rows - 1) + a.kbytes, rows};
+  };
+  a.x = side(p.x, p.ldx, p.m);
+  a.w = side(p.w, p.ldw, p.n);
+  void *scratch = nullptr;
+  st_status s = static_scratch(&scratch);
+  if (s != ST_OK) return s;
+  a.err = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(scratch) + kStaticErrOffset);
+
+  // Columns of the MMA: the tokens, up to 128; m tiles beyond.
+  const int bm = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
+  a.m_tiles = static_cast<int>((p.m + bm - 1) / bm);
+  const int64_t tiles = (p.n + kTileN - 1) / kTileN * a.m_tiles;
+  a.k_blocks = static_cast<int>((a.kbytes + kStageK - 1) / kStageK);
+  // The sum is split until the CTAs fill the SMs twice, each with at least
+  // four stages of work.
+  a.splits = 1;
+  const int64_t want = 2 * sm_count();
+  while (a.splits < kMaxSplit && tiles * a.splits * 2 <= want && a.k_blocks / (a.splits * 2) >= 4) a.splits *= 2;
+  if (tiles * a.splits > 0x7fffffff)
+    return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
+  // Instruction descriptor: binary32 accumulators; formats of the weight (A)
+  // and of x (B); both K-major; 128 x bm.
+  const uint32_t fw = item == 2 ? (p.w_dtype == ST_BF16) : (p.w_dtype == ST_F8_E5M2), fx = item == 2 ? (p.x_dtype == ST_BF16) : 0;
+  a.idesc = (1u << 4) | (fw << 7) | (fx << 10) | (static_cast<uint32_t>(bm / 8) << 17) | ((kTileN / 16) << 24);
+  CUtensorMap wmap{}, xmap{};
+  const bool tma = p.k > 0 && tma_ok(a.w) && tma_ok(a.x);
+  if (tma) {
+    s = encode(&wmap, a.w, p.k, item, kTileN);
+    if (s == ST_OK) s = encode(&xmap, a.x, p.k, item, bm);
+    if (s != ST_OK) return s;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define ST_SPLIT(BM) (tma ? launch_split<BM, true>(a, wmap, xmap, tiles, st) : launch_split<BM, false>(a, wmap, xmap, tiles, st))
+  switch (bm) {
+    case 16: return ST_SPLIT(16);
+    case 32: return ST_SPLIT(32);
+    case 64: return ST_SPLIT(64);
+    default: return ST_SPLIT(128);
+  }
+#undef ST_SPLIT
 }
 
 }  // namespace stmat
