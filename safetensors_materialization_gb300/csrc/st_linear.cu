@@ -10,6 +10,12 @@
 // binary32 partial sums through distributed shared memory in rank order (no
 // workspace, no atomics, the same bits on every run).
 //
+// dense_kernel: many tokens.  A pair of CTAs (two SMs) computes 256 tokens x up
+// to 256 weight rows with one MMA: each holds 128 tokens and half of the
+// weight rows, so a stage's 32 KB per SM feed twice the products of a lone
+// CTA's.  The pairs stay resident and take tiles in turn; a tile's sums are
+// read out of one half of TMEM while the next tile's are formed in the other.
+//
 // Both operands are staged 128 bytes of k at a time in the 128-byte swizzled
 // layout the MMA reads, by TMA, or, where a matrix's address or row stride is
 // not a multiple of 16 bytes, by eight warps that realign it on the way.
@@ -30,6 +36,14 @@ constexpr int kEpilogueWarps = 4;    // one per 32 TMEM lanes
 constexpr int kMmaWarp = 4, kFirstProducer = 5, kCopyWarps = 8;
 constexpr uint32_t kWaitLimit = 1u << 22;
 
+constexpr int kPairM = 256;          // tokens per pair of CTAs
+constexpr int kPairMaxN = 256;       // weight rows per pair, a multiple of 32
+constexpr int kDenseStages = 6;
+constexpr int kDenseEpilogueWarps = 8;  // two per 32 TMEM lanes: halves of the columns
+constexpr int kDenseMmaWarp = 8, kDenseCopyWarp = 9, kDenseThreads = 320;
+constexpr int kDenseStageBytes = 2 * 128 * kStageK;
+constexpr int kChunk = 32;           // columns an epilogue warp reads at a time
+
 // One operand of the product.
 struct Side {
   const uint8_t *p;
@@ -42,6 +56,8 @@ struct LinArgs {
   Side w, x;
   int64_t m, n, kbytes;
   int k_blocks, splits, stages, m_tiles;
+  int n_tiles, tile_n;               // dense_kernel: weight rows per tile
+  int vec;                           // dense_kernel: y and residual rows take 32-byte accesses
   uint32_t idesc;
   int eight;                         // 8-bit operands
   st_act act;
@@ -287,17 +303,290 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         for (int r = 0; r < a.splits; ++r) v += peer_load(&part[c * kTileN + threadIdx.x], r);
       }
       if (a.x_scale) v *= a.x_scale[m * a.x_scale_step];
-      v = activate(v * ws + b[0], a.act);
+      float out[1] = {v * ws + b[0]};
+      activate(out, a.act);
       if (a.residual) {
         float r[1];
         load_any<1>(a.residual, a.y_dtype, m * a.ldr + n, r);
-        v += r[0];
+        out[0] += r[0];
       }
-      const float out[1] = {v};
       store_any<1>(a.y, a.y_dtype, m * a.ldy + n, out);
     }
   }
   if (a.splits > 1) cluster_sync();  // the partial sums stay until every CTA has read them
+}
+
+// ---------------------------------------------------------- dense_kernel
+
+// The address of this CTA's shared variable in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A tile of this CTA whose bytes count on a barrier that may be the peer's.
+__device__ __forceinline__ void pair_load(const CUtensorMap *map, void *dst, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int eight, uint32_t add) {
+  if (eight)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+// Arrives on the barrier at this address in both CTAs once the MMAs so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               ::"r"(smem_addr(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[32]) {
+  uint32_t v[32];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+                 "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+                 "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+}
+__device__ __forceinline__ void ld32(const void *p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void st32(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+
+// Residual and y of one token and kChunk columns, in 32-byte accesses.
+__device__ __forceinline__ void add_row(const void *base, st_dtype dtype, int64_t at, float (&v)[kChunk]) {
+  uint32_t u[8];
+  if (dtype == ST_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ld32(static_cast<const float *>(base) + at + 8 * i, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * i + j] += __uint_as_float(u[j]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ld32(static_cast<const uint16_t *>(base) + at + 16 * i, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float2 f;
+      if (dtype == ST_BF16) f = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+      else f = __half22float2(*reinterpret_cast<const __half2 *>(&u[j]));
+      v[16 * i + 2 * j] += f.x;
+      v[16 * i + 2 * j + 1] += f.y;
+    }
+  }
+}
+__device__ __forceinline__ void put_row(void *base, st_dtype dtype, int64_t at, const float (&v)[kChunk]) {
+  uint32_t u[8];
+  if (dtype == ST_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[8 * i + j]);
+      st32(static_cast<float *>(base) + at + 8 * i, u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      u[j] = dtype == ST_BF16 ? pack_bf16(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]) : pack_f16(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
+    st32(static_cast<uint16_t *>(base) + at + 16 * i, u);
+  }
+}
+
+// Tile t of the launch: groups of eight token tiles, so that the tiles in
+// flight share their operands in L2.
+struct TileAt {
+  int64_t m0, n0;
+};
+__device__ __forceinline__ TileAt tile_at(const LinArgs &a, int t) {
+  constexpr int kGroup = 8;
+  const int per = kGroup * a.n_tiles, g = t / per, in = t % per;
+  const int rows = min(kGroup, a.m_tiles - g * kGroup);
+  return {int64_t(g * kGroup + in % rows) * kPairM, int64_t(in / rows) * a.tile_n};
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads)
+dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+             const __grid_constant__ LinArgs a) {
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  __shared__ uint64_t full[kDenseStages], empty[kDenseStages], sums[2], taken[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed;
+  __shared__ float turn[kDenseEpilogueWarps][32][17];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x & 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.m_tiles * a.n_tiles;
+  const int half_n = a.tile_n / 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kDenseStages; ++i) {
+      bar_init(&full[i], 1);
+      bar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sums[i], 1);
+      bar_init(&taken[i], 2 * kDenseEpilogueWarps);
+    }
+    failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kDenseMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+
+  if (warp == kDenseCopyWarp) {
+    if (lane == 0) {
+      // This CTA's tokens and its half of the weight rows; the bytes of both
+      // CTAs count on the first one's barrier.
+      const uint32_t bytes = (128 + half_n) * kStageK;
+      const int step = a.eight ? kStageK : kStageK / 2;
+      int i = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const TileAt at = tile_at(a, t);
+        for (int b = 0; b < a.k_blocks; ++b, ++i) {
+          const int s = i % kDenseStages;
+          if (i >= kDenseStages && !bar_wait(&empty[s], (i / kDenseStages - 1) & 1)) { ok = false; break; }
+          uint8_t *stage = smem + s * kDenseStageBytes;
+          if (rank == 0) bar_expect(&full[s], 2 * bytes);
+          const uint32_t bar = peer_addr(&full[s], 0);
+          pair_load(&xmap, stage, bar, b * step, static_cast<int32_t>(at.m0 + rank * 128));
+          pair_load(&wmap, stage + 128 * kStageK, bar, b * step, static_cast<int32_t>(at.n0 + rank * half_n));
+        }
+      }
+      if (!ok) failed = 1;
+      // The stages in flight are released (or, after a wait that gave up,
+      // have had their time) before the CTA ends.
+      for (int j = i < kDenseStages ? 0 : i - kDenseStages; j < i; ++j)
+        if (!bar_wait(&empty[j % kDenseStages], (j / kDenseStages) & 1)) failed = 1;
+    }
+  } else if (warp == kDenseMmaWarp) {
+    if (lane == 0 && rank == 0) {
+      int i = 0, n = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs, ++n) {
+        const int buf = n & 1;
+        if (n >= 2 && !bar_wait(&taken[buf], (n / 2 - 1) & 1)) { ok = false; break; }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int b = 0; b < a.k_blocks; ++b, ++i) {
+          const int s = i % kDenseStages;
+          if (!bar_wait(&full[s], (i / kDenseStages) & 1)) { ok = false; break; }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t xd = tile_desc(smem + s * kDenseStageBytes), wd = tile_desc(smem + s * kDenseStageBytes + 128 * kStageK);
+#pragma unroll
+          for (int j = 0; j < kStageK / 32; ++j)
+            pair_mma(tmem + buf * kPairMaxN, xd + 2 * j, wd + 2 * j, a.idesc, a.eight, b > 0 || j > 0);
+          pair_commit(&empty[s]);
+        }
+        pair_commit(&sums[buf]);
+      }
+      if (!ok) failed = 1;
+    }
+  } else {
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t taken_at[2] = {peer_addr(&taken[0], 0), peer_addr(&taken[1], 0)};
+    const int chunks = a.tile_n / kChunk;
+    int n = 0;
+    for (int t = pair; t < tiles; t += pairs, ++n) {
+      const TileAt at = tile_at(a, t);
+      const int buf = n & 1;
+      if (!bar_wait(&sums[buf], (n / 2) & 1)) { failed = 1; break; }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const int64_t m = at.m0 + rank * 128 + quarter * 32 + lane;
+      const bool row = m < a.m;
+      float xs = row && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
+      for (int c = half; c < chunks; c += 2) {
+        const int64_t n0 = at.n0 + c * kChunk;
+        if (n0 >= a.n) break;
+        // One column's scale and bias per lane, handed round below.
+        float wl = 1.0f, bl[1] = {0.0f};
+        if (n0 + lane < a.n) {
+          if (a.w_scale) wl = a.w_scale[(n0 + lane) * a.w_scale_step];
+          if (a.bias) load_any<1>(a.bias, a.bias_dtype, n0 + lane, bl);
+        }
+        float v[kChunk];
+        tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kPairMaxN + c * kChunk, v);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) v[j] *= xs;
+        if (a.w_scale) {
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) v[j] *= __shfl_sync(~0u, wl, j);
+        }
+        if (a.bias) {
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) v[j] += __shfl_sync(~0u, bl[0], j);
+        }
+        activate(v, a.act);
+        if (a.vec && n0 + kChunk <= a.n) {
+          if (row) {
+            if (a.residual) add_row(a.residual, a.y_dtype, m * a.ldr + n0, v);
+            put_row(a.y, a.y_dtype, m * a.ldy + n0, v);
+          }
+        } else {
+          // Rows at any alignment, or a ragged last chunk: 16 columns at a
+          // time are turned in shared memory, so that a half-warp writes one
+          // token's consecutive columns.
+          const int64_t mw = at.m0 + rank * 128 + quarter * 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) turn[warp][lane][j] = v[16 * h + j];
+            __syncwarp();
+            const int64_t col = n0 + 16 * h + (lane & 15);
+#pragma unroll 4
+            for (int r = lane >> 4; r < 32; r += 2) {
+              if (mw + r >= a.m || col >= a.n) continue;
+              float out[1] = {turn[warp][r][lane & 15]};
+              if (a.residual) {
+                float old[1];
+                load_any<1>(a.residual, a.y_dtype, (mw + r) * a.ldr + col, old);
+                out[0] += old[0];
+              }
+              store_any<1>(a.y, a.y_dtype, (mw + r) * a.ldy + col, out);
+            }
+          }
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) peer_arrive(taken_at[buf]);
+    }
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == kDenseMmaWarp) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
 }
 
 // ------------------------------------------------------------------- host
@@ -383,6 +672,20 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   return ST_OK;
 }
 
+st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, int sms, cudaStream_t st) {
+  const int smem = kDenseStages * kDenseStageBytes + 1024;
+  cudaError_t e = cudaFuncSetAttribute(dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) {
+    const int pairs = sms / 2, tiles = a.m_tiles * a.n_tiles;
+    dense_kernel<<<2 * (tiles < pairs ? tiles : pairs), kDenseThreads, smem, st>>>(xmap, wmap, a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess)
+    return set_error(ST_E_CUDA, "st_linear launch (%lld x %lld, %lld bytes of k): %s: %s", (long long)a.m, (long long)a.n,
+                     (long long)a.kbytes, cudaGetErrorName(e), cudaGetErrorString(e));
+  return ST_OK;
+}
+
 }  // namespace
 
 st_status launch_linear(const st_linear_args &p, void *stream) {
@@ -405,30 +708,56 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   if (s != ST_OK) return s;
   a.err = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(scratch) + kStaticErrOffset);
 
+  a.k_blocks = static_cast<int>((a.kbytes + kStageK - 1) / kStageK);
+  const int sms = sm_count();
+  // Instruction descriptor: binary32 accumulators; formats of A and B, both
+  // K-major; rows and columns of one MMA.
+  const uint32_t fw = item == 2 ? (p.w_dtype == ST_BF16) : (p.w_dtype == ST_F8_E5M2), fx = item == 2 ? (p.x_dtype == ST_BF16) : 0;
+  auto idesc = [](uint32_t fa, uint32_t fb, uint32_t rows, uint32_t cols) {
+    return (1u << 4) | (fa << 7) | (fb << 10) | ((cols / 8) << 17) | ((rows / 16) << 24);
+  };
+  const bool tma = p.k > 0 && tma_ok(a.w) && tma_ok(a.x);
+  CUtensorMap wmap{}, xmap{};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  if (tma && p.m >= 512) {
+    const int64_t m_tiles = (p.m + kPairM - 1) / kPairM;
+    // The tile's width: the fewest rounds of tiles over the pairs, each as
+    // long as its columns and a fixed part of the readout.
+    int64_t best = INT64_MAX;
+    for (int tn = kPairMaxN; tn >= 128; tn -= 32) {
+      const int64_t n_tiles = (p.n + tn - 1) / tn, rounds = (m_tiles * n_tiles + sms / 2 - 1) / (sms / 2), cost = rounds * (tn + 16);
+      if (cost < best) best = cost, a.tile_n = tn, a.n_tiles = static_cast<int>(n_tiles);
+    }
+    if (m_tiles * a.n_tiles > 0x3fffffff)
+      return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
+    a.m_tiles = static_cast<int>(m_tiles);
+    a.idesc = idesc(fx, fw, kPairM, a.tile_n);
+    const int out = static_cast<int>(st_dtype_size(p.y_dtype));
+    auto wide = [&](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 32 == 0 && ld * out % 32 == 0; };
+    a.vec = wide(p.y, p.ldy) && (!p.residual || wide(p.residual, p.ldr));
+    s = encode(&xmap, a.x, p.k, item, 128);
+    if (s == ST_OK) s = encode(&wmap, a.w, p.k, item, a.tile_n / 2);
+    return s == ST_OK ? launch_dense(a, xmap, wmap, sms, st) : s;
+  }
+
   // Columns of the MMA: the tokens, up to 128; m tiles beyond.
   const int bm = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
   a.m_tiles = static_cast<int>((p.m + bm - 1) / bm);
   const int64_t tiles = (p.n + kTileN - 1) / kTileN * a.m_tiles;
-  a.k_blocks = static_cast<int>((a.kbytes + kStageK - 1) / kStageK);
   // The sum is split until the CTAs fill the SMs twice, each with at least
   // four stages of work.
   a.splits = 1;
-  const int64_t want = 2 * sm_count();
+  const int64_t want = 2 * sms;
   while (a.splits < kMaxSplit && tiles * a.splits * 2 <= want && a.k_blocks / (a.splits * 2) >= 4) a.splits *= 2;
   if (tiles * a.splits > 0x7fffffff)
     return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
-  // Instruction descriptor: binary32 accumulators; formats of the weight (A)
-  // and of x (B); both K-major; 128 x bm.
-  const uint32_t fw = item == 2 ? (p.w_dtype == ST_BF16) : (p.w_dtype == ST_F8_E5M2), fx = item == 2 ? (p.x_dtype == ST_BF16) : 0;
-  a.idesc = (1u << 4) | (fw << 7) | (fx << 10) | (static_cast<uint32_t>(bm / 8) << 17) | ((kTileN / 16) << 24);
-  CUtensorMap wmap{}, xmap{};
-  const bool tma = p.k > 0 && tma_ok(a.w) && tma_ok(a.x);
+  a.idesc = idesc(fw, fx, kTileN, bm);
   if (tma) {
     s = encode(&wmap, a.w, p.k, item, kTileN);
     if (s == ST_OK) s = encode(&xmap, a.x, p.k, item, bm);
     if (s != ST_OK) return s;
   }
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define ST_SPLIT(BM) (tma ? launch_split<BM, true>(a, wmap, xmap, tiles, st) : launch_split<BM, false>(a, wmap, xmap, tiles, st))
   switch (bm) {
     case 16: return ST_SPLIT(16);

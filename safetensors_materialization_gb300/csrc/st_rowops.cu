@@ -109,8 +109,7 @@ __device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c,
       for (int i = 0; i < V; ++i) v[i] *= r[i];
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = activate(v[i], a.act);
+    activate(v, a.act);
     if (a.r) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= r[i];

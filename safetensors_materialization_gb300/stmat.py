@@ -855,7 +855,7 @@ class Outputs:
 
 # ------------------------------------------- operators on materialized tensors
 
-_TORCH = None  # (torch, {torch dtype: st_dtype}, {output name: (torch dtype, st_dtype)})
+_TORCH = None  # (torch, {torch dtype: st_dtype}, {output name: (torch dtype, st_dtype)}, stream of a device)
 
 
 def _torch():
@@ -864,7 +864,8 @@ def _torch():
         import torch
         names = ("BF16", "F16", "F32", "F8_E4M3", "F8_E5M2")
         _TORCH = (torch, {torch_dtype(n): DTYPES.index(n) for n in names},
-                  {n: (torch_dtype(n), DTYPES.index(n)) for n in names})
+                  {n: (torch_dtype(n), DTYPES.index(n)) for n in names},
+                  torch._C._cuda_getCurrentRawStream)  # 0.1 us; torch.cuda.current_stream() takes 11
     return _TORCH
 
 
@@ -957,7 +958,7 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
     scale None writes one scale per row; scale: a one-element F32 tensor to
     use instead.  Returns (y, scales or None, h in x's dtype, or None without
     a residual); y * scales[..., None] stands for the normed rows."""
-    torch, codes, dsts = _torch()
+    torch, codes, dsts, raw_stream = _torch()
     if stream is not None:
         return _On(torch, stream).run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
                                       (x, weight, residual, scale))
@@ -981,7 +982,7 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
     elif a.y_dtype == _E4M3:
         scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         a.scales = scales.data_ptr()
-    _check(lib().st_rms_norm(a, torch.cuda.current_stream().cuda_stream))
+    _check(lib().st_rms_norm(a, raw_stream(x.get_device())))
     return y, scales, h
 
 
@@ -990,7 +991,7 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
     F16 or F32; gate and up may be the halves of one product's columns.  act:
     "none", "relu", "silu", "gelu" or "gelu_tanh"; dst and scale as for
     rms_norm.  Returns (y, scales or None)."""
-    torch, codes, dsts = _torch()
+    torch, codes, dsts, raw_stream = _torch()
     if stream is not None:
         return _On(torch, stream).run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
     a = GatedActArgs()
@@ -1009,7 +1010,7 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
     elif a.y_dtype == _E4M3:
         scales = torch.empty(gate.shape[:-1], dtype=torch.float32, device=gate.device)
         a.scales = scales.data_ptr()
-    _check(lib().st_gated_act(a, torch.cuda.current_stream().cuda_stream))
+    _check(lib().st_gated_act(a, raw_stream(gate.get_device())))
     return y, scales
 
 
@@ -1024,7 +1025,7 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     dst: "BF16", "F16" or "F32" (default: x's dtype, BF16 for 8-bit x);
     residual has y's shape and dtype.  out: the tensor to write (may be the
     residual); by default a new one."""
-    torch, codes, dsts = _torch()
+    torch, codes, dsts, raw_stream = _torch()
     if stream is not None:
         return _On(torch, stream).run(lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
                                       (x, weight, x_scale, w_scale, bias, residual, out))
@@ -1055,5 +1056,5 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
         if residual.shape != shape or residual.dtype != out.dtype:
             raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, y: {tuple(shape)} {out.dtype}")
         a.residual, a.ldr, _, _ = _matrix(residual, "residual")
-    _check(lib().st_linear(a, torch.cuda.current_stream().cuda_stream))
+    _check(lib().st_linear(a, raw_stream(x.get_device())))
     return out

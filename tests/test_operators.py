@@ -405,7 +405,8 @@ def check_linear(got, want, slack):
 # more than a tile; long sums; single columns.
 LINEAR_SIZES = [(1, 1, 1), (1, 8, 16), (1, 300, 257), (3, 128, 64), (2, 1, 512), (16, 129, 40), (17, 256, 1000),
                 (33, 1111, 72), (65, 64, 2048), (100, 391, 333), (129, 257, 130), (200, 512, 4096), (300, 96, 8),
-                (257, 640, 768), (520, 1000, 520), (1, 2048, 8192), (7, 4104, 1544)]
+                (257, 640, 768), (520, 1000, 520), (1, 2048, 8192), (7, 4104, 1544), (768, 512, 128), (513, 257, 1040),
+                (1111, 2000, 80), (600, 33, 4096), (2560, 2592, 272), (777, 1, 16)]
 PAIRS = [("BF16", "BF16"), ("F16", "F16"), ("F8_E4M3", "F8_E4M3"), ("F8_E4M3", "F8_E5M2")]
 
 
@@ -442,7 +443,8 @@ def test_linear_of_integers_is_exact(stmat, m, n, k, xt, wt):
 
 @gpu
 @pytest.mark.parametrize("act", ACTS)
-@pytest.mark.parametrize("m,n,k", [(1, 200, 136), (5, 328, 64), (40, 130, 96), (150, 391, 300), (300, 520, 128)])
+@pytest.mark.parametrize("m,n,k", [(1, 200, 136), (5, 328, 64), (40, 130, 96), (150, 391, 300), (300, 520, 128), (600, 544, 256),
+                                   (530, 391, 64)])
 def test_linear_epilogue(stmat, m, n, k, act):
     """Scales per row and single, bias in each type, residual, activation."""
     for xt, wt, dst, bt, rows, cols in (("F8_E4M3", "F8_E4M3", "BF16", "BF16", m, 1),
@@ -460,7 +462,7 @@ def test_linear_epilogue(stmat, m, n, k, act):
 
 
 @gpu
-@pytest.mark.parametrize("m,n,k", [(1, 72, 64), (6, 200, 128), (130, 264, 256), (300, 300, 100)])
+@pytest.mark.parametrize("m,n,k", [(1, 72, 64), (6, 200, 128), (130, 264, 256), (300, 300, 100), (515, 304, 192)])
 @pytest.mark.parametrize("xt", ["BF16", "F8_E4M3"])
 @pytest.mark.parametrize("extra,offset", [(16, 0), (16, 16), (1, 0), (0, 1), (7, 3)])
 def test_linear_strides_and_offsets(stmat, m, n, k, xt, extra, offset):
@@ -497,7 +499,7 @@ def test_linear_empty_sum_and_sizes(stmat):
 
 
 @gpu
-@pytest.mark.parametrize("m", [1, 20, 200])
+@pytest.mark.parametrize("m", [1, 20, 200, 700])
 def test_linear_residual_in_place(stmat, m):
     x, w = operands(m, 1024, 512, "BF16", "BF16")
     r = normal(3, m, 1024, dtype=torch.bfloat16)
@@ -509,9 +511,9 @@ def test_linear_residual_in_place(stmat, m):
 
 @gpu
 @pytest.mark.parametrize("xt", ["BF16", "F8_E4M3"])
-def test_linear_nan_and_infinity(stmat, xt):
+@pytest.mark.parametrize("m,n,k", [(40, 150, 200), (600, 150, 208)])
+def test_linear_nan_and_infinity(stmat, m, n, k, xt):
     """They stay in their row and column; a tile's other rows are untouched."""
-    m, n, k = 40, 150, 200
     x, w = operands(m, n, k, xt, xt)
     x[3, 7] = math.nan
     if xt == "BF16":
