@@ -80,6 +80,14 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// One thread of the (converged) warp, chosen so that the compiler knows that
+// it runs alone: the tensor core's and TMA's operands then stay in uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+  return yes;
+}
 // Bounded: false after kWaitLimit polls.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
   for (uint32_t it = 0; it < kWaitLimit; ++it) {
@@ -90,6 +98,21 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
   }
   return false;
 }
+// The same for a whole warp that waits long: one lane polls, and pauses
+// between polls, so that the threads that feed the tensor core are not held up.
+__device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, int lane) {
+  int ok = 0;
+  if (lane == 0) {
+    for (uint32_t it = 0; it < kWaitLimit && !ok; ++it) {
+      asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                   : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+      if (!ok) __nanosleep(64);
+    }
+  }
+  ok = __shfl_sync(~0u, ok, 0);
+  // Every lane sees the phase complete (and what was written before it).
+  return ok && bar_wait(bar, parity);
+}
 __device__ __forceinline__ void tma_load(const CUtensorMap *map, void *dst, uint64_t *bar, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar)) : "memory");
@@ -99,8 +122,9 @@ __device__ __forceinline__ void tma_load(const CUtensorMap *map, void *dst, uint
 __device__ __forceinline__ uint64_t tile_desc(const void *p) {
   return (static_cast<uint64_t>(smem_addr(p) >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int eight, uint32_t add) {
-  if (eight)
+template <bool kEight>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if constexpr (kEight)
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
   else
@@ -128,6 +152,16 @@ __device__ __forceinline__ float peer_load(const float *p, uint32_t rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
+
+// A position in a ring of `stages` stages: its index, and the parity of its
+// barriers' current phase.
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++at == stages) at = 0, phase ^= 1;
+  }
+};
 
 // Sixteen bytes of a matrix row from byte `at` of its `row_bytes` on, at any
 // alignment: zeros past the row's end.  Aligned 16-byte words are read where
@@ -179,7 +213,7 @@ __device__ __forceinline__ void copy_tile(const Side &s, uint8_t *dst, int64_t r
   }
 }
 
-template <int BM, bool kTma>
+template <int BM, bool kTma, bool kEight>
 __global__ void __launch_bounds__((kFirstProducer + (kTma ? 1 : kCopyWarps)) * 32)
 split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
              const __grid_constant__ LinArgs a) {
@@ -216,51 +250,48 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
 
+  Ring r;
   if (warp >= kFirstProducer) {
     if (kTma) {
-      if (lane == 0) {
+      if (elect_one()) {
         int i = 0;
-        bool ok = true;
-        for (; i < blocks && ok; ++i) {
-          const int s = i % a.stages;
-          if (i >= a.stages && !bar_wait(&empty[s], (i / a.stages - 1) & 1)) { ok = false; break; }
-          uint8_t *stage = smem + s * kStageBytes;
-          bar_expect(&full[s], kStageBytes);
-          const int at = (first + i) * (a.eight ? kStageK : kStageK / 2);
-          tma_load(&wmap, stage, &full[s], at, static_cast<int32_t>(n0));
-          tma_load(&xmap, stage + kTileN * kStageK, &full[s], at, static_cast<int32_t>(m0));
+        constexpr int kStep = kEight ? kStageK : kStageK / 2;
+        for (int at = first * kStep; i < blocks; ++i, at += kStep, r.next(a.stages)) {
+          // Before its first use a stage counts as released.
+          if (!bar_wait(&empty[r.at], r.phase ^ 1)) break;
+          uint8_t *stage = smem + r.at * kStageBytes;
+          bar_expect(&full[r.at], kStageBytes);
+          tma_load(&wmap, stage, &full[r.at], at, static_cast<int32_t>(n0));
+          tma_load(&xmap, stage + kTileN * kStageK, &full[r.at], at, static_cast<int32_t>(m0));
         }
-        if (!ok) {  // a wait gave up: the copies in flight land before the CTA ends
+        if (i < blocks) {  // a wait gave up: the copies in flight land before the CTA ends
           failed = 1;
           for (int j = i < a.stages ? 0 : i - a.stages; j < i; ++j) bar_wait(&full[j % a.stages], (j / a.stages) & 1);
         }
       }
     } else {
       const int t = threadIdx.x - kFirstProducer * 32;
-      for (int i = 0; i < blocks; ++i) {
-        const int s = i % a.stages;
-        if (i >= a.stages && !bar_wait(&empty[s], (i / a.stages - 1) & 1)) { failed = 1; break; }
-        uint8_t *stage = smem + s * kStageBytes;
+      for (int i = 0; i < blocks; ++i, r.next(a.stages)) {
+        if (!bar_wait(&empty[r.at], r.phase ^ 1)) { failed = 1; break; }
+        uint8_t *stage = smem + r.at * kStageBytes;
         const int64_t at = int64_t(first + i) * kStageK;
         copy_tile<kTileN>(a.w, stage, n0, at, a.kbytes, t);
         copy_tile<BM>(a.x, stage + kTileN * kStageK, m0, at, a.kbytes, t);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        bar_arrive(&full[s]);
+        bar_arrive(&full[r.at]);
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && blocks > 0) {
-      bool ok = true;
-      for (int i = 0; i < blocks && ok; ++i) {
-        const int s = i % a.stages;
-        if (!bar_wait(&full[s], (i / a.stages) & 1)) { ok = false; break; }
+    if (blocks > 0 && elect_one()) {
+      uint32_t add = 0;
+      for (int i = 0; i < blocks; ++i, r.next(a.stages)) {
+        if (!bar_wait(&full[r.at], r.phase)) { failed = 1; break; }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t wd = tile_desc(smem + s * kStageBytes), xd = tile_desc(smem + s * kStageBytes + kTileN * kStageK);
+        const uint64_t wd = tile_desc(smem + r.at * kStageBytes), xd = wd + (kTileN * kStageK >> 4);
 #pragma unroll
-        for (int j = 0; j < kStageK / 32; ++j) mma(tmem, wd + 2 * j, xd + 2 * j, a.idesc, a.eight, i > 0 || j > 0);
-        mma_commit(&empty[s]);
+        for (int j = 0; j < kStageK / 32; ++j, add = 1) mma<kEight>(tmem, wd + 2 * j, xd + 2 * j, a.idesc, add);
+        mma_commit(&empty[r.at]);
       }
-      if (!ok) failed = 1;
       mma_commit(&done);
     }
   }
@@ -332,8 +363,9 @@ __device__ __forceinline__ void pair_load(const CUtensorMap *map, void *dst, uin
   asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int eight, uint32_t add) {
-  if (eight)
+template <bool kEight>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if constexpr (kEight)
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
   else
@@ -424,6 +456,7 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs &a, int t) {
   return {int64_t(g * kGroup + in % rows) * kPairM, int64_t(in / rows) * a.tile_n};
 }
 
+template <bool kEight>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads)
 dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ LinArgs a) {
@@ -461,51 +494,49 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
 
+  Ring r;
   if (warp == kDenseCopyWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
       // This CTA's tokens and its half of the weight rows; the bytes of both
-      // CTAs count on the first one's barrier.
-      const uint32_t bytes = (128 + half_n) * kStageK;
-      const int step = a.eight ? kStageK : kStageK / 2;
-      int i = 0;
+      // CTAs count on the first one's barriers.
+      const uint32_t bytes = (128 + half_n) * kStageK, bars = peer_addr(full, 0);
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
         const TileAt at = tile_at(a, t);
-        for (int b = 0; b < a.k_blocks; ++b, ++i) {
-          const int s = i % kDenseStages;
-          if (i >= kDenseStages && !bar_wait(&empty[s], (i / kDenseStages - 1) & 1)) { ok = false; break; }
-          uint8_t *stage = smem + s * kDenseStageBytes;
-          if (rank == 0) bar_expect(&full[s], 2 * bytes);
-          const uint32_t bar = peer_addr(&full[s], 0);
-          pair_load(&xmap, stage, bar, b * step, static_cast<int32_t>(at.m0 + rank * 128));
-          pair_load(&wmap, stage + 128 * kStageK, bar, b * step, static_cast<int32_t>(at.n0 + rank * half_n));
+        const int32_t m = static_cast<int32_t>(at.m0 + rank * 128), n = static_cast<int32_t>(at.n0 + rank * half_n);
+        constexpr int kStep = kEight ? kStageK : kStageK / 2;
+        for (int b = 0, k = 0; b < a.k_blocks; ++b, k += kStep, r.next(kDenseStages)) {
+          // Before its first use a stage counts as released.
+          if (!bar_wait(&empty[r.at], r.phase ^ 1)) { ok = false; break; }
+          uint8_t *stage = smem + r.at * kDenseStageBytes;
+          if (rank == 0) bar_expect(&full[r.at], 2 * bytes);
+          pair_load(&xmap, stage, bars + 8 * r.at, k, m);
+          pair_load(&wmap, stage + 128 * kStageK, bars + 8 * r.at, k, n);
         }
       }
-      if (!ok) failed = 1;
       // The stages in flight are released (or, after a wait that gave up,
       // have had their time) before the CTA ends.
-      for (int j = i < kDenseStages ? 0 : i - kDenseStages; j < i; ++j)
-        if (!bar_wait(&empty[j % kDenseStages], (j / kDenseStages) & 1)) failed = 1;
+      for (int i = 0; i < kDenseStages; ++i, r.next(kDenseStages)) ok &= bar_wait(&empty[r.at], r.phase ^ 1);
+      if (!ok) failed = 1;
     }
   } else if (warp == kDenseMmaWarp) {
-    if (lane == 0 && rank == 0) {
-      int i = 0, n = 0;
+    if (rank == 0 && elect_one()) {
+      Ring sum;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs, ++n) {
-        const int buf = n & 1;
-        if (n >= 2 && !bar_wait(&taken[buf], (n / 2 - 1) & 1)) { ok = false; break; }
+      for (int t = pair; t < tiles && ok; t += pairs, sum.next(2)) {
+        if (!bar_wait(&taken[sum.at], sum.phase ^ 1)) { ok = false; break; }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int b = 0; b < a.k_blocks; ++b, ++i) {
-          const int s = i % kDenseStages;
-          if (!bar_wait(&full[s], (i / kDenseStages) & 1)) { ok = false; break; }
+        const uint32_t d = tmem + sum.at * kPairMaxN;
+        uint32_t add = 0;
+        for (int b = 0; b < a.k_blocks; ++b, r.next(kDenseStages)) {
+          if (!bar_wait(&full[r.at], r.phase)) { ok = false; break; }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t xd = tile_desc(smem + s * kDenseStageBytes), wd = tile_desc(smem + s * kDenseStageBytes + 128 * kStageK);
+          const uint64_t xd = tile_desc(smem + r.at * kDenseStageBytes), wd = xd + (128 * kStageK >> 4);
 #pragma unroll
-          for (int j = 0; j < kStageK / 32; ++j)
-            pair_mma(tmem + buf * kPairMaxN, xd + 2 * j, wd + 2 * j, a.idesc, a.eight, b > 0 || j > 0);
-          pair_commit(&empty[s]);
+          for (int j = 0; j < kStageK / 32; ++j, add = 1) pair_mma<kEight>(d, xd + 2 * j, wd + 2 * j, a.idesc, add);
+          pair_commit(&empty[r.at]);
         }
-        pair_commit(&sums[buf]);
+        pair_commit(&sums[sum.at]);
       }
       if (!ok) failed = 1;
     }
@@ -517,7 +548,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     for (int t = pair; t < tiles; t += pairs, ++n) {
       const TileAt at = tile_at(a, t);
       const int buf = n & 1;
-      if (!bar_wait(&sums[buf], (n / 2) & 1)) { failed = 1; break; }
+      if (!bar_wait_warp(&sums[buf], (n / 2) & 1, lane)) { failed = 1; break; }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int64_t m = at.m0 + rank * 128 + quarter * 32 + lane;
       const bool row = m < a.m;
@@ -638,7 +669,7 @@ int sm_count() {
   return sms;
 }
 
-template <int BM, bool kTma>
+template <int BM, bool kTma, bool kEight>
 st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int64_t tiles, cudaStream_t st) {
   constexpr int kStageBytes = (kTileN + BM) * kStageK;
   // About half of the SM's shared memory, so that two CTAs share one, but at
@@ -648,7 +679,7 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   if (a.stages < 3) a.stages = 3;
   const int smem = a.stages * kStageBytes + 1024;
   static_assert(BM * kTileN * 4 <= 3 * kStageBytes, "partial sums fit over the stages");
-  auto kernel = split_kernel<BM, kTma>;
+  auto kernel = split_kernel<BM, kTma, kEight>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
@@ -674,10 +705,11 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
 
 st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, int sms, cudaStream_t st) {
   const int smem = kDenseStages * kDenseStageBytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kernel = a.eight ? dense_kernel<true> : dense_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
     const int pairs = sms / 2, tiles = a.m_tiles * a.n_tiles;
-    dense_kernel<<<2 * (tiles < pairs ? tiles : pairs), kDenseThreads, smem, st>>>(xmap, wmap, a);
+    kernel<<<2 * (tiles < pairs ? tiles : pairs), kDenseThreads, smem, st>>>(xmap, wmap, a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess)
@@ -758,7 +790,9 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
     if (s == ST_OK) s = encode(&xmap, a.x, p.k, item, bm);
     if (s != ST_OK) return s;
   }
-#define ST_SPLIT(BM) (tma ? launch_split<BM, true>(a, wmap, xmap, tiles, st) : launch_split<BM, false>(a, wmap, xmap, tiles, st))
+#define ST_SPLIT(BM)                                                                                             \
+  (tma ? (a.eight ? launch_split<BM, true, true>(a, wmap, xmap, tiles, st) : launch_split<BM, true, false>(a, wmap, xmap, tiles, st)) \
+       : (a.eight ? launch_split<BM, false, true>(a, wmap, xmap, tiles, st) : launch_split<BM, false, false>(a, wmap, xmap, tiles, st)))
   switch (bm) {
     case 16: return ST_SPLIT(16);
     case 32: return ST_SPLIT(32);
