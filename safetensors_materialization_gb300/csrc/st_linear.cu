@@ -225,7 +225,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const uint32_t rank = blockIdx.x % a.splits;
   const int64_t tile = blockIdx.x / a.splits;
   const int64_t m0 = tile % a.m_tiles * BM, n0 = tile / a.m_tiles * kTileN;
@@ -542,7 +542,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     }
   } else {
     const int quarter = warp & 3, half = warp >> 2;
-    const uint32_t taken_at[2] = {peer_addr(&taken[0], 0), peer_addr(&taken[1], 0)};
+    const uint32_t taken_at = peer_addr(taken, 0);
     const int chunks = a.tile_n / kChunk;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {
@@ -608,7 +608,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) peer_arrive(taken_at[buf]);
+      if (lane == 0) peer_arrive(taken_at + 8 * buf);
     }
   }
   __syncwarp();

@@ -39,18 +39,24 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Eight consecutive elements from a 16-byte aligned address.
-template <class T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const T *e = reinterpret_cast<const T *>(&u);
+// V consecutive elements as stored, read with one or two aligned accesses.
+template <class T, int V>
+struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Raw {
+  T e[V];
+};
+
+template <class T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V> &r, float (&v)[V]) {
+  if constexpr (V > 1 && std::is_same<T, __nv_bfloat16>::value) {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(&r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
+    for (int i = 0; i < V / 2; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = to_float(r.e[i]);
   }
 }
 
@@ -58,43 +64,37 @@ __device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
 // branch is the same for every thread).
 template <int V>
 __device__ __forceinline__ void load_any(const void *base, st_dtype dtype, int64_t at, float (&v)[V]) {
-  if constexpr (V == 8) {
-    if (dtype == ST_BF16) load8(static_cast<const __nv_bfloat16 *>(base) + at, v);
-    else if (dtype == ST_F16) load8(static_cast<const __half *>(base) + at, v);
-    else load8(static_cast<const float *>(base) + at, v);
-  } else {
-    static_assert(V == 1, "scalar or eight");
-    if (dtype == ST_BF16) v[0] = to_float(static_cast<const __nv_bfloat16 *>(base)[at]);
-    else if (dtype == ST_F16) v[0] = to_float(static_cast<const __half *>(base)[at]);
-    else v[0] = static_cast<const float *>(base)[at];
-  }
+  auto typed = [&](auto zero) {
+    using T = decltype(zero);
+    unpack(*reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(base) + at), v);
+  };
+  if (dtype == ST_BF16) typed(__nv_bfloat16{});
+  else if (dtype == ST_F16) typed(__half{});
+  else typed(float{});
 }
 
 // V consecutive values rounded to the dtype (F8_E4M3: already divided by the scale).
 template <int V>
 __device__ __forceinline__ void store_any(void *base, st_dtype dtype, int64_t at, const float (&v)[V]) {
-  if constexpr (V == 8) {
-    if (dtype == ST_F8_E4M3) {
-      uint2 u;
-      u.x = pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16;
-      u.y = pack_e4m3(v[4], v[5]) | pack_e4m3(v[6], v[7]) << 16;
-      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(base) + at) = u;
-    } else if (dtype == ST_BF16) {
-      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at) =
-          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else if (dtype == ST_F16) {
-      *reinterpret_cast<uint4 *>(static_cast<__half *>(base) + at) =
-          make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
-    } else {
-      float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
+  if constexpr (V == 1) {
     if (dtype == ST_F8_E4M3) static_cast<uint8_t *>(base)[at] = static_cast<uint8_t>(pack_e4m3(v[0], 0.0f));
     else if (dtype == ST_BF16) static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(v[0]);
     else if (dtype == ST_F16) static_cast<__half *>(base)[at] = __float2half_rn(v[0]);
     else static_cast<float *>(base)[at] = v[0];
+  } else if (dtype == ST_F8_E4M3) {
+    Raw<uint32_t, V / 4> u;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) u.e[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16;
+    *reinterpret_cast<Raw<uint32_t, V / 4> *>(static_cast<uint8_t *>(base) + at) = u;
+  } else if (dtype == ST_F32) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4 *>(static_cast<float *>(base) + at + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+    Raw<uint32_t, V / 2> u;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) u.e[i] = dtype == ST_BF16 ? pack_bf16(v[2 * i], v[2 * i + 1]) : pack_f16(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<Raw<uint32_t, V / 2> *>(static_cast<uint16_t *>(base) + at) = u;
   }
 }
 

@@ -21,6 +21,9 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kRowsPerBlock = 8;  // rows of one warp each
 
+// The largest block of a row kernel: its registers hold NV vectors a thread.
+constexpr int block_threads(int v, int nv) { return v > 1 && nv >= 4 ? 512 : kMaxThreads; }
+
 struct RowArgs {
   const void *x, *r, *w;  // norm: x, residual, weight; gate: gate, up
   void *h, *y;
@@ -87,51 +90,72 @@ __device__ __forceinline__ float scaled(float v, Factor f) {
   return (kNorm ? v * f.rstd : v) * f.inv;
 }
 
-// Reads V elements of the row at column c and returns the values before the
-// row's factor (h w, or z), adding to the statistics and writing h.
-template <class T, int V, bool kNorm, bool kFirst>
-__device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c, float (&v)[V], Stat &s) {
-  const st_dtype dt = sizeof(T) == 4 ? ST_F32 : std::is_same<T, __half>::value ? ST_F16 : ST_BF16;
-  load_any<V>(a.x, dt, row * a.ldx + c, v);
-  float r[V];
-  if (a.r) load_any<V>(a.r, dt, row * a.ldr + c, r);
+template <class T>
+constexpr st_dtype kDtype = sizeof(T) == 4 ? ST_F32 : std::is_same<T, __half>::value ? ST_F16 : ST_BF16;
+
+// The values before the row's factors (h w, or z) of V elements at column c,
+// from the elements as read, adding to the statistics and writing h.
+template <class T, int V, bool kNorm, bool kWrite>
+__device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c, const Raw<T, V> &x, const Raw<T, V> &r,
+                                           float (&v)[V], Stat &s) {
+  unpack(x, v);
+  float o[V];
+  if (a.r) unpack(r, o);
   if constexpr (kNorm) {
     if (a.r) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += r[i];
-      if (a.h && kFirst) store_any<V>(a.h, dt, row * a.ldh + c, v);
+      for (int i = 0; i < V; ++i) v[i] += o[i];
+      if (a.h && kWrite) store_any<V>(a.h, kDtype<T>, row * a.ldh + c, v);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) s.sum = fmaf(v[i], v[i], s.sum);
     if (a.w) {
-      load_any<V>(a.w, a.w_dtype, c, r);
+      load_any<V>(a.w, a.w_dtype, c, o);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= r[i];
+      for (int i = 0; i < V; ++i) v[i] *= o[i];
     }
   } else {
     activate(v, a.act);
     if (a.r) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= r[i];
+      for (int i = 0; i < V; ++i) v[i] *= o[i];
     }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) s.top = max_nan(s.top, fabsf(v[i]));
 }
 
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> row_read(const void *p, int64_t at) {
+  return *reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(p) + at);
+}
+
 // One row in registers: a block (or, kWarpRow, a warp) per row, NV accesses
-// of V elements per thread.
+// of V elements per thread, all of them under way before the first is used.
 template <class T, int V, int NV, bool kNorm, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kMaxThreads) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(V, NV)) row_kernel(const RowArgs a) {
   const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5) : int64_t(blockIdx.x);
   const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x;
   if (kWarpRow && row >= a.rows) return;
+  Raw<T, V> x[NV], r[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + t) * V;
+    if (c < a.cols) x[i] = row_read<T, V>(a.x, row * a.ldx + c);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * nt + t) * V;
+      if (c < a.cols) r[i] = row_read<T, V>(a.r, row * a.ldr + c);
+    }
+  }
   float v[NV][V];
   Stat s{0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * nt + t) * V;
-    if (c < a.cols) row_values<T, V, kNorm, true>(a, row, c, v[i], s);
+    if (c < a.cols) row_values<T, V, kNorm, true>(a, row, c, x[i], r[i], v[i], s);
   }
   s = kWarpRow ? warp_stat(s) : block_stat(s);
   const Factor f = row_factor<kNorm>(a, s, row, t == 0);
@@ -149,18 +173,26 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kMaxThreads) r
 // A row too long for registers: the second pass reads the inputs again (each
 // thread its own elements, so in-place outputs are read before they are
 // written; h is written in the second pass).
-template <class T, bool kNorm>
+template <class T, int V, bool kNorm>
 __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) {
   const int64_t row = blockIdx.x;
   Stat s{0.0f, 0.0f}, unused{0.0f, 0.0f};
-  float v[1];
-  for (int64_t c = threadIdx.x; c < a.cols; c += kMaxThreads) row_values<T, 1, kNorm, false>(a, row, static_cast<int>(c), v, s);
+  Raw<T, V> x, r;
+  float v[V];
+  for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
+    x = row_read<T, V>(a.x, row * a.ldx + c);
+    if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
+    row_values<T, V, kNorm, false>(a, row, static_cast<int>(c), x, r, v, s);
+  }
   s = block_stat(s);
   const Factor f = row_factor<kNorm>(a, s, row, threadIdx.x == 0);
-  for (int64_t c = threadIdx.x; c < a.cols; c += kMaxThreads) {
-    row_values<T, 1, kNorm, true>(a, row, static_cast<int>(c), v, unused);
-    v[0] = scaled<kNorm>(v[0], f);
-    store_any<1>(a.y, a.y_dtype, row * a.ldy + c, v);
+  for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
+    x = row_read<T, V>(a.x, row * a.ldx + c);
+    if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
+    row_values<T, V, kNorm, true>(a, row, static_cast<int>(c), x, r, v, unused);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = scaled<kNorm>(v[j], f);
+    store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v);
   }
 }
 
@@ -173,28 +205,28 @@ void launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
     row_kernel<T, V, NV, kNorm, false><<<static_cast<unsigned>(a.rows), threads, 0, st>>>(a);
 }
 
-template <class T, bool kNorm>
-void launch_typed(const RowArgs &a, bool vec, cudaStream_t st) {
-  const int64_t accesses = vec ? a.cols / 8 : a.cols;
+// Accesses per thread: as few as blocks of 256 threads allow, so that several
+// rows share an SM and one's loads overlap another's reduction; with too few
+// rows for that, blocks of 1024, the shortest way through one row.
+template <class T, int V, bool kNorm>
+void launch_typed(const RowArgs &a, cudaStream_t st) {
+  const int64_t accesses = a.cols / V;
+  const int64_t target = a.rows <= 256 ? kMaxThreads : 256;
+  constexpr int kMost = V == 8 ? 4 : 8;
   auto threads = [&](int nv) { return static_cast<int>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
-  if (vec && accesses <= 4 * kMaxThreads) {
-    if (accesses <= 256) launch_rows<T, 8, 1, kNorm>(a, threads(1), st);
-    else if (accesses <= 512) launch_rows<T, 8, 2, kNorm>(a, threads(2), st);
-    else launch_rows<T, 8, 4, kNorm>(a, threads(4), st);
-  } else if (!vec && accesses <= 16 * kMaxThreads) {
-    if (accesses <= 4 * 256) launch_rows<T, 1, 4, kNorm>(a, threads(4), st);
-    else launch_rows<T, 1, 16, kNorm>(a, threads(16), st);
-  } else {
-    row_loop_kernel<T, kNorm><<<static_cast<unsigned>(a.rows), kMaxThreads, 0, st>>>(a);
-  }
+  if (accesses <= target) launch_rows<T, V, 1, kNorm>(a, threads(1), st);
+  else if (accesses <= 2 * target) launch_rows<T, V, 2, kNorm>(a, threads(2), st);
+  else if (accesses <= 4 * block_threads(V, 4)) launch_rows<T, V, 4, kNorm>(a, threads(4), st);
+  else if (accesses <= kMost * block_threads(V, kMost)) launch_rows<T, V, kMost, kNorm>(a, threads(kMost), st);
+  else row_loop_kernel<T, V, kNorm><<<static_cast<unsigned>(a.rows), kMaxThreads, 0, st>>>(a);
 }
 
 template <bool kNorm>
 st_status launch(const RowArgs &a, st_dtype x_dtype, bool vec, void *stream, const char *op) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (x_dtype == ST_BF16) launch_typed<__nv_bfloat16, kNorm>(a, vec, st);
-  else if (x_dtype == ST_F16) launch_typed<__half, kNorm>(a, vec, st);
-  else launch_typed<float, kNorm>(a, vec, st);
+  if (x_dtype == ST_BF16) vec ? launch_typed<__nv_bfloat16, 8, kNorm>(a, st) : launch_typed<__nv_bfloat16, 1, kNorm>(a, st);
+  else if (x_dtype == ST_F16) vec ? launch_typed<__half, 8, kNorm>(a, st) : launch_typed<__half, 1, kNorm>(a, st);
+  else vec ? launch_typed<float, 4, kNorm>(a, st) : launch_typed<float, 1, kNorm>(a, st);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess)
     return set_error(ST_E_CUDA, "%s launch (%lld rows): %s: %s", op, (long long)a.rows, cudaGetErrorName(e),
@@ -202,8 +234,8 @@ st_status launch(const RowArgs &a, st_dtype x_dtype, bool vec, void *stream, con
   return ST_OK;
 }
 
-// Whether vectors of eight elements of the matrix are aligned for one access
-// (16 bytes; 8 for an 8-bit matrix).
+// Whether the accesses of a row of 16-byte input vectors are aligned in this
+// matrix: 16 bytes, or eight (at least) of an 8-bit one.
 bool vec_ok(const void *p, int64_t ld, st_dtype dtype) {
   if (!p) return true;
   const uint64_t item = dtype == ST_F8_E4M3 ? 1 : dtype == ST_F32 ? 4 : 2, need = item == 1 ? 8 : 16;
