@@ -21,6 +21,7 @@
 // not a multiple of 16 bytes, by eight warps that realign it on the way.
 #include <cuda.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "st_ops_device.h"
@@ -30,7 +31,7 @@ namespace {
 
 constexpr int kTileN = 128;          // weight rows per tile: the MMA's M
 constexpr int kStageK = 128;         // bytes of k per stage: one swizzle row
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 12;         // ring slots
 constexpr int kMaxSplit = 8;         // portable cluster size
 constexpr int kEpilogueWarps = 4;    // one per 32 TMEM lanes
 constexpr int kMmaWarp = 4, kFirstProducer = 5, kCopyWarps = 8;
@@ -38,10 +39,9 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 
 constexpr int kPairM = 256;          // tokens per pair of CTAs
 constexpr int kPairMaxN = 256;       // weight rows per pair, a multiple of 32
-constexpr int kDenseStages = 6;
 constexpr int kDenseEpilogueWarps = 8;  // two per 32 TMEM lanes: halves of the columns
 constexpr int kDenseMmaWarp = 8, kDenseCopyWarp = 9, kDenseThreads = 320;
-constexpr int kDenseStageBytes = 2 * 128 * kStageK;
+constexpr int kDenseSmem = 196 * 1024;  // the ring of stages; room for the rest of a CTA's 227 KB
 constexpr int kChunk = 32;           // columns an epilogue warp reads at a time
 
 // One operand of the product.
@@ -57,7 +57,8 @@ struct LinArgs {
   int64_t m, n, kbytes;
   int k_blocks, splits, stages, m_tiles;
   int n_tiles, tile_n;               // dense_kernel: weight rows per tile
-  int vec;                           // dense_kernel: y and residual rows take 32-byte accesses
+  int x_box;                         // token rows a TMA copy brings
+  int vec;                           // y and residual rows take 32-byte (dense) or four-element (split) accesses
   uint32_t idesc;
   int eight;                         // 8-bit operands
   st_act act;
@@ -144,12 +145,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// The binary32 at the same shared address in the cluster's CTA `rank`.
-__device__ __forceinline__ float peer_load(const float *p, uint32_t rank) {
+// The address of this CTA's shared variable in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
   uint32_t at;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return at;
+}
+__device__ __forceinline__ float4 peer_load(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
   return v;
 }
 
@@ -225,7 +229,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x % a.splits;
   const int64_t tile = blockIdx.x / a.splits;
   const int64_t m0 = tile % a.m_tiles * BM, n0 = tile / a.m_tiles * kTileN;
@@ -260,7 +264,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
           // Before its first use a stage counts as released.
           if (!bar_wait(&empty[r.at], r.phase ^ 1)) break;
           uint8_t *stage = smem + r.at * kStageBytes;
-          bar_expect(&full[r.at], kStageBytes);
+          bar_expect(&full[r.at], kTileN * kStageK + a.x_box * kStageK);
           tma_load(&wmap, stage, &full[r.at], at, static_cast<int32_t>(n0));
           tma_load(&xmap, stage + kTileN * kStageK, &full[r.at], at, static_cast<int32_t>(m0));
         }
@@ -298,6 +302,21 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   __syncwarp();
 
   float *part = reinterpret_cast<float *>(smem);  // [BM][kTileN], over the stages
+  // In the epilogue a lane has four consecutive weight rows, a warp every
+  // fourth token of the CTA's share.
+  const int64_t n = n0 + 4 * lane;
+  const int live = n < a.n ? static_cast<int>(min(int64_t(4), a.n - n)) : 0;
+  const bool quad = live == 4 && a.vec;
+  float ws[4], bias[4];
+  if (warp < kEpilogueWarps) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float b[1] = {0.0f};
+      if (a.bias && j < live) load_any<1>(a.bias, a.bias_dtype, n + j, b);
+      ws[j] = a.w_scale && j < live ? a.w_scale[(n + j) * a.w_scale_step] : 1.0f;
+      bias[j] = b[0];
+    }
+  }
   if (warp < kEpilogueWarps) {
     if (blocks > 0) {
       if (!bar_wait(&done, 0)) failed = 1;
@@ -320,28 +339,73 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   if (a.splits > 1) cluster_sync();
   if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
 
-  const int64_t n = n0 + threadIdx.x;
-  if (warp < kEpilogueWarps && n < a.n) {
-    const float ws = a.w_scale ? a.w_scale[n * a.w_scale_step] : 1.0f;
-    float b[1] = {0.0f};
-    if (a.bias) load_any<1>(a.bias, a.bias_dtype, n, b);
-    const int cols = static_cast<int>(a.m - m0 < BM ? a.m - m0 : BM);
-    for (int c = static_cast<int>(rank); c < cols; c += a.splits) {
-      const int64_t m = m0 + c;
-      float v = part[c * kTileN + threadIdx.x];
-      if (a.splits > 1) {
-        v = 0.0f;
-        for (int r = 0; r < a.splits; ++r) v += peer_load(&part[c * kTileN + threadIdx.x], r);
+  if (warp < kEpilogueWarps) {
+    // Each CTA joins and writes its share of the tokens, four a warp at a
+    // time so that their loads overlap (the residual may be y: a thread reads
+    // its values before it writes them).
+    const int cols = static_cast<int>(a.m - m0 < BM ? a.m - m0 : BM), share = (cols + a.splits - 1) / a.splits;
+    const int begin = static_cast<int>(rank) * share, end = min(cols, begin + share);
+    constexpr int kBatch = 4;
+#pragma unroll 1
+    for (int c = begin + warp; c < end; c += kEpilogueWarps * kBatch) {
+      float v[kBatch][4], old[kBatch][4], xs[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t m = m0 + c + i * kEpilogueWarps;
+        const bool in = c + i * kEpilogueWarps < end;
+        xs[i] = in && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = old[i][j] = 0.0f;
+        if (in && a.residual) {
+          if (quad) load_any<4>(a.residual, a.y_dtype, m * a.ldr + n, old[i]);
+          else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float o[1] = {0.0f};
+              if (j < live) load_any<1>(a.residual, a.y_dtype, m * a.ldr + n + j, o);
+              old[i][j] = o[0];
+            }
+          }
+        }
       }
-      if (a.x_scale) v *= a.x_scale[m * a.x_scale_step];
-      float out[1] = {v * ws + b[0]};
-      activate(out, a.act);
-      if (a.residual) {
-        float r[1];
-        load_any<1>(a.residual, a.y_dtype, m * a.ldr + n, r);
-        out[0] += r[0];
+      // Four CTAs' partial sums are under way at a time.
+      for (int r0 = 0; r0 < a.splits; r0 += 4) {
+        float4 f[4][kBatch];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (r0 + r >= a.splits) break;
+          const uint32_t at = peer_addr(part + c * kTileN + 4 * lane, r0 + r);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (c + i * kEpilogueWarps < end) f[r][i] = peer_load(at + i * kEpilogueWarps * kTileN * 4);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (r0 + r >= a.splits) break;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (c + i * kEpilogueWarps < end)
+              v[i][0] += f[r][i].x, v[i][1] += f[r][i].y, v[i][2] += f[r][i].z, v[i][3] += f[r][i].w;
+        }
       }
-      store_any<1>(a.y, a.y_dtype, m * a.ldy + n, out);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (c + i * kEpilogueWarps >= end) continue;
+        const int64_t m = m0 + c + i * kEpilogueWarps;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = v[i][j] * xs[i] * ws[j] + bias[j];
+        activate(v[i], a.act);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] += old[i][j];
+        if (quad) store_any<4>(a.y, a.y_dtype, m * a.ldy + n, v[i]);
+        else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float out[1] = {v[i][j]};
+            if (j < live) store_any<1>(a.y, a.y_dtype, m * a.ldy + n + j, out);
+          }
+        }
+      }
     }
   }
   if (a.splits > 1) cluster_sync();  // the partial sums stay until every CTA has read them
@@ -349,12 +413,6 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
 
 // ---------------------------------------------------------- dense_kernel
 
-// The address of this CTA's shared variable in the cluster's CTA `rank`.
-__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-  return at;
-}
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -462,7 +520,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
              const __grid_constant__ LinArgs a) {
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
-  __shared__ uint64_t full[kDenseStages], empty[kDenseStages], sums[2], taken[2];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
   __shared__ float turn[kDenseEpilogueWarps][32][17];
@@ -470,10 +528,10 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.m_tiles * a.n_tiles;
-  const int half_n = a.tile_n / 2;
+  const int half_n = a.tile_n / 2, stage_bytes = (128 + half_n) * kStageK;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kDenseStages; ++i) {
+    for (int i = 0; i < a.stages; ++i) {
       bar_init(&full[i], 1);
       bar_init(&empty[i], 1);
     }
@@ -499,24 +557,24 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     if (elect_one()) {
       // This CTA's tokens and its half of the weight rows; the bytes of both
       // CTAs count on the first one's barriers.
-      const uint32_t bytes = (128 + half_n) * kStageK, bars = peer_addr(full, 0);
+      const uint32_t bars = peer_addr(full, 0);
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
         const TileAt at = tile_at(a, t);
         const int32_t m = static_cast<int32_t>(at.m0 + rank * 128), n = static_cast<int32_t>(at.n0 + rank * half_n);
         constexpr int kStep = kEight ? kStageK : kStageK / 2;
-        for (int b = 0, k = 0; b < a.k_blocks; ++b, k += kStep, r.next(kDenseStages)) {
+        for (int b = 0, k = 0; b < a.k_blocks; ++b, k += kStep, r.next(a.stages)) {
           // Before its first use a stage counts as released.
           if (!bar_wait(&empty[r.at], r.phase ^ 1)) { ok = false; break; }
-          uint8_t *stage = smem + r.at * kDenseStageBytes;
-          if (rank == 0) bar_expect(&full[r.at], 2 * bytes);
+          uint8_t *stage = smem + r.at * stage_bytes;
+          if (rank == 0) bar_expect(&full[r.at], 2 * stage_bytes);
           pair_load(&xmap, stage, bars + 8 * r.at, k, m);
           pair_load(&wmap, stage + 128 * kStageK, bars + 8 * r.at, k, n);
         }
       }
       // The stages in flight are released (or, after a wait that gave up,
       // have had their time) before the CTA ends.
-      for (int i = 0; i < kDenseStages; ++i, r.next(kDenseStages)) ok &= bar_wait(&empty[r.at], r.phase ^ 1);
+      for (int i = 0; i < a.stages; ++i, r.next(a.stages)) ok &= bar_wait(&empty[r.at], r.phase ^ 1);
       if (!ok) failed = 1;
     }
   } else if (warp == kDenseMmaWarp) {
@@ -528,10 +586,10 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + sum.at * kPairMaxN;
         uint32_t add = 0;
-        for (int b = 0; b < a.k_blocks; ++b, r.next(kDenseStages)) {
+        for (int b = 0; b < a.k_blocks; ++b, r.next(a.stages)) {
           if (!bar_wait(&full[r.at], r.phase)) { ok = false; break; }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t xd = tile_desc(smem + r.at * kDenseStageBytes), wd = xd + (128 * kStageK >> 4);
+          const uint64_t xd = tile_desc(smem + r.at * stage_bytes), wd = xd + (128 * kStageK >> 4);
 #pragma unroll
           for (int j = 0; j < kStageK / 32; ++j, add = 1) pair_mma<kEight>(d, xd + 2 * j, wd + 2 * j, a.idesc, add);
           pair_commit(&empty[r.at]);
@@ -663,14 +721,88 @@ st_status encode(CUtensorMap *map, const Side &s, int64_t k, int item, int box_r
   return ST_OK;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-  return sms;
+// What launches on a device need, looked up on its first one.
+constexpr int kMaxDevices = 256;
+struct Device {
+  int sms = 0;
+  uint32_t *err = nullptr;
+};
+
+st_status device(int *index, const Device **out) {
+  static std::mutex mu;
+  static Device known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev >= kMaxDevices) e = cudaErrorInvalidDevice;
+  if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_linear: the current device: %s", cudaGetErrorName(e));
+  std::lock_guard<std::mutex> lock(mu);
+  Device &d = known[dev];
+  if (!d.err) {
+    void *scratch = nullptr;
+    const st_status s = static_scratch(&scratch);
+    if (s != ST_OK) return s;
+    e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_linear: counting SMs: %s", cudaGetErrorName(e));
+    d.err = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(scratch) + kStaticErrOffset);
+  }
+  *index = dev;
+  *out = &d;
+  return ST_OK;
+}
+
+// Raises a kernel's limit of dynamic shared memory, once per kernel and device.
+template <auto kKernel>
+cudaError_t allow_smem(int dev, int bytes) {
+  static std::atomic<bool> done[kMaxDevices];
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// How a kernel would cut a product, and its time in units of one 128-byte
+// row brought into an SM (1.2 ns, measured), without what every launch costs.
+struct Shape {
+  int64_t m_tiles, n_tiles;
+  int width, splits;
+  double cost;
+};
+
+// dense_kernel: rounds of tiles over the pairs; a stage takes as long as its
+// rows or its MMAs, whichever is longer.  The width of a tile is the one with
+// the shortest rounds in all (4096 x 4096 x 14336 BF16: 224 columns, four
+// full rounds, 285 us; 256 columns, 314).
+Shape dense_shape(int64_t m, int64_t n, int k_blocks, int sms) {
+  Shape best{};
+  const int64_t m_tiles = (m + kPairM - 1) / kPairM, pairs = sms / 2;
+  for (int w = kPairMaxN; w >= 32; w -= 32) {
+    const int64_t n_tiles = (n + w - 1) / w, rounds = (m_tiles * n_tiles + pairs - 1) / pairs;
+    const double rows = 128 + w / 2, mma = 0.87 * w, cost = static_cast<double>(rounds) * k_blocks * (rows > mma ? rows : mma);
+    if (best.width == 0 || cost < best.cost) best = Shape{m_tiles, n_tiles, w, 1, cost};
+  }
+  return best;
+}
+
+// split_kernel: the MMA's columns are the tokens, up to 128; the sum is split
+// until the CTAs fill the SMs twice, each with at least four stages.  Joining
+// and writing a tile costs 26 units per column.  (4096 x 4096 E4M3, us: 64
+// tokens 10.7 and dense 11.3; 128 tokens 15.0 and dense 11.4; 128 tokens x
+// 4096 x 14336 21.4 and dense 25.9.)
+Shape split_shape(int64_t m, int64_t n, int k_blocks, int sms) {
+  Shape s{};
+  s.width = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  s.m_tiles = (m + s.width - 1) / s.width;
+  s.n_tiles = (n + kTileN - 1) / kTileN;
+  const int64_t tiles = s.m_tiles * s.n_tiles;
+  s.splits = 1;
+  while (s.splits < kMaxSplit && tiles * s.splits <= sms && k_blocks / (s.splits * 2) >= 4) s.splits *= 2;
+  const double waves = static_cast<double>(tiles) * s.splits / sms;
+  s.cost = (waves > 1 ? waves : 1) * ((k_blocks + s.splits - 1) / s.splits * (kTileN + s.width) + 26.0 * s.width);
+  return s;
 }
 
 template <int BM, bool kTma, bool kEight>
-st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int64_t tiles, cudaStream_t st) {
+st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int64_t tiles, int dev, cudaStream_t st) {
   constexpr int kStageBytes = (kTileN + BM) * kStageK;
   // About half of the SM's shared memory, so that two CTAs share one, but at
   // least three stages and room for the partial sums.
@@ -679,8 +811,8 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   if (a.stages < 3) a.stages = 3;
   const int smem = a.stages * kStageBytes + 1024;
   static_assert(BM * kTileN * 4 <= 3 * kStageBytes, "partial sums fit over the stages");
-  auto kernel = split_kernel<BM, kTma, kEight>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr auto kernel = split_kernel<BM, kTma, kEight>;
+  cudaError_t e = allow_smem<kernel>(dev, smem);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits));
@@ -703,13 +835,16 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   return ST_OK;
 }
 
-st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, int sms, cudaStream_t st) {
-  const int smem = kDenseStages * kDenseStageBytes + 1024;
-  auto kernel = a.eight ? dense_kernel<true> : dense_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <bool kEight>
+st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, int dev, int sms, cudaStream_t st) {
+  // As many stages as fit: a narrow tile's are smaller, and need more of them
+  // under way to cover the memory's latency.
+  const int stage_bytes = (128 + a.tile_n / 2) * kStageK;
+  a.stages = kDenseSmem / stage_bytes < kMaxStages ? kDenseSmem / stage_bytes : kMaxStages;
+  cudaError_t e = allow_smem<dense_kernel<kEight>>(dev, kDenseSmem + 1024);
   if (e == cudaSuccess) {
     const int pairs = sms / 2, tiles = a.m_tiles * a.n_tiles;
-    kernel<<<2 * (tiles < pairs ? tiles : pairs), kDenseThreads, smem, st>>>(xmap, wmap, a);
+    dense_kernel<kEight><<<2 * (tiles < pairs ? tiles : pairs), kDenseThreads, a.stages * stage_bytes + 1024, st>>>(xmap, wmap, a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess)
@@ -735,13 +870,13 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   };
   a.x = side(p.x, p.ldx, p.m);
   a.w = side(p.w, p.ldw, p.n);
-  void *scratch = nullptr;
-  st_status s = static_scratch(&scratch);
+  int dev = 0;
+  const Device *gpu = nullptr;
+  st_status s = device(&dev, &gpu);
   if (s != ST_OK) return s;
-  a.err = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(scratch) + kStaticErrOffset);
-
+  a.err = gpu->err;
+  const int sms = gpu->sms;
   a.k_blocks = static_cast<int>((a.kbytes + kStageK - 1) / kStageK);
-  const int sms = sm_count();
   // Instruction descriptor: binary32 accumulators; formats of A and B, both
   // K-major; rows and columns of one MMA.
   const uint32_t fw = item == 2 ? (p.w_dtype == ST_BF16) : (p.w_dtype == ST_F8_E5M2), fx = item == 2 ? (p.x_dtype == ST_BF16) : 0;
@@ -752,47 +887,46 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   CUtensorMap wmap{}, xmap{};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
-  if (tma && p.m >= 512) {
-    const int64_t m_tiles = (p.m + kPairM - 1) / kPairM;
-    // The tile's width: the fewest rounds of tiles over the pairs, each as
-    // long as its columns and a fixed part of the readout.
-    int64_t best = INT64_MAX;
-    for (int tn = kPairMaxN; tn >= 128; tn -= 32) {
-      const int64_t n_tiles = (p.n + tn - 1) / tn, rounds = (m_tiles * n_tiles + sms / 2 - 1) / (sms / 2), cost = rounds * (tn + 16);
-      if (cost < best) best = cost, a.tile_n = tn, a.n_tiles = static_cast<int>(n_tiles);
-    }
-    if (m_tiles * a.n_tiles > 0x3fffffff)
+  const int64_t out = static_cast<int64_t>(st_dtype_size(p.y_dtype));
+  auto aligned = [&](int64_t to) {
+    auto one = [&](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % to == 0 && ld * out % to == 0; };
+    return one(p.y, p.ldy) && (!p.residual || one(p.residual, p.ldr));
+  };
+
+  const Shape d = dense_shape(p.m, p.n, a.k_blocks, sms), c = split_shape(p.m, p.n, a.k_blocks, sms);
+  if (tma && d.cost < c.cost) {
+    if (d.m_tiles * d.n_tiles > 0x3fffffff)
       return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
-    a.m_tiles = static_cast<int>(m_tiles);
+    a.m_tiles = static_cast<int>(d.m_tiles);
+    a.n_tiles = static_cast<int>(d.n_tiles);
+    a.tile_n = d.width;
     a.idesc = idesc(fx, fw, kPairM, a.tile_n);
-    const int out = static_cast<int>(st_dtype_size(p.y_dtype));
-    auto wide = [&](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 32 == 0 && ld * out % 32 == 0; };
-    a.vec = wide(p.y, p.ldy) && (!p.residual || wide(p.residual, p.ldr));
+    a.vec = aligned(32);
     s = encode(&xmap, a.x, p.k, item, 128);
     if (s == ST_OK) s = encode(&wmap, a.w, p.k, item, a.tile_n / 2);
-    return s == ST_OK ? launch_dense(a, xmap, wmap, sms, st) : s;
+    if (s != ST_OK) return s;
+    return a.eight ? launch_dense<true>(a, xmap, wmap, dev, sms, st) : launch_dense<false>(a, xmap, wmap, dev, sms, st);
   }
 
-  // Columns of the MMA: the tokens, up to 128; m tiles beyond.
-  const int bm = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
-  a.m_tiles = static_cast<int>((p.m + bm - 1) / bm);
-  const int64_t tiles = (p.n + kTileN - 1) / kTileN * a.m_tiles;
-  // The sum is split until the CTAs fill the SMs twice, each with at least
-  // four stages of work.
-  a.splits = 1;
-  const int64_t want = 2 * sms;
-  while (a.splits < kMaxSplit && tiles * a.splits * 2 <= want && a.k_blocks / (a.splits * 2) >= 4) a.splits *= 2;
+  a.vec = aligned(4 * out);
+  a.m_tiles = static_cast<int>(c.m_tiles);
+  a.splits = c.splits;
+  const int bm = c.width;
+  const int64_t tiles = c.m_tiles * c.n_tiles;
   if (tiles * a.splits > 0x7fffffff)
     return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
   a.idesc = idesc(fw, fx, kTileN, bm);
   if (tma) {
     s = encode(&wmap, a.w, p.k, item, kTileN);
-    if (s == ST_OK) s = encode(&xmap, a.x, p.k, item, bm);
+    // Fewer tokens than the MMA's columns: only they are copied (what the other
+    // columns hold reaches no sum that is read).
+    a.x_box = p.m < bm ? static_cast<int>(p.m) : bm;
+    if (s == ST_OK) s = encode(&xmap, a.x, p.k, item, a.x_box);
     if (s != ST_OK) return s;
   }
 #define ST_SPLIT(BM)                                                                                             \
-  (tma ? (a.eight ? launch_split<BM, true, true>(a, wmap, xmap, tiles, st) : launch_split<BM, true, false>(a, wmap, xmap, tiles, st)) \
-       : (a.eight ? launch_split<BM, false, true>(a, wmap, xmap, tiles, st) : launch_split<BM, false, false>(a, wmap, xmap, tiles, st)))
+  (tma ? (a.eight ? launch_split<BM, true, true>(a, wmap, xmap, tiles, dev, st) : launch_split<BM, true, false>(a, wmap, xmap, tiles, dev, st)) \
+       : (a.eight ? launch_split<BM, false, true>(a, wmap, xmap, tiles, dev, st) : launch_split<BM, false, false>(a, wmap, xmap, tiles, dev, st)))
   switch (bm) {
     case 16: return ST_SPLIT(16);
     case 32: return ST_SPLIT(32);
