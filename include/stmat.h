@@ -593,8 +593,8 @@ st_status st_materialize_noalloc(const void *data_dev, const st_plan_t *plan, vo
 /* No counterpart on the pages (the library's own status for the two calls
  * that use its static array).  Reads and clears the error word of the
  * library's static device array on the current device: the device flags of
- * every st_materialize_noalloc and st_load_tensors call since the last read
- * (bits as for st_plan_check).
+ * every st_materialize_noalloc, st_load_tensors and st_linear call since the
+ * last read (bits as for st_plan_check).
  * Copies the word to the host on `stream` and waits for the stream, so every
  * such call queued on it before has finished; calls on other streams are
  * seen only once they have finished.  Allocates nothing.  Returns
@@ -622,8 +622,8 @@ st_status st_plan_check(const st_plan_t *plan, void *stream, uint32_t *flags);
  * faster paths).  An output may be the very matrix of an input (same pointer,
  * stride and itemsize: in place); any other overlap gives undefined values.
  * Calls run on `stream` (a cudaStream_t; NULL is the legacy default stream)
- * without host synchronization, workspace or allocation, can be captured in a
- * CUDA graph, and give the same bits on every run.  Zero rows or columns:
+ * without host synchronization or allocation, can be captured in a CUDA graph,
+ * and give the same bits on every run.  Zero rows or columns:
  * nothing is written.  Errors: ST_E_INVAL (sizes, strides, NULL), ST_E_DTYPE,
  * ST_E_ALIGN, ST_E_CUDA (launch failure); nothing is queued then.  Values
  * are computed in binary32 and rounded once (round to nearest even); NaN and
@@ -693,7 +693,16 @@ typedef struct st_linear_args {
   const void *bias;                 /* n entries, or NULL */
   const void *residual; int64_t ldr; /* or NULL */
   void *y;              int64_t ldy;
+  void *workspace;                  /* device memory, 16-byte aligned, of */
+  uint64_t workspace_bytes;         /* at least st_linear_workspace; NULL, 0 where that is 0 */
 } st_linear_args;
+/* The workspace that a product needs: 0 where x and weight lie on 16-byte
+ * boundaries, as do the row strides (the tensor engine's copies read them in
+ * place); else room for an aligned copy of the one, or both, that does not,
+ * made by each call.  The workspace's own fields are not looked at. */
+st_status st_linear_workspace(const st_linear_args *args, uint64_t *bytes);
+/* A wait in a kernel that gave up (bit 1 of st_static_check) leaves y
+ * incomplete. */
 st_status st_linear(const st_linear_args *args, void *stream);
 
 /* ----------------------------------------------------------------- misc */

@@ -17,8 +17,12 @@
 // read out of one half of TMEM while the next tile's are formed in the other.
 //
 // Both operands are staged 128 bytes of k at a time in the 128-byte swizzled
-// layout the MMA reads, by TMA, or, where a matrix's address or row stride is
-// not a multiple of 16 bytes, by eight warps that realign it on the way.
+// layout the MMA reads, by TMA.  A matrix whose address or row stride is not a
+// multiple of 16 bytes, which TMA cannot read, is first copied to rows that
+// are (align_kernel) in a workspace of the caller's.  Measured beside warps
+// that realign rows on their way to shared memory, which take 1.2 us a stage
+// (us, BF16): 4096 x 4097 x 4097 917, this 140; 256 x 4096 x 4097 85, this
+// 34; 1 x 14336 x 4097 85, this 63.
 #include <cuda.h>
 
 #include <atomic>
@@ -34,7 +38,7 @@ constexpr int kStageK = 128;         // bytes of k per stage: one swizzle row
 constexpr int kMaxStages = 12;         // ring slots
 constexpr int kMaxSplit = 8;         // portable cluster size
 constexpr int kEpilogueWarps = 4;    // one per 32 TMEM lanes
-constexpr int kMmaWarp = 4, kFirstProducer = 5, kCopyWarps = 8;
+constexpr int kMmaWarp = 4, kCopyWarp = 5, kSplitThreads = 192;
 constexpr uint32_t kWaitLimit = 1u << 22;
 
 constexpr int kPairM = 256;          // tokens per pair of CTAs
@@ -77,9 +81,6 @@ __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
 }
 __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 // One thread of the (converged) warp, chosen so that the compiler knows that
 // it runs alone: the tensor core's and TMA's operands then stay in uniform
@@ -167,58 +168,82 @@ struct Ring {
   }
 };
 
-// Sixteen bytes of a matrix row from byte `at` of its `row_bytes` on, at any
-// alignment: zeros past the row's end.  Aligned 16-byte words are read where
-// both lie between the matrix's first and last byte.
-__device__ __forceinline__ uint4 row_chunk(const Side &s, int64_t row, int64_t at, int64_t row_bytes) {
-  uint4 out = make_uint4(0, 0, 0, 0);
-  if (row >= s.rows || at >= row_bytes) return out;
-  const uint8_t *p = s.p + row * s.pitch + at;
-  const uint32_t r = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
-  const uint8_t *a = p - r;
-  const int64_t left = row_bytes - at;
-  if (left >= 16 && r == 0) return *reinterpret_cast<const uint4 *>(p);
-  if (left >= 16 && a >= s.p && a + 32 <= s.p + s.span) {
-    const uint4 lo = reinterpret_cast<const uint4 *>(a)[0], hi = reinterpret_cast<const uint4 *>(a)[1];
+// --------------------------------------------------------- align_kernel
+
+// Sixteen bytes of a matrix row at any alignment, read as the two aligned
+// 16-byte words around them.  read() only issues loads, so that several
+// chunks' can be under way; value() realigns.
+struct Chunk {
+  uint4 lo, hi;
+  const uint8_t *p;
+  int left;  // bytes of the row from p on (more than 16: 16); 0: zeros
+
+  // The chunk `at` bytes into `row` of a side whose rows have row_bytes.
+  __device__ __forceinline__ void read(const Side &s, int64_t row, int64_t at, int64_t row_bytes) {
+    const int64_t rest = row < s.rows ? row_bytes - at : 0;
+    left = rest >= 16 ? 16 : rest > 0 ? static_cast<int>(rest) : 0;
+    p = s.p + row * s.pitch + at;
+    const uint32_t r = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint8_t *a = p - r;
+    // Words that leave the matrix are not read: such chunks go byte by byte.
+    const bool whole = left == 16 && a >= s.p && a + (r ? 32 : 16) <= s.p + s.span;
+    if (left && !whole) left |= 32;
+    lo = hi = make_uint4(0, 0, 0, 0);
+    if (whole) lo = *reinterpret_cast<const uint4 *>(a);
+    if (whole && r) hi = *reinterpret_cast<const uint4 *>(a + 16);
+  }
+
+  __device__ __forceinline__ uint4 value() const {
+    if (left & 32) {
+      uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < (left & 31)) v[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+      return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    const uint32_t r = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15), sh = 8 * (r & 3);
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     uint32_t v[6], u[5];
 #pragma unroll
     for (int i = 0; i < 6; ++i) v[i] = r & 8 ? w[i + 2] : w[i];
 #pragma unroll
     for (int i = 0; i < 5; ++i) u[i] = r & 4 ? v[i + 1] : v[i];
-    const uint32_t sh = 8 * (r & 3);
     return make_uint4(__funnelshift_r(u[0], u[1], sh), __funnelshift_r(u[1], u[2], sh), __funnelshift_r(u[2], u[3], sh),
                       __funnelshift_r(u[3], u[4], sh));
   }
-  uint32_t v[4] = {0, 0, 0, 0};
+};
+
+// Copies rows that TMA cannot read (an address or a stride that is no multiple
+// of 16 bytes) to rows that it can.  A warp moves 2 KiB of a row, four chunks
+// a lane, all of them under way before the first is stored.
+struct AlignArgs {
+  Side from[2];
+  uint8_t *to[2];
+  int64_t warps[2];  // warps for each matrix; 0: it stays where it is
+  int64_t row_bytes, pitch;
+  uint32_t segments;  // per row
+};
+constexpr int kAlignWarps = 8, kAlignEach = 4;
+
+__global__ void __launch_bounds__(kAlignWarps * 32) align_kernel(const __grid_constant__ AlignArgs a) {
+  int64_t w = int64_t(blockIdx.x) * kAlignWarps + (threadIdx.x >> 5);
+  const int i = w >= a.warps[0];
+  if (i) w -= a.warps[0];
+  if (w >= a.warps[i]) return;
+  const int64_t row = w / a.segments;
+  const int64_t at0 = (w - row * a.segments) * (512 * kAlignEach) + (threadIdx.x & 31) * 16;
+  Chunk c[kAlignEach];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < left) v[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
-  return make_uint4(v[0], v[1], v[2], v[3]);
+  for (int e = 0; e < kAlignEach; ++e) c[e].read(a.from[i], row, at0 + 512 * e, a.row_bytes);
+#pragma unroll
+  for (int e = 0; e < kAlignEach; ++e)
+    if (at0 + 512 * e < a.pitch) *reinterpret_cast<uint4 *>(a.to[i] + row * a.pitch + at0 + 512 * e) = c[e].value();
 }
 
-// `rows` tile rows of a side into a swizzled stage, by kCopyWarps warps.
-template <int kRows>
-__device__ __forceinline__ void copy_tile(const Side &s, uint8_t *dst, int64_t row0, int64_t at, int64_t row_bytes, int t) {
-  constexpr int kChunks = kRows * 8, kBatch = 4, kThreads = kCopyWarps * 32;
-#pragma unroll 1
-  for (int c0 = t; c0 < kChunks; c0 += kThreads * kBatch) {
-    uint4 v[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int c = c0 + i * kThreads;
-      if (c < kChunks) v[i] = row_chunk(s, row0 + c / 8, at + (c % 8) * 16, row_bytes);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int c = c0 + i * kThreads, row = c / 8;
-      if (c < kChunks) *reinterpret_cast<uint4 *>(dst + row * 128 + (((c % 8) ^ (row & 7)) << 4)) = v[i];
-    }
-  }
-}
+// ---------------------------------------------------------- split_kernel
 
-template <int BM, bool kTma, bool kEight>
-__global__ void __launch_bounds__((kFirstProducer + (kTma ? 1 : kCopyWarps)) * 32)
+template <int BM, bool kEight>
+__global__ void __launch_bounds__(kSplitThreads)
 split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
              const __grid_constant__ LinArgs a) {
   constexpr int kStageBytes = (kTileN + BM) * kStageK;
@@ -238,7 +263,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
-      bar_init(&full[i], kTma ? 1 : kCopyWarps * 32);
+      bar_init(&full[i], 1);
       bar_init(&empty[i], 1);
     }
     bar_init(&done, 1);
@@ -255,34 +280,21 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   const uint32_t tmem = tmem_base;
 
   Ring r;
-  if (warp >= kFirstProducer) {
-    if (kTma) {
-      if (elect_one()) {
-        int i = 0;
-        constexpr int kStep = kEight ? kStageK : kStageK / 2;
-        for (int at = first * kStep; i < blocks; ++i, at += kStep, r.next(a.stages)) {
-          // Before its first use a stage counts as released.
-          if (!bar_wait(&empty[r.at], r.phase ^ 1)) break;
-          uint8_t *stage = smem + r.at * kStageBytes;
-          bar_expect(&full[r.at], kTileN * kStageK + a.x_box * kStageK);
-          tma_load(&wmap, stage, &full[r.at], at, static_cast<int32_t>(n0));
-          tma_load(&xmap, stage + kTileN * kStageK, &full[r.at], at, static_cast<int32_t>(m0));
-        }
-        if (i < blocks) {  // a wait gave up: the copies in flight land before the CTA ends
-          failed = 1;
-          for (int j = i < a.stages ? 0 : i - a.stages; j < i; ++j) bar_wait(&full[j % a.stages], (j / a.stages) & 1);
-        }
-      }
-    } else {
-      const int t = threadIdx.x - kFirstProducer * 32;
-      for (int i = 0; i < blocks; ++i, r.next(a.stages)) {
-        if (!bar_wait(&empty[r.at], r.phase ^ 1)) { failed = 1; break; }
+  if (warp == kCopyWarp) {
+    if (elect_one()) {
+      int i = 0;
+      constexpr int kStep = kEight ? kStageK : kStageK / 2;
+      for (int at = first * kStep; i < blocks; ++i, at += kStep, r.next(a.stages)) {
+        // Before its first use a stage counts as released.
+        if (!bar_wait(&empty[r.at], r.phase ^ 1)) break;
         uint8_t *stage = smem + r.at * kStageBytes;
-        const int64_t at = int64_t(first + i) * kStageK;
-        copy_tile<kTileN>(a.w, stage, n0, at, a.kbytes, t);
-        copy_tile<BM>(a.x, stage + kTileN * kStageK, m0, at, a.kbytes, t);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        bar_arrive(&full[r.at]);
+        bar_expect(&full[r.at], kTileN * kStageK + a.x_box * kStageK);
+        tma_load(&wmap, stage, &full[r.at], at, static_cast<int32_t>(n0));
+        tma_load(&xmap, stage + kTileN * kStageK, &full[r.at], at, static_cast<int32_t>(m0));
+      }
+      if (i < blocks) {  // a wait gave up: the copies in flight land before the CTA ends
+        failed = 1;
+        for (int j = i < a.stages ? 0 : i - a.stages; j < i; ++j) bar_wait(&full[j % a.stages], (j / a.stages) & 1);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -801,7 +813,7 @@ Shape split_shape(int64_t m, int64_t n, int k_blocks, int sms) {
   return s;
 }
 
-template <int BM, bool kTma, bool kEight>
+template <int BM, bool kEight>
 st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int64_t tiles, int dev, cudaStream_t st) {
   constexpr int kStageBytes = (kTileN + BM) * kStageK;
   // About half of the SM's shared memory, so that two CTAs share one, but at
@@ -811,12 +823,12 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   if (a.stages < 3) a.stages = 3;
   const int smem = a.stages * kStageBytes + 1024;
   static_assert(BM * kTileN * 4 <= 3 * kStageBytes, "partial sums fit over the stages");
-  constexpr auto kernel = split_kernel<BM, kTma, kEight>;
+  constexpr auto kernel = split_kernel<BM, kEight>;
   cudaError_t e = allow_smem<kernel>(dev, smem);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits));
-    cfg.blockDim = dim3((kFirstProducer + (kTma ? 1 : kCopyWarps)) * 32);
+    cfg.blockDim = dim3(kSplitThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -855,8 +867,54 @@ st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &w
 
 }  // namespace
 
+namespace {
+
+int item_of(const st_linear_args &p) { return p.x_dtype == ST_BF16 || p.x_dtype == ST_F16 ? 2 : 1; }
+
+Side side_of(const void *ptr, int64_t ld, int64_t rows, int64_t k, int item) {
+  return Side{static_cast<const uint8_t *>(ptr), ld * item, ld * item * (rows - 1) + k * item, rows};
+}
+
+// Copies the operands that TMA cannot read to aligned rows in the workspace
+// and points the arguments at them.
+st_status align(LinArgs &a, uint8_t *workspace, cudaStream_t st) {
+  AlignArgs al{};
+  al.row_bytes = a.kbytes;
+  al.pitch = (a.kbytes + 15) / 16 * 16;
+  al.segments = static_cast<uint32_t>((al.pitch + 512 * kAlignEach - 1) / (512 * kAlignEach));
+  Side *sides[2] = {&a.w, &a.x};
+  for (int i = 0; i < 2; ++i) {
+    Side &s = *sides[i];
+    if (a.kbytes == 0 || tma_ok(s)) continue;
+    al.from[i] = s;
+    al.to[i] = workspace;
+    al.warps[i] = s.rows * al.segments;
+    workspace += s.rows * al.pitch;
+    s.p = al.to[i];
+    s.pitch = al.pitch;
+  }
+  const int64_t blocks = (al.warps[0] + al.warps[1] + kAlignWarps - 1) / kAlignWarps;
+  if (blocks == 0) return ST_OK;
+  if (blocks > 0x7fffffff) return set_error(ST_E_INVAL, "st_linear: too many rows to align in one launch");
+  align_kernel<<<static_cast<unsigned>(blocks), kAlignWarps * 32, 0, st>>>(al);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_linear: aligning rows: %s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
+  return ST_OK;
+}
+
+}  // namespace
+
+int64_t linear_workspace(const st_linear_args &p) {
+  const int item = item_of(p);
+  const int64_t pitch = (p.k * item + 15) / 16 * 16;
+  int64_t bytes = 0;
+  if (p.k > 0 && !tma_ok(side_of(p.w, p.ldw, p.n, p.k, item))) bytes += p.n * pitch;
+  if (p.k > 0 && !tma_ok(side_of(p.x, p.ldx, p.m, p.k, item))) bytes += p.m * pitch;
+  return bytes;
+}
+
 st_status launch_linear(const st_linear_args &p, void *stream) {
-  const int item = p.x_dtype == ST_BF16 || p.x_dtype == ST_F16 ? 2 : 1;
+  const int item = item_of(p);
   LinArgs a{};
   a.m = p.m; a.n = p.n; a.kbytes = p.k * item;
   a.eight = item == 1;
@@ -865,11 +923,8 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   a.x_scale_step = p.x_scale_count > 1; a.w_scale_step = p.w_scale_count > 1;
   a.bias = p.bias; a.residual = p.residual; a.y = p.y;
   a.ldr = p.ldr; a.ldy = p.ldy;
-  auto side = [&](const void *ptr, int64_t ld, int64_t rows) {
-    return Side{static_cast<const uint8_t *>(ptr), ld * item, ld * item * (rows - 1) + a.kbytes, rows};
-  };
-  a.x = side(p.x, p.ldx, p.m);
-  a.w = side(p.w, p.ldw, p.n);
+  a.x = side_of(p.x, p.ldx, p.m, p.k, item);
+  a.w = side_of(p.w, p.ldw, p.n, p.k, item);
   int dev = 0;
   const Device *gpu = nullptr;
   st_status s = device(&dev, &gpu);
@@ -883,9 +938,10 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   auto idesc = [](uint32_t fa, uint32_t fb, uint32_t rows, uint32_t cols) {
     return (1u << 4) | (fa << 7) | (fb << 10) | ((cols / 8) << 17) | ((rows / 16) << 24);
   };
-  const bool tma = p.k > 0 && tma_ok(a.w) && tma_ok(a.x);
   CUtensorMap wmap{}, xmap{};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  s = align(a, static_cast<uint8_t *>(p.workspace), st);
+  if (s != ST_OK) return s;
 
   const int64_t out = static_cast<int64_t>(st_dtype_size(p.y_dtype));
   auto aligned = [&](int64_t to) {
@@ -894,7 +950,7 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   };
 
   const Shape d = dense_shape(p.m, p.n, a.k_blocks, sms), c = split_shape(p.m, p.n, a.k_blocks, sms);
-  if (tma && d.cost < c.cost) {
+  if (p.k > 0 && d.cost < c.cost) {
     if (d.m_tiles * d.n_tiles > 0x3fffffff)
       return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
     a.m_tiles = static_cast<int>(d.m_tiles);
@@ -916,7 +972,7 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   if (tiles * a.splits > 0x7fffffff)
     return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
   a.idesc = idesc(fw, fx, kTileN, bm);
-  if (tma) {
+  if (p.k > 0) {
     s = encode(&wmap, a.w, p.k, item, kTileN);
     // Fewer tokens than the MMA's columns: only they are copied (what the other
     // columns hold reaches no sum that is read).
@@ -924,9 +980,8 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
     if (s == ST_OK) s = encode(&xmap, a.x, p.k, item, a.x_box);
     if (s != ST_OK) return s;
   }
-#define ST_SPLIT(BM)                                                                                             \
-  (tma ? (a.eight ? launch_split<BM, true, true>(a, wmap, xmap, tiles, dev, st) : launch_split<BM, true, false>(a, wmap, xmap, tiles, dev, st)) \
-       : (a.eight ? launch_split<BM, false, true>(a, wmap, xmap, tiles, dev, st) : launch_split<BM, false, false>(a, wmap, xmap, tiles, dev, st)))
+#define ST_SPLIT(BM) \
+  (a.eight ? launch_split<BM, true>(a, wmap, xmap, tiles, dev, st) : launch_split<BM, false>(a, wmap, xmap, tiles, dev, st))
   switch (bm) {
     case 16: return ST_SPLIT(16);
     case 32: return ST_SPLIT(32);

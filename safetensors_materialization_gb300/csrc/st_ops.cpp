@@ -63,6 +63,37 @@ st_status check_output(const char *op, st_dtype y, const float *scale, const flo
     if (try_status != ST_OK) return try_status; \
   } while (0)
 
+st_status check_linear(const st_linear_args *a, bool *empty) {
+  const char *op = "st_linear";
+  ST_TRY(check_sizes(op, a->m, a->n));
+  ST_TRY(check_sizes(op, a->m, a->k));
+  const bool sixteen = (a->x_dtype == ST_BF16 || a->x_dtype == ST_F16) && a->w_dtype == a->x_dtype;
+  const bool eight = a->x_dtype == ST_F8_E4M3 && (a->w_dtype == ST_F8_E4M3 || a->w_dtype == ST_F8_E5M2);
+  if (!sixteen && !eight)
+    return set_error(ST_E_DTYPE, "%s: x and weight are both BF16, both F16, or F8_E4M3 with F8_E4M3 or F8_E5M2 (got %d, %d)",
+                     op, (int)a->x_dtype, (int)a->w_dtype);
+  if (!is_float16or32(a->y_dtype)) return set_error(ST_E_DTYPE, "%s: the output is BF16, F16 or F32, not %d", op, (int)a->y_dtype);
+  if (a->bias && !is_float16or32(a->bias_dtype))
+    return set_error(ST_E_DTYPE, "%s: bias is BF16, F16 or F32, not %d", op, (int)a->bias_dtype);
+  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
+  if (a->x_scale && a->x_scale_count != 1 && a->x_scale_count != a->m)
+    return set_error(ST_E_INVAL, "%s: %lld scales for x (1 or m = %lld)", op, (long long)a->x_scale_count, (long long)a->m);
+  if (a->w_scale && a->w_scale_count != 1 && a->w_scale_count != a->n)
+    return set_error(ST_E_INVAL, "%s: %lld scales for weight (1 or n = %lld)", op, (long long)a->w_scale_count, (long long)a->n);
+  ST_TRY(check_vector(op, "x_scale", a->x_scale, ST_F32));
+  ST_TRY(check_vector(op, "w_scale", a->w_scale, ST_F32));
+  *empty = a->m == 0 || a->n == 0;
+  if (*empty) return ST_OK;
+  if (a->k > 0) {
+    ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->m, a->k, true));
+    ST_TRY(check_matrix(op, "weight", a->w, a->ldw, a->w_dtype, a->n, a->k, true));
+  }
+  if (a->bias) ST_TRY(check_vector(op, "bias", a->bias, a->bias_dtype));
+  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->y_dtype, a->m, a->n, true));
+  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->m, a->n, false));
+  return ST_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -100,34 +131,25 @@ st_status st_gated_act(const st_gated_act_args *a, void *stream) {
   return launch_gated_act(*a, stream);
 }
 
+st_status st_linear_workspace(const st_linear_args *a, uint64_t *bytes) {
+  if (!a || !bytes) return set_error(ST_E_INVAL, "st_linear_workspace: NULL argument");
+  bool empty = false;
+  ST_TRY(check_linear(a, &empty));
+  *bytes = empty ? 0 : static_cast<uint64_t>(linear_workspace(*a));
+  return ST_OK;
+}
+
 st_status st_linear(const st_linear_args *a, void *stream) {
   if (!a) return set_error(ST_E_INVAL, "st_linear: NULL arguments");
-  const char *op = "st_linear";
-  ST_TRY(check_sizes(op, a->m, a->n));
-  ST_TRY(check_sizes(op, a->m, a->k));
-  const bool sixteen = (a->x_dtype == ST_BF16 || a->x_dtype == ST_F16) && a->w_dtype == a->x_dtype;
-  const bool eight = a->x_dtype == ST_F8_E4M3 && (a->w_dtype == ST_F8_E4M3 || a->w_dtype == ST_F8_E5M2);
-  if (!sixteen && !eight)
-    return set_error(ST_E_DTYPE, "%s: x and weight are both BF16, both F16, or F8_E4M3 with F8_E4M3 or F8_E5M2 (got %d, %d)",
-                     op, (int)a->x_dtype, (int)a->w_dtype);
-  if (!is_float16or32(a->y_dtype)) return set_error(ST_E_DTYPE, "%s: the output is BF16, F16 or F32, not %d", op, (int)a->y_dtype);
-  if (a->bias && !is_float16or32(a->bias_dtype))
-    return set_error(ST_E_DTYPE, "%s: bias is BF16, F16 or F32, not %d", op, (int)a->bias_dtype);
-  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
-  if (a->x_scale && a->x_scale_count != 1 && a->x_scale_count != a->m)
-    return set_error(ST_E_INVAL, "%s: %lld scales for x (1 or m = %lld)", op, (long long)a->x_scale_count, (long long)a->m);
-  if (a->w_scale && a->w_scale_count != 1 && a->w_scale_count != a->n)
-    return set_error(ST_E_INVAL, "%s: %lld scales for weight (1 or n = %lld)", op, (long long)a->w_scale_count, (long long)a->n);
-  ST_TRY(check_vector(op, "x_scale", a->x_scale, ST_F32));
-  ST_TRY(check_vector(op, "w_scale", a->w_scale, ST_F32));
-  if (a->m == 0 || a->n == 0) return ST_OK;
-  if (a->k > 0) {
-    ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->m, a->k, true));
-    ST_TRY(check_matrix(op, "weight", a->w, a->ldw, a->w_dtype, a->n, a->k, true));
-  }
-  if (a->bias) ST_TRY(check_vector(op, "bias", a->bias, a->bias_dtype));
-  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->y_dtype, a->m, a->n, true));
-  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->m, a->n, false));
+  bool empty = false;
+  ST_TRY(check_linear(a, &empty));
+  if (empty) return ST_OK;
+  const int64_t need = linear_workspace(*a);
+  if (need && (!a->workspace || a->workspace_bytes < static_cast<uint64_t>(need)))
+    return set_error(ST_E_INVAL, "st_linear: rows that are no multiples of 16 bytes apart need a workspace of %lld bytes, %llu given",
+                     (long long)need, (unsigned long long)(a->workspace ? a->workspace_bytes : 0));
+  if (need && reinterpret_cast<uintptr_t>(a->workspace) % 16)
+    return set_error(ST_E_ALIGN, "st_linear: the workspace is not 16-byte aligned");
   return launch_linear(*a, stream);
 }
 

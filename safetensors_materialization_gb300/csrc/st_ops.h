@@ -17,5 +17,7 @@ constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the smallest scale, so 
 st_status launch_rms_norm(const st_rms_norm_args &a, void *stream);
 st_status launch_gated_act(const st_gated_act_args &a, void *stream);
 st_status launch_linear(const st_linear_args &a, void *stream);
+// Bytes of workspace the product needs (rows that TMA cannot read).
+int64_t linear_workspace(const st_linear_args &a);
 
 }  // namespace stmat

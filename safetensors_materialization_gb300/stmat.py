@@ -35,7 +35,7 @@ EXPORTS = [
     "st_materialize_noalloc", "st_static_check", "st_index_open", "st_files_open", "st_files_close", "st_files_read",
     "st_load_files", "st_cache_create", "st_cache_free", "st_cache_get", "st_cache_release",
     "st_cache_stats", "st_cache_clear", "st_load_tensors", "st_host_affinity", "st_device_reads_pageable",
-    "st_files_prefetch", "st_rms_norm", "st_gated_act", "st_linear",
+    "st_files_prefetch", "st_rms_norm", "st_gated_act", "st_linear", "st_linear_workspace",
     "st_last_error", "st_status_name", "st_dtype_size", "st_dtype_name", "st_version",
 ]
 
@@ -115,7 +115,7 @@ class LinearArgs(C.Structure):
                 ("ldx", C.c_int64), ("w", C.c_void_p), ("ldw", C.c_int64), ("x_scale", C.c_void_p),
                 ("x_scale_count", C.c_int64), ("w_scale", C.c_void_p), ("w_scale_count", C.c_int64),
                 ("bias", C.c_void_p), ("residual", C.c_void_p), ("ldr", C.c_int64), ("y", C.c_void_p),
-                ("ldy", C.c_int64)]
+                ("ldy", C.c_int64), ("workspace", C.c_void_p), ("workspace_bytes", C.c_uint64)]
 
 
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -181,6 +181,7 @@ def lib():
             "st_rms_norm": [C.POINTER(RmsNormArgs), P],
             "st_gated_act": [C.POINTER(GatedActArgs), P],
             "st_linear": [C.POINTER(LinearArgs), P],
+            "st_linear_workspace": [C.POINTER(LinearArgs), C.POINTER(U64)],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -1056,5 +1057,11 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
         if residual.shape != shape or residual.dtype != out.dtype:
             raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, y: {tuple(shape)} {out.dtype}")
         a.residual, a.ldr, _, _ = _matrix(residual, "residual")
+    size = x.element_size()
+    if m and n and k and ((a.x | a.w | a.ldx * size | a.ldw * size) & 15 or not a.ldx or not a.ldw):
+        need = C.c_uint64()
+        _check(lib().st_linear_workspace(a, C.byref(need)))
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), need.value
     _check(lib().st_linear(a, raw_stream(x.get_device())))
     return out

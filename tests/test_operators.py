@@ -163,6 +163,27 @@ def test_null_arguments_and_empty_sizes(stmat, op):
         assert stmat.STATUS[call(C.byref(OPS[op](stmat, **kw)), None)] == "ST_OK"
 
 
+def test_linear_workspace_size_and_refusals(stmat):
+    """Room for an aligned copy of what does not lie on 16-byte boundaries."""
+    call, need = stmat.lib().st_linear_workspace, C.c_uint64()
+    for kw, want in ((dict(), 0), (dict(ldx=17), 2 * 32), (dict(x=(1 << 20) + 2), 2 * 32), (dict(ldw=18), 8 * 32),
+                     (dict(k=13), 0), (dict(k=13, ldx=13, ldw=13), 10 * 32), (dict(m=1, ldx=17), 0), (dict(ldw=0), 8 * 32),
+                     (dict(k=0, ldx=1), 0), (dict(m=0, ldx=17), 0),
+                     (dict(x_dtype=13, w_dtype=13, ldw=24), 8 * 16)):
+        a = linear_args(stmat, **kw)
+        assert stmat.STATUS[call(C.byref(a), C.byref(need))] == "ST_OK"
+        assert need.value == want, kw
+    a = linear_args(stmat, ldx=17)
+    for kw, status in ((dict(), "ST_E_INVAL"), (dict(workspace=5 << 20, workspace_bytes=63), "ST_E_INVAL"),
+                       (dict(workspace=(5 << 20) + 8, workspace_bytes=64), "ST_E_ALIGN")):
+        for k, v in kw.items():
+            setattr(a, k, v)
+        assert stmat.STATUS[stmat.lib().st_linear(C.byref(a), None)] == status
+    assert stmat.STATUS[call(None, C.byref(need))] == "ST_E_INVAL"
+    assert stmat.STATUS[call(C.byref(a), None)] == "ST_E_INVAL"
+    assert stmat.STATUS[call(C.byref(linear_args(stmat, k=-1)), C.byref(need))] == "ST_E_INVAL"
+
+
 def test_binding_refuses_host_tensors_and_unknown_names(stmat):
     x = torch.zeros(2, 8)
     for call in (lambda: stmat.rms_norm(x), lambda: stmat.gated_act(x), lambda: stmat.linear(x, x)):
