@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -856,18 +857,35 @@ class Outputs:
 
 # ------------------------------------------- operators on materialized tensors
 
-_TORCH = None  # (torch, {torch dtype: st_dtype}, {output name: (torch dtype, st_dtype)}, stream of a device)
+# The argument structs' layouts for struct.pack: one call packs a struct in a
+# quarter of the time that setting a ctypes structure's fields takes.
+_NORM_ARGS = struct.Struct("@qqfiiiPqPqPPqPqPP")
+_ACT_ARGS = struct.Struct("@qqiiiPqPqPqPP")
+_LINEAR_ARGS = struct.Struct("@qqqiiiiiPqPqPqPqPPqPqPQ")
+
+_OPS = None
 
 
-def _torch():
-    global _TORCH
-    if _TORCH is None:
+class _Ops:
+    """What every operator call needs, looked up once."""
+
+    def __init__(self):
         import torch
+        self.torch, self.empty, self.empty_like = torch, torch.empty, torch.empty_like
         names = ("BF16", "F16", "F32", "F8_E4M3", "F8_E5M2")
-        _TORCH = (torch, {torch_dtype(n): DTYPES.index(n) for n in names},
-                  {n: (torch_dtype(n), DTYPES.index(n)) for n in names},
-                  torch._C._cuda_getCurrentRawStream)  # 0.1 us; torch.cuda.current_stream() takes 11
-    return _TORCH
+        self.codes = {torch_dtype(n): DTYPES.index(n) for n in names}
+        self.dsts = {n: (torch_dtype(n), DTYPES.index(n)) for n in names}
+        # 0.1 us; torch.cuda.current_stream() takes 11
+        self.stream = torch._C._cuda_getCurrentRawStream
+        call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p)
+        self.rms_norm, self.gated_act, self.linear, self.linear_workspace = (
+            call((n, lib())) for n in ("st_rms_norm", "st_gated_act", "st_linear", "st_linear_workspace"))
+
+
+def _ops():
+    global _OPS
+    _OPS = _Ops()
+    return _OPS
 
 
 def _invalid(msg):
@@ -879,18 +897,18 @@ def _matrix(t, name):
     leading dimensions are the rows (a vector: one row); no copy is made."""
     if not t.is_cuda:
         raise _invalid(f"{name} is not on the GPU")
-    d = t.dim()
-    if d == 2:
-        rows, cols = t.shape
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
         ld, inner = t.stride()
-    elif d == 1:
-        rows, cols, ld, inner = 1, t.shape[0], t.shape[0], t.stride(0)
-    elif d == 0:
+    elif len(shape) == 1:
+        rows, cols, ld, inner = 1, shape[0], shape[0], t.stride(0)
+    elif len(shape) == 0:
         raise _invalid(f"{name} has no dimensions")
     else:
-        cols, inner = t.shape[-1], t.stride(-1)
+        cols, inner = shape[-1], t.stride(-1)
         rows, ld = 1, None
-        for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
             if n == 1:
                 continue
             if ld is None:
@@ -904,17 +922,17 @@ def _matrix(t, name):
     return t.data_ptr(), cols if rows <= 1 else ld, rows, cols
 
 
-def _vector(t, name, counts, dtypes, codes):
-    """(address, entries, st_dtype) of a contiguous vector of one of `counts`
-    entries."""
-    if not t.is_cuda:
-        raise _invalid(f"{name} is not on the GPU")
+def _vector(t, name, count, dtypes, codes, one=False):
+    """(address, entries, st_dtype) of a contiguous vector of `count` entries
+    (or, with `one`, of a single one)."""
     n = t.numel()
-    if n not in counts or not t.is_contiguous():
-        raise _invalid(f"{name}: a contiguous tensor of {' or '.join(map(str, counts))} entries is needed")
+    if (n != count and not (one and n == 1)) or not t.is_contiguous():
+        raise _invalid(f"{name}: a contiguous tensor of {'1 or ' if one else ''}{count} entries is needed")
     code = codes.get(t.dtype)
     if code not in dtypes:
         raise StmatError(6, f"{name}: {t.dtype} is not one of {', '.join(DTYPES[d] for d in dtypes)}")
+    if not t.is_cuda:
+        raise _invalid(f"{name} is not on the GPU")
     return t.data_ptr(), n, code
 
 
@@ -923,12 +941,20 @@ _F32 = (11,)
 _E4M3 = 13
 
 
-def _dst(dst, like, dsts, codes):
+def _dst(dst, like, ops):
     if dst is None:
-        return like, codes.get(like, -1)
-    if dst not in dsts:
-        raise StmatError(6, f"dst {dst!r} is not one of {', '.join(dsts)}")
-    return dsts[dst]
+        return like, ops.codes.get(like, -1)
+    got = ops.dsts.get(dst)
+    if got is None:
+        raise StmatError(6, f"dst {dst!r} is not one of {', '.join(ops.dsts)}")
+    return got
+
+
+def _new(like, shape, dtype, ops):
+    """A contiguous tensor of `shape` = like's."""
+    if like.is_contiguous():
+        return ops.empty_like(like, dtype=dtype)
+    return ops.empty(shape, dtype=dtype, device=like.device)
 
 
 class _On:
@@ -959,31 +985,34 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
     scale None writes one scale per row; scale: a one-element F32 tensor to
     use instead.  Returns (y, scales or None, h in x's dtype, or None without
     a residual); y * scales[..., None] stands for the normed rows."""
-    torch, codes, dsts, raw_stream = _torch()
+    ops = _OPS or _ops()
     if stream is not None:
-        return _On(torch, stream).run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
-                                      (x, weight, residual, scale))
-    a = RmsNormArgs()
-    a.x, a.ldx, rows, cols = _matrix(x, "x")
-    a.rows, a.cols, a.eps, a.x_dtype = rows, cols, eps, codes.get(x.dtype, -1)
-    ydt, a.y_dtype = _dst(dst, x.dtype, dsts, codes)
+        return _On(ops.torch, stream).run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
+                                          (x, weight, residual, scale))
+    codes, shape, x_type = ops.codes, x.shape, x.dtype
+    px, ldx, rows, cols = _matrix(x, "x")
+    x_code = codes.get(x_type, -1)
+    y_type, y_code = _dst(dst, x_type, ops)
+    pw = pr = ph = ldr = ps = pss = 0
+    w_code, h, scales = 10, None, None
     if weight is not None:
-        a.weight, _, a.w_dtype = _vector(weight, "weight", (cols,), _FLOATS, codes)
-    h = scales = None
+        pw, _, w_code = _vector(weight, "weight", cols, _FLOATS, codes)
     if residual is not None:
-        if residual.shape != x.shape or residual.dtype != x.dtype:
-            raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, x: {tuple(x.shape)} {x.dtype}")
-        a.residual, a.ldr, _, _ = _matrix(residual, "residual")
-        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        a.h, a.ldh = h.data_ptr(), cols
-    y = torch.empty(x.shape, dtype=ydt, device=x.device)
-    a.y, a.ldy = y.data_ptr(), cols
+        if residual.shape != shape or residual.dtype != x_type:
+            raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, x: {tuple(shape)} {x_type}")
+        pr, ldr, _, _ = _matrix(residual, "residual")
+        h = _new(x, shape, x_type, ops)
+        ph = h.data_ptr()
+    y = _new(x, shape, y_type, ops)
     if scale is not None:
-        a.scale = _vector(scale, "scale", (1,), _F32, codes)[0]
-    elif a.y_dtype == _E4M3:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        a.scales = scales.data_ptr()
-    _check(lib().st_rms_norm(a, raw_stream(x.get_device())))
+        ps = _vector(scale, "scale", 1, _F32, codes)[0]
+    elif y_code == _E4M3:
+        scales = ops.empty(shape[:-1], dtype=ops.torch.float32, device=x.device)
+        pss = scales.data_ptr()
+    code = ops.rms_norm(_NORM_ARGS.pack(rows, cols, eps, x_code, w_code, y_code, px, ldx, pr, ldr, pw, ph, cols,
+                                        y.data_ptr(), cols, ps, pss), ops.stream(x.get_device()))
+    if code:
+        _check(code)
     return y, scales, h
 
 
@@ -992,26 +1021,28 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
     F16 or F32; gate and up may be the halves of one product's columns.  act:
     "none", "relu", "silu", "gelu" or "gelu_tanh"; dst and scale as for
     rms_norm.  Returns (y, scales or None)."""
-    torch, codes, dsts, raw_stream = _torch()
+    ops = _OPS or _ops()
     if stream is not None:
-        return _On(torch, stream).run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
-    a = GatedActArgs()
-    a.gate, a.ldg, a.rows, a.cols = _matrix(gate, "gate")
-    a.act, a.x_dtype = ACTS.get(act, -1), codes.get(gate.dtype, -1)
-    ydt, a.y_dtype = _dst(dst, gate.dtype, dsts, codes)
-    if up is not None:
-        if up.shape != gate.shape or up.dtype != gate.dtype:
-            raise _invalid(f"up: {tuple(up.shape)} {up.dtype}, gate: {tuple(gate.shape)} {gate.dtype}")
-        a.up, a.ldu, _, _ = _matrix(up, "up")
-    y = torch.empty(gate.shape, dtype=ydt, device=gate.device)
-    a.y, a.ldy = y.data_ptr(), gate.shape[-1]
+        return _On(ops.torch, stream).run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
+    shape, x_type = gate.shape, gate.dtype
+    pg, ldg, rows, cols = _matrix(gate, "gate")
+    y_type, y_code = _dst(dst, x_type, ops)
+    pu = ldu = ps = pss = 0
     scales = None
+    if up is not None:
+        if up.shape != shape or up.dtype != x_type:
+            raise _invalid(f"up: {tuple(up.shape)} {up.dtype}, gate: {tuple(shape)} {x_type}")
+        pu, ldu, _, _ = _matrix(up, "up")
+    y = _new(gate, shape, y_type, ops)
     if scale is not None:
-        a.scale = _vector(scale, "scale", (1,), _F32, codes)[0]
-    elif a.y_dtype == _E4M3:
-        scales = torch.empty(gate.shape[:-1], dtype=torch.float32, device=gate.device)
-        a.scales = scales.data_ptr()
-    _check(lib().st_gated_act(a, raw_stream(gate.get_device())))
+        ps = _vector(scale, "scale", 1, _F32, ops.codes)[0]
+    elif y_code == _E4M3:
+        scales = ops.empty(shape[:-1], dtype=ops.torch.float32, device=gate.device)
+        pss = scales.data_ptr()
+    code = ops.gated_act(_ACT_ARGS.pack(rows, cols, ACTS.get(act, -1), ops.codes.get(x_type, -1), y_code, pg, ldg, pu, ldu,
+                                        y.data_ptr(), cols, ps, pss), ops.stream(gate.get_device()))
+    if code:
+        _check(code)
     return y, scales
 
 
@@ -1026,42 +1057,53 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     dst: "BF16", "F16" or "F32" (default: x's dtype, BF16 for 8-bit x);
     residual has y's shape and dtype.  out: the tensor to write (may be the
     residual); by default a new one."""
-    torch, codes, dsts, raw_stream = _torch()
+    ops = _OPS or _ops()
     if stream is not None:
-        return _On(torch, stream).run(lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
-                                      (x, weight, x_scale, w_scale, bias, residual, out))
-    a = LinearArgs()
-    a.x, a.ldx, m, k = _matrix(x, "x")
-    a.w, a.ldw, n, wk = _matrix(weight, "weight")
+        return _On(ops.torch, stream).run(lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
+                                          (x, weight, x_scale, w_scale, bias, residual, out))
+    codes, x_type = ops.codes, x.dtype
+    px, ldx, m, k = _matrix(x, "x")
+    pw, ldw, n, wk = _matrix(weight, "weight")
     if wk != k or weight.dim() != 2:
         raise _invalid(f"x has rows of {k}, weight is {tuple(weight.shape)}")
-    a.m, a.n, a.k, a.act = m, n, k, ACTS.get(act, -1)
-    a.x_dtype, a.w_dtype = codes.get(x.dtype, -1), codes.get(weight.dtype, -1)
+    x_code = codes.get(x_type, -1)
+    pxs = nxs = pws = nws = pb = pr = ldr = 0
+    b_code = 11
     if x_scale is not None:
-        a.x_scale, a.x_scale_count, _ = _vector(x_scale, "x_scale", (1, m), _F32, codes)
+        pxs, nxs, _ = _vector(x_scale, "x_scale", m, _F32, codes, True)
     if w_scale is not None:
-        a.w_scale, a.w_scale_count, _ = _vector(w_scale, "w_scale", (1, n), _F32, codes)
+        pws, nws, _ = _vector(w_scale, "w_scale", n, _F32, codes, True)
     if bias is not None:
-        a.bias, _, a.bias_dtype = _vector(bias, "bias", (n,), _FLOATS, codes)
+        pb, _, b_code = _vector(bias, "bias", n, _FLOATS, codes)
     shape = x.shape[:-1] + (n,)
     if out is None:
-        ydt, a.y_dtype = _dst(dst, torch.bfloat16 if a.x_dtype == _E4M3 else x.dtype, dsts, codes)
-        out = torch.empty(shape, dtype=ydt, device=x.device)
-        a.y, a.ldy = out.data_ptr(), n
+        y_type, y_code = _dst(dst, ops.torch.bfloat16 if x_code == _E4M3 else x_type, ops)
+        out = ops.empty(shape, dtype=y_type, device=x.device)
+        py, ldy = out.data_ptr(), n
     else:
-        if out.shape != shape or (dst is not None and dsts.get(dst, (None,))[0] != out.dtype):
-            raise _invalid(f"out: {tuple(out.shape)} {out.dtype}, the product is {tuple(shape)} {dst or ''}")
-        a.y_dtype = codes.get(out.dtype, -1)
-        a.y, a.ldy, _, _ = _matrix(out, "out")
+        y_type = out.dtype
+        if out.shape != shape or (dst is not None and _dst(dst, None, ops)[0] != y_type):
+            raise _invalid(f"out: {tuple(out.shape)} {y_type}, the product is {tuple(shape)} {dst or ''}")
+        y_code = codes.get(y_type, -1)
+        py, ldy, _, _ = _matrix(out, "out")
     if residual is not None:
-        if residual.shape != shape or residual.dtype != out.dtype:
-            raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, y: {tuple(shape)} {out.dtype}")
-        a.residual, a.ldr, _, _ = _matrix(residual, "residual")
-    size = x.element_size()
-    if m and n and k and ((a.x | a.w | a.ldx * size | a.ldw * size) & 15 or not a.ldx or not a.ldw):
+        if residual.shape != shape or residual.dtype != y_type:
+            raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, y: {tuple(shape)} {y_type}")
+        pr, ldr, _, _ = _matrix(residual, "residual")
+    w_code, act = codes.get(weight.dtype, -1), ACTS.get(act, -1)
+    args = (m, n, k, act, x_code, w_code, y_code, b_code, px, ldx, pw, ldw, pxs, nxs, pws, nws, pb, pr, ldr, py, ldy)
+    space = size = 0
+    item = x.element_size()
+    if m and n and k and ((px | pw | ldx * item | ldw * item) & 15 or not ldx or not ldw):
         need = C.c_uint64()
-        _check(lib().st_linear_workspace(a, C.byref(need)))
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), need.value
-    _check(lib().st_linear(a, raw_stream(x.get_device())))
+        code = ops.linear_workspace(_LINEAR_ARGS.pack(*args, 0, 0), C.addressof(need))
+        if code:
+            _check(code)
+        size = need.value
+        if size:
+            workspace = ops.empty(size, dtype=ops.torch.uint8, device=x.device)
+            space = workspace.data_ptr()
+    code = ops.linear(_LINEAR_ARGS.pack(*args, space, size), ops.stream(x.get_device()))
+    if code:
+        _check(code)
     return out

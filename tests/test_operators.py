@@ -184,6 +184,15 @@ def test_linear_workspace_size_and_refusals(stmat):
     assert stmat.STATUS[call(C.byref(linear_args(stmat, k=-1)), C.byref(need))] == "ST_E_INVAL"
 
 
+def test_packed_arguments_have_the_structs_layout(stmat):
+    for packed, cls in ((stmat._NORM_ARGS, stmat.RmsNormArgs), (stmat._ACT_ARGS, stmat.GatedActArgs),
+                        (stmat._LINEAR_ARGS, stmat.LinearArgs)):
+        n = len(cls._fields_)
+        got = cls.from_buffer_copy(packed.pack(*range(1, n + 1)))
+        assert packed.size == C.sizeof(cls)
+        assert [getattr(got, f) for f, _ in cls._fields_] == list(range(1, n + 1))
+
+
 def test_binding_refuses_host_tensors_and_unknown_names(stmat):
     x = torch.zeros(2, 8)
     for call in (lambda: stmat.rms_norm(x), lambda: stmat.gated_act(x), lambda: stmat.linear(x, x)):
