@@ -226,6 +226,8 @@ struct AlignArgs {
 constexpr int kAlignWarps = 8, kAlignEach = 4;
 
 __global__ void __launch_bounds__(kAlignWarps * 32) align_kernel(const __grid_constant__ AlignArgs a) {
+  wait_for_previous();
+  let_next_start();
   int64_t w = int64_t(blockIdx.x) * kAlignWarps + (threadIdx.x >> 5);
   const int i = w >= a.warps[0];
   if (i) w -= a.warps[0];
@@ -278,6 +280,8 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
+  wait_for_previous();
+  let_next_start();
 
   Ring r;
   if (warp == kCopyWarp) {
@@ -527,7 +531,7 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs &a, int t) {
 }
 
 template <bool kEight>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads)
+__global__ void __launch_bounds__(kDenseThreads)
 dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ LinArgs a) {
   extern __shared__ uint8_t raw_smem[];
@@ -563,6 +567,8 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
+  wait_for_previous();
+  let_next_start();
 
   Ring r;
   if (warp == kDenseCopyWarp) {
@@ -813,6 +819,11 @@ Shape split_shape(int64_t m, int64_t n, int k_blocks, int sms) {
   return s;
 }
 
+st_status launch_error(const LinArgs &a, cudaError_t e) {
+  return set_error(ST_E_CUDA, "st_linear launch (%lld x %lld, %lld bytes of k): %s: %s", (long long)a.m, (long long)a.n,
+                   (long long)a.kbytes, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
 template <int BM, bool kEight>
 st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int64_t tiles, int dev, cudaStream_t st) {
   constexpr int kStageBytes = (kTileN + BM) * kStageK;
@@ -825,26 +836,9 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   static_assert(BM * kTileN * 4 <= 3 * kStageBytes, "partial sums fit over the stages");
   constexpr auto kernel = split_kernel<BM, kEight>;
   cudaError_t e = allow_smem<kernel>(dev, smem);
-  if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits));
-    cfg.blockDim = dim3(kSplitThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, a);
-  }
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return set_error(ST_E_CUDA, "st_linear launch (%lld x %lld, %lld bytes of k): %s: %s", (long long)a.m, (long long)a.n,
-                     (long long)a.kbytes, cudaGetErrorName(e), cudaGetErrorString(e));
-  }
-  return ST_OK;
+  if (e == cudaSuccess)
+    e = launch(kernel, static_cast<unsigned>(tiles * a.splits), kSplitThreads, smem, a.splits, st, wmap, xmap, a);
+  return e == cudaSuccess ? ST_OK : launch_error(a, e);
 }
 
 template <bool kEight>
@@ -856,13 +850,10 @@ st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &w
   cudaError_t e = allow_smem<dense_kernel<kEight>>(dev, kDenseSmem + 1024);
   if (e == cudaSuccess) {
     const int pairs = sms / 2, tiles = a.m_tiles * a.n_tiles;
-    dense_kernel<kEight><<<2 * (tiles < pairs ? tiles : pairs), kDenseThreads, a.stages * stage_bytes + 1024, st>>>(xmap, wmap, a);
-    e = cudaGetLastError();
+    e = launch(dense_kernel<kEight>, 2 * (tiles < pairs ? tiles : pairs), kDenseThreads, a.stages * stage_bytes + 1024, 2, st,
+               xmap, wmap, a);
   }
-  if (e != cudaSuccess)
-    return set_error(ST_E_CUDA, "st_linear launch (%lld x %lld, %lld bytes of k): %s: %s", (long long)a.m, (long long)a.n,
-                     (long long)a.kbytes, cudaGetErrorName(e), cudaGetErrorString(e));
-  return ST_OK;
+  return e == cudaSuccess ? ST_OK : launch_error(a, e);
 }
 
 }  // namespace
@@ -896,8 +887,7 @@ st_status align(LinArgs &a, uint8_t *workspace, cudaStream_t st) {
   const int64_t blocks = (al.warps[0] + al.warps[1] + kAlignWarps - 1) / kAlignWarps;
   if (blocks == 0) return ST_OK;
   if (blocks > 0x7fffffff) return set_error(ST_E_INVAL, "st_linear: too many rows to align in one launch");
-  align_kernel<<<static_cast<unsigned>(blocks), kAlignWarps * 32, 0, st>>>(al);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch(align_kernel, static_cast<unsigned>(blocks), kAlignWarps * 32, 0, 1, st, al);
   if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_linear: aligning rows: %s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
   return ST_OK;
 }

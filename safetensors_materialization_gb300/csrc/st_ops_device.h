@@ -126,4 +126,32 @@ __device__ __forceinline__ void activate(float (&v)[N], st_act act) {
   }
 }
 
+// A kernel launched by launch() may start while the one before it in the
+// stream still runs (programmatic dependent launch), so that its start-up
+// overlaps that one's end.  It touches no global memory before
+// wait_for_previous(), which returns when the previous kernel has ended and
+// its writes are visible; let_next_start() lets the next one begin.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 }  // namespace stmat

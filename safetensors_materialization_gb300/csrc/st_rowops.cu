@@ -136,6 +136,8 @@ template <class T, int V, int NV, bool kNorm, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(V, NV)) row_kernel(const RowArgs a) {
   const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5) : int64_t(blockIdx.x);
   const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x;
+  wait_for_previous();
+  let_next_start();
   if (kWarpRow && row >= a.rows) return;
   Raw<T, V> x[NV], r[NV];
 #pragma unroll
@@ -176,6 +178,8 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
 template <class T, int V, bool kNorm>
 __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) {
   const int64_t row = blockIdx.x;
+  wait_for_previous();
+  let_next_start();
   Stat s{0.0f, 0.0f}, unused{0.0f, 0.0f};
   Raw<T, V> x, r;
   float v[V];
@@ -197,37 +201,36 @@ __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) 
 }
 
 template <class T, int V, int NV, bool kNorm>
-void launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
+cudaError_t launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
   if (threads == 32)
-    row_kernel<T, V, NV, kNorm, true><<<static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
-                                        32 * kRowsPerBlock, 0, st>>>(a);
-  else
-    row_kernel<T, V, NV, kNorm, false><<<static_cast<unsigned>(a.rows), threads, 0, st>>>(a);
+    return launch(row_kernel<T, V, NV, kNorm, true>, static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
+                  32 * kRowsPerBlock, 0, 1, st, a);
+  return launch(row_kernel<T, V, NV, kNorm, false>, static_cast<unsigned>(a.rows), threads, 0, 1, st, a);
 }
 
 // Accesses per thread: as few as blocks of 256 threads allow, so that several
 // rows share an SM and one's loads overlap another's reduction; with too few
 // rows for that, blocks of 1024, the shortest way through one row.
 template <class T, int V, bool kNorm>
-void launch_typed(const RowArgs &a, cudaStream_t st) {
+cudaError_t launch_typed(const RowArgs &a, cudaStream_t st) {
   const int64_t accesses = a.cols / V;
   const int64_t target = a.rows <= 256 ? kMaxThreads : 256;
   constexpr int kMost = V == 8 ? 4 : 8;
   auto threads = [&](int nv) { return static_cast<int>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
-  if (accesses <= target) launch_rows<T, V, 1, kNorm>(a, threads(1), st);
-  else if (accesses <= 2 * target) launch_rows<T, V, 2, kNorm>(a, threads(2), st);
-  else if (accesses <= 4 * block_threads(V, 4)) launch_rows<T, V, 4, kNorm>(a, threads(4), st);
-  else if (accesses <= kMost * block_threads(V, kMost)) launch_rows<T, V, kMost, kNorm>(a, threads(kMost), st);
-  else row_loop_kernel<T, V, kNorm><<<static_cast<unsigned>(a.rows), kMaxThreads, 0, st>>>(a);
+  if (accesses <= target) return launch_rows<T, V, 1, kNorm>(a, threads(1), st);
+  if (accesses <= 2 * target) return launch_rows<T, V, 2, kNorm>(a, threads(2), st);
+  if (accesses <= 4 * block_threads(V, 4)) return launch_rows<T, V, 4, kNorm>(a, threads(4), st);
+  if (accesses <= kMost * block_threads(V, kMost)) return launch_rows<T, V, kMost, kNorm>(a, threads(kMost), st);
+  return launch(row_loop_kernel<T, V, kNorm>, static_cast<unsigned>(a.rows), kMaxThreads, 0, 1, st, a);
 }
 
 template <bool kNorm>
-st_status launch(const RowArgs &a, st_dtype x_dtype, bool vec, void *stream, const char *op) {
+st_status launch_op(const RowArgs &a, st_dtype x_dtype, bool vec, void *stream, const char *op) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (x_dtype == ST_BF16) vec ? launch_typed<__nv_bfloat16, 8, kNorm>(a, st) : launch_typed<__nv_bfloat16, 1, kNorm>(a, st);
-  else if (x_dtype == ST_F16) vec ? launch_typed<__half, 8, kNorm>(a, st) : launch_typed<__half, 1, kNorm>(a, st);
-  else vec ? launch_typed<float, 4, kNorm>(a, st) : launch_typed<float, 1, kNorm>(a, st);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (x_dtype == ST_BF16) e = vec ? launch_typed<__nv_bfloat16, 8, kNorm>(a, st) : launch_typed<__nv_bfloat16, 1, kNorm>(a, st);
+  else if (x_dtype == ST_F16) e = vec ? launch_typed<__half, 8, kNorm>(a, st) : launch_typed<__half, 1, kNorm>(a, st);
+  else e = vec ? launch_typed<float, 4, kNorm>(a, st) : launch_typed<float, 1, kNorm>(a, st);
   if (e != cudaSuccess)
     return set_error(ST_E_CUDA, "%s launch (%lld rows): %s: %s", op, (long long)a.rows, cudaGetErrorName(e),
                      cudaGetErrorString(e));
@@ -253,7 +256,7 @@ st_status launch_rms_norm(const st_rms_norm_args &p, void *stream) {
   a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.w_dtype; a.y_dtype = p.y_dtype;
   const bool vec = p.cols % 8 == 0 && vec_ok(p.x, p.ldx, p.x_dtype) && vec_ok(p.residual, p.ldr, p.x_dtype) &&
                    vec_ok(p.weight, 0, p.w_dtype) && vec_ok(p.h, p.ldh, p.x_dtype) && vec_ok(p.y, p.ldy, p.y_dtype);
-  return launch<true>(a, p.x_dtype, vec, stream, "st_rms_norm");
+  return launch_op<true>(a, p.x_dtype, vec, stream, "st_rms_norm");
 }
 
 st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
@@ -265,7 +268,7 @@ st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
   a.act = p.act; a.w_dtype = ST_F32; a.y_dtype = p.y_dtype;
   const bool vec = p.cols % 8 == 0 && vec_ok(p.gate, p.ldg, p.x_dtype) && vec_ok(p.up, p.ldu, p.x_dtype) &&
                    vec_ok(p.y, p.ldy, p.y_dtype);
-  return launch<false>(a, p.x_dtype, vec, stream, "st_gated_act");
+  return launch_op<false>(a, p.x_dtype, vec, stream, "st_gated_act");
 }
 
 }  // namespace stmat
