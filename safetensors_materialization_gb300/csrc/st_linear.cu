@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kTileN = 128;          // weight rows per tile: the MMA's M
 constexpr int kStageK = 128;         // bytes of k per stage: one swizzle row
-constexpr int kMaxStages = 12;         // ring slots
+constexpr int kMaxStages = 12;       // ring slots
 constexpr int kMaxSplit = 8;         // portable cluster size
 constexpr int kEpilogueWarps = 4;    // one per 32 TMEM lanes
 constexpr int kMmaWarp = 4, kCopyWarp = 5, kSplitThreads = 192;

@@ -8,8 +8,9 @@ using namespace stmat;
 
 namespace {
 
-constexpr int64_t kMaxRows = 0x7fffffff;  // one grid dimension
-constexpr int64_t kMaxCols = 0x7fffffff;
+// One grid dimension of rows, and tile coordinates that stay in 32 bits.
+constexpr int64_t kMaxRows = 0x7fffff00;
+constexpr int64_t kMaxCols = 0x7fffff00;
 
 bool is_float16or32(st_dtype d) { return d == ST_BF16 || d == ST_F16 || d == ST_F32; }
 
@@ -41,7 +42,7 @@ st_status check_vector(const char *op, const char *name, const void *p, st_dtype
 
 st_status check_sizes(const char *op, int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || rows > kMaxRows || cols > kMaxCols)
-    return set_error(ST_E_INVAL, "%s: %lld x %lld is out of range (0 .. 2^31 - 1)", op, (long long)rows,
+    return set_error(ST_E_INVAL, "%s: %lld x %lld is out of range (0 .. 2^31 - 256)", op, (long long)rows,
                      (long long)cols);
   return ST_OK;
 }

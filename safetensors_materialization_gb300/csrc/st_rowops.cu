@@ -20,6 +20,11 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kRowsPerBlock = 8;  // rows of one warp each
+// A block brings the inputs of the row this far ahead into L2, so that HBM is
+// kept busy while the rows on the SMs are reduced and written (8192 x 4096
+// norm 37.9 -> 36.2 us, 8192 x 14336 gated activation 101 -> 95.5 us; the same
+// within 1 % from 38 to 228 rows, slower from 456 rows of 48 KiB on).
+constexpr int kAhead = 128;
 
 // The largest block of a row kernel: its registers hold NV vectors a thread.
 constexpr int block_threads(int v, int nv) { return v > 1 && nv >= 4 ? 512 : kMaxThreads; }
@@ -130,6 +135,11 @@ __device__ __forceinline__ Raw<T, V> row_read(const void *p, int64_t at) {
   return *reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(p) + at);
 }
 
+template <class T>
+__device__ __forceinline__ void row_prefetch(const void *p, int64_t at, int cols) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const T *>(p) + at), "r"(cols * static_cast<int>(sizeof(T))) : "memory");
+}
+
 // One row in registers: a block (or, kWarpRow, a warp) per row, NV accesses
 // of V elements per thread, all of them under way before the first is used.
 template <class T, int V, int NV, bool kNorm, bool kWarpRow>
@@ -139,6 +149,10 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
   wait_for_previous();
   let_next_start();
   if (kWarpRow && row >= a.rows) return;
+  if (!kWarpRow && V > 1 && t == 0 && row + kAhead < a.rows) {
+    row_prefetch<T>(a.x, (row + kAhead) * a.ldx, a.cols);
+    if (a.r) row_prefetch<T>(a.r, (row + kAhead) * a.ldr, a.cols);
+  }
   Raw<T, V> x[NV], r[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
