@@ -607,3 +607,21 @@ def test_operators_on_another_stream_and_in_a_graph(stmat):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0].float(), want[0].float()) and torch.equal(got[1], want[1])
+
+
+# --------------------------------------------------------------- the example
+
+@gpu
+def test_scaled_fp8_mlp_example():
+    """A checkpoint's MLP through the loader and the operators.  The 8-bit
+    rounding moves a value by at most 2^-4 of itself, in the norm's rows (so in
+    gate and up) and in the activation's: (1 + 2^-4)^3 - 1 of the result, and
+    the BF16 roundings of z, the residual and the output next to it."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "scaled_fp8_mlp.py")
+    spec = importlib.util.spec_from_file_location("scaled_fp8_mlp", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    found = example.main(hidden=1024, inter=2752, tokens=(1, 37, 700))
+    assert set(found) == {1, 37, 700} and all(0 < v < (1 + 2.0 ** -4) ** 3 - 1 for v in found.values()), found
