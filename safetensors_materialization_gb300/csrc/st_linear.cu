@@ -6,9 +6,11 @@
 // split_kernel: the weight's rows are the MMA's rows (128 a tile), the tokens
 // its columns, so that one token costs no more than the 16 columns of the
 // narrowest MMA, and the weight streams through shared memory at the rate of
-// HBM.  The sum's range is split over the CTAs of a cluster, which join their
-// binary32 partial sums through distributed shared memory in rank order (no
-// workspace, no atomics, the same bits on every run).
+// HBM.  The sum's range is split over the CTAs of a cluster; each puts its
+// binary32 partial sums into the shared memory of the CTA that joins them, in
+// rank order (no workspace, no atomics, the same bits on every run).  Pushing
+// them takes one cluster barrier where reading them from their makers took
+// two (1 x 1024 x 4096 E4M3: 4.7 -> 3.3 us).
 //
 // dense_kernel: many tokens.  A pair of CTAs (two SMs) computes 256 tokens x up
 // to 256 weight rows with one MMA: each holds 128 tokens and half of the
@@ -143,19 +145,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
                : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // The address of this CTA's shared variable in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
   return at;
 }
-__device__ __forceinline__ float4 peer_load(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void peer_store(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
 // A position in a ring of `stages` stages: its index, and the parity of its
@@ -250,6 +249,10 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
              const __grid_constant__ LinArgs a) {
   constexpr int kStageBytes = (kTileN + BM) * kStageK;
   constexpr int kCols = BM < 32 ? 32 : BM;  // TMEM columns
+  // The partial sums of 128 tokens (68 KB) lie over the stages, so that two
+  // CTAs still share an SM; fewer tokens' have room of their own, and need not
+  // wait for the whole cluster's MMAs.
+  constexpr bool kOver = BM == 128;
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
@@ -280,6 +283,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
+  if (!kOver) cluster_arrive();
   wait_for_previous();
   let_next_start();
 
@@ -317,9 +321,13 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
   }
   __syncwarp();
 
-  float *part = reinterpret_cast<float *>(smem);  // [BM][kTileN], over the stages
+  // The tile's tokens are shared out: CTA r joins and writes `share` of them
+  // from r * share on.  Every CTA puts its partial sums of a token into the
+  // joining CTA's shared memory, [splits][share][kTileN].
+  const int cols = static_cast<int>(a.m - m0 < BM ? a.m - m0 : BM), share = (cols + a.splits - 1) / a.splits;
+  float *joined = reinterpret_cast<float *>(smem + (kOver ? 0 : a.stages * kStageBytes));
   // In the epilogue a lane has four consecutive weight rows, a warp every
-  // fourth token of the CTA's share.
+  // fourth token.
   const int64_t n = n0 + 4 * lane;
   const int live = n < a.n ? static_cast<int>(min(int64_t(4), a.n - n)) : 0;
   const bool quad = live == 4 && a.vec;
@@ -332,99 +340,89 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
       ws[j] = a.w_scale && j < live ? a.w_scale[(n + j) * a.w_scale_step] : 1.0f;
       bias[j] = b[0];
     }
+    if (blocks > 0 && !bar_wait(&done, 0)) failed = 1;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   }
+  if (kOver) cluster_arrive();
+  cluster_wait();  // every CTA runs (kOver: and is done with its stages)
   if (warp < kEpilogueWarps) {
-    if (blocks > 0) {
-      if (!bar_wait(&done, 0)) failed = 1;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    uint32_t owner = 0, to = peer_addr(joined + rank * share * kTileN + threadIdx.x, 0);
+    int left = share;  // tokens of the owner's share to come
 #pragma unroll 1
-      for (int c = 0; c < BM; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+    for (int c = 0; c < cols; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * kTileN + threadIdx.x] = __uint_as_float(v[j]);
+      for (int j = 0; j < 16; ++j) {
+        if (c + j >= cols) break;
+        if (left == 0) {
+          to = peer_addr(joined + rank * share * kTileN + threadIdx.x, ++owner);
+          left = share;
+        }
+        peer_store(to, blocks > 0 ? __uint_as_float(v[j]) : 0.0f);
+        to += kTileN * 4;
+        --left;
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    } else {
-      for (int c = 0; c < BM; ++c) part[c * kTileN + threadIdx.x] = 0.0f;
     }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
-  __syncthreads();
-  if (warp == kMmaWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
-  if (a.splits > 1) cluster_sync();
-  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
+  cluster_arrive();
 
-  if (warp < kEpilogueWarps) {
-    // Each CTA joins and writes its share of the tokens, four a warp at a
-    // time so that their loads overlap (the residual may be y: a thread reads
-    // its values before it writes them).
-    const int cols = static_cast<int>(a.m - m0 < BM ? a.m - m0 : BM), share = (cols + a.splits - 1) / a.splits;
-    const int begin = static_cast<int>(rank) * share, end = min(cols, begin + share);
-    constexpr int kBatch = 4;
+  // The residual may be y: a thread reads its values of a token, and one
+  // token ahead, before it writes them.
+  const int begin = static_cast<int>(rank) * share, mine = min(share, cols - begin);
+  auto extras = [&](int c, float (&old)[4], float &xs) {
+    const int64_t m = m0 + begin + c;
+    xs = a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) old[j] = 0.0f;
+    if (!a.residual) return;
+    if (quad) load_any<4>(a.residual, a.y_dtype, m * a.ldr + n, old);
+    else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float o[1] = {0.0f};
+        if (j < live) load_any<1>(a.residual, a.y_dtype, m * a.ldr + n + j, o);
+        old[j] = o[0];
+      }
+    }
+  };
+  const bool writes = warp < kEpilogueWarps && warp < mine;
+  float old[4], xs = 1.0f;
+  if (writes) extras(warp, old, xs);
+  cluster_wait();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  }
+  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
+  if (!writes) return;
 #pragma unroll 1
-    for (int c = begin + warp; c < end; c += kEpilogueWarps * kBatch) {
-      float v[kBatch][4], old[kBatch][4], xs[kBatch];
+  for (int c = warp; c < mine; c += kEpilogueWarps) {
+    float next[4], next_xs = 1.0f;
+    if (c + kEpilogueWarps < mine) extras(c + kEpilogueWarps, next, next_xs);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int r = 0; r < a.splits; ++r) {
+      const float4 f = *reinterpret_cast<const float4 *>(joined + (r * share + c) * kTileN + 4 * lane);
+      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+    }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int64_t m = m0 + c + i * kEpilogueWarps;
-        const bool in = c + i * kEpilogueWarps < end;
-        xs[i] = in && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
+    for (int j = 0; j < 4; ++j) v[j] = v[j] * xs * ws[j] + bias[j];
+    activate(v, a.act);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = old[i][j] = 0.0f;
-        if (in && a.residual) {
-          if (quad) load_any<4>(a.residual, a.y_dtype, m * a.ldr + n, old[i]);
-          else {
+    for (int j = 0; j < 4; ++j) v[j] += old[j], old[j] = next[j];
+    xs = next_xs;
+    const int64_t at = (m0 + begin + c) * a.ldy + n;
+    if (quad) store_any<4>(a.y, a.y_dtype, at, v);
+    else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float o[1] = {0.0f};
-              if (j < live) load_any<1>(a.residual, a.y_dtype, m * a.ldr + n + j, o);
-              old[i][j] = o[0];
-            }
-          }
-        }
-      }
-      // Four CTAs' partial sums are under way at a time.
-      for (int r0 = 0; r0 < a.splits; r0 += 4) {
-        float4 f[4][kBatch];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (r0 + r >= a.splits) break;
-          const uint32_t at = peer_addr(part + c * kTileN + 4 * lane, r0 + r);
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (c + i * kEpilogueWarps < end) f[r][i] = peer_load(at + i * kEpilogueWarps * kTileN * 4);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (r0 + r >= a.splits) break;
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (c + i * kEpilogueWarps < end)
-              v[i][0] += f[r][i].x, v[i][1] += f[r][i].y, v[i][2] += f[r][i].z, v[i][3] += f[r][i].w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (c + i * kEpilogueWarps >= end) continue;
-        const int64_t m = m0 + c + i * kEpilogueWarps;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = v[i][j] * xs[i] * ws[j] + bias[j];
-        activate(v[i], a.act);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] += old[i][j];
-        if (quad) store_any<4>(a.y, a.y_dtype, m * a.ldy + n, v[i]);
-        else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float out[1] = {v[i][j]};
-            if (j < live) store_any<1>(a.y, a.y_dtype, m * a.ldy + n + j, out);
-          }
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float out[1] = {v[j]};
+        if (j < live) store_any<1>(a.y, a.y_dtype, at + j, out);
       }
     }
   }
-  if (a.splits > 1) cluster_sync();  // the partial sums stay until every CTA has read them
 }
 
 // ---------------------------------------------------------- dense_kernel
@@ -564,7 +562,8 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
   wait_for_previous();
@@ -690,7 +689,8 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == kDenseMmaWarp) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
@@ -803,9 +803,10 @@ Shape dense_shape(int64_t m, int64_t n, int k_blocks, int sms) {
 
 // split_kernel: the MMA's columns are the tokens, up to 128; the sum is split
 // until the CTAs fill the SMs twice, each with at least four stages.  Joining
-// and writing a tile costs 26 units per column.  (4096 x 4096 E4M3, us: 64
-// tokens 10.7 and dense 11.3; 128 tokens 15.0 and dense 11.4; 128 tokens x
-// 4096 x 14336 21.4 and dense 25.9.)
+// and writing a tile costs 26 units per column, and a part of a round of CTAs
+// costs about half of a whole one.  (Device time in us, this and dense_kernel:
+// 64 x 4096 x 4096 E4M3 8.8, 11.3; 128 x 4096 x 4096 14.3, 10.6; 128 x 4096 x
+// 14336 20.4, 25.9; 384 x 4096 x 14336 BF16 56, 46.)
 Shape split_shape(int64_t m, int64_t n, int k_blocks, int sms) {
   Shape s{};
   s.width = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
@@ -814,8 +815,8 @@ Shape split_shape(int64_t m, int64_t n, int k_blocks, int sms) {
   const int64_t tiles = s.m_tiles * s.n_tiles;
   s.splits = 1;
   while (s.splits < kMaxSplit && tiles * s.splits <= sms && k_blocks / (s.splits * 2) >= 4) s.splits *= 2;
-  const double waves = static_cast<double>(tiles) * s.splits / sms;
-  s.cost = (waves > 1 ? waves : 1) * ((k_blocks + s.splits - 1) / s.splits * (kTileN + s.width) + 26.0 * s.width);
+  const int64_t ctas = tiles * s.splits, rounds = (ctas + sms - 1) / sms;
+  s.cost = 0.5 * (static_cast<double>(rounds) + (ctas > sms ? static_cast<double>(ctas) / sms : 1.0)) * ((k_blocks + s.splits - 1) / s.splits * (kTileN + s.width) + 26.0 * s.width);
   return s;
 }
 
@@ -827,13 +828,12 @@ st_status launch_error(const LinArgs &a, cudaError_t e) {
 template <int BM, bool kEight>
 st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int64_t tiles, int dev, cudaStream_t st) {
   constexpr int kStageBytes = (kTileN + BM) * kStageK;
-  // About half of the SM's shared memory, so that two CTAs share one, but at
-  // least three stages and room for the partial sums.
-  a.stages = 108 * 1024 / kStageBytes;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  if (a.stages < 3) a.stages = 3;
-  const int smem = a.stages * kStageBytes + 1024;
-  static_assert(BM * kTileN * 4 <= 3 * kStageBytes, "partial sums fit over the stages");
+  // About half of the SM's shared memory, so that two CTAs share one.
+  constexpr int kJoined = (BM + kMaxSplit) * kTileN * 4, kBudget = 109 * 1024;
+  constexpr int kStages = BM == 128 ? 3 : (kBudget - kJoined) / kStageBytes;
+  static_assert(kStages >= 3 && kStages <= kMaxStages && (BM < 128 || kJoined <= kStages * kStageBytes), "a ring of stages");
+  a.stages = kStages;
+  constexpr int smem = kStages * kStageBytes + (BM == 128 ? 0 : kJoined) + 1024;
   constexpr auto kernel = split_kernel<BM, kEight>;
   cudaError_t e = allow_smem<kernel>(dev, smem);
   if (e == cudaSuccess)
