@@ -45,9 +45,12 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 
 constexpr int kPairM = 256;          // tokens per pair of CTAs
 constexpr int kPairMaxN = 256;       // weight rows per pair, a multiple of 32
-constexpr int kDenseEpilogueWarps = 8;  // two per 32 TMEM lanes: halves of the columns
-constexpr int kDenseMmaWarp = 8, kDenseCopyWarp = 9, kDenseThreads = 320;
-constexpr int kDenseSmem = 196 * 1024;  // the ring of stages; room for the rest of a CTA's 227 KB
+// Four warps per 32 TMEM lanes, each with every fourth chunk of the columns:
+// a product with a short sum is bound by its readout, whose chains of loads
+// and arithmetic eight warps leave two thirds of the issue slots of.
+constexpr int kDenseEpilogueWarps = 16;
+constexpr int kDenseMmaWarp = 16, kDenseCopyWarp = 17, kDenseThreads = 576;
+constexpr int kDenseSmem = 190 * 1024;  // the ring of stages; room for the rest of a CTA's 227 KB
 constexpr int kChunk = 32;           // columns an epilogue warp reads at a time
 
 // One operand of the product.
@@ -63,6 +66,7 @@ struct LinArgs {
   int64_t m, n, kbytes;
   int k_blocks, splits, stages, m_tiles;
   int n_tiles, tile_n;               // dense_kernel: weight rows per tile
+  int bias_wide;                     // dense_kernel: 16-bit bias at a multiple of 32 bytes
   int x_box;                         // token rows a TMA copy brings
   int vec;                           // y and residual rows take 32-byte (dense) or four-element (split) accesses
   uint32_t idesc;
@@ -471,29 +475,25 @@ __device__ __forceinline__ void st32(void *p, const uint32_t (&v)[8]) {
                ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
 }
 
-// Residual and y of one token and kChunk columns, in 32-byte accesses.
-__device__ __forceinline__ void add_row(const void *base, st_dtype dtype, int64_t at, float (&v)[kChunk]) {
-  uint32_t u[8];
-  if (dtype == ST_F32) {
+// Residual and y of one token and kChunk columns, in 32-byte accesses.  A
+// 16-bit residual is read (issued) well before it is added.
+__device__ __forceinline__ void add16(const uint32_t (&u)[8], bool bf16, float *v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ld32(static_cast<const float *>(base) + at + 8 * i, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 * i + j] += __uint_as_float(u[j]);
-    }
-    return;
+  for (int i = 0; i < 8; ++i) {
+    float2 f;
+    if (bf16) f = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    else f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+    v[2 * i] += f.x;
+    v[2 * i + 1] += f.y;
   }
+}
+__device__ __forceinline__ void add_row32(const void *base, int64_t at, float (&v)[kChunk]) {
+  uint32_t u[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    ld32(static_cast<const uint16_t *>(base) + at + 16 * i, u);
+  for (int i = 0; i < 4; ++i) {
+    ld32(static_cast<const float *>(base) + at + 8 * i, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float2 f;
-      if (dtype == ST_BF16) f = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
-      else f = __half22float2(*reinterpret_cast<const __half2 *>(&u[j]));
-      v[16 * i + 2 * j] += f.x;
-      v[16 * i + 2 * j + 1] += f.y;
-    }
+    for (int j = 0; j < 8; ++j) v[8 * i + j] += __uint_as_float(u[j]);
   }
 }
 __device__ __forceinline__ void put_row(void *base, st_dtype dtype, int64_t at, const float (&v)[kChunk]) {
@@ -616,69 +616,95 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
       if (!ok) failed = 1;
     }
   } else {
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3;
     const uint32_t taken_at = peer_addr(taken, 0);
     const int chunks = a.tile_n / kChunk;
+    const bool columns_scaled = a.w_scale && a.w_scale_step;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {
       const TileAt at = tile_at(a, t);
       const int buf = n & 1;
-      if (!bar_wait_warp(&sums[buf], (n / 2) & 1, lane)) { failed = 1; break; }
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int64_t m = at.m0 + rank * 128 + quarter * 32 + lane;
       const bool row = m < a.m;
       float xs = row && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
-      for (int c = half; c < chunks; c += 2) {
+      if (a.w_scale && !columns_scaled) xs *= *a.w_scale;
+      if (!bar_wait_warp(&sums[buf], (n / 2) & 1, lane)) { failed = 1; break; }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      for (int c = warp >> 2; c < chunks; c += kDenseEpilogueWarps / 4) {
         const int64_t n0 = at.n0 + c * kChunk;
         if (n0 >= a.n) break;
-        // One column's scale and bias per lane, handed round below.
+        const bool wide = a.vec && n0 + kChunk <= a.n;
+        uint32_t old[2][8];
+        if (wide && row && a.residual && a.y_dtype != ST_F32) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ld32(static_cast<const uint16_t *>(a.residual) + m * a.ldr + n0 + 16 * i, old[i]);
+        }
+        // A 16-bit bias is read by every lane, where its alignment allows; else
+        // one column's bias, like its scale, per lane and handed round below.
+        const bool wide_bias = a.bias_wide && n0 + kChunk <= a.n;
         float wl = 1.0f, bl[1] = {0.0f};
         if (n0 + lane < a.n) {
-          if (a.w_scale) wl = a.w_scale[(n0 + lane) * a.w_scale_step];
-          if (a.bias) load_any<1>(a.bias, a.bias_dtype, n0 + lane, bl);
+          if (columns_scaled) wl = a.w_scale[n0 + lane];
+          if (a.bias && !wide_bias) load_any<1>(a.bias, a.bias_dtype, n0 + lane, bl);
         }
         float v[kChunk];
         tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kPairMaxN + c * kChunk, v);
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) v[j] *= xs;
-        if (a.w_scale) {
+        if (columns_scaled) {
 #pragma unroll
           for (int j = 0; j < kChunk; ++j) v[j] *= __shfl_sync(~0u, wl, j);
         }
-        if (a.bias) {
+        if (wide_bias) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t u[8];
+            ld32(static_cast<const uint16_t *>(a.bias) + n0 + 16 * i, u);
+            add16(u, a.bias_dtype == ST_BF16, v + 16 * i);
+          }
+        } else if (a.bias) {
 #pragma unroll
           for (int j = 0; j < kChunk; ++j) v[j] += __shfl_sync(~0u, bl[0], j);
         }
         activate(v, a.act);
-        if (a.vec && n0 + kChunk <= a.n) {
+        if (wide) {
           if (row) {
-            if (a.residual) add_row(a.residual, a.y_dtype, m * a.ldr + n0, v);
+            if (a.residual && a.y_dtype != ST_F32) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) add16(old[i], a.y_dtype == ST_BF16, v + 16 * i);
+            } else if (a.residual) add_row32(a.residual, m * a.ldr + n0, v);
             put_row(a.y, a.y_dtype, m * a.ldy + n0, v);
           }
         } else {
           // Rows at any alignment, or a ragged last chunk: 16 columns at a
           // time are turned in shared memory, so that a half-warp writes one
-          // token's consecutive columns.
-          const int64_t mw = at.m0 + rank * 128 + quarter * 32;
+          // token's consecutive columns; the residual of all of a lane's 16
+          // tokens is under way before the first is written.
+          const int64_t mw = at.m0 + rank * 128 + quarter * 32 + (lane >> 4);
+          const int rows = static_cast<int>(max(int64_t(0), min(int64_t(32), a.m - (mw - (lane >> 4)))));
+          with_type(a.y_dtype, [&](auto zero) {
+            using T = decltype(zero);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            __syncwarp();
+            for (int h = 0; h < 2; ++h) {
+              __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) turn[warp][lane][j] = v[16 * h + j];
-            __syncwarp();
-            const int64_t col = n0 + 16 * h + (lane & 15);
-#pragma unroll 4
-            for (int r = lane >> 4; r < 32; r += 2) {
-              if (mw + r >= a.m || col >= a.n) continue;
-              float out[1] = {turn[warp][r][lane & 15]};
-              if (a.residual) {
-                float old[1];
-                load_any<1>(a.residual, a.y_dtype, (mw + r) * a.ldr + col, old);
-                out[0] += old[0];
+              for (int j = 0; j < 16; ++j) turn[warp][lane][j] = v[16 * h + j];
+              __syncwarp();
+              const int64_t col = n0 + 16 * h + (lane & 15);
+              if (col >= a.n) continue;
+              const T *old = static_cast<const T *>(a.residual) + mw * a.ldr + col;
+              T *out = static_cast<T *>(a.y) + mw * a.ldy + col;
+              float add[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                add[i] = 0.0f;
+                if (a.residual && 2 * i + (lane >> 4) < rows) add[i] = to_float(old[2 * i * a.ldr]);
               }
-              store_any<1>(a.y, a.y_dtype, (mw + r) * a.ldy + col, out);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (2 * i + (lane >> 4) < rows) round_to(turn[warp][2 * i + (lane >> 4)][lane & 15] + add[i], out[2 * i * a.ldy]);
             }
-          }
+          });
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -948,6 +974,7 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
     a.tile_n = d.width;
     a.idesc = idesc(fx, fw, kPairM, a.tile_n);
     a.vec = aligned(32);
+    a.bias_wide = p.bias && p.bias_dtype != ST_F32 && reinterpret_cast<uintptr_t>(p.bias) % 32 == 0;
     s = encode(&xmap, a.x, p.k, item, 128);
     if (s == ST_OK) s = encode(&wmap, a.w, p.k, item, a.tile_n / 2);
     if (s != ST_OK) return s;

@@ -98,11 +98,22 @@ __device__ __forceinline__ float scaled(float v, Factor f) {
 template <class T>
 constexpr st_dtype kDtype = sizeof(T) == 4 ? ST_F32 : std::is_same<T, __half>::value ? ST_F16 : ST_BF16;
 
+// Writes the elements of V values from column c on that the row has.
+template <int V>
+__device__ __forceinline__ void store_part(void *base, st_dtype dtype, int64_t at, int c, int cols, const float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float one[1] = {v[i]};
+    if (c + i >= 0 && c + i < cols) store_any<1>(base, dtype, at + i, one);
+  }
+}
+
 // The values before the row's factors (h w, or z) of V elements at column c,
-// from the elements as read, adding to the statistics and writing h.
-template <class T, int V, bool kNorm, bool kWrite>
-__device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c, const Raw<T, V> &x, const Raw<T, V> &r,
-                                           float (&v)[V], Stat &s) {
+// from the elements as read, adding to the statistics and writing h.  W: the
+// weight's type; whole: the row has all of the elements.
+template <class T, class W, int V, bool kSkew, bool kNorm, bool kWrite>
+__device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c, bool whole, const Raw<T, V> &x,
+                                           const Raw<T, V> &r, float (&v)[V], Stat &s) {
   unpack(x, v);
   float o[V];
   if (a.r) unpack(r, o);
@@ -110,12 +121,21 @@ __device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c,
     if (a.r) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] += o[i];
-      if (a.h && kWrite) store_any<V>(a.h, kDtype<T>, row * a.ldh + c, v);
+      if (a.h && kWrite) {
+        if (!kSkew || whole) store_any<V>(a.h, kDtype<T>, row * a.ldh + c, v);
+        else store_part<V>(a.h, kDtype<T>, row * a.ldh + c, c, a.cols, v);
+      }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) s.sum = fmaf(v[i], v[i], s.sum);
     if (a.w) {
-      load_any<V>(a.w, a.w_dtype, c, o);
+      const W *w = static_cast<const W *>(a.w) + c;
+      if constexpr (kSkew) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = whole || (c + i >= 0 && c + i < a.cols) ? to_float(w[i]) : 0.0f;
+      } else {
+        unpack(*reinterpret_cast<const Raw<W, V> *>(w), o);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= o[i];
     }
@@ -140,50 +160,81 @@ __device__ __forceinline__ void row_prefetch(const void *p, int64_t at, int cols
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const T *>(p) + at), "r"(cols * static_cast<int>(sizeof(T))) : "memory");
 }
 
+// V elements of which the row has those at columns 0 .. cols - 1; zeros else.
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> row_part(const void *p, int64_t at, int c, int cols) {
+  Raw<T, V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    r.e[i] = T(0.0f);
+    if (c + i >= 0 && c + i < cols) r.e[i] = static_cast<const T *>(p)[at + i];
+  }
+  return r;
+}
+
 // One row in registers: a block (or, kWarpRow, a warp) per row, NV accesses
 // of V elements per thread, all of them under way before the first is used.
-template <class T, int V, int NV, bool kNorm, bool kWarpRow>
+// kSkew: rows start anywhere, but at the same place modulo V in every matrix;
+// the accesses are aligned ones around the row, whose first and last may hold
+// fewer of its elements.
+template <class T, int V, int NV, bool kSkew, bool kNorm, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(V, NV)) row_kernel(const RowArgs a) {
   const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5) : int64_t(blockIdx.x);
   const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x;
   wait_for_previous();
   let_next_start();
   if (kWarpRow && row >= a.rows) return;
-  if (!kWarpRow && V > 1 && t == 0 && row + kAhead < a.rows) {
+  if (!kWarpRow && V > 1 && !kSkew && t == 0 && row + kAhead < a.rows) {
     row_prefetch<T>(a.x, (row + kAhead) * a.ldx, a.cols);
     if (a.r) row_prefetch<T>(a.r, (row + kAhead) * a.ldr, a.cols);
   }
+  const int skip = kSkew ? static_cast<int>((reinterpret_cast<uintptr_t>(a.x) / sizeof(T) + row * a.ldx) & (V - 1)) : 0;
+  auto column = [&](int i) { return (i * nt + t) * V - skip; };
+  auto whole = [&](int c) { return !kSkew || (c >= 0 && c + V <= a.cols); };
   Raw<T, V> x[NV], r[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + t) * V;
-    if (c < a.cols) x[i] = row_read<T, V>(a.x, row * a.ldx + c);
-  }
-  if (a.r) {
+  auto read = [&](Raw<T, V>(&to)[NV], const void *p, int64_t ld) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * nt + t) * V;
-      if (c < a.cols) r[i] = row_read<T, V>(a.r, row * a.ldr + c);
+      const int c = column(i);
+      if (c < a.cols && whole(c)) to[i] = row_read<T, V>(p, row * ld + c);
     }
-  }
+    if constexpr (kSkew) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = column(i);
+        if (c < a.cols && !whole(c)) to[i] = row_part<T, V>(p, row * ld + c, c, a.cols);
+      }
+    }
+  };
+  read(x, a.x, a.ldx);
+  if (a.r) read(r, a.r, a.ldr);
   float v[NV][V];
   Stat s{0.0f, 0.0f};
+  with_type(kNorm ? a.w_dtype : kDtype<T>, [&](auto zero) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + t) * V;
-    if (c < a.cols) row_values<T, V, kNorm, true>(a, row, c, x[i], r[i], v[i], s);
-  }
+    for (int i = 0; i < NV; ++i) {
+      const int c = column(i);
+      if (c < a.cols) row_values<T, decltype(zero), V, kSkew, kNorm, true>(a, row, c, whole(c), x[i], r[i], v[i], s);
+    }
+  });
   s = kWarpRow ? warp_stat(s) : block_stat(s);
   const Factor f = row_factor<kNorm>(a, s, row, t == 0);
+  auto write = [&](st_dtype dtype) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + t) * V;
-    if (c < a.cols) {
+    for (int i = 0; i < NV; ++i) {
+      const int c = column(i);
+      if (c < a.cols) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = scaled<kNorm>(v[i][j], f);
-      store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v[i]);
+        for (int j = 0; j < V; ++j) v[i][j] = scaled<kNorm>(v[i][j], f);
+        if (whole(c)) store_any<V>(a.y, dtype, row * a.ldy + c, v[i]);
+        else store_part<V>(a.y, dtype, row * a.ldy + c, c, a.cols, v[i]);
+      }
     }
-  }
+  };
+  if (a.y_dtype == ST_F8_E4M3) write(ST_F8_E4M3);
+  else if (a.y_dtype == ST_BF16) write(ST_BF16);
+  else if (a.y_dtype == ST_F16) write(ST_F16);
+  else write(ST_F32);
 }
 
 // A row too long for registers: the second pass reads the inputs again (each
@@ -195,68 +246,96 @@ __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) 
   wait_for_previous();
   let_next_start();
   Stat s{0.0f, 0.0f}, unused{0.0f, 0.0f};
-  Raw<T, V> x, r;
-  float v[V];
-  for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
-    x = row_read<T, V>(a.x, row * a.ldx + c);
-    if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
-    row_values<T, V, kNorm, false>(a, row, static_cast<int>(c), x, r, v, s);
-  }
-  s = block_stat(s);
-  const Factor f = row_factor<kNorm>(a, s, row, threadIdx.x == 0);
-  for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
-    x = row_read<T, V>(a.x, row * a.ldx + c);
-    if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
-    row_values<T, V, kNorm, true>(a, row, static_cast<int>(c), x, r, v, unused);
+  with_type(kNorm ? a.w_dtype : kDtype<T>, [&](auto zero) {
+    using W = decltype(zero);
+    Raw<T, V> x, r;
+    float v[V];
+    for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
+      x = row_read<T, V>(a.x, row * a.ldx + c);
+      if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
+      row_values<T, W, V, false, kNorm, false>(a, row, static_cast<int>(c), true, x, r, v, s);
+    }
+    s = block_stat(s);
+    const Factor f = row_factor<kNorm>(a, s, row, threadIdx.x == 0);
+    for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
+      x = row_read<T, V>(a.x, row * a.ldx + c);
+      if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
+      row_values<T, W, V, false, kNorm, true>(a, row, static_cast<int>(c), true, x, r, v, unused);
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = scaled<kNorm>(v[j], f);
-    store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v);
-  }
+      for (int j = 0; j < V; ++j) v[j] = scaled<kNorm>(v[j], f);
+      store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v);
+    }
+  });
 }
 
-template <class T, int V, int NV, bool kNorm>
+template <class T, int V, int NV, bool kSkew, bool kNorm>
 cudaError_t launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
-  if (threads == 32)
-    return launch(row_kernel<T, V, NV, kNorm, true>, static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
-                  32 * kRowsPerBlock, 0, 1, st, a);
-  return launch(row_kernel<T, V, NV, kNorm, false>, static_cast<unsigned>(a.rows), threads, 0, 1, st, a);
+  if constexpr (NV == 1)
+    if (threads == 32)
+      return launch(row_kernel<T, V, NV, kSkew, kNorm, true>, static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
+                    32 * kRowsPerBlock, 0, 1, st, a);
+  return launch(row_kernel<T, V, NV, kSkew, kNorm, false>, static_cast<unsigned>(a.rows), threads, 0, 1, st, a);
 }
 
 // Accesses per thread: as few as blocks of 256 threads allow, so that several
 // rows share an SM and one's loads overlap another's reduction; with too few
 // rows for that, blocks of 1024, the shortest way through one row.
-template <class T, int V, bool kNorm>
+template <class T, int V, bool kSkew, bool kNorm>
 cudaError_t launch_typed(const RowArgs &a, cudaStream_t st) {
-  const int64_t accesses = a.cols / V;
+  const int64_t accesses = kSkew ? (a.cols + 2 * V - 2) / V : a.cols / V;
   const int64_t target = a.rows <= 256 ? kMaxThreads : 256;
   constexpr int kMost = V == 8 ? 4 : 8;
   auto threads = [&](int nv) { return static_cast<int>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
-  if (accesses <= target) return launch_rows<T, V, 1, kNorm>(a, threads(1), st);
-  if (accesses <= 2 * target) return launch_rows<T, V, 2, kNorm>(a, threads(2), st);
-  if (accesses <= 4 * block_threads(V, 4)) return launch_rows<T, V, 4, kNorm>(a, threads(4), st);
-  if (accesses <= kMost * block_threads(V, kMost)) return launch_rows<T, V, kMost, kNorm>(a, threads(kMost), st);
-  return launch(row_loop_kernel<T, V, kNorm>, static_cast<unsigned>(a.rows), kMaxThreads, 0, 1, st, a);
+  if (accesses <= target) return launch_rows<T, V, 1, kSkew, kNorm>(a, threads(1), st);
+  if (accesses <= 2 * target) return launch_rows<T, V, 2, kSkew, kNorm>(a, threads(2), st);
+  if (accesses <= 4 * block_threads(V, 4)) return launch_rows<T, V, 4, kSkew, kNorm>(a, threads(4), st);
+  if (accesses <= kMost * block_threads(V, kMost)) return launch_rows<T, V, kMost, kSkew, kNorm>(a, threads(kMost), st);
+  return launch(row_loop_kernel<T, kSkew ? 1 : V, kNorm>, static_cast<unsigned>(a.rows), kMaxThreads, 0, 1, st, a);
+}
+
+// How a row's matrices lie: aligned accesses of V elements; aligned accesses
+// around rows that all start at the same place modulo V (what contiguous rows
+// of an odd length do: 5977 x 2407 BF16 norm to 8 bits NORM_B us, element by
+// element NORM_A); or element by element.
+enum Layout { kAligned, kSkewed, kScattered };
+class Rows {
+ public:
+  Rows(st_dtype x, int64_t cols) : v_(x == ST_F32 ? 4 : 8), same_(true), aligned_(cols % v_ == 0) {}
+  void matrix(const void *p, int64_t ld, st_dtype dtype) {
+    if (!p) return;
+    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / st_dtype_size(dtype) % v_), step = ld % v_;
+    if (at_ < 0) at_ = at, step_ = step;
+    same_ = same_ && at == at_ && step == step_;
+    aligned_ = aligned_ && at == 0 && step == 0;
+  }
+  void weight(const void *p, st_dtype dtype) {
+    aligned_ = aligned_ && reinterpret_cast<uintptr_t>(p) / st_dtype_size(dtype) % v_ == 0;
+  }
+  Layout layout() const { return aligned_ ? kAligned : same_ ? kSkewed : kScattered; }
+
+ private:
+  int64_t v_, at_ = -1, step_ = 0;
+  bool same_, aligned_;
+};
+
+template <class T, bool kNorm>
+cudaError_t launch_layout(const RowArgs &a, Layout layout, cudaStream_t st) {
+  constexpr int V = sizeof(T) == 4 ? 4 : 8;
+  if (layout == kAligned) return launch_typed<T, V, false, kNorm>(a, st);
+  if (layout == kSkewed) return launch_typed<T, V, true, kNorm>(a, st);
+  return launch_typed<T, 1, false, kNorm>(a, st);
 }
 
 template <bool kNorm>
-st_status launch_op(const RowArgs &a, st_dtype x_dtype, bool vec, void *stream, const char *op) {
+st_status launch_op(const RowArgs &a, st_dtype x_dtype, Layout layout, void *stream, const char *op) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (x_dtype == ST_BF16) e = vec ? launch_typed<__nv_bfloat16, 8, kNorm>(a, st) : launch_typed<__nv_bfloat16, 1, kNorm>(a, st);
-  else if (x_dtype == ST_F16) e = vec ? launch_typed<__half, 8, kNorm>(a, st) : launch_typed<__half, 1, kNorm>(a, st);
-  else e = vec ? launch_typed<float, 4, kNorm>(a, st) : launch_typed<float, 1, kNorm>(a, st);
+  const cudaError_t e = x_dtype == ST_BF16  ? launch_layout<__nv_bfloat16, kNorm>(a, layout, st)
+                        : x_dtype == ST_F16 ? launch_layout<__half, kNorm>(a, layout, st)
+                                            : launch_layout<float, kNorm>(a, layout, st);
   if (e != cudaSuccess)
     return set_error(ST_E_CUDA, "%s launch (%lld rows): %s: %s", op, (long long)a.rows, cudaGetErrorName(e),
                      cudaGetErrorString(e));
   return ST_OK;
-}
-
-// Whether the accesses of a row of 16-byte input vectors are aligned in this
-// matrix: 16 bytes, or eight (at least) of an 8-bit one.
-bool vec_ok(const void *p, int64_t ld, st_dtype dtype) {
-  if (!p) return true;
-  const uint64_t item = dtype == ST_F8_E4M3 ? 1 : dtype == ST_F32 ? 4 : 2, need = item == 1 ? 8 : 16;
-  return reinterpret_cast<uintptr_t>(p) % need == 0 && (static_cast<uint64_t>(ld) * item) % need == 0;
 }
 
 }  // namespace
@@ -267,10 +346,14 @@ st_status launch_rms_norm(const st_rms_norm_args &p, void *stream) {
   a.ldx = p.ldx; a.ldr = p.ldr; a.ldh = p.ldh; a.ldy = p.ldy;
   a.scale = p.scale; a.scales = p.scales;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
-  a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.w_dtype; a.y_dtype = p.y_dtype;
-  const bool vec = p.cols % 8 == 0 && vec_ok(p.x, p.ldx, p.x_dtype) && vec_ok(p.residual, p.ldr, p.x_dtype) &&
-                   vec_ok(p.weight, 0, p.w_dtype) && vec_ok(p.h, p.ldh, p.x_dtype) && vec_ok(p.y, p.ldy, p.y_dtype);
-  return launch_op<true>(a, p.x_dtype, vec, stream, "st_rms_norm");
+  a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.weight ? p.w_dtype : p.x_dtype; a.y_dtype = p.y_dtype;
+  Rows rows(p.x_dtype, p.cols);
+  rows.matrix(p.x, p.ldx, p.x_dtype);
+  rows.matrix(p.residual, p.ldr, p.x_dtype);
+  rows.matrix(p.h, p.ldh, p.x_dtype);
+  rows.matrix(p.y, p.ldy, p.y_dtype);
+  if (p.weight) rows.weight(p.weight, p.w_dtype);
+  return launch_op<true>(a, p.x_dtype, rows.layout(), stream, "st_rms_norm");
 }
 
 st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
@@ -279,10 +362,12 @@ st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
   a.ldx = p.ldg; a.ldr = p.ldu; a.ldy = p.ldy;
   a.scale = p.scale; a.scales = p.scales;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
-  a.act = p.act; a.w_dtype = ST_F32; a.y_dtype = p.y_dtype;
-  const bool vec = p.cols % 8 == 0 && vec_ok(p.gate, p.ldg, p.x_dtype) && vec_ok(p.up, p.ldu, p.x_dtype) &&
-                   vec_ok(p.y, p.ldy, p.y_dtype);
-  return launch_op<false>(a, p.x_dtype, vec, stream, "st_gated_act");
+  a.act = p.act; a.w_dtype = p.x_dtype; a.y_dtype = p.y_dtype;
+  Rows rows(p.x_dtype, p.cols);
+  rows.matrix(p.gate, p.ldg, p.x_dtype);
+  rows.matrix(p.up, p.ldu, p.x_dtype);
+  rows.matrix(p.y, p.ldy, p.y_dtype);
+  return launch_op<false>(a, p.x_dtype, rows.layout(), stream, "st_gated_act");
 }
 
 }  // namespace stmat

@@ -311,6 +311,41 @@ def test_norm_strides_and_offsets(stmat, extra, offset, dst):
 
 
 @gpu
+@pytest.mark.parametrize("m,c", [(3, 5), (9, 77), (4, 1111), (300, 2405), (2, 9001)])
+@pytest.mark.parametrize("extra,offset", [(0, 3), (2, 0), (5, 7), (8, 1)])
+@pytest.mark.parametrize("dtype", ["BF16", "F32"])
+@pytest.mark.parametrize("dst", ["BF16", "F32", "F8_E4M3"])
+def test_norm_rows_off_the_same_boundary(stmat, m, c, extra, offset, dtype, dst):
+    """Every matrix with the same stride and offset: accesses around the rows,
+    of whose elements outside the row none is changed (or read into a sum: the
+    buffers hold 77 there)."""
+    dt = TYPES[dtype]
+    x, r, w = normal(1, m, c, dtype=dt), normal(2, m, c, dtype=dt), normal(3, c + 1, dtype=dt)[1:]
+    a = stmat.RmsNormArgs(rows=m, cols=c, eps=1e-6, x_dtype=stmat.DTYPES.index(dtype), w_dtype=stmat.DTYPES.index(dtype),
+                          y_dtype=stmat.DTYPES.index(dst))
+    xv, rv, yv, hv = (padded(t, extra, offset) for t in (x, r, torch.zeros_like(x).to(TYPES[dst]), torch.zeros_like(x)))
+    scales = torch.zeros(m, device="cuda")
+    for field, v in (("x", xv), ("residual", rv), ("h", hv), ("y", yv), ("weight", w)):
+        setattr(a, field, v.data_ptr())
+    a.ldx = a.ldr = a.ldh = a.ldy = c + extra
+    if dst == "F8_E4M3":
+        a.scales = scales.data_ptr()
+    stmat._check(stmat.lib().st_rms_norm(a, torch.cuda.current_stream().cuda_stream))
+    h64, y64 = norm64(x, r, w, 1e-6)
+    check_values(hv, h64, slack=2.0 ** -23)
+    if dst == "F8_E4M3":
+        check_scales(scales, y64)
+        check_codes(yv, scales, y64)
+    else:
+        check_values(yv, y64)
+    for v in (yv, hv):
+        flat = v._base.reshape(-1).float()
+        inside = torch.zeros(flat.numel(), dtype=torch.bool, device="cuda")
+        inside[offset:offset + m * (c + extra)].view(m, c + extra)[:, :c] = True
+        assert (flat[~inside] == torch.tensor(77.0).to(v.dtype).float().item()).all()
+
+
+@gpu
 def test_norm_special_rows(stmat):
     """Zero rows, rows of the smallest numbers, and NaN and infinities, which
     stay in their own rows."""
