@@ -27,7 +27,7 @@ constexpr int kRowsPerBlock = 8;  // rows of one warp each
 constexpr int kAhead = 128;
 
 // The largest block of a row kernel: its registers hold NV vectors a thread.
-constexpr int block_threads(int v, int nv) { return v > 1 && nv >= 4 ? 512 : kMaxThreads; }
+constexpr int block_threads(int nv) { return nv >= 4 ? 512 : kMaxThreads; }
 
 struct RowArgs {
   const void *x, *r, *w;  // norm: x, residual, weight; gate: gate, up
@@ -37,6 +37,7 @@ struct RowArgs {
   int64_t ldx, ldr, ldh, ldy;
   int64_t rows;
   int cols;
+  bool r_same, h_same, y_same;  // skewed rows: the matrix starts where x does, modulo V
   float eps;
   st_act act;
   st_dtype w_dtype, y_dtype;
@@ -122,7 +123,7 @@ __device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c,
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] += o[i];
       if (a.h && kWrite) {
-        if (!kSkew || whole) store_any<V>(a.h, kDtype<T>, row * a.ldh + c, v);
+        if (!kSkew || (whole && a.h_same)) store_any<V>(a.h, kDtype<T>, row * a.ldh + c, v);
         else store_part<V>(a.h, kDtype<T>, row * a.ldh + c, c, a.cols, v);
       }
     }
@@ -174,17 +175,17 @@ __device__ __forceinline__ Raw<T, V> row_part(const void *p, int64_t at, int c, 
 
 // One row in registers: a block (or, kWarpRow, a warp) per row, NV accesses
 // of V elements per thread, all of them under way before the first is used.
-// kSkew: rows start anywhere, but at the same place modulo V in every matrix;
-// the accesses are aligned ones around the row, whose first and last may hold
-// fewer of its elements.
+// kSkew: rows start anywhere; the accesses are aligned ones around the row of
+// x, whose first and last may hold fewer of its elements, and of the other
+// matrices where they start at the same place modulo V, else single elements.
 template <class T, int V, int NV, bool kSkew, bool kNorm, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(V, NV)) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(NV)) row_kernel(const RowArgs a) {
   const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5) : int64_t(blockIdx.x);
   const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x;
   wait_for_previous();
   let_next_start();
   if (kWarpRow && row >= a.rows) return;
-  if (!kWarpRow && V > 1 && !kSkew && t == 0 && row + kAhead < a.rows) {
+  if (!kWarpRow && !kSkew && t == 0 && row + kAhead < a.rows) {
     row_prefetch<T>(a.x, (row + kAhead) * a.ldx, a.cols);
     if (a.r) row_prefetch<T>(a.r, (row + kAhead) * a.ldr, a.cols);
   }
@@ -192,22 +193,22 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
   auto column = [&](int i) { return (i * nt + t) * V - skip; };
   auto whole = [&](int c) { return !kSkew || (c >= 0 && c + V <= a.cols); };
   Raw<T, V> x[NV], r[NV];
-  auto read = [&](Raw<T, V>(&to)[NV], const void *p, int64_t ld) {
+  auto read = [&](Raw<T, V>(&to)[NV], const void *p, int64_t ld, bool same) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = column(i);
-      if (c < a.cols && whole(c)) to[i] = row_read<T, V>(p, row * ld + c);
+      if (c < a.cols && whole(c) && (!kSkew || same)) to[i] = row_read<T, V>(p, row * ld + c);
     }
     if constexpr (kSkew) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = column(i);
-        if (c < a.cols && !whole(c)) to[i] = row_part<T, V>(p, row * ld + c, c, a.cols);
+        if (c < a.cols && !(whole(c) && same)) to[i] = row_part<T, V>(p, row * ld + c, c, a.cols);
       }
     }
   };
-  read(x, a.x, a.ldx);
-  if (a.r) read(r, a.r, a.ldr);
+  read(x, a.x, a.ldx, true);
+  if (a.r) read(r, a.r, a.ldr, a.r_same);
   float v[NV][V];
   Stat s{0.0f, 0.0f};
   with_type(kNorm ? a.w_dtype : kDtype<T>, [&](auto zero) {
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
       if (c < a.cols) {
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i][j] = scaled<kNorm>(v[i][j], f);
-        if (whole(c)) store_any<V>(a.y, dtype, row * a.ldy + c, v[i]);
+        if (whole(c) && (!kSkew || a.y_same)) store_any<V>(a.y, dtype, row * a.ldy + c, v[i]);
         else store_part<V>(a.y, dtype, row * a.ldy + c, c, a.cols, v[i]);
       }
     }
@@ -268,70 +269,68 @@ __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) 
   });
 }
 
+// threads 0: a warp per row.
 template <class T, int V, int NV, bool kSkew, bool kNorm>
 cudaError_t launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
-  if constexpr (NV == 1)
-    if (threads == 32)
-      return launch(row_kernel<T, V, NV, kSkew, kNorm, true>, static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
-                    32 * kRowsPerBlock, 0, 1, st, a);
-  return launch(row_kernel<T, V, NV, kSkew, kNorm, false>, static_cast<unsigned>(a.rows), threads, 0, 1, st, a);
+  if (threads)
+    return launch(row_kernel<T, V, NV, kSkew, kNorm, false>, static_cast<unsigned>(a.rows), threads, 0, 1, st, a);
+  if constexpr (NV <= 4)
+    return launch(row_kernel<T, V, NV, kSkew, kNorm, true>, static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
+                  32 * kRowsPerBlock, 0, 1, st, a);
+  return cudaErrorInvalidValue;
 }
 
 // Accesses per thread: as few as blocks of 256 threads allow, so that several
 // rows share an SM and one's loads overlap another's reduction; with too few
-// rows for that, blocks of 1024, the shortest way through one row.
+// rows for that, blocks of 1024, the shortest way through one row.  A warp
+// takes a short row alone (16384 x 333 F16 norm with residual to 8 bits 16.5
+// us; in blocks of two warps 19.4).
 template <class T, int V, bool kSkew, bool kNorm>
 cudaError_t launch_typed(const RowArgs &a, cudaStream_t st) {
   const int64_t accesses = kSkew ? (a.cols + 2 * V - 2) / V : a.cols / V;
   const int64_t target = a.rows <= 256 ? kMaxThreads : 256;
   constexpr int kMost = V == 8 ? 4 : 8;
   auto threads = [&](int nv) { return static_cast<int>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
+  if (accesses <= 32) return launch_rows<T, V, 1, kSkew, kNorm>(a, 0, st);
+  if (accesses <= 64 && a.rows > 256) return launch_rows<T, V, 2, kSkew, kNorm>(a, 0, st);
+  if (accesses <= 128 && a.rows > 256) return launch_rows<T, V, 4, kSkew, kNorm>(a, 0, st);
   if (accesses <= target) return launch_rows<T, V, 1, kSkew, kNorm>(a, threads(1), st);
   if (accesses <= 2 * target) return launch_rows<T, V, 2, kSkew, kNorm>(a, threads(2), st);
-  if (accesses <= 4 * block_threads(V, 4)) return launch_rows<T, V, 4, kSkew, kNorm>(a, threads(4), st);
-  if (accesses <= kMost * block_threads(V, kMost)) return launch_rows<T, V, kMost, kSkew, kNorm>(a, threads(kMost), st);
+  if (accesses <= 4 * block_threads(4)) return launch_rows<T, V, 4, kSkew, kNorm>(a, threads(4), st);
+  if (accesses <= kMost * block_threads(kMost)) return launch_rows<T, V, kMost, kSkew, kNorm>(a, threads(kMost), st);
   return launch(row_loop_kernel<T, kSkew ? 1 : V, kNorm>, static_cast<unsigned>(a.rows), kMaxThreads, 0, 1, st, a);
 }
 
-// How a row's matrices lie: aligned accesses of V elements; aligned accesses
-// around rows that all start at the same place modulo V (what contiguous rows
-// of an odd length do: 5977 x 2407 BF16 norm to 8 bits NORM_B us, element by
-// element NORM_A); or element by element.
-enum Layout { kAligned, kSkewed, kScattered };
-class Rows {
- public:
-  Rows(st_dtype x, int64_t cols) : v_(x == ST_F32 ? 4 : 8), same_(true), aligned_(cols % v_ == 0) {}
-  void matrix(const void *p, int64_t ld, st_dtype dtype) {
-    if (!p) return;
-    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / st_dtype_size(dtype) % v_), step = ld % v_;
-    if (at_ < 0) at_ = at, step_ = step;
-    same_ = same_ && at == at_ && step == step_;
-    aligned_ = aligned_ && at == 0 && step == 0;
-  }
-  void weight(const void *p, st_dtype dtype) {
-    aligned_ = aligned_ && reinterpret_cast<uintptr_t>(p) / st_dtype_size(dtype) % v_ == 0;
-  }
-  Layout layout() const { return aligned_ ? kAligned : same_ ? kSkewed : kScattered; }
-
- private:
-  int64_t v_, at_ = -1, step_ = 0;
-  bool same_, aligned_;
+// Where rows start, in elements modulo an access of V.  Contiguous rows of an
+// odd length start at the same places in every matrix (5977 x 2407 BF16 norm
+// to 8 bits 15.9 us; element by element 30.9).
+struct Place {
+  int64_t at, step;
+  bool operator==(const Place &o) const { return at == o.at && step == o.step; }
+  bool aligned() const { return at == 0 && step == 0; }
 };
+Place place(const void *p, int64_t ld, st_dtype dtype, int v) {
+  return {static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / st_dtype_size(dtype) % v), ld % v};
+}
 
 template <class T, bool kNorm>
-cudaError_t launch_layout(const RowArgs &a, Layout layout, cudaStream_t st) {
+cudaError_t launch_layout(const RowArgs &a, bool aligned, cudaStream_t st) {
   constexpr int V = sizeof(T) == 4 ? 4 : 8;
-  if (layout == kAligned) return launch_typed<T, V, false, kNorm>(a, st);
-  if (layout == kSkewed) return launch_typed<T, V, true, kNorm>(a, st);
-  return launch_typed<T, 1, false, kNorm>(a, st);
+  return aligned ? launch_typed<T, V, false, kNorm>(a, st) : launch_typed<T, V, true, kNorm>(a, st);
 }
 
 template <bool kNorm>
-st_status launch_op(const RowArgs &a, st_dtype x_dtype, Layout layout, void *stream, const char *op) {
+st_status launch_op(RowArgs &a, st_dtype x_dtype, void *stream, const char *op) {
+  const int v = x_dtype == ST_F32 ? 4 : 8;
+  const Place x = place(a.x, a.ldx, x_dtype, v), y = place(a.y, a.ldy, a.y_dtype, v);
+  const Place r = a.r ? place(a.r, a.ldr, x_dtype, v) : x, h = a.h ? place(a.h, a.ldh, x_dtype, v) : x;
+  a.r_same = r == x, a.h_same = h == x, a.y_same = y == x;
+  const bool aligned = a.cols % v == 0 && x.aligned() && a.r_same && a.h_same && a.y_same &&
+                       place(a.w, 0, a.w_dtype, v).aligned();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = x_dtype == ST_BF16  ? launch_layout<__nv_bfloat16, kNorm>(a, layout, st)
-                        : x_dtype == ST_F16 ? launch_layout<__half, kNorm>(a, layout, st)
-                                            : launch_layout<float, kNorm>(a, layout, st);
+  const cudaError_t e = x_dtype == ST_BF16  ? launch_layout<__nv_bfloat16, kNorm>(a, aligned, st)
+                        : x_dtype == ST_F16 ? launch_layout<__half, kNorm>(a, aligned, st)
+                                            : launch_layout<float, kNorm>(a, aligned, st);
   if (e != cudaSuccess)
     return set_error(ST_E_CUDA, "%s launch (%lld rows): %s: %s", op, (long long)a.rows, cudaGetErrorName(e),
                      cudaGetErrorString(e));
@@ -347,13 +346,7 @@ st_status launch_rms_norm(const st_rms_norm_args &p, void *stream) {
   a.scale = p.scale; a.scales = p.scales;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
   a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.weight ? p.w_dtype : p.x_dtype; a.y_dtype = p.y_dtype;
-  Rows rows(p.x_dtype, p.cols);
-  rows.matrix(p.x, p.ldx, p.x_dtype);
-  rows.matrix(p.residual, p.ldr, p.x_dtype);
-  rows.matrix(p.h, p.ldh, p.x_dtype);
-  rows.matrix(p.y, p.ldy, p.y_dtype);
-  if (p.weight) rows.weight(p.weight, p.w_dtype);
-  return launch_op<true>(a, p.x_dtype, rows.layout(), stream, "st_rms_norm");
+  return launch_op<true>(a, p.x_dtype, stream, "st_rms_norm");
 }
 
 st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
@@ -363,11 +356,7 @@ st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
   a.scale = p.scale; a.scales = p.scales;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
   a.act = p.act; a.w_dtype = p.x_dtype; a.y_dtype = p.y_dtype;
-  Rows rows(p.x_dtype, p.cols);
-  rows.matrix(p.gate, p.ldg, p.x_dtype);
-  rows.matrix(p.up, p.ldu, p.x_dtype);
-  rows.matrix(p.y, p.ldy, p.y_dtype);
-  return launch_op<false>(a, p.x_dtype, rows.layout(), stream, "st_gated_act");
+  return launch_op<false>(a, p.x_dtype, stream, "st_gated_act");
 }
 
 }  // namespace stmat
