@@ -10,18 +10,23 @@
 // binary32 partial sums into the shared memory of the CTA that joins them, in
 // rank order (no workspace, no atomics, the same bits on every run).  Pushing
 // them takes one cluster barrier where reading them from their makers took
-// two (1 x 1024 x 4096 E4M3: 4.7 -> 3.3 us).
+// two (1 x 1024 x 4096 E4M3: 4.7 -> 3.3 us).  Bound by HBM: 1 x 28672 x 8192
+// E4M3 36.5 us (6.4 TB/s), 1 x 14336 x 4096 11.8 us (5.0 TB/s, 3 us of it the
+// chain from the last bytes to y).
 //
 // dense_kernel: many tokens.  A pair of CTAs (two SMs) computes 256 tokens x up
 // to 256 weight rows with one MMA: each holds 128 tokens and half of the
 // weight rows, so a stage's 32 KB per SM feed twice the products of a lone
 // CTA's.  The pairs stay resident and take tiles in turn; a tile's sums are
 // read out of one half of TMEM while the next tile's are formed in the other.
+// Bound by the power limit where sums are long: 4096 x 4096 x 14336 BF16 283
+// us (1.70 PFLOP/s, tensor pipe 91 % active), 8192 x 14336 x 4096 E4M3 with
+// silu 278-301 us (3.2-3.5 PFLOP/s, 89 %); where they are short, by the readout.
 //
 // Both operands are staged 128 bytes of k at a time in the 128-byte swizzled
 // layout the MMA reads, by TMA.  A matrix whose address or row stride is not a
 // multiple of 16 bytes, which TMA cannot read, is first copied to rows that
-// are (align_kernel) in a workspace of the caller's.  Measured beside warps
+// are (align_kernel, 5.7 TB/s) in a workspace of the caller's.  Measured beside warps
 // that realign rows on their way to shared memory, which take 1.2 us a stage
 // (us, BF16): 4096 x 4097 x 4097 917, this 140; 256 x 4096 x 4097 85, this
 // 34; 1 x 14336 x 4097 85, this 63.

@@ -10,7 +10,13 @@
 // the values stay in registers until they are written.  The gated activation
 // z = act(g) u needs max|z| alone.
 //
-// Bound: HBM (norm, BF16 with residual to 8 bits: 7 bytes an element).
+// Roundings: h is rounded to x's type where it is kept, but y is formed from
+// the binary32 h, so that each output is rounded once.
+//
+// Bound: HBM.  Read + written, of the 6.74 TB/s a copy reaches: norm of 8192 x
+// 4096 BF16 with residual to 8 bits (7 bytes an element) 36.2 us, 6.5 TB/s;
+// of 4096 x 12288 to BF16 60.4 us, 6.7 TB/s; gated activation of 8192 x 14336
+// BF16 to 8 bits 92.6 us, 6.3 TB/s.
 #include <string>
 
 #include "st_ops_device.h"
