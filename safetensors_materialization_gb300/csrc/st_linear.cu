@@ -521,6 +521,93 @@ __device__ __forceinline__ void put_row(void *base, st_dtype dtype, int64_t at, 
   }
 }
 
+// Rows at any alignment, or a ragged last chunk.  A warp's 32 tokens x kChunk
+// columns are turned in shared memory, so that a half-warp reads or writes one
+// token's consecutive columns: half h has tokens 16 h + i, lane l of it the
+// pair of columns 2 l, 2 l + 1, or, where a row of y starts at an odd place,
+// 2 l + 1, 2 l + 2 (and the first column alone), so that a pair is one aligned
+// word (5549 x 7887 x 99 F16 with gelu 88 us column by column, TURN_B so).
+__device__ __forceinline__ int rows_from(const LinArgs &a, int64_t m) {
+  return static_cast<int>(max(int64_t(0), min(int64_t(32), a.m - m)));
+}
+__device__ __forceinline__ void read_turned(const LinArgs &a, int64_t m0, int64_t n0, int lane, uint32_t (&old)[2][8]) {
+  const int half = lane >> 4, l = lane & 15, rows = rows_from(a, m0);
+  const int lim = static_cast<int>(min(int64_t(kChunk), a.n - n0));
+  const uint16_t *p = static_cast<const uint16_t *>(a.residual) + (m0 + 16 * half) * a.ldr + n0 + 2 * l;
+#pragma unroll
+  for (int i = 0; i < 16; ++i, p += a.ldr) {
+    uint32_t w = 0;
+    if (i + 16 * half < rows) {
+      if (2 * l + 1 < lim && reinterpret_cast<uintptr_t>(p) % 4 == 0) w = *reinterpret_cast<const uint32_t *>(p);
+      else {
+        if (2 * l < lim) w = p[0];
+        if (2 * l + 1 < lim) w |= static_cast<uint32_t>(p[1]) << 16;
+      }
+    }
+    old[i / 8][i % 8] = w;
+  }
+}
+template <class T>
+__device__ __forceinline__ void put_turned(uint32_t (&w)[32][17], const LinArgs &a, int64_t m0, int64_t n0, int lane,
+                                           const uint32_t (&old)[2][8], float (&v)[kChunk]) {
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  const int half = lane >> 4, l = lane & 15, rows = rows_from(a, m0);
+  const int lim = static_cast<int>(min(int64_t(kChunk), a.n - n0));
+  if (a.residual) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i + 16 * half][l] = old[i / 8][i % 8];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = w[lane][8 * i + j];
+      add16(u, kBf16, v + 16 * i);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[lane][j] = kBf16 ? pack_bf16(v[2 * j], v[2 * j + 1]) : pack_f16(v[2 * j], v[2 * j + 1]);
+  __syncwarp();
+  uint16_t *p = static_cast<uint16_t *>(a.y) + (m0 + 16 * half) * a.ldy + n0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i, p += a.ldy) {
+    if (i + 16 * half >= rows) break;
+    const uint32_t *r = w[i + 16 * half];
+    const uint32_t lo = r[l];
+    if (reinterpret_cast<uintptr_t>(p) % 4 == 0) {
+      if (2 * l + 1 < lim) *reinterpret_cast<uint32_t *>(p + 2 * l) = lo;
+      else if (2 * l < lim) p[2 * l] = static_cast<uint16_t>(lo);
+    } else {
+      if (2 * l + 2 < lim) *reinterpret_cast<uint32_t *>(p + 2 * l + 1) = __funnelshift_r(lo, r[l + 1], 16);
+      else if (2 * l + 1 < lim) p[2 * l + 1] = static_cast<uint16_t>(lo >> 16);
+      if (l == 0) p[0] = static_cast<uint16_t>(lo);
+    }
+  }
+}
+// The same for binary32, 16 columns at a time.
+__device__ __forceinline__ void put_turned32(uint32_t (&w)[32][17], const LinArgs &a, int64_t m0, int64_t n0, int lane,
+                                             const float (&v)[kChunk]) {
+  const int half = lane >> 4, rows = rows_from(a, m0);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[lane][j] = __float_as_uint(v[16 * h + j]);
+    __syncwarp();
+    const int64_t col = n0 + 16 * h + (lane & 15);
+    if (col >= a.n) continue;
+    const float *from = static_cast<const float *>(a.residual) + (m0 + 16 * half) * a.ldr + col;
+    float *to = static_cast<float *>(a.y) + (m0 + 16 * half) * a.ldy + col;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i + 16 * half >= rows) break;
+      to[i * a.ldy] = __uint_as_float(w[i + 16 * half][lane & 15]) + (a.residual ? from[i * a.ldr] : 0.0f);
+    }
+  }
+}
+
 // Tile t of the launch: groups of eight token tiles, so that the tiles in
 // flight share their operands in L2.
 struct TileAt {
@@ -542,7 +629,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
-  __shared__ float turn[kDenseEpilogueWarps][32][17];
+  __shared__ uint32_t turn[kDenseEpilogueWarps][32][17];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;
@@ -640,9 +727,12 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         if (n0 >= a.n) break;
         const bool wide = a.vec && n0 + kChunk <= a.n;
         uint32_t old[2][8];
-        if (wide && row && a.residual && a.y_dtype != ST_F32) {
+        if (a.residual && a.y_dtype != ST_F32) {
+          if (!wide) read_turned(a, at.m0 + rank * 128 + quarter * 32, n0, lane, old);
+          else if (row) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) ld32(static_cast<const uint16_t *>(a.residual) + m * a.ldr + n0 + 16 * i, old[i]);
+            for (int i = 0; i < 2; ++i) ld32(static_cast<const uint16_t *>(a.residual) + m * a.ldr + n0 + 16 * i, old[i]);
+          }
         }
         // A 16-bit bias is read by every lane, where its alignment allows; else
         // one column's bias, like its scale, per lane and handed round below.
@@ -681,35 +771,10 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             put_row(a.y, a.y_dtype, m * a.ldy + n0, v);
           }
         } else {
-          // Rows at any alignment, or a ragged last chunk: 16 columns at a
-          // time are turned in shared memory, so that a half-warp writes one
-          // token's consecutive columns; the residual of all of a lane's 16
-          // tokens is under way before the first is written.
-          const int64_t mw = at.m0 + rank * 128 + quarter * 32 + (lane >> 4);
-          const int rows = static_cast<int>(max(int64_t(0), min(int64_t(32), a.m - (mw - (lane >> 4)))));
-          with_type(a.y_dtype, [&](auto zero) {
-            using T = decltype(zero);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) turn[warp][lane][j] = v[16 * h + j];
-              __syncwarp();
-              const int64_t col = n0 + 16 * h + (lane & 15);
-              if (col >= a.n) continue;
-              const T *old = static_cast<const T *>(a.residual) + mw * a.ldr + col;
-              T *out = static_cast<T *>(a.y) + mw * a.ldy + col;
-              float add[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                add[i] = 0.0f;
-                if (a.residual && 2 * i + (lane >> 4) < rows) add[i] = to_float(old[2 * i * a.ldr]);
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (2 * i + (lane >> 4) < rows) round_to(turn[warp][2 * i + (lane >> 4)][lane & 15] + add[i], out[2 * i * a.ldy]);
-            }
-          });
+          const int64_t mw = at.m0 + rank * 128 + quarter * 32;
+          if (a.y_dtype == ST_BF16) put_turned<__nv_bfloat16>(turn[warp], a, mw, n0, lane, old, v);
+          else if (a.y_dtype == ST_F16) put_turned<__half>(turn[warp], a, mw, n0, lane, old, v);
+          else put_turned32(turn[warp], a, mw, n0, lane, v);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

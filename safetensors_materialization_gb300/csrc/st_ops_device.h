@@ -68,10 +68,6 @@ __device__ __forceinline__ void with_type(st_dtype dtype, F &&f) {
   else if (dtype == ST_F16) f(__half{});
   else f(float{});
 }
-__device__ __forceinline__ void round_to(float v, float &out) { out = v; }
-__device__ __forceinline__ void round_to(float v, __half &out) { out = __float2half_rn(v); }
-__device__ __forceinline__ void round_to(float v, __nv_bfloat16 &out) { out = __float2bfloat16_rn(v); }
-
 // V consecutive elements of an array whose dtype is known at run time (the
 // branch is the same for every thread).
 template <int V>

@@ -634,14 +634,45 @@ def test_operators_on_another_stream_and_in_a_graph(stmat):
         got = chain(stream)
         side.synchronize()
         assert torch.equal(got[0].float(), want[0].float()) and torch.equal(got[1], want[1])
-    graph = torch.cuda.CUDAGraph()
+    # captured after a copy on the same stream, and after work of another one
+    graph, source = torch.cuda.CUDAGraph(), x.clone()
     with torch.cuda.graph(graph):
+        x.copy_(source)
         got = chain()
-    x.copy_(normal(9, 8, 1024, dtype=torch.bfloat16))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            again = chain()
+        torch.cuda.current_stream().wait_stream(side)
+        y, s, _ = stmat.rms_norm(again[0].bfloat16(), dst="F8_E4M3")
+    source.copy_(normal(9, 8, 1024, dtype=torch.bfloat16))
+    x.copy_(source)
     want = chain()
-    graph.replay()
+    last = stmat.rms_norm(want[0].bfloat16(), dst="F8_E4M3")
+    x.zero_()
+    for _ in range(3):
+        graph.replay()
     torch.cuda.synchronize()
-    assert torch.equal(got[0].float(), want[0].float()) and torch.equal(got[1], want[1])
+    for a, b in ((got, want), (again, want), ((y, s), last)):
+        assert torch.equal(a[0].float(), b[0].float()) and torch.equal(a[1], b[1])
+
+
+@gpu
+def test_row_offsets_beyond_32_bits(stmat):
+    """Rows that start more than 2^32 elements in, read and written."""
+    rows, c, ld = 67, 520, 1 << 26
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    buf = torch.zeros(rows * ld, dtype=torch.bfloat16, device="cuda").view(rows, ld)
+    x, w = normal(1, rows, c, dtype=torch.bfloat16), normal(2, c)
+    for at in (0, 3):
+        buf[:, at:at + c] = x
+        want = norm64(x, None, w, 1e-5)[1]
+        check_values(stmat.rms_norm(buf[:, at:at + c], w)[0], want)
+        out = buf[:, 4096 + at:4096 + at + c]
+        a = stmat.GatedActArgs(rows=rows, cols=c, act=1, x_dtype=10, y_dtype=10, gate=buf[:, at:].data_ptr(), ldg=ld,
+                               y=out.data_ptr(), ldy=ld)
+        stmat._check(stmat.lib().st_gated_act(a, torch.cuda.current_stream().cuda_stream))
+        assert torch.equal(out, x.clamp_min(0))
 
 
 # --------------------------------------------------------------- the example
