@@ -71,7 +71,6 @@ struct LinArgs {
   int64_t m, n, kbytes;
   int k_blocks, splits, stages, m_tiles;
   int n_tiles, tile_n;               // dense_kernel: weight rows per tile
-  int bias_wide;                     // dense_kernel: 16-bit bias at a multiple of 32 bytes
   int x_box;                         // token rows a TMA copy brings
   int vec;                           // y and residual rows take 32-byte (dense) or four-element (split) accesses
   uint32_t idesc;
@@ -123,8 +122,8 @@ __device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, in
     }
   }
   ok = __shfl_sync(~0u, ok, 0);
-  // Every lane sees the phase complete (and what was written before it).
-  return ok && bar_wait(bar, parity);
+  __syncwarp();
+  return ok;
 }
 __device__ __forceinline__ void tma_load(const CUtensorMap *map, void *dst, uint64_t *bar, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -436,8 +435,10 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
 
 // ---------------------------------------------------------- dense_kernel
 
+// Orders what the CTA did before, not its global writes (a release to the
+// cluster would wait for y to be written: 2000 cycles a tile).
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A tile of this CTA whose bytes count on a barrier that may be the peer's.
 __device__ __forceinline__ void pair_load(const CUtensorMap *map, void *dst, uint32_t bar, int32_t x, int32_t y) {
@@ -629,7 +630,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
-  __shared__ uint32_t turn[kDenseEpilogueWarps][32][17];
+  __shared__ __align__(16) uint32_t turn[kDenseEpilogueWarps][32][17];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;
@@ -712,19 +713,35 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     const uint32_t taken_at = peer_addr(taken, 0);
     const int chunks = a.tile_n / kChunk;
     const bool columns_scaled = a.w_scale && a.w_scale_step;
+    // The token's scale, and the weight's where it is a single one; a tile's
+    // are read while the one before it is written.
+    auto scale_of = [&](int t) {
+      const int64_t m = tile_at(a, t).m0 + rank * 128 + quarter * 32 + lane;
+      float xs = m < a.m && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
+      if (a.w_scale && !columns_scaled) xs *= *a.w_scale;
+      return xs;
+    };
+    float next_xs = pair < tiles ? scale_of(pair) : 1.0f;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {
       const TileAt at = tile_at(a, t);
       const int buf = n & 1;
       const int64_t m = at.m0 + rank * 128 + quarter * 32 + lane;
       const bool row = m < a.m;
-      float xs = row && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
-      if (a.w_scale && !columns_scaled) xs *= *a.w_scale;
+      const float xs = next_xs;
+      if (t + pairs < tiles) next_xs = scale_of(t + pairs);
+      // The half of TMEM is given back as soon as this warp has read its part.
+      auto release = [&]() {
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) peer_arrive(taken_at + 8 * buf);
+      };
+      const int live = static_cast<int>(min(int64_t(chunks), (a.n - at.n0 + kChunk - 1) / kChunk));
       if (!bar_wait_warp(&sums[buf], (n / 2) & 1, lane)) { failed = 1; break; }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int c = warp >> 2; c < chunks; c += kDenseEpilogueWarps / 4) {
+      if (warp >> 2 >= live) release();
+      for (int c = warp >> 2; c < live; c += kDenseEpilogueWarps / 4) {
         const int64_t n0 = at.n0 + c * kChunk;
-        if (n0 >= a.n) break;
         const bool wide = a.vec && n0 + kChunk <= a.n;
         uint32_t old[2][8];
         if (a.residual && a.y_dtype != ST_F32) {
@@ -734,32 +751,31 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             for (int i = 0; i < 2; ++i) ld32(static_cast<const uint16_t *>(a.residual) + m * a.ldr + n0 + 16 * i, old[i]);
           }
         }
-        // A 16-bit bias is read by every lane, where its alignment allows; else
-        // one column's bias, like its scale, per lane and handed round below.
-        const bool wide_bias = a.bias_wide && n0 + kChunk <= a.n;
+        // One column's scale and bias per lane, handed round below.
         float wl = 1.0f, bl[1] = {0.0f};
         if (n0 + lane < a.n) {
           if (columns_scaled) wl = a.w_scale[n0 + lane];
-          if (a.bias && !wide_bias) load_any<1>(a.bias, a.bias_dtype, n0 + lane, bl);
+          if (a.bias) load_any<1>(a.bias, a.bias_dtype, n0 + lane, bl);
         }
         float v[kChunk];
         tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kPairMaxN + c * kChunk, v);
+        if (c + kDenseEpilogueWarps / 4 >= live) release();
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) v[j] *= xs;
         if (columns_scaled) {
 #pragma unroll
           for (int j = 0; j < kChunk; ++j) v[j] *= __shfl_sync(~0u, wl, j);
         }
-        if (wide_bias) {
+        if (a.bias) {
+          float *const all = reinterpret_cast<float *>(turn[warp]);
+          __syncwarp();
+          all[lane] = bl[0];
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t u[8];
-            ld32(static_cast<const uint16_t *>(a.bias) + n0 + 16 * i, u);
-            add16(u, a.bias_dtype == ST_BF16, v + 16 * i);
+          for (int j = 0; j < kChunk; j += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(all + j);
+            v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
           }
-        } else if (a.bias) {
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) v[j] += __shfl_sync(~0u, bl[0], j);
         }
         activate(v, a.act);
         if (wide) {
@@ -777,9 +793,6 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
           else put_turned32(turn[warp], a, mw, n0, lane, v);
         }
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) peer_arrive(taken_at + 8 * buf);
     }
   }
   __syncwarp();
@@ -883,7 +896,8 @@ struct Shape {
 };
 
 // dense_kernel: rounds of tiles over the pairs; a stage takes as long as its
-// rows or its MMAs, whichever is longer.  The width of a tile is the one with
+// rows (1.08 units each: 64 columns wide, 0.207 us a stage) or its MMAs,
+// whichever is longer.  The width of a tile is the one with
 // the shortest rounds in all (4096 x 4096 x 14336 BF16: 224 columns, four
 // full rounds, 285 us; 256 columns, 314).
 Shape dense_shape(int64_t m, int64_t n, int k_blocks, int sms) {
@@ -891,7 +905,7 @@ Shape dense_shape(int64_t m, int64_t n, int k_blocks, int sms) {
   const int64_t m_tiles = (m + kPairM - 1) / kPairM, pairs = sms / 2;
   for (int w = kPairMaxN; w >= 32; w -= 32) {
     const int64_t n_tiles = (n + w - 1) / w, rounds = (m_tiles * n_tiles + pairs - 1) / pairs;
-    const double rows = 128 + w / 2, mma = 0.87 * w, cost = static_cast<double>(rounds) * k_blocks * (rows > mma ? rows : mma);
+    const double rows = 1.08 * (128 + w / 2), mma = 0.87 * w, cost = static_cast<double>(rounds) * k_blocks * (rows > mma ? rows : mma);
     if (best.width == 0 || cost < best.cost) best = Shape{m_tiles, n_tiles, w, 1, cost};
   }
   return best;
@@ -1044,7 +1058,6 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
     a.tile_n = d.width;
     a.idesc = idesc(fx, fw, kPairM, a.tile_n);
     a.vec = aligned(32);
-    a.bias_wide = p.bias && p.bias_dtype != ST_F32 && reinterpret_cast<uintptr_t>(p.bias) % 32 == 0;
     s = encode(&xmap, a.x, p.k, item, 128);
     if (s == ST_OK) s = encode(&wmap, a.w, p.k, item, a.tile_n / 2);
     if (s != ST_OK) return s;
