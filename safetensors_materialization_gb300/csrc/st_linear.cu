@@ -50,12 +50,14 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 
 constexpr int kPairM = 256;          // tokens per pair of CTAs
 constexpr int kPairMaxN = 256;       // weight rows per pair, a multiple of 32
-// Four warps per 32 TMEM lanes, each with every fourth chunk of the columns:
-// a product with a short sum is bound by its readout, whose chains of loads
-// and arithmetic eight warps leave two thirds of the issue slots of.
-constexpr int kDenseEpilogueWarps = 16;
-constexpr int kDenseMmaWarp = 16, kDenseCopyWarp = 17, kDenseThreads = 576;
-constexpr int kDenseSmem = 190 * 1024;  // the ring of stages; room for the rest of a CTA's 227 KB
+// Three warps per 32 TMEM lanes, each with every third chunk of the columns: a
+// product with a short sum is bound by its readout, whose chains of loads and
+// arithmetic eight warps leave two thirds of the issue slots of; sixteen leave
+// a thread 96 registers, twelve 128 (8192 x 4096 x 1024 E4M3: 39.0, 32.0, 28.2
+// us).
+constexpr int kDenseEpilogueWarps = 12;
+constexpr int kDenseMmaWarp = 12, kDenseCopyWarp = 13, kDenseThreads = 448;
+constexpr int kDenseSmem = 196 * 1024;  // the ring of stages; room for the rest of a CTA's 227 KB
 constexpr int kChunk = 32;           // columns an epilogue warp reads at a time
 
 // One operand of the product.
@@ -622,7 +624,7 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs &a, int t) {
 }
 
 template <bool kEight>
-__global__ void __launch_bounds__(kDenseThreads)
+__global__ void __launch_bounds__(kDenseThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ LinArgs a) {
   extern __shared__ uint8_t raw_smem[];
