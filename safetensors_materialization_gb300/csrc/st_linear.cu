@@ -32,6 +32,7 @@
 // 34; 1 x 14336 x 4097 85, this 63.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -899,17 +900,23 @@ struct Shape {
 
 // dense_kernel: rounds of tiles over the pairs; a stage takes as long as its
 // rows (1.08 units each: 64 columns wide, 0.207 us a stage) or its MMAs,
-// whichever is longer.  The width of a tile is the one with
-// the shortest rounds in all (4096 x 4096 x 14336 BF16: 224 columns, four
-// full rounds, 285 us; 256 columns, 314).
+// whichever is longer, and a tile as long as its stages or its readout (1500
+// units and 8 a column).  The width of a tile is the one with the shortest rounds in
+// all (4096 x 4096 x 14336 BF16: 224 columns, four full rounds, 285 us; 256
+// columns, 314).  The cost compared with split_kernel's is that of the shortest
+// stages alone: its readouts are not in its cost either.
 Shape dense_shape(int64_t m, int64_t n, int k_blocks, int sms) {
   Shape best{};
+  double shortest = 0, cost = 0;
   const int64_t m_tiles = (m + kPairM - 1) / kPairM, pairs = sms / 2;
   for (int w = kPairMaxN; w >= 32; w -= 32) {
-    const int64_t n_tiles = (n + w - 1) / w, rounds = (m_tiles * n_tiles + pairs - 1) / pairs;
-    const double rows = 1.08 * (128 + w / 2), mma = 0.87 * w, cost = static_cast<double>(rounds) * k_blocks * (rows > mma ? rows : mma);
-    if (best.width == 0 || cost < best.cost) best = Shape{m_tiles, n_tiles, w, 1, cost};
+    const int64_t n_tiles = (n + w - 1) / w;
+    const double rounds = static_cast<double>((m_tiles * n_tiles + pairs - 1) / pairs);
+    const double stages = k_blocks * std::max(1.08 * (128 + w / 2), 0.87 * w), all = rounds * std::max(stages, 1500 + 8.0 * w);
+    cost = best.width == 0 ? rounds * stages : std::min(cost, rounds * stages);
+    if (best.width == 0 || all < shortest) best = Shape{m_tiles, n_tiles, w, 1, 0}, shortest = all;
   }
+  best.cost = cost;
   return best;
 }
 
