@@ -19,9 +19,10 @@
 // weight rows, so a stage's 32 KB per SM feed twice the products of a lone
 // CTA's.  The pairs stay resident and take tiles in turn; a tile's sums are
 // read out of one half of TMEM while the next tile's are formed in the other.
-// Bound by the power limit where sums are long: 4096 x 4096 x 14336 BF16 283
-// us (1.70 PFLOP/s, tensor pipe 91 % active), 8192 x 14336 x 4096 E4M3 with
-// silu 278-301 us (3.2-3.5 PFLOP/s, 89 %); where they are short, by the readout.
+// Bound by the power limit where sums are long: 4096 x 4096 x 14336 BF16 258
+// us alone and 280 in a row (1.87 and 1.72 PFLOP/s, tensor pipe 92 % active),
+// 8192 x 14336 x 4096 E4M3 with silu 264 and 296 us (3.64 and 3.25 PFLOP/s, 91
+// %); where they are short, by the readout.
 //
 // Both operands are staged 128 bytes of k at a time in the 128-byte swizzled
 // layout the MMA reads, by TMA.  A matrix whose address or row stride is not a
@@ -530,7 +531,8 @@ __device__ __forceinline__ void put_row(void *base, st_dtype dtype, int64_t at, 
 // token's consecutive columns: half h has tokens 16 h + i, lane l of it the
 // pair of columns 2 l, 2 l + 1, or, where a row of y starts at an odd place,
 // 2 l + 1, 2 l + 2 (and the first column alone), so that a pair is one aligned
-// word (5549 x 7887 x 99 F16 with gelu 88 us column by column, TURN_B so).
+// word (5598 x 6526 x 391 BF16 with gelu and residual 145 us column by column,
+// 102 so).
 __device__ __forceinline__ int rows_from(const LinArgs &a, int64_t m) {
   return static_cast<int>(max(int64_t(0), min(int64_t(32), a.m - m)));
 }
