@@ -507,6 +507,20 @@ def test_linear_of_integers_is_exact(stmat, m, n, k, xt, wt):
 
 
 @gpu
+@pytest.mark.parametrize("m,n,k", [(100003, 17, 40), (70000, 300, 48), (3, 100001, 64), (17, 30000, 64), (3, 5, 200000),
+                                   (5, 7, 100001), (700, 700, 20000)])
+@pytest.mark.parametrize("xt", ["BF16", "F8_E4M3"])
+def test_linear_of_integers_far_out(stmat, m, n, k, xt):
+    """Many tokens, many weight rows, long sums, compared on the GPU: integers
+    of magnitude 2, whose sums a binary32 product holds exactly too."""
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    x = torch.randint(-2, 3, (m, k), generator=g, device="cuda").float()
+    w = torch.randint(-2, 3, (n, k), generator=g, device="cuda").float()
+    y = stmat.linear(x.to(TYPES[xt]), w.to(TYPES[xt]), dst="F32")
+    assert torch.equal(y, x @ w.t())
+
+
+@gpu
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("m,n,k", [(1, 200, 136), (5, 328, 64), (40, 130, 96), (150, 391, 300), (300, 520, 128), (600, 544, 256),
                                    (530, 391, 64)])
@@ -691,3 +705,9 @@ def test_scaled_fp8_mlp_example():
     spec.loader.exec_module(example)
     found = example.main(hidden=1024, inter=2752, tokens=(1, 37, 700))
     assert set(found) == {1, 37, 700} and all(0 < v < (1 + 2.0 ** -4) ** 3 - 1 for v in found.values()), found
+
+
+@gpu
+def test_no_wait_gave_up(stmat):
+    """After every other test of this file: the error word is clear."""
+    assert stmat.static_check() == 0
