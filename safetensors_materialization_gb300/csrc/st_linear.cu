@@ -19,6 +19,8 @@
 // weight rows, so a stage's 32 KB per SM feed twice the products of a lone
 // CTA's.  The pairs stay resident and take tiles in turn; a tile's sums are
 // read out of one half of TMEM while the next tile's are formed in the other.
+// Few tiles with long sums are shared by the pairs of a cluster, which join
+// their sums as split_kernel's CTAs do.
 // Bound by the power limit where sums are long: 4096 x 4096 x 14336 BF16 258
 // us alone and 280 in a row (1.87 and 1.72 PFLOP/s, tensor pipe 92 % active),
 // 8192 x 14336 x 4096 E4M3 with silu 264 and 296 us (3.64 and 3.25 PFLOP/s, 91
@@ -51,6 +53,7 @@ constexpr int kMmaWarp = 4, kCopyWarp = 5, kSplitThreads = 192;
 constexpr uint32_t kWaitLimit = 1u << 22;
 
 constexpr int kPairM = 256;          // tokens per pair of CTAs
+constexpr int kMaxPairs = 4;         // pairs that share a tile's sum: portable clusters
 constexpr int kPairMaxN = 256;       // weight rows per pair, a multiple of 32
 // Three warps per 32 TMEM lanes, each with every third chunk of the columns: a
 // product with a short sum is bound by its readout, whose chains of loads and
@@ -458,10 +461,11 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
 }
-// Arrives on the barrier at this address in both CTAs once the MMAs so far are done.
-__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+// Arrives on the barrier at this address in both CTAs of the pair whose first
+// is `leader` once the MMAs so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t *bar, uint32_t leader) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-               ::"r"(smem_addr(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+               ::"r"(smem_addr(bar)), "h"(static_cast<uint16_t>(3u << leader)) : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[32]) {
   uint32_t v[32];
@@ -626,7 +630,8 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs &a, int t) {
   return {int64_t(g * kGroup + in % rows) * kPairM, int64_t(in / rows) * a.tile_n};
 }
 
-template <bool kEight>
+// kShared: one tile a cluster, its sum over k shared by the cluster's pairs.
+template <bool kEight, bool kShared>
 __global__ void __launch_bounds__(kDenseThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ LinArgs a) {
@@ -638,9 +643,13 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   __shared__ __align__(16) uint32_t turn[kDenseEpilogueWarps][32][17];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = blockIdx.x & 1;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.m_tiles * a.n_tiles;
+  const int splits = kShared ? a.splits : 1;
+  const uint32_t in_cluster = blockIdx.x % (2 * splits), rank = in_cluster & 1, leader = in_cluster & ~1u;
+  const int split = static_cast<int>(in_cluster >> 1), tiles = a.m_tiles * a.n_tiles;
+  const int pair = blockIdx.x / (2 * splits), pairs = gridDim.x / (2 * splits);
   const int half_n = a.tile_n / 2, stage_bytes = (128 + half_n) * kStageK;
+  const int first = static_cast<int>(int64_t(a.k_blocks) * split / splits);
+  const int blocks = static_cast<int>(int64_t(a.k_blocks) * (split + 1) / splits) - first;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -667,18 +676,79 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   wait_for_previous();
   let_next_start();
 
+  const int quarter = warp & 3, chunks = a.tile_n / kChunk;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const bool columns_scaled = a.w_scale && a.w_scale_step;
+  // The token's scale, and the weight's where it is a single one.
+  auto scale_of = [&](int t) {
+    const int64_t m = tile_at(a, t).m0 + rank * 128 + quarter * 32 + lane;
+    float xs = m < a.m && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
+    if (a.w_scale && !columns_scaled) xs *= *a.w_scale;
+    return xs;
+  };
+  // Chunk c of a tile: its sums, read by `sums_of`, to y.
+  auto finish = [&](const TileAt &at, int c, float xs, auto sums_of) {
+    const int64_t mw = at.m0 + rank * 128 + quarter * 32, m = mw + lane, n0 = at.n0 + c * kChunk;
+    const bool row = m < a.m, wide = a.vec && n0 + kChunk <= a.n;
+    uint32_t old[2][8];
+    if (a.residual && a.y_dtype != ST_F32) {
+      if (!wide) read_turned(a, mw, n0, lane, old);
+      else if (row) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ld32(static_cast<const uint16_t *>(a.residual) + m * a.ldr + n0 + 16 * i, old[i]);
+      }
+    }
+    // One column's scale and bias per lane, handed round below.
+    float wl = 1.0f, bl[1] = {0.0f};
+    if (n0 + lane < a.n) {
+      if (columns_scaled) wl = a.w_scale[n0 + lane];
+      if (a.bias) load_any<1>(a.bias, a.bias_dtype, n0 + lane, bl);
+    }
+    float v[kChunk];
+    sums_of(v);
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) v[j] *= xs;
+    if (columns_scaled) {
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) v[j] *= __shfl_sync(~0u, wl, j);
+    }
+    if (a.bias) {
+      float *const all = reinterpret_cast<float *>(turn[warp]);
+      __syncwarp();
+      all[lane] = bl[0];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kChunk; j += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(all + j);
+        v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
+      }
+    }
+    activate(v, a.act);
+    if (wide) {
+      if (row) {
+        if (a.residual && a.y_dtype != ST_F32) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) add16(old[i], a.y_dtype == ST_BF16, v + 16 * i);
+        } else if (a.residual) add_row32(a.residual, m * a.ldr + n0, v);
+        put_row(a.y, a.y_dtype, m * a.ldy + n0, v);
+      }
+    } else if (a.y_dtype == ST_BF16) put_turned<__nv_bfloat16>(turn[warp], a, mw, n0, lane, old, v);
+    else if (a.y_dtype == ST_F16) put_turned<__half>(turn[warp], a, mw, n0, lane, old, v);
+    else put_turned32(turn[warp], a, mw, n0, lane, v);
+  };
+
   Ring r;
   if (warp == kDenseCopyWarp) {
     if (elect_one()) {
       // This CTA's tokens and its half of the weight rows; the bytes of both
       // CTAs count on the first one's barriers.
-      const uint32_t bars = peer_addr(full, 0);
+      const uint32_t bars = peer_addr(full, leader);
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
         const TileAt at = tile_at(a, t);
         const int32_t m = static_cast<int32_t>(at.m0 + rank * 128), n = static_cast<int32_t>(at.n0 + rank * half_n);
         constexpr int kStep = kEight ? kStageK : kStageK / 2;
-        for (int b = 0, k = 0; b < a.k_blocks; ++b, k += kStep, r.next(a.stages)) {
+        for (int b = 0, k = first * kStep; b < blocks; ++b, k += kStep, r.next(a.stages)) {
           // Before its first use a stage counts as released.
           if (!bar_wait(&empty[r.at], r.phase ^ 1)) { ok = false; break; }
           uint8_t *stage = smem + r.at * stage_bytes;
@@ -701,38 +771,26 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + sum.at * kPairMaxN;
         uint32_t add = 0;
-        for (int b = 0; b < a.k_blocks; ++b, r.next(a.stages)) {
+        for (int b = 0; b < blocks; ++b, r.next(a.stages)) {
           if (!bar_wait(&full[r.at], r.phase)) { ok = false; break; }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint64_t xd = tile_desc(smem + r.at * stage_bytes), wd = xd + (128 * kStageK >> 4);
 #pragma unroll
           for (int j = 0; j < kStageK / 32; ++j, add = 1) pair_mma<kEight>(d, xd + 2 * j, wd + 2 * j, a.idesc, add);
-          pair_commit(&empty[r.at]);
+          pair_commit(&empty[r.at], leader);
         }
-        pair_commit(&sums[sum.at]);
+        pair_commit(&sums[sum.at], leader);
       }
       if (!ok) failed = 1;
     }
-  } else {
-    const int quarter = warp & 3;
-    const uint32_t taken_at = peer_addr(taken, 0);
-    const int chunks = a.tile_n / kChunk;
-    const bool columns_scaled = a.w_scale && a.w_scale_step;
-    // The token's scale, and the weight's where it is a single one; a tile's
-    // are read while the one before it is written.
-    auto scale_of = [&](int t) {
-      const int64_t m = tile_at(a, t).m0 + rank * 128 + quarter * 32 + lane;
-      float xs = m < a.m && a.x_scale ? a.x_scale[m * a.x_scale_step] : 1.0f;
-      if (a.w_scale && !columns_scaled) xs *= *a.w_scale;
-      return xs;
-    };
+  } else if (!kShared) {
+    const uint32_t taken_at = peer_addr(taken, leader);
+    // A tile's scales are read while the one before it is written.
     float next_xs = pair < tiles ? scale_of(pair) : 1.0f;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {
       const TileAt at = tile_at(a, t);
       const int buf = n & 1;
-      const int64_t m = at.m0 + rank * 128 + quarter * 32 + lane;
-      const bool row = m < a.m;
       const float xs = next_xs;
       if (t + pairs < tiles) next_xs = scale_of(t + pairs);
       // The half of TMEM is given back as soon as this warp has read its part.
@@ -745,59 +803,55 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
       if (!bar_wait_warp(&sums[buf], (n / 2) & 1, lane)) { failed = 1; break; }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (warp >> 2 >= live) release();
-      for (int c = warp >> 2; c < live; c += kDenseEpilogueWarps / 4) {
-        const int64_t n0 = at.n0 + c * kChunk;
-        const bool wide = a.vec && n0 + kChunk <= a.n;
-        uint32_t old[2][8];
-        if (a.residual && a.y_dtype != ST_F32) {
-          if (!wide) read_turned(a, at.m0 + rank * 128 + quarter * 32, n0, lane, old);
-          else if (row) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) ld32(static_cast<const uint16_t *>(a.residual) + m * a.ldr + n0 + 16 * i, old[i]);
-          }
-        }
-        // One column's scale and bias per lane, handed round below.
-        float wl = 1.0f, bl[1] = {0.0f};
-        if (n0 + lane < a.n) {
-          if (columns_scaled) wl = a.w_scale[n0 + lane];
-          if (a.bias) load_any<1>(a.bias, a.bias_dtype, n0 + lane, bl);
-        }
+      for (int c = warp >> 2; c < live; c += kDenseEpilogueWarps / 4)
+        finish(at, c, xs, [&](float(&v)[kChunk]) {
+          tmem_ld32(lanes + buf * kPairMaxN + c * kChunk, v);
+          if (c + kDenseEpilogueWarps / 4 >= live) release();
+        });
+    }
+  }
+  __syncwarp();
+  if constexpr (kShared) {
+    // Once every pair is done with its stages, each CTA
+    // puts its partial sums of a chunk of columns into the CTA that joins it:
+    // pair s has chunks [s per, (s + 1) per), from every pair's CTA with the
+    // same tokens, [splits][per][column][token] over the stages.
+    const int per = chunks / splits;
+    float *joined = reinterpret_cast<float *>(smem);
+    const bool reads = warp < kDenseEpilogueWarps;
+    float xs = 1.0f;
+    if (reads) {
+      xs = scale_of(pair);
+      if (!bar_wait_warp(&sums[0], 0, lane)) failed = 1;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (reads) {
+      for (int c = warp >> 2; c < chunks; c += kDenseEpilogueWarps / 4) {
         float v[kChunk];
-        tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kPairMaxN + c * kChunk, v);
-        if (c + kDenseEpilogueWarps / 4 >= live) release();
+        tmem_ld32(lanes + c * kChunk, v);
+        const uint32_t to = peer_addr(joined + ((split * per + c % per) * kChunk * 128 + quarter * 32 + lane), 2 * (c / per) + rank);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] *= xs;
-        if (columns_scaled) {
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) v[j] *= __shfl_sync(~0u, wl, j);
-        }
-        if (a.bias) {
-          float *const all = reinterpret_cast<float *>(turn[warp]);
-          __syncwarp();
-          all[lane] = bl[0];
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < kChunk; j += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(all + j);
-            v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
-          }
-        }
-        activate(v, a.act);
-        if (wide) {
-          if (row) {
-            if (a.residual && a.y_dtype != ST_F32) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) add16(old[i], a.y_dtype == ST_BF16, v + 16 * i);
-            } else if (a.residual) add_row32(a.residual, m * a.ldr + n0, v);
-            put_row(a.y, a.y_dtype, m * a.ldy + n0, v);
-          }
-        } else {
-          const int64_t mw = at.m0 + rank * 128 + quarter * 32;
-          if (a.y_dtype == ST_BF16) put_turned<__nv_bfloat16>(turn[warp], a, mw, n0, lane, old, v);
-          else if (a.y_dtype == ST_F16) put_turned<__half>(turn[warp], a, mw, n0, lane, old, v);
-          else put_turned32(turn[warp], a, mw, n0, lane, v);
-        }
+        for (int j = 0; j < kChunk; ++j) peer_store(to + j * 128 * 4, v[j]);
       }
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (reads) {
+      const TileAt at = tile_at(a, pair);
+      const int live = static_cast<int>(min(int64_t(chunks), (a.n - at.n0 + kChunk - 1) / kChunk));
+      for (int c = warp >> 2; c < per && split * per + c < live; c += kDenseEpilogueWarps / 4)
+        finish(at, split * per + c, xs, [&](float(&v)[kChunk]) {
+          const float *from = joined + c * kChunk * 128 + quarter * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) v[j] = from[j * 128];
+          for (int s = 1; s < splits; ++s) {
+            from += per * kChunk * 128;
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) v[j] += from[j * 128];
+          }
+        });
     }
   }
   __syncwarp();
@@ -857,8 +911,20 @@ st_status encode(CUtensorMap *map, const Side &s, int64_t k, int item, int box_r
 constexpr int kMaxDevices = 256;
 struct Device {
   int sms = 0;
+  int clusters[kMaxPairs + 1] = {};  // clusters of so many pairs that dense_kernel runs at a time
   uint32_t *err = nullptr;
 };
+
+void cluster_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, unsigned blocks, unsigned threads, size_t smem, unsigned cluster) {
+  cfg->gridDim = dim3(blocks);
+  cfg->blockDim = dim3(threads);
+  cfg->dynamicSmemBytes = smem;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
 
 st_status device(int *index, const Device **out) {
   static std::mutex mu;
@@ -874,7 +940,15 @@ st_status device(int *index, const Device **out) {
     const st_status s = static_scratch(&scratch);
     if (s != ST_OK) return s;
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_linear: counting SMs: %s", cudaGetErrorName(e));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(dense_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem + 1024);
+    for (int pairs = 1; pairs <= kMaxPairs && e == cudaSuccess; pairs *= 2) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      cluster_config(&cfg, attr, 2 * pairs, kDenseThreads, kDenseSmem + 1024, 2 * pairs);
+      e = cudaOccupancyMaxActiveClusters(&d.clusters[pairs], dense_kernel<true, true>, &cfg);
+    }
+    if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_linear: counting SMs and clusters: %s", cudaGetErrorName(e));
     d.err = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(scratch) + kStaticErrOffset);
   }
   *index = dev;
@@ -905,18 +979,26 @@ struct Shape {
 // whichever is longer, and a tile as long as its stages or its readout (1500
 // units and 8 a column).  The width of a tile is the one with the shortest rounds in
 // all (4096 x 4096 x 14336 BF16: 224 columns, four full rounds, 285 us; 256
-// columns, 314).  The cost compared with split_kernel's is that of the shortest
-// stages alone: its readouts are not in its cost either.
-Shape dense_shape(int64_t m, int64_t n, int k_blocks, int sms) {
+// columns, 314).  Few tiles with long sums are each shared by a cluster of pairs,
+// if all of the clusters run at a time, for 18 units a column of joining (us,
+// without and with: 256 x 4096 x 14336 E4M3 23.8, 19.6, BF16 35.8, 31.0; 256 x
+// 1024 x 4096 E4M3 10.5, 8.7; 512 x 4096 x 4096 BF16 18.4, 20.3).  The cost
+// compared with split_kernel's is that of the shortest stages alone: its
+// readouts are not in its cost either.
+Shape dense_shape(int64_t m, int64_t n, int k_blocks, const Device &gpu) {
   Shape best{};
   double shortest = 0, cost = 0;
-  const int64_t m_tiles = (m + kPairM - 1) / kPairM, pairs = sms / 2;
-  for (int w = kPairMaxN; w >= 32; w -= 32) {
-    const int64_t n_tiles = (n + w - 1) / w;
-    const double rounds = static_cast<double>((m_tiles * n_tiles + pairs - 1) / pairs);
-    const double stages = k_blocks * std::max(1.08 * (128 + w / 2), 0.87 * w), all = rounds * std::max(stages, 1500 + 8.0 * w);
-    cost = best.width == 0 ? rounds * stages : std::min(cost, rounds * stages);
-    if (best.width == 0 || all < shortest) best = Shape{m_tiles, n_tiles, w, 1, 0}, shortest = all;
+  const int64_t m_tiles = (m + kPairM - 1) / kPairM;
+  for (int pairs = 1; pairs <= kMaxPairs; pairs *= 2) {
+    for (int w = kPairMaxN; w >= 32 * pairs; w -= 32) {
+      const int64_t n_tiles = (n + w - 1) / w, tiles = m_tiles * n_tiles;
+      if (pairs > 1 && (w % (32 * pairs) || tiles > gpu.clusters[pairs] || k_blocks < 4 * pairs)) continue;
+      const double rounds = pairs > 1 ? 1 : static_cast<double>((tiles + gpu.sms / 2 - 1) / (gpu.sms / 2));
+      const double stages = (k_blocks + pairs - 1) / pairs * std::max(1.08 * (128 + w / 2), 0.87 * w);
+      const double join = pairs > 1 ? 18.0 * w : 0, all = rounds * std::max(stages, 1500 + 8.0 * w) + join;
+      cost = best.width == 0 ? rounds * stages + join : std::min(cost, rounds * stages + join);
+      if (best.width == 0 || all < shortest) best = Shape{m_tiles, n_tiles, w, pairs, 0}, shortest = all;
+    }
   }
   best.cost = cost;
   return best;
@@ -962,17 +1044,17 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   return e == cudaSuccess ? ST_OK : launch_error(a, e);
 }
 
-template <bool kEight>
+template <bool kEight, bool kShared>
 st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, int dev, int sms, cudaStream_t st) {
   // As many stages as fit: a narrow tile's are smaller, and need more of them
   // under way to cover the memory's latency.
   const int stage_bytes = (128 + a.tile_n / 2) * kStageK;
   a.stages = kDenseSmem / stage_bytes < kMaxStages ? kDenseSmem / stage_bytes : kMaxStages;
-  cudaError_t e = allow_smem<dense_kernel<kEight>>(dev, kDenseSmem + 1024);
+  cudaError_t e = allow_smem<dense_kernel<kEight, kShared>>(dev, kDenseSmem + 1024);
   if (e == cudaSuccess) {
     const int pairs = sms / 2, tiles = a.m_tiles * a.n_tiles;
-    e = launch(dense_kernel<kEight>, 2 * (tiles < pairs ? tiles : pairs), kDenseThreads, a.stages * stage_bytes + 1024, 2, st,
-               xmap, wmap, a);
+    e = launch(dense_kernel<kEight, kShared>, 2 * (kShared ? tiles * a.splits : std::min(tiles, pairs)), kDenseThreads,
+               a.stages * stage_bytes + 1024, 2 * a.splits, st, xmap, wmap, a);
   }
   return e == cudaSuccess ? ST_OK : launch_error(a, e);
 }
@@ -1060,19 +1142,22 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
     return one(p.y, p.ldy) && (!p.residual || one(p.residual, p.ldr));
   };
 
-  const Shape d = dense_shape(p.m, p.n, a.k_blocks, sms), c = split_shape(p.m, p.n, a.k_blocks, sms);
+  const Shape d = dense_shape(p.m, p.n, a.k_blocks, *gpu), c = split_shape(p.m, p.n, a.k_blocks, sms);
   if (p.k > 0 && d.cost < c.cost) {
     if (d.m_tiles * d.n_tiles > 0x3fffffff)
       return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
     a.m_tiles = static_cast<int>(d.m_tiles);
     a.n_tiles = static_cast<int>(d.n_tiles);
     a.tile_n = d.width;
+    a.splits = d.splits;
     a.idesc = idesc(fx, fw, kPairM, a.tile_n);
     a.vec = aligned(32);
     s = encode(&xmap, a.x, p.k, item, 128);
     if (s == ST_OK) s = encode(&wmap, a.w, p.k, item, a.tile_n / 2);
     if (s != ST_OK) return s;
-    return a.eight ? launch_dense<true>(a, xmap, wmap, dev, sms, st) : launch_dense<false>(a, xmap, wmap, dev, sms, st);
+    if (a.splits > 1)
+      return a.eight ? launch_dense<true, true>(a, xmap, wmap, dev, sms, st) : launch_dense<false, true>(a, xmap, wmap, dev, sms, st);
+    return a.eight ? launch_dense<true, false>(a, xmap, wmap, dev, sms, st) : launch_dense<false, false>(a, xmap, wmap, dev, sms, st);
   }
 
   a.vec = aligned(4 * out);
