@@ -617,7 +617,8 @@ st_status st_plan_check(const st_plan_t *plan, void *stream, uint32_t *flags);
  *
  * Conventions: matrices are row-major with unit stride inside a row; ld* is
  * the number of elements between rows (at least the row's length; 0 for an
- * input: the same row for all).  All pointers are device memory, aligned to
+ * input: the same row for all).  All pointers are memory of the current
+ * device, and `stream` is one of its streams; pointers are aligned to
  * their itemsize only (16-byte aligned pointers and row strides take the
  * faster paths).  An output may be the very matrix of an input (same pointer,
  * stride and itemsize: in place); any other overlap gives undefined values.

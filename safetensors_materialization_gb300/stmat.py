@@ -856,6 +856,9 @@ class Outputs:
 
 
 # ------------------------------------------- operators on materialized tensors
+#
+# All operands of a call lie on one GPU, which the call makes current; without
+# `stream` it runs on that GPU's current stream.
 
 # The argument structs' layouts for struct.pack: one call packs a struct in a
 # quarter of the time that setting a ctypes structure's fields takes.
@@ -875,8 +878,8 @@ class _Ops:
         names = ("BF16", "F16", "F32", "F8_E4M3", "F8_E5M2")
         self.codes = {torch_dtype(n): DTYPES.index(n) for n in names}
         self.dsts = {n: (torch_dtype(n), DTYPES.index(n)) for n in names}
-        # 0.1 us; torch.cuda.current_stream() takes 11
-        self.stream = torch._C._cuda_getCurrentRawStream
+        # 0.1 us each; torch.cuda.current_stream() takes 11
+        self.stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p)
         self.rms_norm, self.gated_act, self.linear, self.linear_workspace = (
             call((n, lib())) for n in ("st_rms_norm", "st_gated_act", "st_linear", "st_linear_workspace"))
@@ -892,11 +895,25 @@ def _invalid(msg):
     return StmatError(1, msg)
 
 
-def _matrix(t, name):
-    """(address, elements between rows, rows, columns) of a tensor whose
-    leading dimensions are the rows (a vector: one row); no copy is made."""
+def _gpu(t, name):
+    """The number of the GPU that a call's first operand is on."""
     if not t.is_cuda:
         raise _invalid(f"{name} is not on the GPU")
+    return t.get_device()
+
+
+def _elsewhere(t, name, gpu):
+    if not t.is_cuda:
+        return _invalid(f"{name} is not on the GPU")
+    return _invalid(f"{name} is on GPU {t.get_device()}, the call's first operand on GPU {gpu}")
+
+
+def _matrix(t, name, gpu):
+    """(address, elements between rows, rows, columns) of a tensor on this GPU
+    whose leading dimensions are the rows (a vector: one row); no copy is
+    made."""
+    if t.get_device() != gpu:
+        raise _elsewhere(t, name, gpu)
     shape = t.shape
     if len(shape) == 2:
         rows, cols = shape
@@ -922,17 +939,17 @@ def _matrix(t, name):
     return t.data_ptr(), cols if rows <= 1 else ld, rows, cols
 
 
-def _vector(t, name, count, dtypes, codes, one=False):
+def _vector(t, name, gpu, count, dtypes, codes, one=False):
     """(address, entries, st_dtype) of a contiguous vector of `count` entries
-    (or, with `one`, of a single one)."""
+    (or, with `one`, of a single one) on this GPU."""
     n = t.numel()
     if (n != count and not (one and n == 1)) or not t.is_contiguous():
         raise _invalid(f"{name}: a contiguous tensor of {'1 or ' if one else ''}{count} entries is needed")
     code = codes.get(t.dtype)
     if code not in dtypes:
         raise StmatError(6, f"{name}: {t.dtype} is not one of {', '.join(DTYPES[d] for d in dtypes)}")
-    if not t.is_cuda:
-        raise _invalid(f"{name} is not on the GPU")
+    if t.get_device() != gpu:
+        raise _elsewhere(t, name, gpu)
     return t.data_ptr(), n, code
 
 
@@ -958,14 +975,16 @@ def _new(like, shape, dtype, ops):
 
 
 class _On:
-    """Runs a call on `stream` (None: torch's current stream): outputs are
+    """Runs a call on `stream`, one of its operands' GPU's: outputs are
     allocated there, and inputs stay allocated until its work is done."""
 
     __slots__ = ("ctx", "stream")
 
-    def __init__(self, torch, stream):
+    def __init__(self, torch, stream, gpu):
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
+            stream = torch.cuda.ExternalStream(stream, device=gpu)
+        elif stream.device_index != gpu:
+            raise _invalid(f"stream is one of GPU {stream.device_index}, the operands are on GPU {gpu}")
         self.stream, self.ctx = stream, torch.cuda.stream(stream)
 
     def run(self, fn, tensors):
@@ -986,31 +1005,35 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
     use instead.  Returns (y, scales or None, h in x's dtype, or None without
     a residual); y * scales[..., None] stands for the normed rows."""
     ops = _OPS or _ops()
+    gpu = _gpu(x, "x")
     if stream is not None:
-        return _On(ops.torch, stream).run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
-                                          (x, weight, residual, scale))
+        return _On(ops.torch, stream, gpu).run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
+                                               (x, weight, residual, scale))
+    if gpu != ops.device():
+        with ops.torch.cuda.device(gpu):
+            return rms_norm(x, weight, eps, residual, dst, scale)
     codes, shape, x_type = ops.codes, x.shape, x.dtype
-    px, ldx, rows, cols = _matrix(x, "x")
+    px, ldx, rows, cols = _matrix(x, "x", gpu)
     x_code = codes.get(x_type, -1)
     y_type, y_code = _dst(dst, x_type, ops)
     pw = pr = ph = ldr = ps = pss = 0
     w_code, h, scales = 10, None, None
     if weight is not None:
-        pw, _, w_code = _vector(weight, "weight", cols, _FLOATS, codes)
+        pw, _, w_code = _vector(weight, "weight", gpu, cols, _FLOATS, codes)
     if residual is not None:
         if residual.shape != shape or residual.dtype != x_type:
             raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, x: {tuple(shape)} {x_type}")
-        pr, ldr, _, _ = _matrix(residual, "residual")
+        pr, ldr, _, _ = _matrix(residual, "residual", gpu)
         h = _new(x, shape, x_type, ops)
         ph = h.data_ptr()
     y = _new(x, shape, y_type, ops)
     if scale is not None:
-        ps = _vector(scale, "scale", 1, _F32, codes)[0]
+        ps = _vector(scale, "scale", gpu, 1, _F32, codes)[0]
     elif y_code == _E4M3:
         scales = ops.empty(shape[:-1], dtype=ops.torch.float32, device=x.device)
         pss = scales.data_ptr()
     code = ops.rms_norm(_NORM_ARGS.pack(rows, cols, eps, x_code, w_code, y_code, px, ldx, pr, ldr, pw, ph, cols,
-                                        y.data_ptr(), cols, ps, pss), ops.stream(x.get_device()))
+                                        y.data_ptr(), cols, ps, pss), ops.stream(gpu))
     if code:
         _check(code)
     return y, scales, h
@@ -1022,25 +1045,29 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
     "none", "relu", "silu", "gelu" or "gelu_tanh"; dst and scale as for
     rms_norm.  Returns (y, scales or None)."""
     ops = _OPS or _ops()
+    gpu = _gpu(gate, "gate")
     if stream is not None:
-        return _On(ops.torch, stream).run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
+        return _On(ops.torch, stream, gpu).run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
+    if gpu != ops.device():
+        with ops.torch.cuda.device(gpu):
+            return gated_act(gate, up, act, dst, scale)
     shape, x_type = gate.shape, gate.dtype
-    pg, ldg, rows, cols = _matrix(gate, "gate")
+    pg, ldg, rows, cols = _matrix(gate, "gate", gpu)
     y_type, y_code = _dst(dst, x_type, ops)
     pu = ldu = ps = pss = 0
     scales = None
     if up is not None:
         if up.shape != shape or up.dtype != x_type:
             raise _invalid(f"up: {tuple(up.shape)} {up.dtype}, gate: {tuple(shape)} {x_type}")
-        pu, ldu, _, _ = _matrix(up, "up")
+        pu, ldu, _, _ = _matrix(up, "up", gpu)
     y = _new(gate, shape, y_type, ops)
     if scale is not None:
-        ps = _vector(scale, "scale", 1, _F32, ops.codes)[0]
+        ps = _vector(scale, "scale", gpu, 1, _F32, ops.codes)[0]
     elif y_code == _E4M3:
         scales = ops.empty(shape[:-1], dtype=ops.torch.float32, device=gate.device)
         pss = scales.data_ptr()
     code = ops.gated_act(_ACT_ARGS.pack(rows, cols, ACTS.get(act, -1), ops.codes.get(x_type, -1), y_code, pg, ldg, pu, ldu,
-                                        y.data_ptr(), cols, ps, pss), ops.stream(gate.get_device()))
+                                        y.data_ptr(), cols, ps, pss), ops.stream(gpu))
     if code:
         _check(code)
     return y, scales
@@ -1058,23 +1085,27 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     residual has y's shape and dtype.  out: the tensor to write (may be the
     residual); by default a new one."""
     ops = _OPS or _ops()
+    gpu = _gpu(x, "x")
     if stream is not None:
-        return _On(ops.torch, stream).run(lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
-                                          (x, weight, x_scale, w_scale, bias, residual, out))
+        return _On(ops.torch, stream, gpu).run(lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
+                                               (x, weight, x_scale, w_scale, bias, residual, out))
+    if gpu != ops.device():
+        with ops.torch.cuda.device(gpu):
+            return linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out)
     codes, x_type = ops.codes, x.dtype
-    px, ldx, m, k = _matrix(x, "x")
-    pw, ldw, n, wk = _matrix(weight, "weight")
+    px, ldx, m, k = _matrix(x, "x", gpu)
+    pw, ldw, n, wk = _matrix(weight, "weight", gpu)
     if wk != k or weight.dim() != 2:
         raise _invalid(f"x has rows of {k}, weight is {tuple(weight.shape)}")
     x_code = codes.get(x_type, -1)
     pxs = nxs = pws = nws = pb = pr = ldr = 0
     b_code = 11
     if x_scale is not None:
-        pxs, nxs, _ = _vector(x_scale, "x_scale", m, _F32, codes, True)
+        pxs, nxs, _ = _vector(x_scale, "x_scale", gpu, m, _F32, codes, True)
     if w_scale is not None:
-        pws, nws, _ = _vector(w_scale, "w_scale", n, _F32, codes, True)
+        pws, nws, _ = _vector(w_scale, "w_scale", gpu, n, _F32, codes, True)
     if bias is not None:
-        pb, _, b_code = _vector(bias, "bias", n, _FLOATS, codes)
+        pb, _, b_code = _vector(bias, "bias", gpu, n, _FLOATS, codes)
     shape = x.shape[:-1] + (n,)
     if out is None:
         y_type, y_code = _dst(dst, ops.torch.bfloat16 if x_code == _E4M3 else x_type, ops)
@@ -1085,11 +1116,11 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
         if out.shape != shape or (dst is not None and _dst(dst, None, ops)[0] != y_type):
             raise _invalid(f"out: {tuple(out.shape)} {y_type}, the product is {tuple(shape)} {dst or ''}")
         y_code = codes.get(y_type, -1)
-        py, ldy, _, _ = _matrix(out, "out")
+        py, ldy, _, _ = _matrix(out, "out", gpu)
     if residual is not None:
         if residual.shape != shape or residual.dtype != y_type:
             raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, y: {tuple(shape)} {y_type}")
-        pr, ldr, _, _ = _matrix(residual, "residual")
+        pr, ldr, _, _ = _matrix(residual, "residual", gpu)
     w_code, act = codes.get(weight.dtype, -1), ACTS.get(act, -1)
     args = (m, n, k, act, x_code, w_code, y_code, b_code, px, ldx, pw, ldw, pxs, nxs, pws, nws, pb, pr, ldr, py, ldy)
     space = size = 0
@@ -1103,7 +1134,7 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
         if size:
             workspace = ops.empty(size, dtype=ops.torch.uint8, device=x.device)
             space = workspace.data_ptr()
-    code = ops.linear(_LINEAR_ARGS.pack(*args, space, size), ops.stream(x.get_device()))
+    code = ops.linear(_LINEAR_ARGS.pack(*args, space, size), ops.stream(gpu))
     if code:
         _check(code)
     return out
