@@ -620,8 +620,10 @@ st_status st_plan_check(const st_plan_t *plan, void *stream, uint32_t *flags);
  * input: the same row for all).  All pointers are memory of the current
  * device, and `stream` is one of its streams; pointers are aligned to
  * their itemsize only (16-byte aligned pointers and row strides take the
- * faster paths).  An output may be the very matrix of an input (same pointer,
- * stride and itemsize: in place); any other overlap gives undefined values.
+ * faster paths).  An output of a row operator may be the very matrix of an
+ * input (same pointer, stride and itemsize: in place); any other overlap gives
+ * undefined values.  st_linear's y may be the very matrix of its residual; an
+ * overlap of y with another operand is refused (ST_E_INVAL).
  * Calls run on `stream` (a cudaStream_t; NULL is the legacy default stream)
  * without host synchronization or allocation, can be captured in a CUDA graph,
  * and give the same bits on every run.  Zero rows or columns:

@@ -58,6 +58,42 @@ st_status check_output(const char *op, st_dtype y, const float *scale, const flo
   return s != ST_OK ? s : check_vector(op, "scales", scales, ST_F32);
 }
 
+// The bytes of an operand: rows of `row` bytes, `pitch` apart.
+struct Bytes {
+  uintptr_t p;
+  int64_t rows, pitch, row;
+  uintptr_t end() const { return p + static_cast<uintptr_t>((rows - 1) * pitch + row); }
+};
+
+Bytes matrix_bytes(const void *p, int64_t ld, st_dtype dtype, int64_t rows, int64_t cols) {
+  const int64_t item = static_cast<int64_t>(st_dtype_size(dtype));
+  if (rows == 1 || ld == 0) return {reinterpret_cast<uintptr_t>(p), 1, 0, cols * item};
+  if (ld == cols) return {reinterpret_cast<uintptr_t>(p), 1, 0, rows * cols * item};
+  return {reinterpret_cast<uintptr_t>(p), rows, ld * item, cols * item};
+}
+Bytes array_bytes(const void *p, uint64_t bytes) { return {reinterpret_cast<uintptr_t>(p), 1, 0, static_cast<int64_t>(bytes)}; }
+
+// Whether they share a byte.  Column ranges of one buffer interleave without.
+bool overlap(const Bytes &a, const Bytes &b) {
+  if (a.end() <= b.p || b.end() <= a.p) return false;
+  if (a.rows > 1 && b.rows > 1 && a.pitch == b.pitch) {
+    // Where b's rows start between two of a's; the ranges meet, so some pair
+    // of rows is next to each other.
+    const int64_t d = b.p >= a.p ? static_cast<int64_t>((b.p - a.p) % static_cast<uintptr_t>(a.pitch))
+                                 : (a.pitch - static_cast<int64_t>((a.p - b.p) % static_cast<uintptr_t>(a.pitch))) % a.pitch;
+    return d < a.row || d > a.pitch - b.row;
+  }
+  const Bytes &few = a.rows <= b.rows ? a : b, &many = a.rows <= b.rows ? b : a;
+  for (int64_t i = 0; i < few.rows; ++i) {
+    const uintptr_t from = few.p + static_cast<uintptr_t>(i * few.pitch), to = from + static_cast<uintptr_t>(few.row);
+    // The first of the other's rows that ends beyond `from`.
+    const uintptr_t first_end = many.p + static_cast<uintptr_t>(many.row);
+    const int64_t j = first_end > from ? 0 : many.pitch ? static_cast<int64_t>((from - first_end) / static_cast<uintptr_t>(many.pitch)) + 1 : many.rows;
+    if (j < many.rows && many.p + static_cast<uintptr_t>(j * many.pitch) < to) return true;
+  }
+  return false;
+}
+
 #define ST_TRY(expr)                         \
   do {                                       \
     const st_status try_status = (expr);     \
@@ -92,6 +128,21 @@ st_status check_linear(const st_linear_args *a, bool *empty) {
   if (a->bias) ST_TRY(check_vector(op, "bias", a->bias, a->bias_dtype));
   if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->y_dtype, a->m, a->n, true));
   ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->m, a->n, false));
+  // Other tiles still read x, the weight and the vectors while the first are
+  // written; a residual's element is read by the thread that writes it in y.
+  const Bytes y = matrix_bytes(a->y, a->ldy, a->y_dtype, a->m, a->n);
+  auto apart = [&](const char *name, const Bytes &b) {
+    return overlap(y, b) ? set_error(ST_E_INVAL, "%s: y overlaps %s (it may be the residual, the very matrix, and no other operand)", op, name) : ST_OK;
+  };
+  if (a->k > 0) {
+    ST_TRY(apart("x", matrix_bytes(a->x, a->ldx, a->x_dtype, a->m, a->k)));
+    ST_TRY(apart("weight", matrix_bytes(a->w, a->ldw, a->w_dtype, a->n, a->k)));
+  }
+  if (a->x_scale) ST_TRY(apart("x_scale", array_bytes(a->x_scale, 4 * a->x_scale_count)));
+  if (a->w_scale) ST_TRY(apart("w_scale", array_bytes(a->w_scale, 4 * a->w_scale_count)));
+  if (a->bias) ST_TRY(apart("bias", array_bytes(a->bias, a->n * st_dtype_size(a->bias_dtype))));
+  if (a->residual && !(a->residual == a->y && (a->m == 1 || a->ldr == a->ldy)))
+    ST_TRY(apart("the residual in part", matrix_bytes(a->residual, a->ldr, a->y_dtype, a->m, a->n)));
   return ST_OK;
 }
 
@@ -151,6 +202,14 @@ st_status st_linear(const st_linear_args *a, void *stream) {
                      (long long)need, (unsigned long long)(a->workspace ? a->workspace_bytes : 0));
   if (need && reinterpret_cast<uintptr_t>(a->workspace) % 16)
     return set_error(ST_E_ALIGN, "st_linear: the workspace is not 16-byte aligned");
+  if (need) {
+    const Bytes space = array_bytes(a->workspace, static_cast<uint64_t>(need));
+    if (overlap(space, matrix_bytes(a->y, a->ldy, a->y_dtype, a->m, a->n)) ||
+        overlap(space, matrix_bytes(a->x, a->ldx, a->x_dtype, a->m, a->k)) ||
+        overlap(space, matrix_bytes(a->w, a->ldw, a->w_dtype, a->n, a->k)) ||
+        (a->residual && overlap(space, matrix_bytes(a->residual, a->ldr, a->y_dtype, a->m, a->n))))
+      return set_error(ST_E_INVAL, "st_linear: the workspace overlaps an operand");
+  }
   return launch_linear(*a, stream);
 }
 

@@ -1082,8 +1082,8 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     with dst="F8_E4M3") with an F8_E4M3 or F8_E5M2 weight.  x_scale: F32, one
     entry or one per row; w_scale: F32, one entry or one per row of weight.
     dst: "BF16", "F16" or "F32" (default: x's dtype, BF16 for 8-bit x);
-    residual has y's shape and dtype.  out: the tensor to write (may be the
-    residual); by default a new one."""
+    residual has y's shape and dtype.  out: the tensor to write, which may be
+    the residual itself but overlap no other operand; by default a new one."""
     ops = _OPS or _ops()
     gpu = _gpu(x, "x")
     if stream is not None:

@@ -1,6 +1,8 @@
 """Calls at the edges of what the operators take: which GPU they run on (with
-stand-ins for tensors of several GPUs, on the CPU)."""
+stand-ins for tensors of several GPUs, on the CPU), operands that overlap."""
 import contextlib
+import ctypes as C
+import random
 import types
 
 import pytest
@@ -141,3 +143,98 @@ def test_a_stream_of_another_gpu_is_refused(stmat, machine):
             call(Stream(100, 0))
         assert e.value.status == "ST_E_INVAL" and "GPU" in str(e.value)
     assert machine.calls == []
+
+
+# ------------------------------------------------------ overlapping operands
+
+X, W, Y = 1 << 20, 2 << 20, 3 << 20
+
+
+def linear_args(stmat, **kw):
+    """A BF16 product of 8 tokens of 16 with a 16 x 16 weight."""
+    a = stmat.LinearArgs(m=8, n=16, k=16, act=0, x_dtype=10, w_dtype=10, y_dtype=10, bias_dtype=10, x=X, ldx=16, w=W,
+                         ldw=16, y=Y, ldy=16)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+# y over x (all of it, its last row, from its middle, a strided one), over the
+# weight, the vectors, and over a part of the residual.
+OVERLAPS = [
+    dict(y=X), dict(y=X + 7 * 32), dict(y=X - 7 * 32), dict(y=X + 16), dict(y=X, ldy=24), dict(y=X - 100 * 2, ldy=40),
+    dict(y=X + 2, ldx=40, ldy=40), dict(y=X + 15 * 2, ldx=40, ldy=40), dict(y=X - 15 * 2, ldx=40, ldy=40),
+    dict(y=X + 40 * 2 * 7 + 15 * 2, ldx=40, ldy=40), dict(y=X, m=1, ldy=0), dict(y=X, ldx=0), dict(y=X - 7 * 32, ldx=0),
+    dict(y=W), dict(y=W + 15 * 32), dict(y=W, m=16), dict(y=W - 8 * 32 + 2), dict(y=W, w_dtype=13, x_dtype=13, y_dtype=11),
+    dict(x_scale=Y, x_scale_count=1), dict(x_scale=Y + 252, x_scale_count=1), dict(w_scale=Y - 60, w_scale_count=16),
+    dict(bias=Y + 128), dict(bias=Y - 30), dict(bias=Y + 16 * 2, ldy=20, n=18),
+    dict(residual=Y + 2, ldr=16), dict(residual=Y, ldr=18), dict(residual=Y, ldr=0), dict(residual=Y - 32, ldr=16),
+]
+# Neighbours, columns of one buffer between one another, operands of length 0,
+# and the residual itself.
+APART = [
+    dict(y=X + 8 * 32), dict(y=X - 8 * 32), dict(y=W + 16 * 32), dict(y=X + 32, ldx=32, ldy=32),
+    dict(y=X + 16 * 2, ldx=40, ldy=40), dict(y=X + 24 * 2, ldx=40, ldy=40), dict(y=X - 16 * 2, ldx=40, ldy=40),
+    dict(y=X + 32, ldx=32, ldy=64), dict(y=X, k=0), dict(y=X + 32, ldx=0), dict(bias=Y + 8 * 32), dict(bias=Y - 32),
+    dict(bias=Y + 16 * 2, ldy=32), dict(x_scale=Y + 8 * 32, x_scale_count=8), dict(w_scale=Y - 64, w_scale_count=16),
+    dict(residual=Y, ldr=16), dict(residual=Y, ldr=99, m=1), dict(residual=Y + 32, ldr=32, ldy=32),
+]
+
+
+@pytest.mark.parametrize("kw", OVERLAPS, ids=range(len(OVERLAPS)))
+def test_linear_refuses_y_over_another_operand(stmat, kw):
+    """Tiles that are written would change what other tiles still read.  (On
+    the host, before anything is queued: the addresses are made up.)"""
+    a, need = linear_args(stmat, **kw), C.c_uint64()
+    for code in (stmat.lib().st_linear(C.byref(a), None), stmat.lib().st_linear_workspace(C.byref(a), C.byref(need))):
+        assert stmat.STATUS[code] == "ST_E_INVAL"
+        assert "overlaps" in stmat.lib().st_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", APART, ids=range(len(APART)))
+def test_linear_takes_neighbours_and_the_residual(stmat, kw):
+    need = C.c_uint64()
+    assert stmat.STATUS[stmat.lib().st_linear_workspace(C.byref(linear_args(stmat, **kw)), C.byref(need))] == "ST_OK"
+
+
+def test_linear_overlaps_against_every_byte(stmat):
+    """Random placements of y and x against the sets of their bytes."""
+    rng, need, seen = random.Random(3), C.c_uint64(), set()
+    for _ in range(4000):
+        m, n, k = rng.randint(1, 6), rng.randint(1, 9), rng.randint(1, 9)
+        ldx, ldy = k + rng.choice([0, 0, 1, 5, 12]), n + rng.choice([0, 0, 1, 5, 12])
+        if rng.random() < 0.3:
+            ldx = ldy = max(ldx, ldy)
+        y = X + 2 * rng.randint(-130, 130)
+        got = stmat.lib().st_linear_workspace(C.byref(linear_args(stmat, m=m, n=n, k=k, ldx=ldx, ldw=k, y=y, ldy=ldy)),
+                                              C.byref(need))
+        meet = {X + 2 * (i * ldx + j) for i in range(m) for j in range(k)} & {
+            y + 2 * (i * ldy + j) for i in range(m) for j in range(n)}
+        assert stmat.STATUS[got] == ("ST_E_INVAL" if meet else "ST_OK"), (m, n, k, ldx, ldy, y - X)
+        seen.add(bool(meet))
+    assert seen == {True, False}
+
+
+def test_linear_refuses_a_workspace_over_an_operand(stmat):
+    base = dict(ldx=17, ldw=17, ldy=16, residual=4 << 20, ldr=16)
+    a, need = linear_args(stmat, **base), C.c_uint64()
+    stmat._check(stmat.lib().st_linear_workspace(C.byref(a), C.byref(need)))
+    for at in (X, X + 256, W, W + 512, Y - 16, (4 << 20) + 240):
+        a = linear_args(stmat, workspace=at, workspace_bytes=need.value, **base)
+        assert stmat.STATUS[stmat.lib().st_linear(C.byref(a), None)] == "ST_E_INVAL"
+        assert "workspace" in stmat.lib().st_last_error().decode()
+
+
+@gpu
+def test_linear_binding_refuses_out_over_x_and_weight(stmat):
+    buf = torch.zeros(64, 96, dtype=torch.bfloat16, device="cuda")
+    x, w = buf[:, :32], torch.eye(32, dtype=torch.bfloat16, device="cuda")
+    x.copy_(torch.arange(64 * 32).view(64, 32) % 250)
+    sq = torch.zeros(32, 32, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: stmat.linear(x, w, out=x), lambda: stmat.linear(x, w, out=buf[:, 31:63]),
+                 lambda: stmat.linear(sq, w, out=w), lambda: stmat.linear(sq, w, out=sq)):
+        with pytest.raises(stmat.StmatError) as e:
+            call()
+        assert e.value.status == "ST_E_INVAL"
+    # columns of one buffer
+    assert torch.equal(stmat.linear(x, w, out=buf[:, 32:64]), x)
