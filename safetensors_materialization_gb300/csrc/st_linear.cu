@@ -424,7 +424,8 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = v[j] * xs * ws[j] + bias[j];
-    activate(v, a.act);
+    if (a.y_dtype == ST_F32) activate<true>(v, a.act);
+    else activate<false>(v, a.act);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] += old[j], old[j] = next[j];
     xs = next_xs;
@@ -631,7 +632,8 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs &a, int t) {
 }
 
 // kShared: one tile a cluster, its sum over k shared by the cluster's pairs.
-template <bool kEight, bool kShared>
+// kF32: y's type, with an activation (exact_act).
+template <bool kEight, bool kShared, bool kF32>
 __global__ void __launch_bounds__(kDenseThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ LinArgs a) {
@@ -723,7 +725,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
       }
     }
-    activate(v, a.act);
+    activate<kF32>(v, a.act);
     if (wide) {
       if (row) {
         if (a.residual && a.y_dtype != ST_F32) {
@@ -941,12 +943,12 @@ st_status device(int *index, const Device **out) {
     if (s != ST_OK) return s;
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(dense_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem + 1024);
+      e = cudaFuncSetAttribute(dense_kernel<true, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem + 1024);
     for (int pairs = 1; pairs <= kMaxPairs && e == cudaSuccess; pairs *= 2) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       cluster_config(&cfg, attr, 2 * pairs, kDenseThreads, kDenseSmem + 1024, 2 * pairs);
-      e = cudaOccupancyMaxActiveClusters(&d.clusters[pairs], dense_kernel<true, true>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&d.clusters[pairs], dense_kernel<true, true, false>, &cfg);
     }
     if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_linear: counting SMs and clusters: %s", cudaGetErrorName(e));
     d.err = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(scratch) + kStaticErrOffset);
@@ -1044,16 +1046,16 @@ st_status launch_split(LinArgs &a, const CUtensorMap &wmap, const CUtensorMap &x
   return e == cudaSuccess ? ST_OK : launch_error(a, e);
 }
 
-template <bool kEight, bool kShared>
+template <bool kEight, bool kShared, bool kF32>
 st_status launch_dense(LinArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, int dev, int sms, cudaStream_t st) {
   // As many stages as fit: a narrow tile's are smaller, and need more of them
   // under way to cover the memory's latency.
   const int stage_bytes = (128 + a.tile_n / 2) * kStageK;
   a.stages = kDenseSmem / stage_bytes < kMaxStages ? kDenseSmem / stage_bytes : kMaxStages;
-  cudaError_t e = allow_smem<dense_kernel<kEight, kShared>>(dev, kDenseSmem + 1024);
+  cudaError_t e = allow_smem<dense_kernel<kEight, kShared, kF32>>(dev, kDenseSmem + 1024);
   if (e == cudaSuccess) {
     const int pairs = sms / 2, tiles = a.m_tiles * a.n_tiles;
-    e = launch(dense_kernel<kEight, kShared>, 2 * (kShared ? tiles * a.splits : std::min(tiles, pairs)), kDenseThreads,
+    e = launch(dense_kernel<kEight, kShared, kF32>, 2 * (kShared ? tiles * a.splits : std::min(tiles, pairs)), kDenseThreads,
                a.stages * stage_bytes + 1024, 2 * a.splits, st, xmap, wmap, a);
   }
   return e == cudaSuccess ? ST_OK : launch_error(a, e);
@@ -1155,9 +1157,14 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
     s = encode(&xmap, a.x, p.k, item, 128);
     if (s == ST_OK) s = encode(&wmap, a.w, p.k, item, a.tile_n / 2);
     if (s != ST_OK) return s;
-    if (a.splits > 1)
-      return a.eight ? launch_dense<true, true>(a, xmap, wmap, dev, sms, st) : launch_dense<false, true>(a, xmap, wmap, dev, sms, st);
-    return a.eight ? launch_dense<true, false>(a, xmap, wmap, dev, sms, st) : launch_dense<false, false>(a, xmap, wmap, dev, sms, st);
+    auto with = [](bool yes, auto &&f) { return yes ? f(std::true_type{}) : f(std::false_type{}); };
+    return with(a.eight, [&](auto eight) {
+      return with(a.splits > 1, [&](auto shared) {
+        return with(exact_act(a.act, a.y_dtype), [&](auto f32) {
+          return launch_dense<decltype(eight)::value, decltype(shared)::value, decltype(f32)::value>(a, xmap, wmap, dev, sms, st);
+        });
+      });
+    });
   }
 
   a.vec = aligned(4 * out);

@@ -116,43 +116,59 @@ __device__ __forceinline__ float fast_rcp(float v) {
   return d;
 }
 
-// Activations, in 5 (silu), 7 (gelu_tanh) and 14 (gelu) operations a value:
-// with the library's exp, tanh and erf and an exact division the gated
-// activation ran at half the memory's rate, and a product's readout took 330
-// us where it now takes 100 (3814 x 6612 x 1723 E4M3, gelu_tanh).  Their error,
-// (|v| + 4) 2^-23 of the result, is a binary32 rounding of the exponent's
-// argument; gelu's is 1e-7 |v| besides.
-//   silu:      v / (1 + exp(-v))
-//   gelu_tanh: (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), u = sqrt(2 / pi) (v + 0.044715 v^3)
-//   gelu:      v Phi(v), Phi(-|v|) = erfc(x) / 2 with x = |v| / sqrt(2) by
-//              Abramowitz and Stegun, Handbook of Mathematical Functions,
-//              7.1.26: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) with t = 1 /
-//              (1 + p x), off by at most 1.5e-7.
+// Activations.  For outputs of 16 and 8 bits they are formed in 5 (silu), 7
+// (gelu_tanh) and 17 (gelu) operations a value: with the library's exp, tanh
+// and erf and an exact division the gated activation ran at half the memory's
+// rate, and a product's readout took 330 us where it now takes 100 (3814 x 6612
+// x 1723 E4M3, gelu_tanh).  With e the exponential's argument they are within
+// (2 |e| + 6) 2^-23 of the value, mostly the binary32 rounding of e, and 0
+// where exp(|e|) is beyond 2^126.
+//   silu:      v / (1 + exp(-v)), e = v
+//   gelu_tanh: (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), u = sqrt(2 / pi) (v + 0.044715 v^3), e = 2u
+//   gelu:      v Phi(v), e = v^2 / 2.  Phi(-|v|) exp(v^2 / 2) is smooth in t =
+//              1 / (1 + 0.304 |v|); t times a polynomial of degree 7 in t, fitted
+//              to it for the least largest relative error over |v| <= 13.5 (by
+//              Lawson's reweighted least squares), is off by at most 8.4e-8 of it.
+// For F32 outputs (kF32) the library's exp and normal distribution and an exact
+// division: silu within 4 2^-23 of the value, gelu 7, gelu_tanh 2 |e| + 4.  A
+// negative v takes v exp(e) / (1 + exp(e)), whose exponential does not overflow.
 constexpr float kLog2e = 1.44269504f;
+constexpr float kTanh1 = 1.59576912f, kTanh3 = 0.0713548128f;  // 2 sqrt(2 / pi), that times 0.044715
 __device__ __forceinline__ float gelu(float v) {
-  const float t = fast_rcp(fmaf(fabsf(v), 0.3275911f * 0.70710678f, 1.0f));
-  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-  q = fmaf(t, q, 0.5f * 1.421413741f);
-  q = fmaf(t, q, 0.5f * -0.284496736f);
-  q = fmaf(t, q, 0.5f * 0.254829592f);
+  const float t = fast_rcp(fmaf(fabsf(v), 0.304f, 1.0f));
+  float q = fmaf(t, 0.0368598551f, -0.155304030f);
+  q = fmaf(t, q, 0.192196801f);
+  q = fmaf(t, q, -0.0431365334f);
+  q = fmaf(t, q, 0.123556770f);
+  q = fmaf(t, q, 0.102421626f);
+  q = fmaf(t, q, 0.122170880f);
+  q = fmaf(t, q, 0.121234670f);
   q = q * t * fast_exp2(v * v * (-0.5f * kLog2e));
   return v * (v < 0.0f ? q : 1.0f - q);
 }
-template <st_act A>
+// v / (1 + exp(-e)) for an e of v's sign.
+__device__ __forceinline__ float gated_exactly(float v, float e) {
+  const float x = expf(-fabsf(e));
+  return (v < 0.0f ? v * x : v) / (1.0f + x);
+}
+template <bool kF32, st_act A>
 __device__ __forceinline__ float activate1(float v) {
   if constexpr (A == ST_ACT_RELU) return v < 0.0f ? 0.0f : v;
+  else if constexpr (kF32 && A == ST_ACT_SILU) return gated_exactly(v, v);
+  else if constexpr (kF32 && A == ST_ACT_GELU) return v * normcdff(v);
+  else if constexpr (kF32 && A == ST_ACT_GELU_TANH) return gated_exactly(v, v * fmaf(v * v, kTanh3, kTanh1));
   else if constexpr (A == ST_ACT_SILU) return v * fast_rcp(1.0f + fast_exp2(-kLog2e * v));
   else if constexpr (A == ST_ACT_GELU) return gelu(v);
   else if constexpr (A == ST_ACT_GELU_TANH)
-    return v * fast_rcp(1.0f + fast_exp2(v * fmaf(v * v, -1.59576912f * 0.044715f * kLog2e, -1.59576912f * kLog2e)));
+    return v * fast_rcp(1.0f + fast_exp2(v * fmaf(v * v, -kTanh3 * kLog2e, -kTanh1 * kLog2e)));
   else return v;
 }
 
-template <int N>
+template <bool kF32, int N>
 __device__ __forceinline__ void activate(float (&v)[N], st_act act) {
   auto each = [&](auto tag) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = activate1<decltype(tag)::value>(v[i]);
+    for (int i = 0; i < N; ++i) v[i] = activate1<kF32, decltype(tag)::value>(v[i]);
   };
   switch (act) {
     case ST_ACT_RELU: return each(std::integral_constant<st_act, ST_ACT_RELU>{});
@@ -162,6 +178,9 @@ __device__ __forceinline__ void activate(float (&v)[N], st_act act) {
     default: return;
   }
 }
+
+// Whether a call's activation is one of those that differ for F32 outputs.
+inline bool exact_act(st_act act, st_dtype y_dtype) { return y_dtype == ST_F32 && act > ST_ACT_RELU; }
 
 // A kernel launched by launch() may start while the one before it in the
 // stream still runs (programmatic dependent launch), so that its start-up

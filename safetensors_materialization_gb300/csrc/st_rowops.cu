@@ -32,6 +32,10 @@ constexpr int kRowsPerBlock = 8;  // rows of one warp each
 // within 1 % from 38 to 228 rows, slower from 456 rows of 48 KiB on).
 constexpr int kAhead = 128;
 
+// The operators: the norm, the gated activation, and that with an F32 output
+// (exact_act).
+enum Op { kNormOp, kActOp, kActF32Op };
+
 // The largest block of a row kernel: its registers hold NV vectors a thread.
 constexpr int block_threads(int nv) { return nv >= 4 ? 512 : kMaxThreads; }
 
@@ -81,10 +85,10 @@ struct Factor {
 };
 
 // The row's factors from its statistics; writes the row's scale.
-template <bool kNorm>
+template <Op kOp>
 __device__ __forceinline__ Factor row_factor(const RowArgs &a, Stat s, int64_t row, bool first) {
   Factor f{1.0f, 1.0f};
-  if (kNorm) f.rstd = rsqrtf(s.sum / static_cast<float>(a.cols) + a.eps);
+  if (kOp == kNormOp) f.rstd = rsqrtf(s.sum / static_cast<float>(a.cols) + a.eps);
   if (a.y_dtype != ST_F8_E4M3) return f;
   float scale;
   if (a.scales) {
@@ -97,9 +101,9 @@ __device__ __forceinline__ Factor row_factor(const RowArgs &a, Stat s, int64_t r
   return f;
 }
 
-template <bool kNorm>
+template <Op kOp>
 __device__ __forceinline__ float scaled(float v, Factor f) {
-  return (kNorm ? v * f.rstd : v) * f.inv;
+  return (kOp == kNormOp ? v * f.rstd : v) * f.inv;
 }
 
 template <class T>
@@ -118,13 +122,13 @@ __device__ __forceinline__ void store_part(void *base, st_dtype dtype, int64_t a
 // The values before the row's factors (h w, or z) of V elements at column c,
 // from the elements as read, adding to the statistics and writing h.  W: the
 // weight's type; whole: the row has all of the elements.
-template <class T, class W, int V, bool kSkew, bool kNorm, bool kWrite>
+template <class T, class W, int V, bool kSkew, Op kOp, bool kWrite>
 __device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c, bool whole, const Raw<T, V> &x,
                                            const Raw<T, V> &r, float (&v)[V], Stat &s) {
   unpack(x, v);
   float o[V];
   if (a.r) unpack(r, o);
-  if constexpr (kNorm) {
+  if constexpr (kOp == kNormOp) {
     if (a.r) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] += o[i];
@@ -147,7 +151,7 @@ __device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c,
       for (int i = 0; i < V; ++i) v[i] *= o[i];
     }
   } else {
-    activate(v, a.act);
+    activate<kOp == kActF32Op>(v, a.act);
     if (a.r) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= o[i];
@@ -184,7 +188,7 @@ __device__ __forceinline__ Raw<T, V> row_part(const void *p, int64_t at, int c, 
 // kSkew: rows start anywhere; the accesses are aligned ones around the row of
 // x, whose first and last may hold fewer of its elements, and of the other
 // matrices where they start at the same place modulo V, else single elements.
-template <class T, int V, int NV, bool kSkew, bool kNorm, bool kWarpRow>
+template <class T, int V, int NV, bool kSkew, Op kOp, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(NV)) row_kernel(const RowArgs a) {
   const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5) : int64_t(blockIdx.x);
   const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x;
@@ -217,22 +221,22 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
   if (a.r) read(r, a.r, a.ldr, a.r_same);
   float v[NV][V];
   Stat s{0.0f, 0.0f};
-  with_type(kNorm ? a.w_dtype : kDtype<T>, [&](auto zero) {
+  with_type(kOp == kNormOp ? a.w_dtype : kDtype<T>, [&](auto zero) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = column(i);
-      if (c < a.cols) row_values<T, decltype(zero), V, kSkew, kNorm, true>(a, row, c, whole(c), x[i], r[i], v[i], s);
+      if (c < a.cols) row_values<T, decltype(zero), V, kSkew, kOp, true>(a, row, c, whole(c), x[i], r[i], v[i], s);
     }
   });
   s = kWarpRow ? warp_stat(s) : block_stat(s);
-  const Factor f = row_factor<kNorm>(a, s, row, t == 0);
+  const Factor f = row_factor<kOp>(a, s, row, t == 0);
   auto write = [&](st_dtype dtype) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = column(i);
       if (c < a.cols) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = scaled<kNorm>(v[i][j], f);
+        for (int j = 0; j < V; ++j) v[i][j] = scaled<kOp>(v[i][j], f);
         if (whole(c) && (!kSkew || a.y_same)) store_any<V>(a.y, dtype, row * a.ldy + c, v[i]);
         else store_part<V>(a.y, dtype, row * a.ldy + c, c, a.cols, v[i]);
       }
@@ -247,41 +251,41 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
 // A row too long for registers: the second pass reads the inputs again (each
 // thread its own elements, so in-place outputs are read before they are
 // written; h is written in the second pass).
-template <class T, int V, bool kNorm>
+template <class T, int V, Op kOp>
 __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) {
   const int64_t row = blockIdx.x;
   wait_for_previous();
   let_next_start();
   Stat s{0.0f, 0.0f}, unused{0.0f, 0.0f};
-  with_type(kNorm ? a.w_dtype : kDtype<T>, [&](auto zero) {
+  with_type(kOp == kNormOp ? a.w_dtype : kDtype<T>, [&](auto zero) {
     using W = decltype(zero);
     Raw<T, V> x, r;
     float v[V];
     for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
       x = row_read<T, V>(a.x, row * a.ldx + c);
       if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
-      row_values<T, W, V, false, kNorm, false>(a, row, static_cast<int>(c), true, x, r, v, s);
+      row_values<T, W, V, false, kOp, false>(a, row, static_cast<int>(c), true, x, r, v, s);
     }
     s = block_stat(s);
-    const Factor f = row_factor<kNorm>(a, s, row, threadIdx.x == 0);
+    const Factor f = row_factor<kOp>(a, s, row, threadIdx.x == 0);
     for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
       x = row_read<T, V>(a.x, row * a.ldx + c);
       if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
-      row_values<T, W, V, false, kNorm, true>(a, row, static_cast<int>(c), true, x, r, v, unused);
+      row_values<T, W, V, false, kOp, true>(a, row, static_cast<int>(c), true, x, r, v, unused);
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = scaled<kNorm>(v[j], f);
+      for (int j = 0; j < V; ++j) v[j] = scaled<kOp>(v[j], f);
       store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v);
     }
   });
 }
 
 // threads 0: a warp per row.
-template <class T, int V, int NV, bool kSkew, bool kNorm>
+template <class T, int V, int NV, bool kSkew, Op kOp>
 cudaError_t launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
   if (threads)
-    return launch(row_kernel<T, V, NV, kSkew, kNorm, false>, static_cast<unsigned>(a.rows), threads, 0, 1, st, a);
+    return launch(row_kernel<T, V, NV, kSkew, kOp, false>, static_cast<unsigned>(a.rows), threads, 0, 1, st, a);
   if constexpr (NV <= 4)
-    return launch(row_kernel<T, V, NV, kSkew, kNorm, true>, static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
+    return launch(row_kernel<T, V, NV, kSkew, kOp, true>, static_cast<unsigned>((a.rows + kRowsPerBlock - 1) / kRowsPerBlock),
                   32 * kRowsPerBlock, 0, 1, st, a);
   return cudaErrorInvalidValue;
 }
@@ -291,20 +295,20 @@ cudaError_t launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
 // rows for that, blocks of 1024, the shortest way through one row.  A warp
 // takes a short row alone (16384 x 333 F16 norm with residual to 8 bits 16.5
 // us; in blocks of two warps 19.4).
-template <class T, int V, bool kSkew, bool kNorm>
+template <class T, int V, bool kSkew, Op kOp>
 cudaError_t launch_typed(const RowArgs &a, cudaStream_t st) {
   const int64_t accesses = kSkew ? (a.cols + 2 * V - 2) / V : a.cols / V;
   const int64_t target = a.rows <= 256 ? kMaxThreads : 256;
   constexpr int kMost = V == 8 ? 4 : 8;
   auto threads = [&](int nv) { return static_cast<int>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
-  if (accesses <= 32) return launch_rows<T, V, 1, kSkew, kNorm>(a, 0, st);
-  if (accesses <= 64 && a.rows > 256) return launch_rows<T, V, 2, kSkew, kNorm>(a, 0, st);
-  if (accesses <= 128 && a.rows > 256) return launch_rows<T, V, 4, kSkew, kNorm>(a, 0, st);
-  if (accesses <= target) return launch_rows<T, V, 1, kSkew, kNorm>(a, threads(1), st);
-  if (accesses <= 2 * target) return launch_rows<T, V, 2, kSkew, kNorm>(a, threads(2), st);
-  if (accesses <= 4 * block_threads(4)) return launch_rows<T, V, 4, kSkew, kNorm>(a, threads(4), st);
-  if (accesses <= kMost * block_threads(kMost)) return launch_rows<T, V, kMost, kSkew, kNorm>(a, threads(kMost), st);
-  return launch(row_loop_kernel<T, kSkew ? 1 : V, kNorm>, static_cast<unsigned>(a.rows), kMaxThreads, 0, 1, st, a);
+  if (accesses <= 32) return launch_rows<T, V, 1, kSkew, kOp>(a, 0, st);
+  if (accesses <= 64 && a.rows > 256) return launch_rows<T, V, 2, kSkew, kOp>(a, 0, st);
+  if (accesses <= 128 && a.rows > 256) return launch_rows<T, V, 4, kSkew, kOp>(a, 0, st);
+  if (accesses <= target) return launch_rows<T, V, 1, kSkew, kOp>(a, threads(1), st);
+  if (accesses <= 2 * target) return launch_rows<T, V, 2, kSkew, kOp>(a, threads(2), st);
+  if (accesses <= 4 * block_threads(4)) return launch_rows<T, V, 4, kSkew, kOp>(a, threads(4), st);
+  if (accesses <= kMost * block_threads(kMost)) return launch_rows<T, V, kMost, kSkew, kOp>(a, threads(kMost), st);
+  return launch(row_loop_kernel<T, kSkew ? 1 : V, kOp>, static_cast<unsigned>(a.rows), kMaxThreads, 0, 1, st, a);
 }
 
 // Where rows start, in elements modulo an access of V.  Contiguous rows of an
@@ -319,13 +323,13 @@ Place place(const void *p, int64_t ld, st_dtype dtype, int v) {
   return {static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / st_dtype_size(dtype) % v), ld % v};
 }
 
-template <class T, bool kNorm>
+template <class T, Op kOp>
 cudaError_t launch_layout(const RowArgs &a, bool aligned, cudaStream_t st) {
   constexpr int V = sizeof(T) == 4 ? 4 : 8;
-  return aligned ? launch_typed<T, V, false, kNorm>(a, st) : launch_typed<T, V, true, kNorm>(a, st);
+  return aligned ? launch_typed<T, V, false, kOp>(a, st) : launch_typed<T, V, true, kOp>(a, st);
 }
 
-template <bool kNorm>
+template <Op kOp>
 st_status launch_op(RowArgs &a, st_dtype x_dtype, void *stream, const char *op) {
   const int v = x_dtype == ST_F32 ? 4 : 8;
   const Place x = place(a.x, a.ldx, x_dtype, v), y = place(a.y, a.ldy, a.y_dtype, v);
@@ -334,9 +338,9 @@ st_status launch_op(RowArgs &a, st_dtype x_dtype, void *stream, const char *op) 
   const bool aligned = a.cols % v == 0 && x.aligned() && a.r_same && a.h_same && a.y_same &&
                        place(a.w, 0, a.w_dtype, v).aligned();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = x_dtype == ST_BF16  ? launch_layout<__nv_bfloat16, kNorm>(a, aligned, st)
-                        : x_dtype == ST_F16 ? launch_layout<__half, kNorm>(a, aligned, st)
-                                            : launch_layout<float, kNorm>(a, aligned, st);
+  const cudaError_t e = x_dtype == ST_BF16  ? launch_layout<__nv_bfloat16, kOp>(a, aligned, st)
+                        : x_dtype == ST_F16 ? launch_layout<__half, kOp>(a, aligned, st)
+                                            : launch_layout<float, kOp>(a, aligned, st);
   if (e != cudaSuccess)
     return set_error(ST_E_CUDA, "%s launch (%lld rows): %s: %s", op, (long long)a.rows, cudaGetErrorName(e),
                      cudaGetErrorString(e));
@@ -352,7 +356,7 @@ st_status launch_rms_norm(const st_rms_norm_args &p, void *stream) {
   a.scale = p.scale; a.scales = p.scales;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
   a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.weight ? p.w_dtype : p.x_dtype; a.y_dtype = p.y_dtype;
-  return launch_op<true>(a, p.x_dtype, stream, "st_rms_norm");
+  return launch_op<kNormOp>(a, p.x_dtype, stream, "st_rms_norm");
 }
 
 st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
@@ -362,7 +366,8 @@ st_status launch_gated_act(const st_gated_act_args &p, void *stream) {
   a.scale = p.scale; a.scales = p.scales;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
   a.act = p.act; a.w_dtype = p.x_dtype; a.y_dtype = p.y_dtype;
-  return launch_op<false>(a, p.x_dtype, stream, "st_gated_act");
+  return exact_act(p.act, p.y_dtype) ? launch_op<kActF32Op>(a, p.x_dtype, stream, "st_gated_act")
+                                     : launch_op<kActOp>(a, p.x_dtype, stream, "st_gated_act");
 }
 
 }  // namespace stmat

@@ -1,7 +1,9 @@
 """Calls at the edges of what the operators take: which GPU they run on (with
-stand-ins for tensors of several GPUs, on the CPU), operands that overlap."""
+stand-ins for tensors of several GPUs, on the CPU), operands that overlap,
+activations far out."""
 import contextlib
 import ctypes as C
+import math
 import random
 import types
 
@@ -238,3 +240,108 @@ def test_linear_binding_refuses_out_over_x_and_weight(stmat):
         assert e.value.status == "ST_E_INVAL"
     # columns of one buffer
     assert torch.equal(stmat.linear(x, w, out=buf[:, 32:64]), x)
+
+
+# -------------------------------------------------------------- activations
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -149}
+ACTS = ["silu", "gelu", "gelu_tanh"]
+
+
+def act64(v, act):
+    """(act(v), |e|): the value in 64 bits and the size of its exponential's
+    argument."""
+    if act == "gelu":
+        # erfc: torch's ndtr is 1 + erf, which keeps no digits far below 0
+        return v * torch.special.erfc(-v * math.sqrt(0.5)) / 2, v * v / 2
+    e = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    return v * torch.special.expit(e), e.abs()
+
+
+def act_error(v, act, dtype):
+    """(act(v), bound of the error), from the header's: relative to the value,
+    then its rounding to dtype.  Below binary32's normal range the bound is
+    absolute: an exponential there is off by half a unit of 2^-149 and the
+    gate's at most 2^7 of them (F32), or 0 from 2^-126 on."""
+    want, e = act64(v, act)
+    far = 2.0 ** -142 if dtype == torch.float32 else 2.0 ** -126 * v.abs()
+    if dtype != torch.float32:
+        own = 2 * e + 6
+    else:
+        own = {"silu": 4, "gelu": 7}.get(act, 2 * e + 4)
+    own = own * 2.0 ** -23 * want.abs()
+    return want, own + U[dtype] * (want.abs() + own) + far + TINY[dtype]
+
+
+def far_and_near():
+    """Arguments of either sign from 2^-30 to 120, dense where the activations
+    bend."""
+    v = torch.cat([torch.linspace(-14, 14, 1 << 19), torch.linspace(-120, 120, 1 << 16),
+                   torch.logspace(-30, 0, 1 << 15, base=2.0), -torch.logspace(-30, 0, 1 << 15, base=2.0)])
+    return v[torch.randperm(v.numel(), generator=torch.Generator().manual_seed(1))].cuda().view(-1, 1024)
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dst", ["F32", "BF16", "F16"])
+def test_activations_relative_to_their_value(stmat, act, dst):
+    v = far_and_near()
+    y, _ = stmat.gated_act(v, act=act, dst=dst)
+    want, tol = act_error(v.double(), act, y.dtype)
+    off = (y.double() - want).abs() / tol
+    assert (off <= 1).all(), (off.max().item(), v.flatten()[off.argmax()].item())
+    # halves of an odd length, with up
+    both = v.reshape(-1)[:1022 * 400].view(400, 1022)
+    gate, up = both[:, :511], both[:, 511:]
+    y, _ = stmat.gated_act(gate, up, act=act, dst=dst)
+    want, tol = act_error(gate.double(), act, torch.float32 if dst == "F32" else torch.bfloat16)
+    want, tol = want * up.double(), tol * up.double().abs() + (U[y.dtype] + 2.0 ** -24) * (want * up.double()).abs() + TINY[y.dtype]
+    keep = want.abs() < 65000
+    assert ((y.double() - want).abs() <= tol)[keep].all()
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_of_rows_far_out_in_eight_bits(stmat, act):
+    """Rows whose values all lie in one tail: their scale and codes hold the
+    values' own digits."""
+    for lo, hi in ((-4, -3), (-6, -5), (-7.5, -6.5), (-9, -8.5)):
+        v = torch.linspace(lo, hi, 3 * 512).cuda().view(3, 512)
+        y, scales = stmat.gated_act(v, act=act, dst="F8_E4M3")
+        want, e = act64(v.double(), act)
+        own = (2 * e.max() + 8) * 2.0 ** -23
+        top = want.abs().amax(1) / 448
+        assert ((scales.double() - top).abs() <= own * top).all()
+        q = want / scales.double()[:, None]
+        assert ((y.double() - q).abs() <= torch.clamp(q.abs() * 2.0 ** -4, min=2.0 ** -10) * (1 + 16 * own) + 2 * own * q.abs()).all()
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dst", ["F32", "BF16"])
+@pytest.mark.parametrize("m,n,k", [(3, 500, 4096), (40, 1201, 4096), (600, 512, 64), (600, 510, 64), (256, 1024, 4096)])
+def test_product_activations_relative_to_their_value(stmat, act, dst, m, n, k):
+    """Sums that are exact (one term each), so that the activation's error is
+    all there is."""
+    x, w = torch.zeros(m, k, device="cuda"), torch.zeros(n, k, device="cuda")
+    at = k - 5
+    x[:, at] = torch.linspace(-9, 9, m, device="cuda")
+    w[:, at] = torch.linspace(0.25, 1.4, n, device="cuda")
+    x, w = x.bfloat16(), w.bfloat16()
+    y = stmat.linear(x, w, act=act, dst=dst)
+    want, tol = act_error(x[:, at].double()[:, None] * w[:, at].double()[None], act, y.dtype)
+    off = (y.double() - want).abs() / tol
+    assert (off <= 1).all(), off.max().item()
+
+
+@gpu
+@pytest.mark.parametrize("dst", ["F32", "BF16"])
+def test_activations_of_infinities(stmat, dst):
+    v = torch.tensor([[math.inf, -math.inf, math.nan, 3e38, -3e38, 0.0, -0.0, 1e-45]], device="cuda")
+    x = v.clone().bfloat16().view(8, 1)
+    w = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda")
+    for act in ACTS:
+        for y in (stmat.gated_act(v, act=act, dst=dst)[0][0], stmat.linear(x, w, act=act, dst=dst)[:, 0]):
+            assert y[0] == math.inf and torch.isnan(y[1:3]).all() and y[3] > 2.9e38
+            assert (y[4:7] == 0).all() and 0 <= y[7] <= 1e-44
