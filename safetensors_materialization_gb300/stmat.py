@@ -895,24 +895,17 @@ def _invalid(msg):
     return StmatError(1, msg)
 
 
-def _gpu(t, name):
-    """The number of the GPU that a call's first operand is on."""
-    if not t.is_cuda:
-        raise _invalid(f"{name} is not on the GPU")
-    return t.get_device()
-
-
 def _elsewhere(t, name, gpu):
     if not t.is_cuda:
         return _invalid(f"{name} is not on the GPU")
     return _invalid(f"{name} is on GPU {t.get_device()}, the call's first operand on GPU {gpu}")
 
 
-def _matrix(t, name, gpu):
+def _matrix(t, name, gpu=None):
     """(address, elements between rows, rows, columns) of a tensor on this GPU
-    whose leading dimensions are the rows (a vector: one row); no copy is
-    made."""
-    if t.get_device() != gpu:
+    (None: known to be) whose leading dimensions are the rows (a vector: one
+    row); no copy is made."""
+    if gpu is not None and t.get_device() != gpu:
         raise _elsewhere(t, name, gpu)
     shape = t.shape
     if len(shape) == 2:
@@ -975,22 +968,26 @@ def _new(like, shape, dtype, ops):
 
 
 class _On:
-    """Runs a call on `stream`, one of its operands' GPU's: outputs are
-    allocated there, and inputs stay allocated until its work is done."""
+    """Runs a call with its operands' GPU current and on `stream` (None:
+    torch's current one there): outputs are allocated there, and inputs stay
+    allocated until a given stream's work is done."""
 
     __slots__ = ("ctx", "stream")
 
-    def __init__(self, torch, stream, gpu):
+    def __init__(self, torch, stream, gpu, name):
+        if gpu < 0:
+            raise _invalid(f"{name} is not on the GPU")
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=gpu)
-        elif stream.device_index != gpu:
-            raise _invalid(f"stream is one of GPU {stream.device_index}, the operands are on GPU {gpu}")
-        self.stream, self.ctx = stream, torch.cuda.stream(stream)
+        elif stream is not None and stream.device_index != gpu:
+            raise _invalid(f"stream is one of GPU {stream.device_index}, {name} is on GPU {gpu}")
+        self.stream = stream
+        self.ctx = torch.cuda.device(gpu) if stream is None else torch.cuda.stream(stream)
 
     def run(self, fn, tensors):
         with self.ctx:
             got = fn()
-        for t in tensors:
+        for t in tensors if self.stream is not None else ():
             if t is not None:
                 t.record_stream(self.stream)
         return got
@@ -1005,15 +1002,12 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
     use instead.  Returns (y, scales or None, h in x's dtype, or None without
     a residual); y * scales[..., None] stands for the normed rows."""
     ops = _OPS or _ops()
-    gpu = _gpu(x, "x")
-    if stream is not None:
-        return _On(ops.torch, stream, gpu).run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
-                                               (x, weight, residual, scale))
-    if gpu != ops.device():
-        with ops.torch.cuda.device(gpu):
-            return rms_norm(x, weight, eps, residual, dst, scale)
+    gpu = x.get_device()
+    if stream is not None or gpu < 0 or gpu != ops.device():
+        return _On(ops.torch, stream, gpu, "x").run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
+                                                    (x, weight, residual, scale))
     codes, shape, x_type = ops.codes, x.shape, x.dtype
-    px, ldx, rows, cols = _matrix(x, "x", gpu)
+    px, ldx, rows, cols = _matrix(x, "x")
     x_code = codes.get(x_type, -1)
     y_type, y_code = _dst(dst, x_type, ops)
     pw = pr = ph = ldr = ps = pss = 0
@@ -1045,14 +1039,11 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
     "none", "relu", "silu", "gelu" or "gelu_tanh"; dst and scale as for
     rms_norm.  Returns (y, scales or None)."""
     ops = _OPS or _ops()
-    gpu = _gpu(gate, "gate")
-    if stream is not None:
-        return _On(ops.torch, stream, gpu).run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
-    if gpu != ops.device():
-        with ops.torch.cuda.device(gpu):
-            return gated_act(gate, up, act, dst, scale)
+    gpu = gate.get_device()
+    if stream is not None or gpu < 0 or gpu != ops.device():
+        return _On(ops.torch, stream, gpu, "gate").run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
     shape, x_type = gate.shape, gate.dtype
-    pg, ldg, rows, cols = _matrix(gate, "gate", gpu)
+    pg, ldg, rows, cols = _matrix(gate, "gate")
     y_type, y_code = _dst(dst, x_type, ops)
     pu = ldu = ps = pss = 0
     scales = None
@@ -1085,15 +1076,13 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     residual has y's shape and dtype.  out: the tensor to write, which may be
     the residual itself but overlap no other operand; by default a new one."""
     ops = _OPS or _ops()
-    gpu = _gpu(x, "x")
-    if stream is not None:
-        return _On(ops.torch, stream, gpu).run(lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
-                                               (x, weight, x_scale, w_scale, bias, residual, out))
-    if gpu != ops.device():
-        with ops.torch.cuda.device(gpu):
-            return linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out)
+    gpu = x.get_device()
+    if stream is not None or gpu < 0 or gpu != ops.device():
+        return _On(ops.torch, stream, gpu, "x").run(
+            lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
+            (x, weight, x_scale, w_scale, bias, residual, out))
     codes, x_type = ops.codes, x.dtype
-    px, ldx, m, k = _matrix(x, "x", gpu)
+    px, ldx, m, k = _matrix(x, "x")
     pw, ldw, n, wk = _matrix(weight, "weight", gpu)
     if wk != k or weight.dim() != 2:
         raise _invalid(f"x has rows of {k}, weight is {tuple(weight.shape)}")
