@@ -627,7 +627,7 @@ st_status st_plan_check(const st_plan_t *plan, void *stream, uint32_t *flags);
  * Calls run on `stream` (a cudaStream_t; NULL is the legacy default stream)
  * without host synchronization or allocation, can be captured in a CUDA graph,
  * and give the same bits on every run.  Zero rows or columns:
- * nothing is written.  Errors: ST_E_INVAL (sizes, strides, NULL), ST_E_DTYPE,
+ * nothing is written, but 2^-126 to the scales of rows without columns.  Errors: ST_E_INVAL (sizes, strides, NULL), ST_E_DTYPE,
  * ST_E_ALIGN, ST_E_CUDA (launch failure); nothing is queued then.  Values
  * are computed in binary32 and rounded once (round to nearest even); NaN and
  * infinities go through the formulas.

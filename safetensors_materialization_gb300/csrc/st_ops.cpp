@@ -160,7 +160,8 @@ st_status st_rms_norm(const st_rms_norm_args *a, void *stream) {
   if (!(a->eps >= 0.0f)) return set_error(ST_E_INVAL, "%s: eps %g is not a non-negative number", op, (double)a->eps);
   if (a->h && !a->residual) return set_error(ST_E_INVAL, "%s: h without a residual", op);
   ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales));
-  if (a->rows == 0 || a->cols == 0) return ST_OK;
+  if (a->rows == 0) return ST_OK;
+  if (a->cols == 0) return a->scales ? launch_empty_rows(a->scales, a->rows, stream, op) : ST_OK;
   ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->rows, a->cols, true));
   if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->x_dtype, a->rows, a->cols, true));
   if (a->weight) ST_TRY(check_vector(op, "weight", a->weight, a->w_dtype));
@@ -176,7 +177,8 @@ st_status st_gated_act(const st_gated_act_args *a, void *stream) {
   if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: gate is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
   if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
   ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales));
-  if (a->rows == 0 || a->cols == 0) return ST_OK;
+  if (a->rows == 0) return ST_OK;
+  if (a->cols == 0) return a->scales ? launch_empty_rows(a->scales, a->rows, stream, op) : ST_OK;
   ST_TRY(check_matrix(op, "gate", a->gate, a->ldg, a->x_dtype, a->rows, a->cols, true));
   if (a->up) ST_TRY(check_matrix(op, "up", a->up, a->ldu, a->x_dtype, a->rows, a->cols, true));
   ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->rows, a->cols, false));

@@ -16,6 +16,8 @@ constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the smallest scale, so 
 // aligned to their itemsize, rows, cols > 0.
 st_status launch_rms_norm(const st_rms_norm_args &a, void *stream);
 st_status launch_gated_act(const st_gated_act_args &a, void *stream);
+// 2^-126 to the scales of rows without columns.
+st_status launch_empty_rows(float *scales, int64_t rows, void *stream, const char *op);
 st_status launch_linear(const st_linear_args &a, void *stream);
 // Bytes of workspace the product needs (rows that TMA cannot read).
 int64_t linear_workspace(const st_linear_args &a);

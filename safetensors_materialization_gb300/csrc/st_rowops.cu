@@ -279,6 +279,14 @@ __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) 
   });
 }
 
+// The scales of rows without columns, whose largest magnitude is 0.
+__global__ void __launch_bounds__(kMaxThreads) empty_rows_kernel(float *scales, int64_t rows) {
+  wait_for_previous();
+  let_next_start();
+  const int64_t row = int64_t(blockIdx.x) * kMaxThreads + threadIdx.x;
+  if (row < rows) scales[row] = kMinScale;
+}
+
 // threads 0: a warp per row.
 template <class T, int V, int NV, bool kSkew, Op kOp>
 cudaError_t launch_rows(const RowArgs &a, int threads, cudaStream_t st) {
@@ -348,6 +356,14 @@ st_status launch_op(RowArgs &a, st_dtype x_dtype, void *stream, const char *op) 
 }
 
 }  // namespace
+
+st_status launch_empty_rows(float *scales, int64_t rows, void *stream, const char *op) {
+  const cudaError_t e = launch(empty_rows_kernel, static_cast<unsigned>((rows + kMaxThreads - 1) / kMaxThreads), kMaxThreads, 0, 1,
+                               static_cast<cudaStream_t>(stream), scales, rows);
+  if (e != cudaSuccess)
+    return set_error(ST_E_CUDA, "%s launch (%lld empty rows): %s: %s", op, (long long)rows, cudaGetErrorName(e), cudaGetErrorString(e));
+  return ST_OK;
+}
 
 st_status launch_rms_norm(const st_rms_norm_args &p, void *stream) {
   RowArgs a{};

@@ -1,6 +1,7 @@
 """Calls at the edges of what the operators take: which GPU they run on (with
 stand-ins for tensors of several GPUs, on the CPU), operands that overlap,
-activations far out."""
+activations far out, rows without columns, batches without rows, the smallest
+scales, inputs that want a gradient."""
 import contextlib
 import ctypes as C
 import math
@@ -345,3 +346,17 @@ def test_activations_of_infinities(stmat, dst):
         for y in (stmat.gated_act(v, act=act, dst=dst)[0][0], stmat.linear(x, w, act=act, dst=dst)[:, 0]):
             assert y[0] == math.inf and torch.isnan(y[1:3]).all() and y[3] > 2.9e38
             assert (y[4:7] == 0).all() and 0 <= y[7] <= 1e-44
+
+
+# -------------------------------------------------------------- empty sizes
+
+@gpu
+@pytest.mark.parametrize("shape", [(3, 0), (2, 5, 0), (0, 0), (2500, 0), (0,)])
+def test_rows_without_columns_have_the_smallest_scale(stmat, shape):
+    """The largest magnitude of no value is 0."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.empty(shape, dtype=dtype, device="cuda")
+        torch.full((1 << 16,), math.nan, device="cuda")  # what new scales would hold
+        for y, scales in (stmat.rms_norm(x, residual=x, dst="F8_E4M3")[:2], stmat.gated_act(x, x, dst="F8_E4M3")):
+            assert y.shape == shape and scales.shape == shape[:-1] and (scales == 2.0 ** -126).all()
+        assert stmat.rms_norm(x)[0].shape == shape
