@@ -666,7 +666,7 @@ typedef struct st_rms_norm_args {
   void *h;              int64_t ldh; /* the new residual, or NULL: not kept */
   void *y;              int64_t ldy;
   const float *scale;               /* F8_E4M3: the given scale, or */
-  float *scales;                    /* rows entries, written */
+  float *scales;                    /* rows entries, written (no rows: or NULL) */
 } st_rms_norm_args;
 st_status st_rms_norm(const st_rms_norm_args *args, void *stream);
 

@@ -48,11 +48,11 @@ st_status check_sizes(const char *op, int64_t rows, int64_t cols) {
 }
 
 // The output's dtype and, for 8 bits, exactly one of a given scale and an
-// array for the rows' scales.
-st_status check_output(const char *op, st_dtype y, const float *scale, const float *scales) {
+// array for the rows' scales (no rows: which may be NULL).
+st_status check_output(const char *op, st_dtype y, const float *scale, const float *scales, int64_t rows) {
   if (!is_float16or32(y) && y != ST_F8_E4M3)
     return set_error(ST_E_DTYPE, "%s: the output is BF16, F16, F32 or F8_E4M3, not %d", op, static_cast<int>(y));
-  if (y == ST_F8_E4M3 ? !scale == !scales : (scale || scales))
+  if (y == ST_F8_E4M3 ? (scale && scales) || (rows > 0 && !scale && !scales) : (scale || scales))
     return set_error(ST_E_INVAL, "%s: an F8_E4M3 output takes either scale or scales, another output neither", op);
   st_status s = check_vector(op, "scale", scale, ST_F32);
   return s != ST_OK ? s : check_vector(op, "scales", scales, ST_F32);
@@ -159,7 +159,7 @@ st_status st_rms_norm(const st_rms_norm_args *a, void *stream) {
     return set_error(ST_E_DTYPE, "%s: weight is BF16, F16 or F32, not %d", op, (int)a->w_dtype);
   if (!(a->eps >= 0.0f)) return set_error(ST_E_INVAL, "%s: eps %g is not a non-negative number", op, (double)a->eps);
   if (a->h && !a->residual) return set_error(ST_E_INVAL, "%s: h without a residual", op);
-  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales));
+  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales, a->rows));
   if (a->rows == 0) return ST_OK;
   if (a->cols == 0) return a->scales ? launch_empty_rows(a->scales, a->rows, stream, op) : ST_OK;
   ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->rows, a->cols, true));
@@ -176,7 +176,7 @@ st_status st_gated_act(const st_gated_act_args *a, void *stream) {
   ST_TRY(check_sizes(op, a->rows, a->cols));
   if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: gate is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
   if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
-  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales));
+  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales, a->rows));
   if (a->rows == 0) return ST_OK;
   if (a->cols == 0) return a->scales ? launch_empty_rows(a->scales, a->rows, stream, op) : ST_OK;
   ST_TRY(check_matrix(op, "gate", a->gate, a->ldg, a->x_dtype, a->rows, a->cols, true));

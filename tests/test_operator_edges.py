@@ -360,3 +360,22 @@ def test_rows_without_columns_have_the_smallest_scale(stmat, shape):
         for y, scales in (stmat.rms_norm(x, residual=x, dst="F8_E4M3")[:2], stmat.gated_act(x, x, dst="F8_E4M3")):
             assert y.shape == shape and scales.shape == shape[:-1] and (scales == 2.0 ** -126).all()
         assert stmat.rms_norm(x)[0].shape == shape
+
+
+@pytest.mark.parametrize("op,cls", [("st_rms_norm", "RmsNormArgs"), ("st_gated_act", "GatedActArgs")])
+def test_no_rows_need_no_scales(stmat, op, cls):
+    """An array of no entries has no address."""
+    a = getattr(stmat, cls)(rows=0, cols=96, x_dtype=10, y_dtype=13)
+    call = getattr(stmat.lib(), op)
+    assert stmat.STATUS[call(C.byref(a), None)] == "ST_OK"
+    a.scale = a.scales = X
+    assert stmat.STATUS[call(C.byref(a), None)] == "ST_E_INVAL"
+    a.scale, a.y_dtype = None, 10
+    assert stmat.STATUS[call(C.byref(a), None)] == "ST_E_INVAL"
+
+
+@gpu
+def test_no_rows_in_eight_bits(stmat):
+    x = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
+    for y, scales in (stmat.rms_norm(x, residual=x, dst="F8_E4M3")[:2], stmat.gated_act(x, x, dst="F8_E4M3")):
+        assert y.shape == (0, 96) and scales.shape == (0,)
