@@ -919,6 +919,9 @@ def _matrix(t, name, gpu=None):
         cols, inner = shape[-1], t.stride(-1)
         rows, ld = 1, None
         for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+            if n == 0:
+                rows, ld = 0, cols
+                break
             if n == 1:
                 continue
             if ld is None:

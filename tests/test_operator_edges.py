@@ -379,3 +379,27 @@ def test_no_rows_in_eight_bits(stmat):
     x = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
     for y, scales in (stmat.rms_norm(x, residual=x, dst="F8_E4M3")[:2], stmat.gated_act(x, x, dst="F8_E4M3")):
         assert y.shape == (0, 96) and scales.shape == (0,)
+
+
+@pytest.mark.parametrize("shape", [(2, 0, 96), (0, 3, 96), (2, 0, 5, 96), (2, 3, 0, 96), (4, 0), (0, 0, 0), (1, 0, 1, 7)])
+def test_batches_without_rows_are_no_stride_error(stmat, machine, shape):
+    """Whatever strides such a tensor has: it has no row."""
+    n = shape[-1]
+    for x in (Tensor(shape), Tensor(shape, strides=tuple(range(41, 40 + len(shape))) + (1,))):
+        machine.calls.clear()
+        y, scales, h = stmat.rms_norm(x, residual=x, dst="F8_E4M3")
+        assert y.shape == h.shape == shape and scales.shape == shape[:-1]
+        assert stmat.gated_act(x, x)[0].shape == shape
+        assert stmat.linear(x, Tensor((8, n))).shape == shape[:-1] + (8,)
+        assert [c[0] for c in machine.calls] == ["rms_norm", "gated_act", "linear"]
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(2, 0, 96), (0, 3, 96), (2, 3, 0, 96)])
+def test_batches_without_rows(stmat, shape):
+    x, w = torch.empty(shape, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 96, dtype=torch.bfloat16, device="cuda")
+    assert stmat.rms_norm(x, w[0], residual=x, dst="F8_E4M3")[0].shape == shape
+    assert stmat.gated_act(x, x)[0].shape == shape
+    assert stmat.linear(x, w, residual=None).shape == shape[:-1] + (8,)
+    big = torch.zeros(2, 4, 96, dtype=torch.bfloat16, device="cuda")
+    assert stmat.rms_norm(big[:, :0])[0].shape == (2, 0, 96) and stmat.linear(big[:, 4:], w).shape == (2, 0, 8)
