@@ -79,7 +79,8 @@ __device__ __forceinline__ Stat block_stat(Stat s) {
 // What every value of the row is multiplied by before it is stored: rstd (1
 // for the gated activation), then 1 / scale (1 unless 8 bits).  Two factors,
 // since their product can leave binary32's range (a zero row: 1 / scale =
-// 2^126).
+// 2^126).  A given scale below binary32's normal range, whose reciprocal may
+// be infinite, has 2^24 of it in the first.
 struct Factor {
   float rstd, inv;
 };
@@ -96,14 +97,20 @@ __device__ __forceinline__ Factor row_factor(const RowArgs &a, Stat s, int64_t r
     if (first) a.scales[row] = scale;
   } else {
     scale = *a.scale;
+    if (fabsf(scale) < kMinScale) f.rstd *= 0x1p24f, scale *= 0x1p24f;
   }
   f.inv = 1.0f / scale;
   return f;
 }
 
-template <Op kOp>
-__device__ __forceinline__ float scaled(float v, Factor f) {
-  return (kOp == kNormOp ? v * f.rstd : v) * f.inv;
+template <Op kOp, int V>
+__device__ __forceinline__ void scale_values(float (&v)[V], Factor f) {
+  if (kOp == kNormOp || f.rstd != 1.0f) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] *= f.rstd;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] *= f.inv;
 }
 
 template <class T>
@@ -235,8 +242,7 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
     for (int i = 0; i < NV; ++i) {
       const int c = column(i);
       if (c < a.cols) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = scaled<kOp>(v[i][j], f);
+        scale_values<kOp>(v[i], f);
         if (whole(c) && (!kSkew || a.y_same)) store_any<V>(a.y, dtype, row * a.ldy + c, v[i]);
         else store_part<V>(a.y, dtype, row * a.ldy + c, c, a.cols, v[i]);
       }
@@ -272,8 +278,7 @@ __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) 
       x = row_read<T, V>(a.x, row * a.ldx + c);
       if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
       row_values<T, W, V, false, kOp, true>(a, row, static_cast<int>(c), true, x, r, v, unused);
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = scaled<kOp>(v[j], f);
+      scale_values<kOp>(v, f);
       store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v);
     }
   });

@@ -403,3 +403,45 @@ def test_batches_without_rows(stmat, shape):
     assert stmat.linear(x, w, residual=None).shape == shape[:-1] + (8,)
     big = torch.zeros(2, 4, 96, dtype=torch.bfloat16, device="cuda")
     assert stmat.rms_norm(big[:, :0])[0].shape == (2, 0, 96) and stmat.linear(big[:, 4:], w).shape == (2, 0, 8)
+
+
+# ----------------------------------------------------------- smallest scales
+
+@gpu
+@pytest.mark.parametrize("exponent", [-149, -146, -140, -129, -128, -127, -126, -120, -20])
+@pytest.mark.parametrize("c", [40, 43, 20000])
+def test_given_scales_of_any_size(stmat, exponent, c):
+    """Codes are the clamped quotients, whether or not 1 / scale is a binary32
+    number.  The values are whole multiples of 2^-149 (or of the scale's
+    2^-5), so that the quotients have no error of their own."""
+    scale = torch.tensor([2.0 ** exponent], device="cuda")
+    unit = 2.0 ** max(-149, exponent - 5)
+    g = torch.Generator().manual_seed(c)
+    k = torch.randint(-20000, 20001, (3, c), generator=g).float()
+    k[:, 1] = 0
+    v = (k.double() * unit).float().cuda()
+    v[0, 0], v[1, 0], v[2, 0] = 3e38, -1e-10, math.nan
+    want = (v.double() / 2.0 ** exponent).clamp(-448, 448)
+
+    def same(y):
+        y = y.double()
+        assert torch.equal(torch.isnan(y), torch.isnan(want))
+        tol = torch.clamp(want.abs() * 2.0 ** -4, min=2.0 ** -10)
+        assert torch.nan_to_num((y - want).abs() - tol, nan=0.0).max() <= 0
+
+    same(stmat.gated_act(v, act="none", dst="F8_E4M3", scale=scale)[0])
+    same(stmat.gated_act(v, torch.ones_like(v), act="none", dst="F8_E4M3", scale=scale)[0])
+    # rows of ones: y is the weight (rstd is 1 to 2^-23)
+    for row in range(3):
+        y = stmat.rms_norm(torch.ones(1, c, device="cuda"), v[row], eps=0.0, dst="F8_E4M3", scale=scale)[0].double()
+        q = want[row:row + 1]
+        assert torch.equal(torch.isnan(y), torch.isnan(q))
+        tol = torch.clamp(q.abs() * 2.0 ** -4, min=2.0 ** -10) * (1 + 2.0 ** -18) + q.abs() * 2.0 ** -22 + unit / scale.double() / 2
+        assert torch.nan_to_num((y - q).abs() - tol, nan=0.0).max() <= 0
+
+
+@gpu
+def test_a_given_scale_of_zero(stmat):
+    v = torch.tensor([[0.0, 1.0, -1e-40, math.nan]], device="cuda")
+    y = stmat.gated_act(v, act="none", dst="F8_E4M3", scale=torch.zeros(1, device="cuda"))[0].float()
+    assert torch.isnan(y[0, 0]) and y[0, 1] == 448 and y[0, 2] == -448 and torch.isnan(y[0, 3])
