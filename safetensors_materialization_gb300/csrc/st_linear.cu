@@ -107,9 +107,16 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
   return yes;
 }
-// Bounded: false after kWaitLimit polls.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
-  for (uint32_t it = 0; it < kWaitLimit; ++it) {
+// The polls allowed to a wait for a sum of `blocks` stages: kWaitLimit, which
+// is room for one stage, and 256 a stage.  A poll takes 10 ns at the least, a
+// stage 0.2 us, and under 1 us where every SM streams from HBM.
+__device__ __forceinline__ uint32_t sum_limit(int blocks) {
+  const uint64_t polls = kWaitLimit + 256ull * static_cast<uint32_t>(blocks);
+  return polls < 0xffffffffu ? static_cast<uint32_t>(polls) : 0xffffffffu;
+}
+// Bounded: false after `limit` polls.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, uint32_t limit = kWaitLimit) {
+  for (uint32_t it = 0; it < limit; ++it) {
     uint32_t ok;
     asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
                  : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
@@ -119,10 +126,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
 }
 // The same for a whole warp that waits long: one lane polls, and pauses
 // between polls, so that the threads that feed the tensor core are not held up.
-__device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, int lane) {
+__device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, int lane, uint32_t limit) {
   int ok = 0;
   if (lane == 0) {
-    for (uint32_t it = 0; it < kWaitLimit && !ok; ++it) {
+    for (uint32_t it = 0; it < limit && !ok; ++it) {
       asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
                    : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
       if (!ok) __nanosleep(64);
@@ -331,7 +338,10 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         for (int j = 0; j < kStageK / 32; ++j, add = 1) mma<kEight>(tmem, wd + 2 * j, xd + 2 * j, a.idesc, add);
         mma_commit(&empty[r.at]);
       }
+      // The MMAs are done with the stages and TMEM before this warp moves on,
+      // whatever the readout's wait came to.
       mma_commit(&done);
+      if (!bar_wait(&done, 0, sum_limit(blocks))) failed = 1;
     }
   }
   __syncwarp();
@@ -355,7 +365,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
       ws[j] = a.w_scale && j < live ? a.w_scale[(n + j) * a.w_scale_step] : 1.0f;
       bias[j] = b[0];
     }
-    if (blocks > 0 && !bar_wait(&done, 0)) failed = 1;
+    if (blocks > 0 && !bar_wait(&done, 0, sum_limit(blocks))) failed = 1;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   }
   if (kOver) cluster_arrive();
@@ -802,7 +812,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         if (lane == 0) peer_arrive(taken_at + 8 * buf);
       };
       const int live = static_cast<int>(min(int64_t(chunks), (a.n - at.n0 + kChunk - 1) / kChunk));
-      if (!bar_wait_warp(&sums[buf], (n / 2) & 1, lane)) { failed = 1; break; }
+      if (!bar_wait_warp(&sums[buf], (n / 2) & 1, lane, sum_limit(blocks))) { failed = 1; break; }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (warp >> 2 >= live) release();
       for (int c = warp >> 2; c < live; c += kDenseEpilogueWarps / 4)
@@ -824,7 +834,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     float xs = 1.0f;
     if (reads) {
       xs = scale_of(pair);
-      if (!bar_wait_warp(&sums[0], 0, lane)) failed = 1;
+      if (!bar_wait_warp(&sums[0], 0, lane, sum_limit(blocks))) failed = 1;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     }
     cluster_arrive();

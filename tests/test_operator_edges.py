@@ -1,7 +1,7 @@
 """Calls at the edges of what the operators take: which GPU they run on (with
 stand-ins for tensors of several GPUs, on the CPU), operands that overlap,
 activations far out, rows without columns, batches without rows, the smallest
-scales, inputs that want a gradient."""
+scales, sums of more stages than any wait's polls."""
 import contextlib
 import ctypes as C
 import math
@@ -445,3 +445,20 @@ def test_a_given_scale_of_zero(stmat):
     v = torch.tensor([[0.0, 1.0, -1e-40, math.nan]], device="cuda")
     y = stmat.gated_act(v, act="none", dst="F8_E4M3", scale=torch.zeros(1, device="cuda"))[0].float()
     assert torch.isnan(y[0, 0]) and y[0, 1] == 448 and y[0, 2] == -448 and torch.isnan(y[0, 3])
+
+
+# ----------------------------------------------------------------- long sums
+
+@gpu
+def test_a_sum_that_takes_longer_than_a_stages_wait(stmat):
+    """2^29 terms: a quarter of a second between a readout's first poll and its
+    last, in which a wait that allows for one stage can run out."""
+    k = 1 << 29
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB of device memory")
+    x, w = torch.zeros(1, k, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, k, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 63, 64, k // 8 - 1, k // 8, k // 2 + 77, k - 65, k - 1], device="cuda")
+    x[0, at] = torch.arange(1, 9, device="cuda").bfloat16()
+    w[0, at], w[1, at[[0, 2, 4, 6]]] = 3, 5
+    y = stmat.linear(x, w, dst="F32")
+    assert y.tolist() == [[3.0 * 36, 5.0 * (1 + 3 + 5 + 7)]] and stmat.static_check() == 0
