@@ -590,11 +590,13 @@ st_status st_load_files(const st_files_t *files, void *data_dev, const st_plan_t
 st_status st_materialize_noalloc(const void *data_dev, const st_plan_t *plan, void *const *dst_ptrs,
                                  const float *scales, void *stream);
 
-/* No counterpart on the pages (the library's own status for the two calls
- * that use its static array).  Reads and clears the error word of the
+/* No counterpart on the pages (the library's own status for the calls that
+ * use its static array).  Reads and clears the error word of the
  * library's static device array on the current device: the device flags of
  * every st_materialize_noalloc, st_load_tensors and st_linear call since the
- * last read (bits as for st_plan_check).
+ * last read (bits 0 and 1 as for st_plan_check; bit 2 = a bounded wait in
+ * st_linear gave up, its y is incomplete).  All of these calls share the one
+ * word, so whoever reads it reads and clears the others' flags too.
  * Copies the word to the host on `stream` and waits for the stream, so every
  * such call queued on it before has finished; calls on other streams are
  * seen only once they have finished.  Allocates nothing.  Returns
@@ -710,8 +712,8 @@ typedef struct st_linear_args {
  * place); else room for an aligned copy of the one, or both, that does not,
  * made by each call.  The workspace's own fields are not looked at. */
 st_status st_linear_workspace(const st_linear_args *args, uint64_t *bytes);
-/* A wait in a kernel that gave up (bit 1 of st_static_check) leaves y
- * incomplete. */
+/* A wait in a kernel that gave up leaves y incomplete; the call has returned
+ * by then, and bit 2 of st_static_check tells. */
 st_status st_linear(const st_linear_args *args, void *stream);
 
 /* ----------------------------------------------------------------- misc */

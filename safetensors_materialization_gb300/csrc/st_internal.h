@@ -70,9 +70,11 @@ constexpr uint32_t kMaxOutputs = 1u << (32 - kClsBits);
 constexpr int kWarpsPerBlock = 8;
 
 // Bits of the device error word: an output's destination is NULL or not
-// aligned to its itemsize; a bounded wait for a staged copy gave up.
+// aligned to its itemsize; a bounded wait for a staged copy gave up; one of
+// st_linear's did.
 constexpr uint32_t kErrBadDst = 1u;
 constexpr uint32_t kErrTimeout = 2u;
+constexpr uint32_t kErrProduct = 4u;
 
 // Block scales of a block-scaled output (device table indexed by output).
 struct alignas(16) QuantInfo {

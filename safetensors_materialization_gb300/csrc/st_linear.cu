@@ -420,7 +420,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
   }
-  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
+  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrProduct);
   if (!writes) return;
 #pragma unroll 1
   for (int c = warp; c < mine; c += kEpilogueWarps) {
@@ -873,7 +873,7 @@ dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
   cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == kDenseMmaWarp) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrTimeout);
+  if (threadIdx.x == 0 && failed) atomicOr(a.err, kErrProduct);
 }
 
 // ------------------------------------------------------------------- host

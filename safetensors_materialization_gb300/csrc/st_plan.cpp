@@ -1546,9 +1546,10 @@ st_status st_static_check(void *stream, uint32_t *flags) {
   if (e != cudaSuccess) return set_error(ST_E_CUDA, "reading the static error word: %s", cuda_msg(e).c_str());
   *flags = v;
   if (v)
-    return set_error(ST_E_DEVICE, "static-scratch device flags 0x%x:%s%s", v,
+    return set_error(ST_E_DEVICE, "static-scratch device flags 0x%x:%s%s%s", v,
                      (v & kErrBadDst) ? " a non-empty output had a NULL or misaligned destination;" : "",
-                     (v & kErrTimeout) ? " a wait for a staged copy gave up;" : "");
+                     (v & kErrTimeout) ? " a wait for a staged copy gave up;" : "",
+                     (v & kErrProduct) ? " a wait in st_linear gave up, its y is incomplete;" : "");
   return ST_OK;
 }
 

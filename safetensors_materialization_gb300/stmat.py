@@ -785,9 +785,10 @@ def class_step(cls):
 
 def static_check(stream=None):
     """st_static_check: reads and clears the device flags that
-    st_materialize_noalloc and st_load_tensors calls left in the library's
-    static array on the current device (waits for `stream` first); 0 when
-    none (bit 0: bad destination, bit 1: a wait for a staged copy gave up)."""
+    st_materialize_noalloc, st_load_tensors and st_linear calls left in the
+    library's static array on the current device (waits for `stream` first); 0
+    when none (bit 0: bad destination, bit 1: a wait for a staged copy gave up,
+    bit 2: a wait in linear() gave up, its result is incomplete)."""
     flags = C.c_uint32()
     code = lib().st_static_check(_stream(stream), C.byref(flags))
     if code not in (0, 14):
@@ -1077,7 +1078,9 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     entry or one per row; w_scale: F32, one entry or one per row of weight.
     dst: "BF16", "F16" or "F32" (default: x's dtype, BF16 for 8-bit x);
     residual has y's shape and dtype.  out: the tensor to write, which may be
-    the residual itself but overlap no other operand; by default a new one."""
+    the residual itself but overlap no other operand; by default a new one.
+    Nothing waits for the product: that a kernel gave up on it (a bounded wait
+    ran out) shows in static_check()."""
     ops = _OPS or _ops()
     gpu = x.get_device()
     if stream is not None or gpu < 0 or gpu != ops.device():
