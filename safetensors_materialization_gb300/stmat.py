@@ -859,7 +859,8 @@ class Outputs:
 # ------------------------------------------- operators on materialized tensors
 #
 # All operands of a call lie on one GPU, which the call makes current; without
-# `stream` it runs on that GPU's current stream.
+# `stream` it runs on that GPU's current stream.  Nothing here differentiates:
+# results never require a gradient, whatever the inputs do.
 
 # The argument structs' layouts for struct.pack: one call packs a struct in a
 # quarter of the time that setting a ctypes structure's fields takes.
@@ -1004,7 +1005,8 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
     dst: "BF16", "F16", "F32" or "F8_E4M3" (default: x's dtype).  F8_E4M3 with
     scale None writes one scale per row; scale: a one-element F32 tensor to
     use instead.  Returns (y, scales or None, h in x's dtype, or None without
-    a residual); y * scales[..., None] stands for the normed rows."""
+    a residual); y * scales[..., None] stands for the normed rows.  No gradient
+    passes through."""
     ops = _OPS or _ops()
     gpu = x.get_device()
     if stream is not None or gpu < 0 or gpu != ops.device():
@@ -1041,7 +1043,7 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
     """st_gated_act: y = act(gate) * up (act(gate) without up) on rows of BF16,
     F16 or F32; gate and up may be the halves of one product's columns.  act:
     "none", "relu", "silu", "gelu" or "gelu_tanh"; dst and scale as for
-    rms_norm.  Returns (y, scales or None)."""
+    rms_norm.  Returns (y, scales or None).  No gradient passes through."""
     ops = _OPS or _ops()
     gpu = gate.get_device()
     if stream is not None or gpu < 0 or gpu != ops.device():
@@ -1079,7 +1081,7 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     dst: "BF16", "F16" or "F32" (default: x's dtype, BF16 for 8-bit x);
     residual has y's shape and dtype.  out: the tensor to write, which may be
     the residual itself but overlap no other operand; by default a new one.
-    Nothing waits for the product: that a kernel gave up on it (a bounded wait
+    No gradient passes through.  Nothing waits for the product: that a kernel gave up on it (a bounded wait
     ran out) shows in static_check()."""
     ops = _OPS or _ops()
     gpu = x.get_device()

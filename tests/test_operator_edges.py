@@ -462,3 +462,12 @@ def test_a_sum_that_takes_longer_than_a_stages_wait(stmat):
     w[0, at], w[1, at[[0, 2, 4, 6]]] = 3, 5
     y = stmat.linear(x, w, dst="F32")
     assert y.tolist() == [[3.0 * 36, 5.0 * (1 + 3 + 5 + 7)]] and stmat.static_check() == 0
+
+
+@gpu
+def test_no_gradient_passes_through(stmat):
+    """As their documentation says."""
+    x, w = (torch.ones(4, 16, device="cuda", dtype=torch.bfloat16, requires_grad=True) for _ in range(2))
+    for op, got in ((stmat.rms_norm, stmat.rms_norm(x, w[0].detach(), residual=x)), (stmat.gated_act, stmat.gated_act(x, x)),
+                    (stmat.linear, (stmat.linear(x, w),))):
+        assert all(t is None or not t.requires_grad for t in got) and "No gradient" in op.__doc__
