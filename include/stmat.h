@@ -716,6 +716,26 @@ st_status st_linear_workspace(const st_linear_args *args, uint64_t *bytes);
  * by then, and bit 2 of st_static_check tells. */
 st_status st_linear(const st_linear_args *args, void *stream);
 
+/* How a product is cut into tiles and launched.  The results differ in the
+ * order of the sums alone. */
+typedef enum st_linear_kernel {
+  ST_LINEAR_SPLIT = 0,  /* few tokens: tiles of 128 weight rows, each CTA of a cluster with a part of k */
+  ST_LINEAR_DENSE = 1   /* many: tiles of 256 tokens, each for a pair of CTAs or a cluster of pairs */
+} st_linear_kernel;
+typedef struct st_linear_form {
+  int32_t kernel;
+  int32_t width;   /* of a tile; split: 16, 32, 64 or 128 tokens; dense: weight rows, a multiple of 32 up to 256 */
+  int32_t splits;  /* parts of the sum; split: 1, 2, 4 or 8 CTAs; dense: 1, 2 or 4 pairs, each with whole 32 rows of a tile */
+} st_linear_form;
+/* The form st_linear takes on a device of `sms` SMs on which so many clusters
+ * of two and of four pairs of CTAs run at a time (a GB300: 152, 36, 15); on
+ * the host, without a device. */
+st_status st_linear_choose(const st_linear_args *args, int32_t sms, int32_t clusters_of_2, int32_t clusters_of_4,
+                           st_linear_form *form);
+/* st_linear in the given form (for tests and measurements): ST_E_INVAL for one
+ * that does not exist or has more parts than the sum has runs of 128 bytes. */
+st_status st_linear_as(const st_linear_args *args, const st_linear_form *form, void *stream);
+
 /* ----------------------------------------------------------------- misc */
 
 /* Message of the calling thread's last failure ("" if none). */

@@ -982,7 +982,7 @@ cudaError_t allow_smem(int dev, int bytes) {
 // row brought into an SM (1.2 ns, measured), without what every launch costs.
 struct Shape {
   int64_t m_tiles, n_tiles;
-  int width, splits;
+  int width, splits;  // as in st_linear_form
   double cost;
 };
 
@@ -1118,7 +1118,50 @@ int64_t linear_workspace(const st_linear_args &p) {
   return bytes;
 }
 
-st_status launch_linear(const st_linear_args &p, void *stream) {
+namespace {
+
+int blocks_of(const st_linear_args &p) { return static_cast<int>((p.k * item_of(p) + kStageK - 1) / kStageK); }
+
+// The cheaper kernel's shape.
+Shape choose(const st_linear_args &p, const Device &gpu, bool *dense) {
+  const int k_blocks = blocks_of(p);
+  const Shape d = dense_shape(p.m, p.n, k_blocks, gpu), c = split_shape(p.m, p.n, k_blocks, gpu.sms);
+  *dense = p.k > 0 && d.cost < c.cost;
+  return *dense ? d : c;
+}
+
+Shape shape_of(const st_linear_args &p, const st_linear_form &f) {
+  const bool dense = f.kernel == ST_LINEAR_DENSE;
+  const int64_t rows = dense ? kPairM : f.width, columns = dense ? f.width : kTileN;
+  return Shape{(p.m + rows - 1) / rows, (p.n + columns - 1) / columns, f.width, f.splits, 0};
+}
+
+}  // namespace
+
+st_status check_linear_form(const st_linear_args &p, const st_linear_form &f) {
+  const bool dense = f.kernel == ST_LINEAR_DENSE;
+  const int most = dense ? kMaxPairs : kMaxSplit;
+  bool ok = (dense || f.kernel == ST_LINEAR_SPLIT) && f.splits >= 1 && f.splits <= most && !(f.splits & (f.splits - 1));
+  ok = ok && (dense ? f.width >= 32 && f.width <= kPairMaxN && f.width % (32 * f.splits) == 0
+                    : f.width == 16 || f.width == 32 || f.width == 64 || f.width == 128);
+  if (!ok) return set_error(ST_E_INVAL, "st_linear: no kernel %d has tiles of width %d and sums in %d parts", f.kernel, f.width, f.splits);
+  if (f.splits > std::max(1, blocks_of(p)) || (dense && p.k == 0))
+    return set_error(ST_E_INVAL, "st_linear: a sum of %d runs of 128 bytes in %d parts", blocks_of(p), f.splits);
+  return ST_OK;
+}
+
+st_linear_form choose_linear_form(const st_linear_args &p, int sms, int clusters_of_2, int clusters_of_4) {
+  Device gpu{};
+  gpu.sms = sms;
+  gpu.clusters[1] = sms / 2;
+  gpu.clusters[2] = clusters_of_2;
+  gpu.clusters[4] = clusters_of_4;
+  bool dense = false;
+  const Shape s = choose(p, gpu, &dense);
+  return {dense ? ST_LINEAR_DENSE : ST_LINEAR_SPLIT, s.width, s.splits};
+}
+
+st_status launch_linear(const st_linear_args &p, const st_linear_form *form, void *stream) {
   const int item = item_of(p);
   LinArgs a{};
   a.m = p.m; a.n = p.n; a.kbytes = p.k * item;
@@ -1136,7 +1179,7 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   if (s != ST_OK) return s;
   a.err = gpu->err;
   const int sms = gpu->sms;
-  a.k_blocks = static_cast<int>((a.kbytes + kStageK - 1) / kStageK);
+  a.k_blocks = blocks_of(p);
   // Instruction descriptor: binary32 accumulators; formats of A and B, both
   // K-major; rows and columns of one MMA.
   const uint32_t fw = item == 2 ? (p.w_dtype == ST_BF16) : (p.w_dtype == ST_F8_E5M2), fx = item == 2 ? (p.x_dtype == ST_BF16) : 0;
@@ -1154,14 +1197,16 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
     return one(p.y, p.ldy) && (!p.residual || one(p.residual, p.ldr));
   };
 
-  const Shape d = dense_shape(p.m, p.n, a.k_blocks, *gpu), c = split_shape(p.m, p.n, a.k_blocks, sms);
-  if (p.k > 0 && d.cost < c.cost) {
-    if (d.m_tiles * d.n_tiles > 0x3fffffff)
+  bool dense = form && form->kernel == ST_LINEAR_DENSE;
+  const Shape shape = form ? shape_of(p, *form) : choose(p, *gpu, &dense);
+  const int64_t tiles = shape.m_tiles * shape.n_tiles;
+  a.splits = shape.splits;
+  if (dense) {
+    if (2 * tiles * a.splits > 0x7fffffff)
       return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
-    a.m_tiles = static_cast<int>(d.m_tiles);
-    a.n_tiles = static_cast<int>(d.n_tiles);
-    a.tile_n = d.width;
-    a.splits = d.splits;
+    a.m_tiles = static_cast<int>(shape.m_tiles);
+    a.n_tiles = static_cast<int>(shape.n_tiles);
+    a.tile_n = shape.width;
     a.idesc = idesc(fx, fw, kPairM, a.tile_n);
     a.vec = aligned(32);
     s = encode(&xmap, a.x, p.k, item, 128);
@@ -1178,10 +1223,8 @@ st_status launch_linear(const st_linear_args &p, void *stream) {
   }
 
   a.vec = aligned(4 * out);
-  a.m_tiles = static_cast<int>(c.m_tiles);
-  a.splits = c.splits;
-  const int bm = c.width;
-  const int64_t tiles = c.m_tiles * c.n_tiles;
+  a.m_tiles = static_cast<int>(shape.m_tiles);
+  const int bm = shape.width;
   if (tiles * a.splits > 0x7fffffff)
     return set_error(ST_E_INVAL, "st_linear: %lld x %lld needs more tiles than one launch has", (long long)p.m, (long long)p.n);
   a.idesc = idesc(fw, fx, kTileN, bm);

@@ -146,6 +146,29 @@ st_status check_linear(const st_linear_args *a, bool *empty) {
   return ST_OK;
 }
 
+st_status run_linear(const st_linear_args *a, const st_linear_form *form, void *stream) {
+  if (!a) return set_error(ST_E_INVAL, "st_linear: NULL arguments");
+  bool empty = false;
+  ST_TRY(check_linear(a, &empty));
+  if (empty) return ST_OK;
+  if (form) ST_TRY(check_linear_form(*a, *form));
+  const int64_t need = linear_workspace(*a);
+  if (need && (!a->workspace || a->workspace_bytes < static_cast<uint64_t>(need)))
+    return set_error(ST_E_INVAL, "st_linear: rows that are no multiples of 16 bytes apart need a workspace of %lld bytes, %llu given",
+                     (long long)need, (unsigned long long)(a->workspace ? a->workspace_bytes : 0));
+  if (need && reinterpret_cast<uintptr_t>(a->workspace) % 16)
+    return set_error(ST_E_ALIGN, "st_linear: the workspace is not 16-byte aligned");
+  if (need) {
+    const Bytes space = array_bytes(a->workspace, static_cast<uint64_t>(need));
+    if (overlap(space, matrix_bytes(a->y, a->ldy, a->y_dtype, a->m, a->n)) ||
+        overlap(space, matrix_bytes(a->x, a->ldx, a->x_dtype, a->m, a->k)) ||
+        overlap(space, matrix_bytes(a->w, a->ldw, a->w_dtype, a->n, a->k)) ||
+        (a->residual && overlap(space, matrix_bytes(a->residual, a->ldr, a->y_dtype, a->m, a->n))))
+      return set_error(ST_E_INVAL, "st_linear: the workspace overlaps an operand");
+  }
+  return launch_linear(*a, form, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -193,26 +216,22 @@ st_status st_linear_workspace(const st_linear_args *a, uint64_t *bytes) {
   return ST_OK;
 }
 
-st_status st_linear(const st_linear_args *a, void *stream) {
-  if (!a) return set_error(ST_E_INVAL, "st_linear: NULL arguments");
+st_status st_linear_choose(const st_linear_args *a, int32_t sms, int32_t clusters_of_2, int32_t clusters_of_4, st_linear_form *form) {
+  if (!a || !form) return set_error(ST_E_INVAL, "st_linear_choose: NULL argument");
+  if (sms < 2 || clusters_of_2 < 0 || clusters_of_4 < 0)
+    return set_error(ST_E_INVAL, "st_linear_choose: no device has %d SMs and %d, %d clusters", sms, clusters_of_2, clusters_of_4);
   bool empty = false;
   ST_TRY(check_linear(a, &empty));
-  if (empty) return ST_OK;
-  const int64_t need = linear_workspace(*a);
-  if (need && (!a->workspace || a->workspace_bytes < static_cast<uint64_t>(need)))
-    return set_error(ST_E_INVAL, "st_linear: rows that are no multiples of 16 bytes apart need a workspace of %lld bytes, %llu given",
-                     (long long)need, (unsigned long long)(a->workspace ? a->workspace_bytes : 0));
-  if (need && reinterpret_cast<uintptr_t>(a->workspace) % 16)
-    return set_error(ST_E_ALIGN, "st_linear: the workspace is not 16-byte aligned");
-  if (need) {
-    const Bytes space = array_bytes(a->workspace, static_cast<uint64_t>(need));
-    if (overlap(space, matrix_bytes(a->y, a->ldy, a->y_dtype, a->m, a->n)) ||
-        overlap(space, matrix_bytes(a->x, a->ldx, a->x_dtype, a->m, a->k)) ||
-        overlap(space, matrix_bytes(a->w, a->ldw, a->w_dtype, a->n, a->k)) ||
-        (a->residual && overlap(space, matrix_bytes(a->residual, a->ldr, a->y_dtype, a->m, a->n))))
-      return set_error(ST_E_INVAL, "st_linear: the workspace overlaps an operand");
-  }
-  return launch_linear(*a, stream);
+  if (empty) return set_error(ST_E_INVAL, "st_linear_choose: a product without rows or columns is not launched");
+  *form = choose_linear_form(*a, sms, clusters_of_2, clusters_of_4);
+  return ST_OK;
+}
+
+st_status st_linear(const st_linear_args *a, void *stream) { return run_linear(a, nullptr, stream); }
+
+st_status st_linear_as(const st_linear_args *a, const st_linear_form *form, void *stream) {
+  if (!form) return set_error(ST_E_INVAL, "st_linear_as: NULL form");
+  return run_linear(a, form, stream);
 }
 
 }  // extern "C"

@@ -18,7 +18,10 @@ st_status launch_rms_norm(const st_rms_norm_args &a, void *stream);
 st_status launch_gated_act(const st_gated_act_args &a, void *stream);
 // 2^-126 to the scales of rows without columns.
 st_status launch_empty_rows(float *scales, int64_t rows, void *stream, const char *op);
-st_status launch_linear(const st_linear_args &a, void *stream);
+// form: NULL, or a checked one.
+st_status launch_linear(const st_linear_args &a, const st_linear_form *form, void *stream);
+st_status check_linear_form(const st_linear_args &a, const st_linear_form &form);
+st_linear_form choose_linear_form(const st_linear_args &a, int sms, int clusters_of_2, int clusters_of_4);
 // Bytes of workspace the product needs (rows that TMA cannot read).
 int64_t linear_workspace(const st_linear_args &a);
 

@@ -37,6 +37,7 @@ EXPORTS = [
     "st_load_files", "st_cache_create", "st_cache_free", "st_cache_get", "st_cache_release",
     "st_cache_stats", "st_cache_clear", "st_load_tensors", "st_host_affinity", "st_device_reads_pageable",
     "st_files_prefetch", "st_rms_norm", "st_gated_act", "st_linear", "st_linear_workspace",
+    "st_linear_choose", "st_linear_as",
     "st_last_error", "st_status_name", "st_dtype_size", "st_dtype_name", "st_version",
 ]
 
@@ -119,6 +120,11 @@ class LinearArgs(C.Structure):
                 ("ldy", C.c_int64), ("workspace", C.c_void_p), ("workspace_bytes", C.c_uint64)]
 
 
+class LinearForm(C.Structure):
+    _fields_ = [("kernel", C.c_int32), ("width", C.c_int32), ("splits", C.c_int32)]
+
+
+LINEAR_KERNELS = ("split", "dense")
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _lib = None
@@ -183,6 +189,8 @@ def lib():
             "st_gated_act": [C.POINTER(GatedActArgs), P],
             "st_linear": [C.POINTER(LinearArgs), P],
             "st_linear_workspace": [C.POINTER(LinearArgs), C.POINTER(U64)],
+            "st_linear_choose": [C.POINTER(LinearArgs), I, I, I, C.POINTER(LinearForm)],
+            "st_linear_as": [C.POINTER(LinearArgs), C.POINTER(LinearForm), P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -885,6 +893,7 @@ class _Ops:
         call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p)
         self.rms_norm, self.gated_act, self.linear, self.linear_workspace = (
             call((n, lib())) for n in ("st_rms_norm", "st_gated_act", "st_linear", "st_linear_workspace"))
+        self.linear_as = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p, C.c_void_p)(("st_linear_as", lib()))
 
 
 def _ops():
@@ -1071,7 +1080,7 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
 
 
 def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residual=None, dst=None, out=None,
-           stream=None):
+           stream=None, form=None):
     """st_linear: act(x_scale * w_scale * (x @ weight.T) + bias) + residual with
     a checkpoint's [n, k] weight; leading dimensions of x are rows.
 
@@ -1081,13 +1090,15 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     dst: "BF16", "F16" or "F32" (default: x's dtype, BF16 for 8-bit x);
     residual has y's shape and dtype.  out: the tensor to write, which may be
     the residual itself but overlap no other operand; by default a new one.
+    form: (kernel, width, splits) of st_linear_form, kernel "split" or "dense",
+    in place of the library's choice (linear_choice).
     No gradient passes through.  Nothing waits for the product: that a kernel gave up on it (a bounded wait
     ran out) shows in static_check()."""
     ops = _OPS or _ops()
     gpu = x.get_device()
     if stream is not None or gpu < 0 or gpu != ops.device():
         return _On(ops.torch, stream, gpu, "x").run(
-            lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out),
+            lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out, form=form),
             (x, weight, x_scale, w_scale, bias, residual, out))
     codes, x_type = ops.codes, x.dtype
     px, ldx, m, k = _matrix(x, "x")
@@ -1131,7 +1142,23 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
         if size:
             workspace = ops.empty(size, dtype=ops.torch.uint8, device=x.device)
             space = workspace.data_ptr()
-    code = ops.linear(_LINEAR_ARGS.pack(*args, space, size), ops.stream(gpu))
+    if form is None:
+        code = ops.linear(_LINEAR_ARGS.pack(*args, space, size), ops.stream(gpu))
+    else:
+        form = LinearForm(LINEAR_KERNELS.index(form[0]) if form[0] in LINEAR_KERNELS else -1, *form[1:])
+        code = ops.linear_as(_LINEAR_ARGS.pack(*args, space, size), C.addressof(form), ops.stream(gpu))
     if code:
         _check(code)
     return out
+
+
+def linear_choice(m, n, k, dtype="BF16", sms=152, clusters=(36, 15)):
+    """st_linear_choose: the (kernel, width, splits) that linear takes for m
+    rows of x through an [n, k] weight of `dtype` on a device of so many SMs and
+    clusters of two and four pairs of CTAs at a time (by default a GB300's)."""
+    code, at = DTYPES.index(dtype), 1 << 40
+    args = LinearArgs(m=m, n=n, k=k, x_dtype=_E4M3 if code == 14 else code, w_dtype=code, y_dtype=10, x=at, ldx=k,
+                      w=2 * at, ldw=k, y=3 * at, ldy=n)
+    form = LinearForm()
+    _check(lib().st_linear_choose(C.byref(args), sms, *clusters, C.byref(form)))
+    return LINEAR_KERNELS[form.kernel], form.width, form.splits
