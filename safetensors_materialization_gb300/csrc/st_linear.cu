@@ -995,8 +995,9 @@ struct Shape {
 // if all of the clusters run at a time, for 18 units a column of joining (us,
 // without and with: 256 x 4096 x 14336 E4M3 23.8, 19.6, BF16 35.8, 31.0; 256 x
 // 1024 x 4096 E4M3 10.5, 8.7; 512 x 4096 x 4096 BF16 18.4, 20.3).  The cost
-// compared with split_kernel's is that of the shortest stages alone: its
-// readouts are not in its cost either.
+// compared with split_kernel's is that of the shortest stages and the joining,
+// without the start and the readout, which count for a few tokens only
+// (choose).
 Shape dense_shape(int64_t m, int64_t n, int k_blocks, const Device &gpu) {
   Shape best{};
   double shortest = 0, cost = 0;
@@ -1034,6 +1035,15 @@ Shape split_shape(int64_t m, int64_t n, int k_blocks, int sms) {
   s.cost = 0.5 * (static_cast<double>(rounds) + (ctas > sms ? static_cast<double>(ctas) / sms : 1.0)) * ((k_blocks + s.splits - 1) / s.splits * (kTileN + s.width) + 26.0 * s.width);
   return s;
 }
+
+// For up to so many tokens dense_kernel's start and readout, 1300 units and 8 a
+// column more than split_kernel's, outweigh its shorter stages wherever sums are
+// short (device time in us, split_kernel and dense_kernel: 1 x 28672 x 64 BF16
+// 2.9, 6.5; 1 x 304 x 256 3.6, 4.1; 8 x 4096 x 256 3.9, 5.7; 8 x 64 x 448 4.7,
+// 4.7; 0.7 of the time in the middle of 276 sizes with up to 1 KB of k).  With
+// 16 tokens split_kernel's readout has caught up (16 x 64 x 256 BF16 5.4, 4.2;
+// 16 x 4096 x 448 5.3, 5.9).
+constexpr int64_t kFewTokens = 8;
 
 st_status launch_error(const LinArgs &a, cudaError_t e) {
   return set_error(ST_E_CUDA, "st_linear launch (%lld x %lld, %lld bytes of k): %s: %s", (long long)a.m, (long long)a.n,
@@ -1126,7 +1136,8 @@ int blocks_of(const st_linear_args &p) { return static_cast<int>((p.k * item_of(
 Shape choose(const st_linear_args &p, const Device &gpu, bool *dense) {
   const int k_blocks = blocks_of(p);
   const Shape d = dense_shape(p.m, p.n, k_blocks, gpu), c = split_shape(p.m, p.n, k_blocks, gpu.sms);
-  *dense = p.k > 0 && d.cost < c.cost;
+  const double more = p.m <= kFewTokens ? 1300 + 8.0 * d.width : 0;
+  *dense = p.k > 0 && d.cost + more < c.cost;
   return *dense ? d : c;
 }
 

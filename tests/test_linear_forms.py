@@ -36,7 +36,7 @@ CHOSEN = [
     ((600, 1024, 8192, "BF16"), ("dense", 256, 4)), ((200, 8192, 8192, "BF16"), ("dense", 256, 2)),
     ((8192, 14336, 4096, "F8_E4M3"), ("dense", 256, 1)), ((4096, 4096, 14336, "BF16"), ("dense", 224, 1)),
     ((600, 2048, 64, "BF16"), ("dense", 96, 1)), ((8192, 300, 64, "BF16"), ("dense", 160, 1)),
-    ((1, 300, 257, "BF16"), ("dense", 32, 1)), ((5, 7, 0, "BF16"), ("split", 16, 1)),
+    ((1, 300, 257, "BF16"), ("split", 16, 1)), ((16, 304, 256, "BF16"), ("dense", 32, 1)), ((5, 7, 0, "BF16"), ("split", 16, 1)),
 ]
 
 
@@ -44,6 +44,15 @@ CHOSEN = [
 def test_the_form_taken_on_a_gb300(stmat, size, form):
     assert stmat.linear_choice(*size) == form
     assert form in FORMS
+
+
+def test_a_few_tokens_take_the_kernel_for_them(stmat):
+    """However short the sum, and however many weight rows."""
+    for m in (1, 2, 5, 8):
+        for n in (1, 64, 300, 1024, 4096, 14336, 28672, 100000):
+            for k in (1, 64, 100, 256, 512, 1000, 4096, 14336):
+                for dtype in ("BF16", "F8_E4M3"):
+                    assert stmat.linear_choice(m, n, k, dtype)[:2] == ("split", 16), (m, n, k, dtype)
 
 
 def test_the_form_fits_any_device(stmat):
