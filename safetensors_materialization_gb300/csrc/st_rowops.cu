@@ -103,14 +103,10 @@ __device__ __forceinline__ Factor row_factor(const RowArgs &a, Stat s, int64_t r
   return f;
 }
 
-template <Op kOp, int V>
-__device__ __forceinline__ void scale_values(float (&v)[V], Factor f) {
-  if (kOp == kNormOp || f.rstd != 1.0f) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= f.rstd;
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j) v[j] *= f.inv;
+// (The gated activation's first factor, seldom other than 1, is in the values.)
+template <Op kOp>
+__device__ __forceinline__ float scaled(float v, Factor f) {
+  return (kOp == kNormOp ? v * f.rstd : v) * f.inv;
 }
 
 template <class T>
@@ -237,12 +233,19 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : block_threads(
   });
   s = kWarpRow ? warp_stat(s) : block_stat(s);
   const Factor f = row_factor<kOp>(a, s, row, t == 0);
+  if (kOp != kNormOp && f.rstd != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] *= f.rstd;
+  }
   auto write = [&](st_dtype dtype) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = column(i);
       if (c < a.cols) {
-        scale_values<kOp>(v[i], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] = scaled<kOp>(v[i][j], f);
         if (whole(c) && (!kSkew || a.y_same)) store_any<V>(a.y, dtype, row * a.ldy + c, v[i]);
         else store_part<V>(a.y, dtype, row * a.ldy + c, c, a.cols, v[i]);
       }
@@ -278,7 +281,8 @@ __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) 
       x = row_read<T, V>(a.x, row * a.ldx + c);
       if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
       row_values<T, W, V, false, kOp, true>(a, row, static_cast<int>(c), true, x, r, v, unused);
-      scale_values<kOp>(v, f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = scaled<kOp>(kOp != kNormOp && f.rstd != 1.0f ? v[j] * f.rstd : v[j], f);
       store_any<V>(a.y, a.y_dtype, row * a.ldy + c, v);
     }
   });
