@@ -129,13 +129,24 @@ __device__ __forceinline__ float fast_rcp(float v) {
 //              1 / (1 + 0.304 |v|); t times a polynomial of degree 7 in t, fitted
 //              to it for the least largest relative error over |v| <= 13.5 (by
 //              Lawson's reweighted least squares), is off by at most 8.4e-8 of it.
-// For F32 outputs (kF32) the library's exp and normal distribution and an exact
-// division: silu within 4 2^-23 of the value, gelu 7, gelu_tanh 2 |e| + 4.  A
-// negative v takes v exp(e) / (1 + exp(e)), whose exponential does not overflow.
+// For F32 outputs (kF32) the library's exp, a reciprocal refined by a step of
+// Newton's iteration, and v^2's rounding error taken into gelu's exponential:
+// silu within 4 2^-23 of the value, gelu 7, gelu_tanh 2 |e| + 4.  A negative v
+// takes v exp(e) / (1 + exp(e)), whose exponential does not overflow.  (Gated
+// 8192 x 14336 F32 249 us with silu, 288 with gelu, 209 without; by an exact
+// division and the library's normal distribution 316 and 416.)
 constexpr float kLog2e = 1.44269504f;
 constexpr float kTanh1 = 1.59576912f, kTanh3 = 0.0713548128f;  // 2 sqrt(2 / pi), that times 0.044715
+// 1 / v for v from 1 to 2^24, within a unit of the last place.
+__device__ __forceinline__ float near_rcp(float v) {
+  const float r = fast_rcp(v);
+  return fmaf(r, fmaf(-v, r, 1.0f), r);
+}
+template <bool kF32>
 __device__ __forceinline__ float gelu(float v) {
-  const float t = fast_rcp(fmaf(fabsf(v), 0.304f, 1.0f));
+  // Beyond 16 the exponential is 0, and infinities would meet in the steps.
+  const float a = kF32 ? fminf(fabsf(v), 16.0f) : fabsf(v), d = fmaf(a, 0.304f, 1.0f);
+  const float t = kF32 ? near_rcp(d) : fast_rcp(d);
   float q = fmaf(t, 0.0368598551f, -0.155304030f);
   q = fmaf(t, q, 0.192196801f);
   q = fmaf(t, q, -0.0431365334f);
@@ -143,22 +154,26 @@ __device__ __forceinline__ float gelu(float v) {
   q = fmaf(t, q, 0.102421626f);
   q = fmaf(t, q, 0.122170880f);
   q = fmaf(t, q, 0.121234670f);
-  q = q * t * fast_exp2(v * v * (-0.5f * kLog2e));
+  if constexpr (kF32) {
+    const float h = a * a, x = expf(-0.5f * h);
+    q = q * t * fmaf(x, -0.5f * fmaf(a, a, -h), x);
+  } else {
+    q = q * t * fast_exp2(v * v * (-0.5f * kLog2e));
+  }
   return v * (v < 0.0f ? q : 1.0f - q);
 }
 // v / (1 + exp(-e)) for an e of v's sign.
 __device__ __forceinline__ float gated_exactly(float v, float e) {
   const float x = expf(-fabsf(e));
-  return (v < 0.0f ? v * x : v) / (1.0f + x);
+  return (v < 0.0f ? v * x : v) * near_rcp(1.0f + x);
 }
 template <bool kF32, st_act A>
 __device__ __forceinline__ float activate1(float v) {
   if constexpr (A == ST_ACT_RELU) return v < 0.0f ? 0.0f : v;
   else if constexpr (kF32 && A == ST_ACT_SILU) return gated_exactly(v, v);
-  else if constexpr (kF32 && A == ST_ACT_GELU) return v * normcdff(v);
   else if constexpr (kF32 && A == ST_ACT_GELU_TANH) return gated_exactly(v, v * fmaf(v * v, kTanh3, kTanh1));
   else if constexpr (A == ST_ACT_SILU) return v * fast_rcp(1.0f + fast_exp2(-kLog2e * v));
-  else if constexpr (A == ST_ACT_GELU) return gelu(v);
+  else if constexpr (A == ST_ACT_GELU) return gelu<kF32>(v);
   else if constexpr (A == ST_ACT_GELU_TANH)
     return v * fast_rcp(1.0f + fast_exp2(v * fmaf(v * v, -kTanh3 * kLog2e, -kTanh1 * kLog2e)));
   else return v;
