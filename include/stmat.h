@@ -645,7 +645,7 @@ st_status st_plan_check(const st_plan_t *plan, void *stream, uint32_t *flags);
  * exponential's argument (silu: v; gelu: v^2 / 2; gelu_tanh: 2 sqrt(2 / pi) (v
  * + 0.044715 v^3)), outputs in F32 are within 4 2^-23 (silu), 7 2^-23 (gelu) and
  * (2 |e| + 4) 2^-23 (gelu_tanh); outputs in 16 and 8 bits within (2 |e| + 6)
- * 2^-23, and 0 where exp(|e|) is beyond 2^126. */
+ * 2^-23, and for negative v 0 where exp(|e|) is beyond 2^126. */
 typedef enum st_act {
   ST_ACT_NONE = 0,
   ST_ACT_RELU = 1,      /* v < 0 ? 0 : v */

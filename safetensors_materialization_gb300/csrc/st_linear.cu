@@ -21,9 +21,9 @@
 // read out of one half of TMEM while the next tile's are formed in the other.
 // Few tiles with long sums are shared by the pairs of a cluster, which join
 // their sums as split_kernel's CTAs do.
-// Bound by the power limit where sums are long: 4096 x 4096 x 14336 BF16 258
-// us alone and 280 in a row (1.87 and 1.72 PFLOP/s, tensor pipe 92 % active),
-// 8192 x 14336 x 4096 E4M3 with silu 264 and 296 us (3.64 and 3.25 PFLOP/s, 91
+// Bound by the power limit where sums are long: 4096 x 4096 x 14336 BF16 261
+// us alone and 280 in a row (1.84 and 1.72 PFLOP/s, tensor pipe 93 % active),
+// 8192 x 14336 x 4096 E4M3 with silu 267 and 296 us (3.60 and 3.25 PFLOP/s, 92
 // %); where they are short, by the readout.
 //
 // Both operands are staged 128 bytes of k at a time in the 128-byte swizzled
@@ -549,7 +549,7 @@ __device__ __forceinline__ void put_row(void *base, st_dtype dtype, int64_t at, 
 // pair of columns 2 l, 2 l + 1, or, where a row of y starts at an odd place,
 // 2 l + 1, 2 l + 2 (and the first column alone), so that a pair is one aligned
 // word (5598 x 6526 x 391 BF16 with gelu and residual 145 us column by column,
-// 102 so).
+// 103 so; 109 with gelu's present polynomial).
 __device__ __forceinline__ int rows_from(const LinArgs &a, int64_t m) {
   return static_cast<int>(max(int64_t(0), min(int64_t(32), a.m - m)));
 }

@@ -16,7 +16,7 @@
 // Bound: HBM.  Read + written, of the 6.74 TB/s a copy reaches: norm of 8192 x
 // 4096 BF16 with residual to 8 bits (7 bytes an element) 36.2 us, 6.5 TB/s;
 // of 4096 x 12288 to BF16 60.4 us, 6.7 TB/s; gated activation of 8192 x 14336
-// BF16 to 8 bits 92.6 us, 6.3 TB/s.
+// BF16 to 8 bits 93.5 us, 6.3 TB/s.
 #include <string>
 
 #include "st_ops_device.h"
