@@ -419,6 +419,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     // The MMAs are done with the stages and TMEM, whatever the readout's wait
     // came to.
     if (blocks > 0 && !bar_wait(&done, 0, sum_limit(a.k_blocks))) failed = 1;
+    __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
   }
