@@ -687,6 +687,14 @@ typedef struct st_gated_act_args {
 } st_gated_act_args;
 st_status st_gated_act(const st_gated_act_args *args, void *stream);
 
+/* The same with a scale for every 128 columns of a row, as st_block_linear
+ * takes them: y_dtype is ST_F8_E4M3, scale is NULL and scales, written, has
+ * rows x ceil(cols / 128) entries, row by row (none for rows without columns).
+ * A scale is its block's max(max |v| / 448, 2^-126), NaN for a block with a
+ * NaN.  At most 2^27 columns. */
+st_status st_rms_norm_blocks(const st_rms_norm_args *args, void *stream);
+st_status st_gated_act_blocks(const st_gated_act_args *args, void *stream);
+
 /* Matrix product with a checkpoint's [n, k] weight:
  *   y[i, j] = act(x_scale[i] * w_scale[j] * sum_l x[i, l] * weight[j, l] + bias[j]) + residual[i, j].
  * x and weight are both BF16, both F16, or F8_E4M3 with F8_E4M3 or F8_E5M2;
@@ -735,6 +743,37 @@ st_status st_linear_choose(const st_linear_args *args, int32_t sms, int32_t clus
 /* st_linear in the given form (for tests and measurements): ST_E_INVAL for one
  * that does not exist or has more parts than the sum has runs of 128 bytes. */
 st_status st_linear_as(const st_linear_args *args, const st_linear_form *form, void *stream);
+
+/* Matrix product of 8-bit rows with a checkpoint's [n, k] weight in 8 bits,
+ * both with block scales:
+ *   y[i, j] = act(sum_b x_scale[i, b] * w_scale[j / 128, b] * sum_{l in b} x[i, l] * weight[j, l] + bias[j]) + residual[i, j]
+ * over blocks b of 128 of k (the last one may be shorter).  x is F8_E4M3
+ * (st_rms_norm_blocks, st_gated_act_blocks), weight F8_E4M3 or F8_E5M2 as
+ * st_plan keeps it with ST_KEEP, its scales the checkpoint's.  Conventions,
+ * overlaps, workspace and error word as for st_linear. */
+typedef struct st_block_linear_args {
+  int64_t m, n, k;
+  st_act act;
+  st_dtype x_dtype, w_dtype;
+  st_dtype y_dtype;                 /* BF16, F16 or F32: y and residual */
+  st_dtype bias_dtype;              /* BF16, F16 or F32 */
+  const void *x;        int64_t ldx;
+  const void *w;        int64_t ldw;
+  const float *x_scale; int64_t ldxs; /* [m, ceil(k / 128)] */
+  const float *w_scale; int64_t ldws; /* [ceil(n / 128), ceil(k / 128)] */
+  const void *bias;                 /* n entries, or NULL */
+  const void *residual; int64_t ldr; /* or NULL */
+  void *y;              int64_t ldy;
+  void *workspace;                  /* device memory, 16-byte aligned, of */
+  uint64_t workspace_bytes;         /* at least st_block_linear_workspace; NULL, 0 where that is 0 */
+} st_block_linear_args;
+st_status st_block_linear_workspace(const st_block_linear_args *args, uint64_t *bytes);
+st_status st_block_linear(const st_block_linear_args *args, void *stream);
+/* Its form on a device of `sms` SMs, and the product in a given one, as for
+ * st_linear: split, of 16, 32, 64 or 128 tokens in 1, 2, 4 or 8 parts; dense,
+ * of 64, 128, 192 or 256 weight rows, in 1. */
+st_status st_block_linear_choose(const st_block_linear_args *args, int32_t sms, st_linear_form *form);
+st_status st_block_linear_as(const st_block_linear_args *args, const st_linear_form *form, void *stream);
 
 /* ----------------------------------------------------------------- misc */
 

@@ -1,0 +1,363 @@
+// st_blockrows.cu -- the row operators with an 8-bit output that has a scale
+// for every 128 columns of a row (GB300, sm_103a): what the product with a
+// block-scaled weight takes.
+//
+// Mathematics.  With v the row operator's values (st_rowops.cu) and block b the
+// columns 128 b .. 128 b + 127 of a row:
+//   scale[b] = max(max over b of |v| / 448, 2^-126),  code = e4m3(v / scale[b]).
+// A block is 16 (16-bit inputs) or 32 (binary32) neighbouring threads' vectors,
+// so its largest magnitude is a few shuffles.  The norm's rstd is one positive
+// number per row, known after the row's reduction: max|v| = max|h w| rstd as
+// computed, and the row stays in registers between the two.  The gated
+// activation has no reduction over the row: its rows are cut into pieces.
+//
+// Bound: HBM (7 bytes an element for a 16-bit norm with residual, 5 for a gated
+// activation, and a scale's 4 bytes every 128).
+#include "st_rows_device.h"
+
+namespace stmat {
+namespace {
+
+constexpr int kBlock = 128;      // columns of a scale
+constexpr int kWarps = 8;        // rows of one warp each, in a block
+constexpr int kPieceThreads = 256;
+
+enum Op { kNormOp, kActOp };
+
+struct BlockRowArgs {
+  const void *x, *r, *w;  // norm: x, residual, weight; gate: gate, up
+  void *h;
+  uint8_t *y;
+  float *scales;
+  int64_t ldx, ldr, ldh, ldy, blocks;
+  int64_t rows;
+  int cols;
+  float eps;
+  st_act act;
+  st_dtype w_dtype;
+};
+
+// V elements from column c on of the row that starts at p, which may start at
+// any element: two aligned accesses, shifted.  Those that would leave the row,
+// and all of binary32's, go by element.  Zeros behind the row's end.
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> any_read(const T *p, int c, int cols) {
+  Raw<T, V> out;
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t q = (reinterpret_cast<uintptr_t>(p) / 2) & 7;  // c is a multiple of 8
+    const int from = c - static_cast<int>(q);
+    if (from >= 0 && from + (q ? 16 : 8) <= cols) {
+      const uint4 lo = *reinterpret_cast<const uint4 *>(p + from);
+      const uint4 hi = q ? *reinterpret_cast<const uint4 *>(p + from + 8) : lo;
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, sh = 16 * (q & 1);
+      uint32_t a[6], b[5];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) a[i] = q & 4 ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) b[i] = q & 2 ? a[i + 1] : a[i];
+      uint32_t *u = reinterpret_cast<uint32_t *>(&out);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(b[i], b[i + 1], sh);
+      return out;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) out.e[i] = c + i < cols ? p[c + i] : T(0.0f);
+  return out;
+}
+
+// Eight codes of every lane, from its column c on, in a row that starts at any
+// byte: a lane writes the aligned word that its first codes lie in, with the
+// last codes of the lane before.  The whole warp calls it, with consecutive
+// columns.
+__device__ __forceinline__ void put_codes8(uint8_t *row, int c, int cols, uint64_t codes, int lane) {
+  const int q = static_cast<int>(reinterpret_cast<uintptr_t>(row + c) & 7);
+  const uint64_t before = __shfl_up_sync(~0u, codes, 1);
+  if (q == 0) {
+    if (c + 8 <= cols) *reinterpret_cast<uint64_t *>(row + c) = codes;
+    else
+      for (int j = 0; c + j < cols && j < 8; ++j) row[c + j] = static_cast<uint8_t>(codes >> (8 * j));
+    return;
+  }
+  if (lane > 0 && c + 8 - q <= cols) {
+    *reinterpret_cast<uint64_t *>(row + c - q) = before >> (8 * (8 - q)) | codes << (8 * q);
+  } else {
+    if (lane > 0)
+      for (int j = 0; j < q && c - q + j < cols; ++j) row[c - q + j] = static_cast<uint8_t>(before >> (8 * (8 - q + j)));
+    for (int j = 0; j < 8 - q && c + j < cols; ++j) row[c + j] = static_cast<uint8_t>(codes >> (8 * j));
+  }
+  if (lane == 31)
+    for (int j = 8 - q; j < 8 && c + j < cols; ++j) row[c + j] = static_cast<uint8_t>(codes >> (8 * j));
+}
+
+// V values of h from column c on, by the widest accesses that its row's start
+// allows.
+template <class T, int V>
+__device__ __forceinline__ void put_any(T *p, int c, int cols, const float (&v)[V]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p + c);
+  if (c + V <= cols && at % (V * sizeof(T)) == 0) return store_any<V>(p, kDtype<T>, c, v);
+  if (sizeof(T) == 2 && c + V <= cols && at % 4 == 0) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(p + c);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      u[i] = kDtype<T> == ST_BF16 ? pack_bf16(v[2 * i], v[2 * i + 1]) : pack_f16(v[2 * i], v[2 * i + 1]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float one[1] = {v[i]};
+    if (c + i < cols) store_any<1>(p, kDtype<T>, c + i, one);
+  }
+}
+
+// One row (kWarpRow: of a warp) in registers, NV accesses of V elements a
+// thread; the gated activation's block has columns from blockIdx.y on instead
+// of a whole row.  kAny: rows start anywhere, or end inside an access.
+template <class T, int V, int NV, bool kAny, Op kOp, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kWarps : kOp == kActOp ? kPieceThreads : NV >= 4 ? 512 : kMaxThreads)
+block_row_kernel(const BlockRowArgs a) {
+  const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+  const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x, lane = threadIdx.x & 31;
+  const int first = kOp == kActOp && !kWarpRow ? blockIdx.y * nt * V * NV : 0;
+  wait_for_previous();
+  let_next_start();
+  if (kWarpRow && row >= a.rows) return;
+  if (kOp == kNormOp && !kWarpRow && !kAny && t == 0 && row + kAhead < a.rows) {
+    row_prefetch<T>(a.x, (row + kAhead) * a.ldx, a.cols);
+    if (a.r) row_prefetch<T>(a.r, (row + kAhead) * a.ldr, a.cols);
+  }
+  auto column = [&](int i) { return first + (i * nt + t) * V; };
+  const T *const px = static_cast<const T *>(a.x) + row * a.ldx, *const pr = static_cast<const T *>(a.r) + row * a.ldr;
+  Raw<T, V> x[NV], r[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = column(i);
+    if (c >= a.cols) continue;
+    if constexpr (kAny) {
+      x[i] = any_read<T, V>(px, c, a.cols);
+      if (a.r) r[i] = any_read<T, V>(pr, c, a.cols);
+    } else {
+      x[i] = row_read<T, V>(px, c);
+      if (a.r) r[i] = row_read<T, V>(pr, c);
+    }
+  }
+  float v[NV][V], top[NV];
+  Stat s{0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = column(i);
+    top[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
+    if (c >= a.cols) continue;
+    float o[V];
+    unpack(x[i], v[i]);
+    if (a.r) unpack(r[i], o);
+    if constexpr (kOp == kNormOp) {
+      if (a.r) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] += o[j];
+        if (a.h) {
+          T *const ph = static_cast<T *>(a.h) + row * a.ldh;
+          if constexpr (kAny) put_any<T, V>(ph, c, a.cols, v[i]);
+          else store_any<V>(ph, kDtype<T>, c, v[i]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) s.sum = fmaf(v[i][j], v[i][j], s.sum);
+      if (a.w) {
+        with_type(a.w_dtype, [&](auto zero) {
+          using W = decltype(zero);
+          const W *w = static_cast<const W *>(a.w) + c;
+          if constexpr (kAny) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[j] = c + j < a.cols ? to_float(w[j]) : 0.0f;
+          } else {
+            unpack(*reinterpret_cast<const Raw<W, V> *>(w), o);
+          }
+        });
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] *= o[j];
+      }
+    } else {
+      activate<false>(v[i], a.act);
+      if (a.r) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] *= o[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) top[i] = max_nan(top[i], fabsf(v[i][j]));
+  }
+  float rstd = 1.0f;
+  if constexpr (kOp == kNormOp) {
+    s = kWarpRow ? warp_stat(s) : block_stat(s);
+    rstd = rsqrtf(s.sum / static_cast<float>(a.cols) + a.eps);
+  }
+  uint8_t *const py = a.y + row * a.ldy;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = column(i);
+    // The columns of a warp lie before the row's end or behind it, with the
+    // shuffles' lanes all here.
+    if (c - lane * V >= a.cols) continue;
+#pragma unroll
+    for (int d = kBlock / V / 2; d; d >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(~0u, top[i], d));
+    const float scale = max_nan(top[i] * rstd / kE4M3Max, kMinScale), inv = 1.0f / scale;
+    if (lane % (kBlock / V) == 0 && c < a.cols) a.scales[row * a.blocks + c / kBlock] = scale;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rstd * inv;
+    uint32_t u[V / 4];
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j)
+      u[j] = pack_e4m3(v[i][4 * j], v[i][4 * j + 1]) | pack_e4m3(v[i][4 * j + 2], v[i][4 * j + 3]) << 16;
+    if constexpr (V == 8) {
+      const uint64_t codes = u[0] | static_cast<uint64_t>(u[1]) << 32;
+      if constexpr (kAny) put_codes8(py, c, a.cols, codes, lane);
+      else if (c < a.cols) *reinterpret_cast<uint64_t *>(py + c) = codes;
+    } else if (c < a.cols) {
+      if (!kAny || (c + V <= a.cols && reinterpret_cast<uintptr_t>(py + c) % V == 0)) *reinterpret_cast<uint32_t *>(py + c) = u[0];
+      else
+        for (int j = 0; j < V && c + j < a.cols; ++j) py[c + j] = static_cast<uint8_t>(u[0] >> (8 * j));
+    }
+  }
+}
+
+// A norm's row too long for registers: a warp has a run of 32 columns of four
+// elements, one block of a binary32 or 16-bit row, and the second pass reads
+// the inputs again (each thread its own elements, so that an h in place of an
+// input is written after its last use).
+template <class T>
+__global__ void __launch_bounds__(kMaxThreads) block_row_loop_kernel(const BlockRowArgs a) {
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  wait_for_previous();
+  let_next_start();
+  const T *const px = static_cast<const T *>(a.x) + row * a.ldx, *const pr = static_cast<const T *>(a.r) + row * a.ldr;
+  T *const ph = static_cast<T *>(a.h) + row * a.ldh;
+  uint8_t *const py = a.y + row * a.ldy;
+  auto value = [&](int64_t c) {
+    return c < a.cols ? to_float(px[c]) + (a.r ? to_float(pr[c]) : 0.0f) : 0.0f;
+  };
+  Stat s{0.0f, 0.0f};
+  for (int64_t c0 = threadIdx.x / 32 * kBlock; c0 < a.cols; c0 += kMaxThreads / 32 * kBlock) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = value(c0 + 32 * j + lane);
+      s.sum = fmaf(v, v, s.sum);
+    }
+  }
+  s = block_stat(s);
+  const float rstd = rsqrtf(s.sum / static_cast<float>(a.cols) + a.eps);
+  for (int64_t c0 = threadIdx.x / 32 * kBlock; c0 < a.cols; c0 += kMaxThreads / 32 * kBlock) {
+    float v[4], top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = c0 + 32 * j + lane;
+      v[j] = value(c);
+      if (c >= a.cols) continue;
+      const float h[1] = {v[j]};
+      if (a.h && a.r) store_any<1>(ph, kDtype<T>, c, h);
+      float w[1] = {1.0f};
+      if (a.w) load_any<1>(a.w, a.w_dtype, c, w);
+      v[j] *= w[0];
+      top = max_nan(top, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+    const float scale = max_nan(top * rstd / kE4M3Max, kMinScale), inv = 1.0f / scale;
+    if (lane == 0) a.scales[row * a.blocks + c0 / kBlock] = scale;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = c0 + 32 * j + lane;
+      if (c < a.cols) py[c] = static_cast<uint8_t>(pack_e4m3(v[j] * rstd * inv, 0.0f));
+    }
+  }
+}
+
+// Threads and accesses of a row: as for st_rowops.cu's kernels, a warp for a
+// short row, else blocks of 256 threads so that several rows share an SM, or,
+// with few rows, the shortest way through one.
+template <class T, int V, bool kAny>
+cudaError_t launch_norm(const BlockRowArgs &a, cudaStream_t st) {
+  const int64_t accesses = (int64_t(a.cols) + V - 1) / V;
+  const unsigned rows = static_cast<unsigned>(a.rows), groups = static_cast<unsigned>((a.rows + kWarps - 1) / kWarps);
+  auto threads = [&](int nv) { return static_cast<unsigned>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
+  const int64_t target = a.rows <= 256 ? kMaxThreads : 256;
+  if (accesses <= 32) return launch(block_row_kernel<T, V, 1, kAny, kNormOp, true>, groups, 32 * kWarps, 0, 1, st, a);
+  if (accesses <= 64 && a.rows > 256) return launch(block_row_kernel<T, V, 2, kAny, kNormOp, true>, groups, 32 * kWarps, 0, 1, st, a);
+  if (accesses <= 128 && a.rows > 256) return launch(block_row_kernel<T, V, 4, kAny, kNormOp, true>, groups, 32 * kWarps, 0, 1, st, a);
+  if (accesses <= target) return launch(block_row_kernel<T, V, 1, kAny, kNormOp, false>, rows, threads(1), 0, 1, st, a);
+  if (accesses <= 2 * target) return launch(block_row_kernel<T, V, 2, kAny, kNormOp, false>, rows, threads(2), 0, 1, st, a);
+  if (accesses <= 4 * 512) return launch(block_row_kernel<T, V, 4, kAny, kNormOp, false>, rows, threads(4), 0, 1, st, a);
+  if constexpr (V == 4) {
+    if (accesses <= 8 * 512) return launch(block_row_kernel<T, V, 8, kAny, kNormOp, false>, rows, threads(8), 0, 1, st, a);
+  }
+  return launch(block_row_loop_kernel<T>, rows, kMaxThreads, 0, 1, st, a);
+}
+
+template <class T, int V, int NV, bool kAny>
+cudaError_t launch_pieces(const BlockRowArgs &a, int64_t accesses, cudaStream_t st) {
+  const int64_t pieces = (accesses + kPieceThreads * NV - 1) / (kPieceThreads * NV);
+  // The pieces' threads, as even as whole warps allow.
+  const unsigned nt = static_cast<unsigned>(((accesses + pieces * NV - 1) / (pieces * NV) + 31) / 32 * 32);
+  return launch(block_row_kernel<T, V, NV, kAny, kActOp, false>, dim3(static_cast<unsigned>(a.rows), static_cast<unsigned>(pieces)), nt, 0, 1, st, a);
+}
+
+// Pieces of 256 threads, two accesses a thread of each matrix; one where rows
+// are too few to fill the SMs so.
+template <class T, int V, bool kAny>
+cudaError_t launch_act(const BlockRowArgs &a, cudaStream_t st) {
+  const int64_t accesses = (int64_t(a.cols) + V - 1) / V;
+  const unsigned groups = static_cast<unsigned>((a.rows + kWarps - 1) / kWarps);
+  if (accesses <= 32) return launch(block_row_kernel<T, V, 1, kAny, kActOp, true>, groups, 32 * kWarps, 0, 1, st, a);
+  if (accesses <= 64) return launch(block_row_kernel<T, V, 2, kAny, kActOp, true>, groups, 32 * kWarps, 0, 1, st, a);
+  if (a.rows * accesses <= 152 * 8 * kPieceThreads) return launch_pieces<T, V, 1, kAny>(a, accesses, st);
+  return launch_pieces<T, V, 2, kAny>(a, accesses, st);
+}
+
+template <Op kOp>
+st_status launch_blocks(const BlockRowArgs &a, st_dtype x_dtype, void *stream, const char *op) {
+  const int v = x_dtype == ST_F32 ? 4 : 8;
+  const bool aligned = a.cols % v == 0 && place(a.x, a.ldx, x_dtype, v).aligned() && place(a.y, a.ldy, ST_F8_E4M3, v).aligned() &&
+                       (!a.r || place(a.r, a.ldr, x_dtype, v).aligned()) && (!a.h || place(a.h, a.ldh, x_dtype, v).aligned()) &&
+                       (!a.w || place(a.w, 0, a.w_dtype, v).aligned());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto run = [&](auto zero, auto any) {
+    using T = decltype(zero);
+    constexpr int V = sizeof(T) == 4 ? 4 : 8;
+    if constexpr (kOp == kNormOp) return launch_norm<T, V, decltype(any)::value>(a, st);
+    else return launch_act<T, V, decltype(any)::value>(a, st);
+  };
+  auto typed = [&](auto zero) { return aligned ? run(zero, std::false_type{}) : run(zero, std::true_type{}); };
+  const cudaError_t e = x_dtype == ST_BF16 ? typed(__nv_bfloat16{}) : x_dtype == ST_F16 ? typed(__half{}) : typed(float{});
+  if (e != cudaSuccess)
+    return set_error(ST_E_CUDA, "%s launch (%lld rows): %s: %s", op, (long long)a.rows, cudaGetErrorName(e), cudaGetErrorString(e));
+  return ST_OK;
+}
+
+}  // namespace
+
+st_status launch_rms_norm_blocks(const st_rms_norm_args &p, void *stream) {
+  BlockRowArgs a{};
+  a.x = p.x; a.r = p.residual; a.w = p.weight; a.h = p.h;
+  a.y = static_cast<uint8_t *>(p.y);
+  a.scales = p.scales;
+  a.ldx = p.ldx; a.ldr = p.ldr; a.ldh = p.ldh; a.ldy = p.ldy; a.blocks = (p.cols + kBlock - 1) / kBlock;
+  a.rows = p.rows; a.cols = static_cast<int>(p.cols);
+  a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.weight ? p.w_dtype : p.x_dtype;
+  return launch_blocks<kNormOp>(a, p.x_dtype, stream, "st_rms_norm_blocks");
+}
+
+st_status launch_gated_act_blocks(const st_gated_act_args &p, void *stream) {
+  BlockRowArgs a{};
+  a.x = p.gate; a.r = p.up;
+  a.y = static_cast<uint8_t *>(p.y);
+  a.scales = p.scales;
+  a.ldx = p.ldg; a.ldr = p.ldu; a.ldy = p.ldy; a.blocks = (p.cols + kBlock - 1) / kBlock;
+  a.rows = p.rows; a.cols = static_cast<int>(p.cols);
+  a.act = p.act; a.w_dtype = p.x_dtype;
+  return launch_blocks<kActOp>(a, p.x_dtype, stream, "st_gated_act_blocks");
+}
+
+}  // namespace stmat

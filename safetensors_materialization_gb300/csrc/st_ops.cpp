@@ -11,6 +11,7 @@ namespace {
 // One grid dimension of rows, and tile coordinates that stay in 32 bits.
 constexpr int64_t kMaxRows = 0x7fffff00;
 constexpr int64_t kMaxCols = 0x7fffff00;
+constexpr int64_t kMaxBlockCols = int64_t(1) << 27;  // pieces of rows that one launch has
 
 bool is_float16or32(st_dtype d) { return d == ST_BF16 || d == ST_F16 || d == ST_F32; }
 
@@ -100,6 +101,47 @@ bool overlap(const Bytes &a, const Bytes &b) {
     if (try_status != ST_OK) return try_status; \
   } while (0)
 
+// An output whose rows have a scale for every 128 columns.
+st_status check_block_output(const char *op, st_dtype y, const float *scale, const float *scales, int64_t rows, int64_t cols) {
+  if (cols > kMaxBlockCols) return set_error(ST_E_INVAL, "%s: rows of %lld columns (at most 2^27)", op, (long long)cols);
+  if (y != ST_F8_E4M3) return set_error(ST_E_DTYPE, "%s: the output is F8_E4M3, not %d", op, static_cast<int>(y));
+  if (scale || (rows > 0 && cols > 0 && !scales)) return set_error(ST_E_INVAL, "%s: scales are written, one for every 128 columns, and none is given", op);
+  return check_vector(op, "scales", scales, ST_F32);
+}
+
+st_status check_rms_norm(const char *op, const st_rms_norm_args *a, bool blocks, bool *empty) {
+  if (!a) return set_error(ST_E_INVAL, "%s: NULL arguments", op);
+  ST_TRY(check_sizes(op, a->rows, a->cols));
+  if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: x is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
+  if (a->weight && !is_float16or32(a->w_dtype))
+    return set_error(ST_E_DTYPE, "%s: weight is BF16, F16 or F32, not %d", op, (int)a->w_dtype);
+  if (!(a->eps >= 0.0f)) return set_error(ST_E_INVAL, "%s: eps %g is not a non-negative number", op, (double)a->eps);
+  if (a->h && !a->residual) return set_error(ST_E_INVAL, "%s: h without a residual", op);
+  if (blocks) ST_TRY(check_block_output(op, a->y_dtype, a->scale, a->scales, a->rows, a->cols));
+  else ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales, a->rows));
+  *empty = a->rows == 0 || a->cols == 0;
+  if (*empty) return ST_OK;
+  ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->rows, a->cols, true));
+  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->x_dtype, a->rows, a->cols, true));
+  if (a->weight) ST_TRY(check_vector(op, "weight", a->weight, a->w_dtype));
+  if (a->h) ST_TRY(check_matrix(op, "h", a->h, a->ldh, a->x_dtype, a->rows, a->cols, false));
+  return check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->rows, a->cols, false);
+}
+
+st_status check_gated_act(const char *op, const st_gated_act_args *a, bool blocks, bool *empty) {
+  if (!a) return set_error(ST_E_INVAL, "%s: NULL arguments", op);
+  ST_TRY(check_sizes(op, a->rows, a->cols));
+  if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: gate is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
+  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
+  if (blocks) ST_TRY(check_block_output(op, a->y_dtype, a->scale, a->scales, a->rows, a->cols));
+  else ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales, a->rows));
+  *empty = a->rows == 0 || a->cols == 0;
+  if (*empty) return ST_OK;
+  ST_TRY(check_matrix(op, "gate", a->gate, a->ldg, a->x_dtype, a->rows, a->cols, true));
+  if (a->up) ST_TRY(check_matrix(op, "up", a->up, a->ldu, a->x_dtype, a->rows, a->cols, true));
+  return check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->rows, a->cols, false);
+}
+
 st_status check_linear(const st_linear_args *a, bool *empty) {
   const char *op = "st_linear";
   ST_TRY(check_sizes(op, a->m, a->n));
@@ -146,6 +188,69 @@ st_status check_linear(const st_linear_args *a, bool *empty) {
   return ST_OK;
 }
 
+st_status check_block_linear(const st_block_linear_args *a, bool *empty) {
+  const char *op = "st_block_linear";
+  ST_TRY(check_sizes(op, a->m, a->n));
+  ST_TRY(check_sizes(op, a->m, a->k));
+  if (a->x_dtype != ST_F8_E4M3 || (a->w_dtype != ST_F8_E4M3 && a->w_dtype != ST_F8_E5M2))
+    return set_error(ST_E_DTYPE, "%s: x is F8_E4M3 and weight F8_E4M3 or F8_E5M2 (got %d, %d)", op, (int)a->x_dtype, (int)a->w_dtype);
+  if (!is_float16or32(a->y_dtype)) return set_error(ST_E_DTYPE, "%s: the output is BF16, F16 or F32, not %d", op, (int)a->y_dtype);
+  if (a->bias && !is_float16or32(a->bias_dtype))
+    return set_error(ST_E_DTYPE, "%s: bias is BF16, F16 or F32, not %d", op, (int)a->bias_dtype);
+  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
+  *empty = a->m == 0 || a->n == 0;
+  if (*empty) return ST_OK;
+  const int64_t nb = (a->n + 127) / 128, kb = (a->k + 127) / 128;
+  if (a->k > 0) {
+    ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->m, a->k, true));
+    ST_TRY(check_matrix(op, "weight", a->w, a->ldw, a->w_dtype, a->n, a->k, true));
+    ST_TRY(check_matrix(op, "x_scale", a->x_scale, a->ldxs, ST_F32, a->m, kb, true));
+    ST_TRY(check_matrix(op, "w_scale", a->w_scale, a->ldws, ST_F32, nb, kb, true));
+  }
+  if (a->bias) ST_TRY(check_vector(op, "bias", a->bias, a->bias_dtype));
+  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->y_dtype, a->m, a->n, true));
+  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->m, a->n, false));
+  const Bytes y = matrix_bytes(a->y, a->ldy, a->y_dtype, a->m, a->n);
+  auto apart = [&](const char *name, const Bytes &b) {
+    return overlap(y, b) ? set_error(ST_E_INVAL, "%s: y overlaps %s (it may be the residual, the very matrix, and no other operand)", op, name) : ST_OK;
+  };
+  if (a->k > 0) {
+    ST_TRY(apart("x", matrix_bytes(a->x, a->ldx, a->x_dtype, a->m, a->k)));
+    ST_TRY(apart("weight", matrix_bytes(a->w, a->ldw, a->w_dtype, a->n, a->k)));
+    ST_TRY(apart("x_scale", matrix_bytes(a->x_scale, a->ldxs, ST_F32, a->m, kb)));
+    ST_TRY(apart("w_scale", matrix_bytes(a->w_scale, a->ldws, ST_F32, nb, kb)));
+  }
+  if (a->bias) ST_TRY(apart("bias", array_bytes(a->bias, a->n * st_dtype_size(a->bias_dtype))));
+  if (a->residual && !(a->residual == a->y && (a->m == 1 || a->ldr == a->ldy)))
+    ST_TRY(apart("the residual in part", matrix_bytes(a->residual, a->ldr, a->y_dtype, a->m, a->n)));
+  return ST_OK;
+}
+
+st_status run_block_linear(const st_block_linear_args *a, const st_linear_form *form, void *stream) {
+  const char *op = "st_block_linear";
+  if (!a) return set_error(ST_E_INVAL, "%s: NULL arguments", op);
+  bool empty = false;
+  ST_TRY(check_block_linear(a, &empty));
+  if (empty) return ST_OK;
+  if (form) ST_TRY(check_block_linear_form(*a, *form));
+  const int64_t need = block_linear_workspace(*a);
+  if (need && (!a->workspace || a->workspace_bytes < static_cast<uint64_t>(need)))
+    return set_error(ST_E_INVAL, "%s: rows that are no multiples of 16 bytes apart need a workspace of %lld bytes, %llu given", op,
+                     (long long)need, (unsigned long long)(a->workspace ? a->workspace_bytes : 0));
+  if (need && reinterpret_cast<uintptr_t>(a->workspace) % 16) return set_error(ST_E_ALIGN, "%s: the workspace is not 16-byte aligned", op);
+  if (need) {
+    const Bytes space = array_bytes(a->workspace, static_cast<uint64_t>(need));
+    const int64_t nb = (a->n + 127) / 128, kb = (a->k + 127) / 128;
+    if (overlap(space, matrix_bytes(a->y, a->ldy, a->y_dtype, a->m, a->n)) || overlap(space, matrix_bytes(a->x, a->ldx, a->x_dtype, a->m, a->k)) ||
+        overlap(space, matrix_bytes(a->w, a->ldw, a->w_dtype, a->n, a->k)) || overlap(space, matrix_bytes(a->x_scale, a->ldxs, ST_F32, a->m, kb)) ||
+        overlap(space, matrix_bytes(a->w_scale, a->ldws, ST_F32, nb, kb)) ||
+        (a->bias && overlap(space, array_bytes(a->bias, a->n * st_dtype_size(a->bias_dtype)))) ||
+        (a->residual && overlap(space, matrix_bytes(a->residual, a->ldr, a->y_dtype, a->m, a->n))))
+      return set_error(ST_E_INVAL, "%s: the workspace overlaps an operand", op);
+  }
+  return launch_block_linear(*a, form, stream);
+}
+
 st_status run_linear(const st_linear_args *a, const st_linear_form *form, void *stream) {
   if (!a) return set_error(ST_E_INVAL, "st_linear: NULL arguments");
   bool empty = false;
@@ -174,38 +279,29 @@ st_status run_linear(const st_linear_args *a, const st_linear_form *form, void *
 extern "C" {
 
 st_status st_rms_norm(const st_rms_norm_args *a, void *stream) {
-  if (!a) return set_error(ST_E_INVAL, "st_rms_norm: NULL arguments");
-  const char *op = "st_rms_norm";
-  ST_TRY(check_sizes(op, a->rows, a->cols));
-  if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: x is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
-  if (a->weight && !is_float16or32(a->w_dtype))
-    return set_error(ST_E_DTYPE, "%s: weight is BF16, F16 or F32, not %d", op, (int)a->w_dtype);
-  if (!(a->eps >= 0.0f)) return set_error(ST_E_INVAL, "%s: eps %g is not a non-negative number", op, (double)a->eps);
-  if (a->h && !a->residual) return set_error(ST_E_INVAL, "%s: h without a residual", op);
-  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales, a->rows));
-  if (a->rows == 0) return ST_OK;
-  if (a->cols == 0) return a->scales ? launch_empty_rows(a->scales, a->rows, stream, op) : ST_OK;
-  ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->rows, a->cols, true));
-  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->x_dtype, a->rows, a->cols, true));
-  if (a->weight) ST_TRY(check_vector(op, "weight", a->weight, a->w_dtype));
-  if (a->h) ST_TRY(check_matrix(op, "h", a->h, a->ldh, a->x_dtype, a->rows, a->cols, false));
-  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->rows, a->cols, false));
+  bool empty = false;
+  ST_TRY(check_rms_norm("st_rms_norm", a, false, &empty));
+  if (empty) return a->rows > 0 && a->scales ? launch_empty_rows(a->scales, a->rows, stream, "st_rms_norm") : ST_OK;
   return launch_rms_norm(*a, stream);
 }
 
+st_status st_rms_norm_blocks(const st_rms_norm_args *a, void *stream) {
+  bool empty = false;
+  ST_TRY(check_rms_norm("st_rms_norm_blocks", a, true, &empty));
+  return empty ? ST_OK : launch_rms_norm_blocks(*a, stream);
+}
+
 st_status st_gated_act(const st_gated_act_args *a, void *stream) {
-  if (!a) return set_error(ST_E_INVAL, "st_gated_act: NULL arguments");
-  const char *op = "st_gated_act";
-  ST_TRY(check_sizes(op, a->rows, a->cols));
-  if (!is_float16or32(a->x_dtype)) return set_error(ST_E_DTYPE, "%s: gate is BF16, F16 or F32, not %d", op, (int)a->x_dtype);
-  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
-  ST_TRY(check_output(op, a->y_dtype, a->scale, a->scales, a->rows));
-  if (a->rows == 0) return ST_OK;
-  if (a->cols == 0) return a->scales ? launch_empty_rows(a->scales, a->rows, stream, op) : ST_OK;
-  ST_TRY(check_matrix(op, "gate", a->gate, a->ldg, a->x_dtype, a->rows, a->cols, true));
-  if (a->up) ST_TRY(check_matrix(op, "up", a->up, a->ldu, a->x_dtype, a->rows, a->cols, true));
-  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->rows, a->cols, false));
+  bool empty = false;
+  ST_TRY(check_gated_act("st_gated_act", a, false, &empty));
+  if (empty) return a->rows > 0 && a->scales ? launch_empty_rows(a->scales, a->rows, stream, "st_gated_act") : ST_OK;
   return launch_gated_act(*a, stream);
+}
+
+st_status st_gated_act_blocks(const st_gated_act_args *a, void *stream) {
+  bool empty = false;
+  ST_TRY(check_gated_act("st_gated_act_blocks", a, true, &empty));
+  return empty ? ST_OK : launch_gated_act_blocks(*a, stream);
 }
 
 st_status st_linear_workspace(const st_linear_args *a, uint64_t *bytes) {
@@ -232,6 +328,31 @@ st_status st_linear(const st_linear_args *a, void *stream) { return run_linear(a
 st_status st_linear_as(const st_linear_args *a, const st_linear_form *form, void *stream) {
   if (!form) return set_error(ST_E_INVAL, "st_linear_as: NULL form");
   return run_linear(a, form, stream);
+}
+
+st_status st_block_linear_workspace(const st_block_linear_args *a, uint64_t *bytes) {
+  if (!a || !bytes) return set_error(ST_E_INVAL, "st_block_linear_workspace: NULL argument");
+  bool empty = false;
+  ST_TRY(check_block_linear(a, &empty));
+  *bytes = empty ? 0 : static_cast<uint64_t>(block_linear_workspace(*a));
+  return ST_OK;
+}
+
+st_status st_block_linear_choose(const st_block_linear_args *a, int32_t sms, st_linear_form *form) {
+  if (!a || !form) return set_error(ST_E_INVAL, "st_block_linear_choose: NULL argument");
+  if (sms < 2) return set_error(ST_E_INVAL, "st_block_linear_choose: no device has %d SMs", sms);
+  bool empty = false;
+  ST_TRY(check_block_linear(a, &empty));
+  if (empty) return set_error(ST_E_INVAL, "st_block_linear_choose: a product without rows or columns is not launched");
+  *form = choose_block_linear_form(*a, sms);
+  return ST_OK;
+}
+
+st_status st_block_linear(const st_block_linear_args *a, void *stream) { return run_block_linear(a, nullptr, stream); }
+
+st_status st_block_linear_as(const st_block_linear_args *a, const st_linear_form *form, void *stream) {
+  if (!form) return set_error(ST_E_INVAL, "st_block_linear_as: NULL form");
+  return run_block_linear(a, form, stream);
 }
 
 }  // extern "C"

@@ -16,6 +16,9 @@ constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the smallest scale, so 
 // aligned to their itemsize, rows, cols > 0.
 st_status launch_rms_norm(const st_rms_norm_args &a, void *stream);
 st_status launch_gated_act(const st_gated_act_args &a, void *stream);
+// The same with a scale for every 128 columns: F8_E4M3 output, scales of its own.
+st_status launch_rms_norm_blocks(const st_rms_norm_args &a, void *stream);
+st_status launch_gated_act_blocks(const st_gated_act_args &a, void *stream);
 // 2^-126 to the scales of rows without columns.
 st_status launch_empty_rows(float *scales, int64_t rows, void *stream, const char *op);
 // form: NULL, or a checked one.
@@ -24,5 +27,10 @@ st_status check_linear_form(const st_linear_args &a, const st_linear_form &form)
 st_linear_form choose_linear_form(const st_linear_args &a, int sms, int clusters_of_2, int clusters_of_4);
 // Bytes of workspace the product needs (rows that TMA cannot read).
 int64_t linear_workspace(const st_linear_args &a);
+
+st_status launch_block_linear(const st_block_linear_args &a, const st_linear_form *form, void *stream);
+st_status check_block_linear_form(const st_block_linear_args &a, const st_linear_form &form);
+st_linear_form choose_block_linear_form(const st_block_linear_args &a, int sms);
+int64_t block_linear_workspace(const st_block_linear_args &a);
 
 }  // namespace stmat

@@ -206,9 +206,9 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st, const A &...args) {
+cudaError_t launch(void (*kernel)(P...), dim3 blocks, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st, const A &...args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
+  cfg.gridDim = blocks;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -19,19 +19,12 @@
 // BF16 to 8 bits 93.5 us, 6.3 TB/s.
 #include <string>
 
-#include "st_ops_device.h"
+#include "st_rows_device.h"
 
 namespace stmat {
 namespace {
 
-constexpr int kMaxThreads = 1024;
 constexpr int kRowsPerBlock = 8;  // rows of one warp each
-// A block brings the inputs of the row this far ahead into L2, so that HBM is
-// kept busy while the rows on the SMs are reduced and written (8192 x 4096
-// norm 37.9 -> 36.2 us, 8192 x 14336 gated activation 101 -> 95.5 us; the same
-// within 1 % from 38 to 228 rows, slower from 456 rows of 48 KiB on).
-constexpr int kAhead = 128;
-
 // The operators: the norm, the gated activation, and that with an F32 output
 // (exact_act).
 enum Op { kNormOp, kActOp, kActF32Op };
@@ -57,29 +50,6 @@ struct RowArgs {
   st_act act;
   st_dtype w_dtype, y_dtype;
 };
-
-struct Stat {
-  float sum, top;  // sum of squares (norm), largest magnitude
-};
-
-__device__ __forceinline__ Stat warp_stat(Stat s) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    s.sum += __shfl_xor_sync(~0u, s.sum, d);
-    s.top = max_nan(s.top, __shfl_xor_sync(~0u, s.top, d));
-  }
-  return s;
-}
-
-// The block's joint statistics, in a fixed order.
-__device__ __forceinline__ Stat block_stat(Stat s) {
-  __shared__ Stat part[kMaxThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  s = warp_stat(s);
-  if (lane == 0) part[warp] = s;
-  __syncthreads();
-  return warp_stat(lane < warps ? part[lane] : Stat{0.0f, 0.0f});
-}
 
 // What every value of the row is multiplied by before it is stored: rstd (1
 // for the gated activation), then 1 / scale (1 unless 8 bits).  Two factors,
@@ -113,9 +83,6 @@ template <Op kOp>
 __device__ __forceinline__ float scaled(float v, Factor f) {
   return (kOp == kNormOp ? v * f.rstd : v) * f.inv;
 }
-
-template <class T>
-constexpr st_dtype kDtype = sizeof(T) == 4 ? ST_F32 : std::is_same<T, __half>::value ? ST_F16 : ST_BF16;
 
 // Writes the elements of V values from column c on that the row has.
 template <int V>
@@ -167,16 +134,6 @@ __device__ __forceinline__ void row_values(const RowArgs &a, int64_t row, int c,
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) s.top = max_nan(s.top, fabsf(v[i]));
-}
-
-template <class T, int V>
-__device__ __forceinline__ Raw<T, V> row_read(const void *p, int64_t at) {
-  return *reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(p) + at);
-}
-
-template <class T>
-__device__ __forceinline__ void row_prefetch(const void *p, int64_t at, int cols) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const T *>(p) + at), "r"(cols * static_cast<int>(sizeof(T))) : "memory");
 }
 
 // V elements of which the row has those at columns 0 .. cols - 1; zeros else.
@@ -335,18 +292,6 @@ cudaError_t launch_typed(const RowArgs &a, cudaStream_t st) {
   if (accesses <= 4 * block_threads(4)) return launch_rows<T, V, 4, kSkew, kOp>(a, threads(4), st);
   if (accesses <= kMost * block_threads(kMost)) return launch_rows<T, V, kMost, kSkew, kOp>(a, threads(kMost), st);
   return launch(row_loop_kernel<T, kSkew ? 1 : V, kOp>, static_cast<unsigned>(a.rows), kMaxThreads, 0, 1, st, a);
-}
-
-// Where rows start, in elements modulo an access of V.  Contiguous rows of an
-// odd length start at the same places in every matrix (5977 x 2407 BF16 norm
-// to 8 bits 15.9 us; element by element 30.9).
-struct Place {
-  int64_t at, step;
-  bool operator==(const Place &o) const { return at == o.at && step == o.step; }
-  bool aligned() const { return at == 0 && step == 0; }
-};
-Place place(const void *p, int64_t ld, st_dtype dtype, int v) {
-  return {static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / st_dtype_size(dtype) % v), ld % v};
 }
 
 template <class T, Op kOp>

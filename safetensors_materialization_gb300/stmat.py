@@ -124,6 +124,15 @@ class LinearForm(C.Structure):
     _fields_ = [("kernel", C.c_int32), ("width", C.c_int32), ("splits", C.c_int32)]
 
 
+class BlockLinearArgs(C.Structure):
+    _fields_ = [("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64), ("act", C.c_int), ("x_dtype", C.c_int),
+                ("w_dtype", C.c_int), ("y_dtype", C.c_int), ("bias_dtype", C.c_int), ("x", C.c_void_p),
+                ("ldx", C.c_int64), ("w", C.c_void_p), ("ldw", C.c_int64), ("x_scale", C.c_void_p),
+                ("ldxs", C.c_int64), ("w_scale", C.c_void_p), ("ldws", C.c_int64),
+                ("bias", C.c_void_p), ("residual", C.c_void_p), ("ldr", C.c_int64), ("y", C.c_void_p),
+                ("ldy", C.c_int64), ("workspace", C.c_void_p), ("workspace_bytes", C.c_uint64)]
+
+
 LINEAR_KERNELS = ("split", "dense")
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
@@ -187,6 +196,12 @@ def lib():
             "st_files_prefetch": [P, U64, U64, U32],
             "st_rms_norm": [C.POINTER(RmsNormArgs), P],
             "st_gated_act": [C.POINTER(GatedActArgs), P],
+            "st_rms_norm_blocks": [C.POINTER(RmsNormArgs), P],
+            "st_gated_act_blocks": [C.POINTER(GatedActArgs), P],
+            "st_block_linear": [C.POINTER(BlockLinearArgs), P],
+            "st_block_linear_workspace": [C.POINTER(BlockLinearArgs), C.POINTER(U64)],
+            "st_block_linear_choose": [C.POINTER(BlockLinearArgs), I, C.POINTER(LinearForm)],
+            "st_block_linear_as": [C.POINTER(BlockLinearArgs), C.POINTER(LinearForm), P],
             "st_linear": [C.POINTER(LinearArgs), P],
             "st_linear_workspace": [C.POINTER(LinearArgs), C.POINTER(U64)],
             "st_linear_choose": [C.POINTER(LinearArgs), I, I, I, C.POINTER(LinearForm)],
@@ -891,9 +906,11 @@ class _Ops:
         # 0.1 us each; torch.cuda.current_stream() takes 11
         self.stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p)
-        self.rms_norm, self.gated_act, self.linear, self.linear_workspace = (
-            call((n, lib())) for n in ("st_rms_norm", "st_gated_act", "st_linear", "st_linear_workspace"))
-        self.linear_as = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p, C.c_void_p)(("st_linear_as", lib()))
+        for n in ("rms_norm", "gated_act", "linear", "linear_workspace", "rms_norm_blocks", "gated_act_blocks",
+                  "block_linear", "block_linear_workspace"):
+            setattr(self, n, call(("st_" + n, lib())))
+        call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p, C.c_void_p)
+        self.linear_as, self.block_linear_as = call(("st_linear_as", lib())), call(("st_block_linear_as", lib()))
 
 
 def _ops():
@@ -1007,19 +1024,31 @@ class _On:
         return got
 
 
-def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stream=None):
+_BLOCK = 128
+
+
+def _check_block(block, y_code, scale):
+    if block != _BLOCK:
+        raise _invalid(f"block={block!r}: a scale is for {_BLOCK} columns")
+    if y_code != _E4M3 or scale is not None:
+        raise _invalid("scales for blocks of columns are written, with dst F8_E4M3; none can be given")
+
+
+def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stream=None, block=None):
     """st_rms_norm on the rows of x (BF16, F16 or F32; leading dimensions are
     rows): h = x + residual, y = h * weight / sqrt(mean(h^2) + eps).
 
     dst: "BF16", "F16", "F32" or "F8_E4M3" (default: x's dtype).  F8_E4M3 with
     scale None writes one scale per row; scale: a one-element F32 tensor to
-    use instead.  Returns (y, scales or None, h in x's dtype, or None without
-    a residual); y * scales[..., None] stands for the normed rows.  No gradient
-    passes through."""
+    use instead; block=128: one scale for every 128 columns of a row, as
+    block_linear takes them (st_rms_norm_blocks; scales has ceil(columns / 128)
+    in place of the last dimension).  Returns (y, scales or None, h in x's dtype,
+    or None without a residual); y * scales[..., None] stands for the normed rows.
+    No gradient passes through."""
     ops = _OPS or _ops()
     gpu = x.get_device()
     if stream is not None or gpu < 0 or gpu != ops.device():
-        return _On(ops.torch, stream, gpu, "x").run(lambda: rms_norm(x, weight, eps, residual, dst, scale),
+        return _On(ops.torch, stream, gpu, "x").run(lambda: rms_norm(x, weight, eps, residual, dst, scale, block=block),
                                                     (x, weight, residual, scale))
     codes, shape, x_type = ops.codes, x.shape, x.dtype
     px, ldx, rows, cols = _matrix(x, "x")
@@ -1036,27 +1065,33 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
         h = _new(x, shape, x_type, ops)
         ph = h.data_ptr()
     y = _new(x, shape, y_type, ops)
+    call = ops.rms_norm
+    if block is not None:
+        _check_block(block, y_code, scale)
+        call = ops.rms_norm_blocks
     if scale is not None:
         ps = _vector(scale, "scale", gpu, 1, _F32, codes)[0]
     elif y_code == _E4M3:
-        scales = ops.empty(shape[:-1], dtype=ops.torch.float32, device=x.device)
+        scales = ops.empty(shape[:-1] if block is None else shape[:-1] + (-(-cols // _BLOCK),), dtype=ops.torch.float32,
+                           device=x.device)
         pss = scales.data_ptr()
-    code = ops.rms_norm(_NORM_ARGS.pack(rows, cols, eps, x_code, w_code, y_code, px, ldx, pr, ldr, pw, ph, cols,
+    code = call(_NORM_ARGS.pack(rows, cols, eps, x_code, w_code, y_code, px, ldx, pr, ldr, pw, ph, cols,
                                         y.data_ptr(), cols, ps, pss), ops.stream(gpu))
     if code:
         _check(code)
     return y, scales, h
 
 
-def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
+def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None, block=None):
     """st_gated_act: y = act(gate) * up (act(gate) without up) on rows of BF16,
     F16 or F32; gate and up may be the halves of one product's columns.  act:
-    "none", "relu", "silu", "gelu" or "gelu_tanh"; dst and scale as for
+    "none", "relu", "silu", "gelu" or "gelu_tanh"; dst, scale and block as for
     rms_norm.  Returns (y, scales or None).  No gradient passes through."""
     ops = _OPS or _ops()
     gpu = gate.get_device()
     if stream is not None or gpu < 0 or gpu != ops.device():
-        return _On(ops.torch, stream, gpu, "gate").run(lambda: gated_act(gate, up, act, dst, scale), (gate, up, scale))
+        return _On(ops.torch, stream, gpu, "gate").run(lambda: gated_act(gate, up, act, dst, scale, block=block),
+                                                       (gate, up, scale))
     shape, x_type = gate.shape, gate.dtype
     pg, ldg, rows, cols = _matrix(gate, "gate")
     y_type, y_code = _dst(dst, x_type, ops)
@@ -1067,12 +1102,17 @@ def gated_act(gate, up=None, act="silu", dst=None, scale=None, stream=None):
             raise _invalid(f"up: {tuple(up.shape)} {up.dtype}, gate: {tuple(shape)} {x_type}")
         pu, ldu, _, _ = _matrix(up, "up", gpu)
     y = _new(gate, shape, y_type, ops)
+    call = ops.gated_act
+    if block is not None:
+        _check_block(block, y_code, scale)
+        call = ops.gated_act_blocks
     if scale is not None:
         ps = _vector(scale, "scale", gpu, 1, _F32, ops.codes)[0]
     elif y_code == _E4M3:
-        scales = ops.empty(shape[:-1], dtype=ops.torch.float32, device=gate.device)
+        scales = ops.empty(shape[:-1] if block is None else shape[:-1] + (-(-cols // _BLOCK),), dtype=ops.torch.float32,
+                           device=gate.device)
         pss = scales.data_ptr()
-    code = ops.gated_act(_ACT_ARGS.pack(rows, cols, ACTS.get(act, -1), ops.codes.get(x_type, -1), y_code, pg, ldg, pu, ldu,
+    code = call(_ACT_ARGS.pack(rows, cols, ACTS.get(act, -1), ops.codes.get(x_type, -1), y_code, pg, ldg, pu, ldu,
                                         y.data_ptr(), cols, ps, pss), ops.stream(gpu))
     if code:
         _check(code)
@@ -1100,6 +1140,43 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
         return _On(ops.torch, stream, gpu, "x").run(
             lambda: linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out, form=form),
             (x, weight, x_scale, w_scale, bias, residual, out))
+    return _product(ops, gpu, False, x, weight, x_scale, w_scale, bias, act, residual, dst, out, form)
+
+
+def block_linear(x, weight, x_scale, w_scale, bias=None, act="none", residual=None, dst=None, out=None, stream=None,
+                 form=None):
+    """st_block_linear: act(x' @ weight'.T + bias) + residual with x' = x and
+    weight' = weight times their scales for blocks of 128: a block-scaled FP8
+    checkpoint's [n, k] weight as stored.
+
+    x: F8_E4M3 rows (rms_norm and gated_act with block=128), x_scale their F32
+    scales, [..., ceil(k / 128)].  weight: F8_E4M3 or F8_E5M2, w_scale its F32
+    scales, [ceil(n / 128), ceil(k / 128)] (an expanded one is one scale for
+    all).  The rest as for linear; form: (kernel, width, splits) in place of the
+    library's choice (block_linear_choice)."""
+    ops = _OPS or _ops()
+    gpu = x.get_device()
+    if stream is not None or gpu < 0 or gpu != ops.device():
+        return _On(ops.torch, stream, gpu, "x").run(
+            lambda: block_linear(x, weight, x_scale, w_scale, bias, act, residual, dst, out, form=form),
+            (x, weight, x_scale, w_scale, bias, residual, out))
+    return _product(ops, gpu, True, x, weight, x_scale, w_scale, bias, act, residual, dst, out, form)
+
+
+def _scales(t, name, gpu, rows, cols):
+    """(address, elements between rows) of [rows, cols] F32 scales; an expanded
+    matrix of one scale is no such rows, and is written out."""
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        t = t.contiguous()
+    p, ld, n, c = _matrix(t, name, gpu)
+    if n != rows or c != cols:
+        raise _invalid(f"{name}: {tuple(t.shape)}, {rows} rows of {cols} are needed")
+    if str(t.dtype) != "torch.float32":
+        raise StmatError(6, f"{name}: {t.dtype} is not F32")
+    return p, ld, t
+
+
+def _product(ops, gpu, block, x, weight, x_scale, w_scale, bias, act, residual, dst, out, form):
     codes, x_type = ops.codes, x.dtype
     px, ldx, m, k = _matrix(x, "x")
     pw, ldw, n, wk = _matrix(weight, "weight", gpu)
@@ -1108,10 +1185,14 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     x_code = codes.get(x_type, -1)
     pxs = nxs = pws = nws = pb = pr = ldr = 0
     b_code = 11
-    if x_scale is not None:
-        pxs, nxs, _ = _vector(x_scale, "x_scale", gpu, m, _F32, codes, True)
-    if w_scale is not None:
-        pws, nws, _ = _vector(w_scale, "w_scale", gpu, n, _F32, codes, True)
+    if block:
+        pxs, nxs, x_scale = _scales(x_scale, "x_scale", gpu, m, -(-k // _BLOCK))
+        pws, nws, w_scale = _scales(w_scale, "w_scale", gpu, -(-n // _BLOCK), -(-k // _BLOCK))
+    else:
+        if x_scale is not None:
+            pxs, nxs, _ = _vector(x_scale, "x_scale", gpu, m, _F32, codes, True)
+        if w_scale is not None:
+            pws, nws, _ = _vector(w_scale, "w_scale", gpu, n, _F32, codes, True)
     if bias is not None:
         pb, _, b_code = _vector(bias, "bias", gpu, n, _FLOATS, codes)
     shape = x.shape[:-1] + (n,)
@@ -1135,7 +1216,7 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
     item = x.element_size()
     if m and n and k and ((px | pw | ldx * item | ldw * item) & 15 or not ldx or not ldw):
         need = C.c_uint64()
-        code = ops.linear_workspace(_LINEAR_ARGS.pack(*args, 0, 0), C.addressof(need))
+        code = (ops.block_linear_workspace if block else ops.linear_workspace)(_LINEAR_ARGS.pack(*args, 0, 0), C.addressof(need))
         if code:
             _check(code)
         size = need.value
@@ -1143,10 +1224,10 @@ def linear(x, weight, x_scale=None, w_scale=None, bias=None, act="none", residua
             workspace = ops.empty(size, dtype=ops.torch.uint8, device=x.device)
             space = workspace.data_ptr()
     if form is None:
-        code = ops.linear(_LINEAR_ARGS.pack(*args, space, size), ops.stream(gpu))
+        code = (ops.block_linear if block else ops.linear)(_LINEAR_ARGS.pack(*args, space, size), ops.stream(gpu))
     else:
         form = LinearForm(LINEAR_KERNELS.index(form[0]) if form[0] in LINEAR_KERNELS else -1, *form[1:])
-        code = ops.linear_as(_LINEAR_ARGS.pack(*args, space, size), C.addressof(form), ops.stream(gpu))
+        code = (ops.block_linear_as if block else ops.linear_as)(_LINEAR_ARGS.pack(*args, space, size), C.addressof(form), ops.stream(gpu))
     if code:
         _check(code)
     return out
@@ -1161,4 +1242,15 @@ def linear_choice(m, n, k, dtype="BF16", sms=152, clusters=(36, 15)):
                       w=2 * at, ldw=k, y=3 * at, ldy=n)
     form = LinearForm()
     _check(lib().st_linear_choose(C.byref(args), sms, *clusters, C.byref(form)))
+    return LINEAR_KERNELS[form.kernel], form.width, form.splits
+
+
+def block_linear_choice(m, n, k, sms=152):
+    """st_block_linear_choose: the (kernel, width, splits) that block_linear
+    takes for m rows of x through an [n, k] weight on a device of so many SMs."""
+    at, kb = 1 << 40, -(-k // _BLOCK)
+    args = BlockLinearArgs(m=m, n=n, k=k, x_dtype=_E4M3, w_dtype=_E4M3, y_dtype=10, x=at, ldx=k, w=2 * at, ldw=k,
+                           x_scale=3 * at, ldxs=kb, w_scale=4 * at, ldws=kb, y=5 * at, ldy=n)
+    form = LinearForm()
+    _check(lib().st_block_linear_choose(C.byref(args), sms, C.byref(form)))
     return LINEAR_KERNELS[form.kernel], form.width, form.splits
