@@ -7,8 +7,8 @@
 // A block's scales are binary32 numbers, which the tensor core cannot apply: a
 // stage of 128 columns is one block, its products are summed by the tensor
 // core alone (four MMAs), and the block's sums go from TMEM through one
-// multiplication and addition each into registers, while the next block's are
-// formed in the other half of TMEM.
+// multiplication and addition each into registers, while the next blocks'
+// are formed elsewhere in TMEM.
 //
 // block_split_kernel, few tokens: as st_linear's split_kernel the weight's rows
 // (128 a tile, so one scale a block) are the MMA's rows and the tokens its
@@ -36,8 +36,8 @@ constexpr int kPairMaxN = 256;       // weight rows per pair, a multiple of 64
 constexpr int kDenseSumWarps = 8;
 constexpr int kDenseMmaWarp = 8, kDenseCopyWarp = 9, kDenseThreads = 384;
 // Three warpgroups start with 168 registers a thread; the two that hold sums
-// take 224, the third gives the rest (2 x 224 + 56 = 3 x 168).
-constexpr int kSumRegisters = 224, kFeedRegisters = 56;
+// take 240, the third gives the rest (2 x 240 + 24 = 3 x 168).
+constexpr int kSumRegisters = 240, kFeedRegisters = 24;
 constexpr int kDenseSmem = 192 * 1024;  // the ring of stages
 
 struct BlockArgs : OutArgs {
@@ -290,25 +290,26 @@ __device__ __forceinline__ TileAt tile_at(const BlockArgs &a, int t) {
   return {int64_t(g * kGroup + in % rows) * kPairM, int64_t(in / rows) * W};
 }
 
-// Issues the read of 16 columns; they are there after tmem_wait().
-__device__ __forceinline__ void tmem_issue16(uint32_t addr, uint32_t (&v)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+// Issues the read of 32 columns; they are there after tmem_wait32().
+__device__ __forceinline__ void tmem_issue32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+                 "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]),
+                 "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+                 "=r"(v[30]), "=r"(v[31])
                : "r"(addr));
 }
 // (The values pass through the wait, so that no use of them is moved before it.)
-__device__ __forceinline__ void tmem_wait16(uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
                :: "memory");
-}
-// acc += v s, two values an instruction.
-__device__ __forceinline__ void add_scaled(float2 &acc, uint32_t lo, uint32_t hi, float s) {
-  uint64_t &c = reinterpret_cast<uint64_t &>(acc);
-  asm("{\n .reg .b64 v, s;\n mov.b64 v, {%1, %2};\n mov.b64 s, {%3, %3};\n fma.rn.f32x2 %0, v, s, %0;\n}"
-      : "+l"(c) : "r"(lo), "r"(hi), "f"(s));
 }
 
 // W: weight rows of a tile.  kF32: y's type, with an activation (exact_act).
@@ -318,9 +319,12 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
                    const __grid_constant__ BlockArgs a) {
   constexpr int kHalf = W / 2;       // columns of a thread; weight rows of a CTA's stage
   constexpr int kStageBytes = (128 + kHalf) * kStageK;
+  // Blocks whose sums TMEM holds (8192 x 14336 x 4096 by tiles of 128: two 519
+  // us, four 481).
+  constexpr int kBuffers = W <= 128 ? 4 : 2, kBufferColumns = 512 / kBuffers;
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums[kBuffers], taken[kBuffers];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
   __shared__ __align__(16) uint32_t turn[kDenseSumWarps][32][17];
@@ -334,7 +338,7 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
       bar_init(&full[i], 1);
       bar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBuffers; ++i) {
       bar_init(&sums[i], 1);
       bar_init(&taken[i], 2 * kDenseSumWarps);
     }
@@ -372,10 +376,10 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
       const bool two = edge < kHalf && first + edge < a.n;
       const float *xs = a.x_scale + (row ? m : 0) * a.ldxs, *ws = a.w_scale + (first < a.n ? first / kBlockK : 0) * a.ldws;
       float nx = xs[0], n0 = ws[0], n1 = two ? ws[a.ldws] : 0.0f;
-      float2 acc[kHalf / 2];
+      float acc[kHalf];
 #pragma unroll
-      for (int j = 0; j < kHalf / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-      for (int b = 0; b < a.k_blocks; ++b, sum.next(2)) {
+      for (int j = 0; j < kHalf; ++j) acc[j] = 0.0f;
+      for (int b = 0; b < a.k_blocks; ++b, sum.next(kBuffers)) {
         const float s0 = nx * n0, s1 = nx * n1;
         if (b + 1 < a.k_blocks) {
           nx = xs[b + 1], n0 = ws[b + 1];
@@ -383,23 +387,21 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
         }
         if (!bar_wait(&sums[sum.at], sum.phase, sum_limit(a.k_blocks))) { ok = false; break; }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t from = lanes + sum.at * kPairMaxN;
-        uint32_t v[2][16];
-        tmem_issue16(from, v[0]);
+        const uint32_t from = lanes + sum.at * kBufferColumns;
+        uint32_t v[32];
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 16) {
-          uint32_t(&now)[16] = v[c / 16 & 1];
-          tmem_wait16(now);
-          if (c + 16 < kHalf) tmem_issue16(from + c + 16, v[(c / 16 & 1) ^ 1]);
-          else {
-            // The half of TMEM is given back as soon as this warp has read its part.
+        for (int c = 0; c < kHalf; c += 32) {
+          tmem_issue32(from + c, v);
+          tmem_wait32(v);
+          if (c + 32 >= kHalf) {
+            // The buffer is given back as soon as this warp has read its part.
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) peer_arrive(taken_at + 8 * sum.at);
           }
           const float s = kHalf > 32 && W % 256 != 0 && c >= edge ? s1 : s0;
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) add_scaled(acc[(c + j) / 2], now[j], now[j + 1], s);
+          for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[j]), s, acc[c + j]);
         }
       }
       if (!ok) break;
@@ -418,7 +420,7 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
         }
         float v[kChunk];
 #pragma unroll
-        for (int j = 0; j < kChunk; j += 2) v[j] = acc[(c + j) / 2].x, v[j + 1] = acc[(c + j) / 2].y;
+        for (int j = 0; j < kChunk; ++j) v[j] = acc[c + j];
         if (a.bias) {
           float bl[1] = {0.0f};
           if (n0c + lane < a.n) load_any<1>(a.bias, a.bias_dtype, n0c + lane, bl);
@@ -478,12 +480,12 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
         Ring r, sum;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
-          for (int b = 0; b < a.k_blocks; ++b, r.next(a.stages), sum.next(2)) {
+          for (int b = 0; b < a.k_blocks; ++b, r.next(a.stages), sum.next(kBuffers)) {
             if (!bar_wait(&full[r.at], r.phase) || !bar_wait(&taken[sum.at], sum.phase ^ 1)) { ok = false; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint64_t xd = tile_desc(smem + r.at * kStageBytes), wd = xd + (128 * kStageK >> 4);
   #pragma unroll
-            for (int j = 0; j < kStageK / 32; ++j) pair_mma<true>(tmem + sum.at * kPairMaxN, xd + 2 * j, wd + 2 * j, a.idesc, j > 0);
+            for (int j = 0; j < kStageK / 32; ++j) pair_mma<true>(tmem + sum.at * kBufferColumns, xd + 2 * j, wd + 2 * j, a.idesc, j > 0);
             pair_commit(&empty[r.at], 0);
             pair_commit(&sums[sum.at], 0);
           }
@@ -568,11 +570,14 @@ st_linear_form choose_block_linear_form(const st_block_linear_args &p, int sms) 
     while (splits < kMaxSplit && tiles * splits <= sms && k_blocks / (splits * 2) >= 4) splits *= 2;
     return {ST_LINEAR_SPLIT, width, splits};
   }
+  // Rounds of tiles, each as long as its blocks (ns a block, 8192 x 14336 x
+  // 4096: tiles of 64 to 256 rows 824, 481, 463, 401 us).
+  static constexpr double kNs[] = {270, 313, 452, 522};
   int width = 0;
   double best = 0;
   for (int w = kPairMaxN; w >= 64; w -= 64) {
     const int64_t tiles = (p.m + kPairM - 1) / kPairM * ((p.n + w - 1) / w);
-    const double all = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * std::max(1.08 * (128 + w / 2), 0.87 * w);
+    const double all = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * kNs[w / 64 - 1];
     if (width == 0 || all < best) width = w, best = all;
   }
   return {ST_LINEAR_DENSE, width, 1};
