@@ -593,9 +593,9 @@ st_status st_materialize_noalloc(const void *data_dev, const st_plan_t *plan, vo
 /* No counterpart on the pages (the library's own status for the calls that
  * use its static array).  Reads and clears the error word of the
  * library's static device array on the current device: the device flags of
- * every st_materialize_noalloc, st_load_tensors and st_linear call since the
- * last read (bits 0 and 1 as for st_plan_check; bit 2 = a bounded wait in
- * st_linear gave up, its y is incomplete).  All of these calls share the one
+ * every st_materialize_noalloc, st_load_tensors, st_linear, st_block_linear and
+ * st_moe call since the last read (bits 0 and 1 as for st_plan_check; bit 2 = a
+ * bounded wait in one of the last three gave up, its y is incomplete).  All of these calls share the one
  * word, so whoever reads it reads and clears the others' flags too.
  * Copies the word to the host on `stream` and waits for the stream, so every
  * such call queued on it before has finished; calls on other streams are
@@ -774,6 +774,54 @@ st_status st_block_linear(const st_block_linear_args *args, void *stream);
  * of 64, 128, 192 or 256 weight rows, in 1. */
 st_status st_block_linear_choose(const st_block_linear_args *args, int32_t sms, st_linear_form *form);
 st_status st_block_linear_as(const st_block_linear_args *args, const st_linear_form *form, void *stream);
+
+/* A mixture-of-experts layer for a few tokens (up to ST_MOE_MAX_TOKENS; for
+ * more, group the tokens by expert and run st_linear or st_block_linear):
+ *   l = x router^T;  s = softmax(l) or sigmoid(l)
+ *   chosen: the top_k experts with the largest s + router_bias, by size (of
+ *           equal ones the lowest index, a NaN before all numbers)
+ *   p = factor * s / (normalize ? sum of the chosen s : 1)
+ *   y = sum over the chosen e of p_e down_e (act(gate_e x) * (up_e x)) + residual
+ * Weights are 16-bit (x's dtype), or F8_E4M3 or F8_E5M2 with a scale for every
+ * 128 x 128 block; x and the values between the products are not rounded to 8
+ * bits for them (within 2^-12 of a value and 2^-21 of the largest of its run of
+ * 128).  Values between the products that are not finite make the token's y NaN.
+ * Logits are summed with their rounding errors (products that leave binary32's
+ * range are not).  y may be the very matrix of the residual and overlap no other
+ * operand.  Four launches; the same bits on every run. */
+#define ST_MOE_MAX_TOKENS 64
+typedef enum st_moe_score { ST_MOE_SOFTMAX = 0, ST_MOE_SIGMOID = 1 } st_moe_score;
+/* The experts' matrices: [rows, k] each, `expert` elements apart, with `ld`
+ * between rows; address and both distances multiples of 16 bytes. */
+typedef struct st_moe_weight {
+  const void *w;
+  int64_t expert, ld;
+  const float *scale;               /* 8 bits: [experts, ceil(rows / 128), ceil(k / 128)], */
+  int64_t scale_expert, scale_row, scale_col; /* so many entries apart (0: one for all); else NULL */
+} st_moe_weight;
+typedef struct st_moe_args {
+  int64_t tokens, hidden, inter, experts, top_k; /* at most 64, 2^24, 2^24, 1024 and 32 */
+  st_act act;
+  st_moe_score score;
+  int32_t normalize;
+  float factor;
+  st_dtype x_dtype;                 /* BF16 or F16 */
+  st_dtype router_dtype;            /* BF16, F16 or F32 */
+  st_dtype w_dtype;                 /* x_dtype, F8_E4M3 or F8_E5M2 */
+  st_dtype y_dtype;                 /* BF16, F16 or F32: y and residual */
+  const void *x;        int64_t ldx;
+  const void *router;   int64_t ld_router; /* [experts, hidden] */
+  const float *router_bias;         /* experts entries, or NULL: 0 */
+  st_moe_weight gate, up, down;     /* [inter, hidden] (up.w NULL: 1), [hidden, inter] */
+  const void *residual; int64_t ldr; /* or NULL */
+  void *y;              int64_t ldy;
+  int32_t *chosen;                  /* [tokens, top_k], written, or NULL */
+  float *weights;                   /* p of the chosen, likewise */
+  void *workspace;                  /* device memory, 256-byte aligned, of */
+  uint64_t workspace_bytes;         /* at least st_moe_workspace */
+} st_moe_args;
+st_status st_moe_workspace(const st_moe_args *args, uint64_t *bytes);
+st_status st_moe(const st_moe_args *args, void *stream);
 
 /* ----------------------------------------------------------------- misc */
 

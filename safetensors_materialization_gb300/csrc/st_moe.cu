@@ -1,0 +1,1049 @@
+// st_moe.cu -- a mixture-of-experts layer for a few tokens, from its router to
+// the sum of its experts, for GB300 (sm_103a).
+//
+//   l = x router^T,  s = softmax(l) or sigmoid(l)
+//   chosen: the top_k experts with the largest s + router_bias,  p = factor s / (sum of the chosen s, or 1)
+//   y = sum over the chosen e of  p_e down_e (act(gate_e x) (up_e x))  + residual
+//
+// A few tokens choose most of a batch's experts once or twice, so the layer is
+// as long as the chosen experts' weights take to come from HBM.  Four launches,
+// each of which starts while the one before it ends:
+//   logits_kernel  the router's product, and x in the columns (below) that the
+//                  tensor core takes
+//   route_kernel   the choice, its weights, and the list of the chosen experts
+//                  with their tokens ("slots", ordered by expert and token)
+//   up_kernel      h = p act(gate x) (up x): 128 rows of one expert's gate and
+//                  up, of its tokens alone
+//   down_kernel    128 rows of y: every chosen expert's down in turn
+// As in st_linear's split_kernel the weight's rows are the MMA's rows, the
+// tokens its columns (as many as the expert has, in steps of 16), and the sum
+// is split over the CTAs of a cluster that join in rank order: no atomics, the
+// same bits on every run.
+//
+// Eight-bit experts.  The weights go to the tensor core as they are stored, and
+// it multiplies eight bits with eight; x and h are not rounded to eight bits
+// for that.  A run of 128 values is divided by a power of two to below 256 and
+// written as two or three columns of E4M3 codes, each the rounding error of
+// those before it: c0, 2^-4 c1, 2^-9 c2.  Four significant bits a column hold a
+// BF16's eight in two, an F16's eleven (and 12 of h, a binary32) in three, down
+// to 2^-21 of the run's largest.  The extra columns cost no time while the
+// weights come from HBM.  Sixteen-bit experts take x as it is and h as two
+// columns of their type.
+//
+// The choice turns on the last digits of the logits: they are summed in two
+// binary32 words with the rounding errors kept (Knuth's two-sum).
+#include "st_tensor_device.h"
+
+namespace stmat {
+namespace {
+
+constexpr int kRows = 128;           // weight rows of a tile: the MMA's M
+constexpr int kRun = 128;            // values with a common scale
+constexpr int kMaxTokens = ST_MOE_MAX_TOKENS;
+static_assert(kMaxTokens <= 64, "bits of an expert's mask");
+constexpr int kMaxTop = 32;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxSplit = 8;         // portable cluster size
+constexpr int kSumWarps = 4;         // one per 32 TMEM lanes
+constexpr int kMmaWarp = 4, kCopyWarp = 5, kThreads = 192;
+constexpr int kLogitWarps = 8, kLogitTokens = 4;
+constexpr int kRouteWarps = 8;       // tokens of a CTA of route_kernel
+// Stages and sums to join: half of an SM's shared memory where three stages fit
+// in that, so that one CTA's start and end lie beside another's copies.
+constexpr int kHalfSmem = 108 * 1024, kSmem = 204 * 1024;
+
+// What route_kernel finds.  Arrays of as many entries as can be needed.
+struct Lists {
+  int *count;         // chosen experts
+  int *expert;        // [i]: the i-th of them, ascending
+  int *first;         // [i]: its first slot; [count]: the number of slots
+  int *token;         // [slot]
+  float *weight;      // [slot]
+};
+
+struct MoeArgs {
+  const void *x, *router, *residual;
+  const float *bias;
+  void *y;
+  int *chosen;
+  float *weights;
+  int64_t ldx, ld_router, ldr, ldy;
+  int tokens, hidden, inter, experts, top_k;
+  int sigmoid, normalize;
+  float factor;
+  st_act act;
+  st_dtype x_dtype, router_dtype, y_dtype, w_dtype;
+  int has_up;
+  // Block scales of gate, up and down (8 bits): [expert, row block, block].
+  const float *scale[3];
+  int64_t scale_expert[3], scale_row[3], scale_col[3];
+  // Workspace.
+  double *logits, *keys;  // keys: what is compared, where that is not the logit
+  uint8_t *xq, *hq;       // columns of x and h, rows of pitch bytes
+  float *xs, *hs;         // their runs' scales (x: 8 bits alone)
+  int64_t x_pitch, h_pitch;
+  int h_blocks, in_blocks, h_runs, in_runs;  // stages and runs of hidden and inter
+  Lists list;
+  uint32_t idesc;         // without the number of columns
+  int splits, stages, tiles;
+  uint32_t *err;
+};
+
+// ------------------------------------------------------------ columns
+
+// The power of two that takes a run's largest magnitude below 2^below (8 bits:
+// 256, BF16: 4, F16: 2^15); NaN where that is not finite.
+__device__ __forceinline__ float run_scale(float top, int below) {
+  if (!(top < __int_as_float(0x7f800000))) return __int_as_float(0x7fffffff);
+  const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - (below - 1), 1);
+  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+__device__ __forceinline__ float exact_inverse(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half *>(&h));
+}
+// The codes of v's columns.
+template <int C>
+__device__ __forceinline__ void columns8(float v, uint32_t (&c)[C]) {
+  constexpr float kUp[3] = {1.0f, 16.0f, 512.0f};
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    c[i] = pack_e4m3(v * kUp[i], 0.0f) & 0xff;
+    v -= e4m3_value(c[i]) * (1.0f / kUp[i]);
+  }
+}
+
+__device__ __forceinline__ float warp_top(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, d));
+  return v;
+}
+
+// ------------------------------------------------------- logits_kernel
+
+// A sum in two words: hi + lo, with the error of every addition to hi in lo.
+struct Two {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float s = hi + v, b = s - hi;
+    lo += (hi - (s - b)) + (v - b);
+    hi = s;
+  }
+};
+
+template <class T>
+__device__ __forceinline__ float element(const void *p, int64_t at) { return to_float(static_cast<const T *>(p)[at]); }
+
+// A warp has an expert and up to four tokens.
+template <class X, class R>
+__device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0, int lane) {
+  const int live = min(kLogitTokens, a.tokens - t0);
+  const R *const w = static_cast<const R *>(a.router) + expert * a.ld_router;
+  const X *const x = static_cast<const X *>(a.x) + t0 * a.ldx;
+  Two sum[kLogitTokens];
+  auto step = [&](int t, float xv, float wv) {
+    const float p = __fmul_rn(xv, wv);
+    // Two 16-bit numbers' product is exact.
+    if (sizeof(R) == 4) sum[t].lo += fmaf(xv, wv, -p);
+    sum[t].add(p);
+  };
+  constexpr int V = sizeof(R) == 4 ? 4 : 8;
+  const bool wide = a.hidden % V == 0 && a.ldx % V == 0 && a.ld_router % V == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
+  if (wide) {
+#pragma unroll 2
+    for (int c = lane * V; c < a.hidden; c += 32 * V) {
+      float wv[V], xv[V];
+      unpack(*reinterpret_cast<const Raw<R, V> *>(w + c), wv);
+#pragma unroll
+      for (int t = 0; t < kLogitTokens; ++t) {
+        if (t >= live) continue;
+        unpack(*reinterpret_cast<const Raw<X, V> *>(x + t * a.ldx + c), xv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) step(t, xv[i], wv[i]);
+      }
+    }
+  } else {
+    for (int c = lane; c < a.hidden; c += 32) {
+      const float wv = to_float(w[c]);
+#pragma unroll
+      for (int t = 0; t < kLogitTokens; ++t)
+        if (t < live) step(t, to_float(x[t * a.ldx + c]), wv);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kLogitTokens; ++t) {
+    if (t >= live) continue;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const float hi = __shfl_xor_sync(~0u, sum[t].hi, d), lo = __shfl_xor_sync(~0u, sum[t].lo, d);
+      sum[t].lo += lo;
+      sum[t].add(hi);
+    }
+    if (lane == 0) {
+      // Where the sum has left binary32's range its error has no meaning.
+      const double l = isfinite(sum[t].hi) ? static_cast<double>(sum[t].hi) + sum[t].lo : sum[t].hi;
+      const int64_t at = int64_t(t0 + t) * a.experts + expert;
+      a.logits[at] = l;
+      if (a.bias && a.sigmoid) a.keys[at] = 1.0 / (1.0 + exp(-l)) + a.bias[expert];
+    }
+  }
+}
+
+// A block has a token's columns.
+template <class X>
+__device__ __forceinline__ void x_columns(const MoeArgs &a, int token) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const X *const x = static_cast<const X *>(a.x) + token * a.ldx;
+  if (a.w_dtype == ST_BF16 || a.w_dtype == ST_F16) {
+    X *const to = reinterpret_cast<X *>(a.xq + token * a.x_pitch);
+    for (int c = threadIdx.x; c < a.hidden; c += 32 * kLogitWarps) to[c] = x[c];
+    return;
+  }
+  constexpr int C = std::is_same<X, __half>::value ? 3 : 2;
+  uint8_t *const to = a.xq + int64_t(token) * C * a.x_pitch;
+  for (int run = warp; run < a.h_runs; run += kLogitWarps) {
+    const int c0 = run * kRun + 4 * lane;
+    float v[4], top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = c0 + i < a.hidden ? to_float(x[c0 + i]) : 0.0f;
+      top = max_nan(top, fabsf(v[i]));
+    }
+    const float s = run_scale(warp_top(top), 8), inv = exact_inverse(s);
+    if (lane == 0) a.xs[token * a.h_runs + run] = s;
+    uint32_t packed[C] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t c[C];
+      columns8<C>(v[i] * inv, c);
+#pragma unroll
+      for (int j = 0; j < C; ++j) packed[j] |= c[j] << (8 * i);
+    }
+    if (c0 < a.x_pitch) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) *reinterpret_cast<uint32_t *>(to + j * a.x_pitch + c0) = packed[j];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(32 * kLogitWarps) logits_kernel(const __grid_constant__ MoeArgs a) {
+  wait_for_previous();
+  let_next_start();
+  const int groups = (a.tokens + kLogitTokens - 1) / kLogitTokens, items = a.experts * groups;
+  const int blocks = (items + kLogitWarps - 1) / kLogitWarps;
+  auto with_x = [&](auto &&f) {
+    if (a.x_dtype == ST_BF16) f(__nv_bfloat16{});
+    else f(__half{});
+  };
+  if (blockIdx.x >= blocks) {
+    with_x([&](auto x) { x_columns<decltype(x)>(a, blockIdx.x - blocks); });
+    return;
+  }
+  const int item = blockIdx.x * kLogitWarps + (threadIdx.x >> 5);
+  if (item >= items) return;
+  with_x([&](auto x) {
+    with_type(a.router_dtype, [&](auto r) { logits<decltype(x), decltype(r)>(a, item / groups, item % groups * kLogitTokens, threadIdx.x & 31); });
+  });
+}
+
+// -------------------------------------------------------- route_kernel
+
+// Order of the choice: NaN before all, then by size.
+__device__ __forceinline__ bool before(double k, int e, double best, int best_e) {
+  const bool kn = isnan(k), bn = isnan(best);
+  if (kn != bn) return kn;
+  if (!kn && k != best) return k > best;
+  return e < best_e;
+}
+
+// A warp chooses for a token; kPer of the experts a lane (expert 32 j + lane).
+template <int kPer>
+__device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int lane, int *chosen, float *weight) {
+  const double *const l = a.logits + int64_t(token) * a.experts;
+  double key[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) key[j] = 32 * j + lane < a.experts ? l[32 * j + lane] : 0.0;
+  // Softmax: relative to the largest logit.
+  double top = 0.0;
+  float all = 0.0f;
+  if (!a.sigmoid) {
+    top = __longlong_as_double(0xfff0000000000000ll);
+    bool none = true;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (32 * j + lane < a.experts) top = none || key[j] > top || isnan(key[j]) ? key[j] : top, none = false;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const double o = __shfl_xor_sync(~0u, top, d);
+      if (o > top || isnan(o)) top = o;
+    }
+    if (!a.normalize || a.bias) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (32 * j + lane < a.experts) all += expf(static_cast<float>(key[j] - top));
+#pragma unroll
+      for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
+    }
+    if (a.bias) {
+      double sum = 0.0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (32 * j + lane < a.experts) key[j] = exp(key[j] - top), sum += key[j];
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (32 * j + lane < a.experts) key[j] = key[j] / sum + a.bias[32 * j + lane];
+    }
+  } else if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (32 * j + lane < a.experts) key[j] = a.keys[int64_t(token) * a.experts + 32 * j + lane];
+  }
+  uint32_t taken = 0;
+  int mine = 0;
+  for (int i = 0; i < a.top_k; ++i) {
+    double best = 0.0;
+    int best_e = 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = 32 * j + lane;
+      if (e < a.experts && !(taken >> j & 1) && (best_e == 0x7fffffff || before(key[j], e, best, best_e))) best = key[j], best_e = e;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const double k = __shfl_xor_sync(~0u, best, d);
+      const int e = __shfl_xor_sync(~0u, best_e, d);
+      if (e != 0x7fffffff && (best_e == 0x7fffffff || before(k, e, best, best_e))) best = k, best_e = e;
+    }
+    if ((best_e & 31) == lane) taken |= 1u << (best_e >> 5);
+    if (lane == i) mine = best_e;
+  }
+  // Lane i has the i-th chosen expert.
+  float s = 0.0f;
+  if (lane < a.top_k) {
+    const double v = l[mine];
+    s = a.sigmoid ? 1.0f / (1.0f + expf(static_cast<float>(-v))) : expf(static_cast<float>(v - top));
+  }
+  float sum = s;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  const float p = a.factor * (a.normalize ? s / sum : a.sigmoid ? s : s / all);
+  if (lane < a.top_k) {
+    chosen[lane] = mine;
+    weight[lane] = p;
+    if (a.chosen) a.chosen[int64_t(token) * a.top_k + lane] = mine;
+    if (a.weights) a.weights[int64_t(token) * a.top_k + lane] = p;
+  }
+}
+
+// The CTAs of one cluster have eight tokens each; the first then lists the
+// experts.
+template <int kPer>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ MoeArgs a) {
+  __shared__ uint64_t mask[kMaxExperts];             // tokens of an expert
+  __shared__ int slots[kMaxExperts], totals[kRouteWarps][2];
+  __shared__ int chosen[kRouteWarps][kMaxTop];
+  __shared__ float weight[kRouteWarps][kMaxTop];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = blockIdx.x * kRouteWarps + warp;
+  constexpr int kThreadsHere = 32 * kRouteWarps;
+  for (int e = threadIdx.x; e < a.experts; e += kThreadsHere) mask[e] = 0;
+  wait_for_previous();
+  let_next_start();
+  if (token < a.tokens) choose_experts<kPer>(a, token, lane, chosen[warp], weight[warp]);
+  cluster_arrive();
+  cluster_wait();
+  // Every CTA reads all CTAs' choices, so that each can place its own.
+  for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreadsHere) {
+    const int t = i / a.top_k;
+    int e;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(e) : "r"(peer_addr(&chosen[t % kRouteWarps][i % a.top_k], t / kRouteWarps)) : "memory");
+    atomicOr(reinterpret_cast<unsigned long long *>(&mask[e]), 1ull << t);
+  }
+  cluster_arrive();
+  __syncthreads();
+  // Slots, and places in the list: running counts over the experts, four (of up
+  // to 1024) a thread.
+  constexpr int kEach = kMaxExperts / kThreadsHere;
+  int n[kEach], used[kEach], all_n = 0, all_used = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x * kEach + i;
+    n[i] = e < a.experts ? __popcll(mask[e]) : 0;
+    used[i] = n[i] > 0;
+    all_n += n[i], all_used += used[i];
+  }
+  int before_n = all_n, before_used = all_used;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(~0u, before_n, d), u = __shfl_up_sync(~0u, before_used, d);
+    if (lane >= d) before_n += o, before_used += u;
+  }
+  if (lane == 31) totals[warp][0] = before_n, totals[warp][1] = before_used;
+  __syncthreads();
+  before_n -= all_n, before_used -= all_used;
+  for (int w = 0; w < warp; ++w) before_n += totals[w][0], before_used += totals[w][1];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x * kEach + i;
+    if (e < a.experts) {
+      slots[e] = before_n;
+      if (blockIdx.x == 0 && used[i]) {
+        a.list.expert[before_used] = e;
+        a.list.first[before_used] = before_n;
+      }
+    }
+    before_n += n[i], before_used += used[i];
+  }
+  if (blockIdx.x == 0 && threadIdx.x == kThreadsHere - 1) {
+    *a.list.count = before_used;
+    a.list.first[before_used] = before_n;
+  }
+  __syncthreads();
+  if (token < a.tokens && lane < a.top_k) {
+    const int e = chosen[warp][lane], slot = slots[e] + __popcll(mask[e] & ((1ull << token) - 1));
+    a.list.token[slot] = token;
+    a.list.weight[slot] = weight[warp][lane];
+  }
+  cluster_wait();  // no CTA ends while another reads its choices
+}
+
+// -------------------------------------------------- the experts' products
+
+__device__ __forceinline__ void tma_load3(const CUtensorMap *map, void *dst, uint64_t *bar, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)) : "memory");
+}
+
+// The TMEM columns of eight tokens, C each.
+template <int C>
+__device__ __forceinline__ void read_tokens(uint32_t addr, uint32_t (&v)[8 * C]) {
+  if constexpr (C != 2)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]) : "r"(addr));
+  if constexpr (C != 1) {
+    constexpr int o = C == 3 ? 8 : 0;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7]),
+                   "=r"(v[o + 8]), "=r"(v[o + 9]), "=r"(v[o + 10]), "=r"(v[o + 11]), "=r"(v[o + 12]), "=r"(v[o + 13]), "=r"(v[o + 14]), "=r"(v[o + 15])
+                 : "r"(addr + o));
+  }
+  if constexpr (C == 1)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]) :: "memory");
+  if constexpr (C > 1)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]),
+                   "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]) :: "memory");
+  if constexpr (C == 3)
+    asm volatile("" : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]) :: "memory");
+}
+// A token's sum of its columns' sums.
+template <int C, bool kEight>
+__device__ __forceinline__ float of_columns(const uint32_t (&v)[8 * C], int t) {
+  float s = __uint_as_float(v[C * t]);
+  if constexpr (C > 1) s = fmaf(__uint_as_float(v[C * t + 1]), kEight ? 0x1p-4f : 1.0f, s);
+  if constexpr (C > 2) s = fmaf(__uint_as_float(v[C * t + 2]), 0x1p-9f, s);
+  return s;
+}
+
+__host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
+__host__ __device__ constexpr int tmem_columns(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512; }
+
+// What both kernels' CTAs have.
+struct Pipe {
+  uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2];
+  uint32_t tmem;
+  int failed;
+};
+__device__ __forceinline__ void pipe_start(Pipe &p, int stages, int warp, int columns) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      bar_init(&p.full[i], 1);
+      bar_init(&p.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&p.sums[i], 1);
+      bar_init(&p.taken[i], kSumWarps);
+    }
+    p.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&p.tmem)), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void pipe_end(Pipe &p, int warp, int columns, uint32_t *err) {
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(p.tmem), "r"(columns));
+  if (threadIdx.x == 0 && p.failed) atomicOr(err, kErrProduct);
+}
+// The four summing warps.
+__device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void local_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// h of 128 rows of one chosen expert.  BT: tokens an expert may have; C: columns
+// of an x.  Gate's and up's sums of a stage lie side by side in TMEM.
+template <int BT, int C, bool kEight>
+__global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CUtensorMap gate, const __grid_constant__ CUtensorMap up,
+                                                      const __grid_constant__ CUtensorMap xmap, const __grid_constant__ MoeArgs a) {
+  constexpr int kN = round16(BT * C), kBuffers = 4 * kN <= 512 ? 2 : 1, kColumns = tmem_columns(kBuffers * 2 * kN);
+  constexpr int kStageBytes = (2 * kRows + kN) * kStageK, kStep = kEight ? kStageK : kStageK / 2;
+  constexpr int kOutColumns = kEight ? 3 : 2;
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  __shared__ Pipe pipe;
+  __shared__ __align__(16) float scales[kSumWarps][2][2][BT];
+  __shared__ float tops[kSumWarps][BT];
+  __shared__ int tokens[BT];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x % a.splits;
+  const int item = blockIdx.x / a.splits, which = item / a.tiles, n0 = item % a.tiles * kRows;
+  const int first = static_cast<int>(int64_t(a.h_blocks) * rank / a.splits);
+  const int blocks = static_cast<int>(int64_t(a.h_blocks) * (rank + 1) / a.splits) - first;
+  pipe_start(pipe, a.stages, warp, kColumns);
+  wait_for_previous();
+  let_next_start();
+  if (which >= *a.list.count) {  // every CTA of the cluster
+    pipe_end(pipe, warp, kColumns, a.err);
+    return;
+  }
+  const int expert = a.list.expert[which], slot0 = a.list.first[which], count = a.list.first[which + 1] - slot0;
+  const uint32_t tmem = pipe.tmem;
+
+  Ring r;
+  float g[BT], u[BT];
+  if (warp == kCopyWarp) {
+    for (int i = lane; i < count; i += 32) tokens[i] = a.list.token[slot0 + i];
+    __syncwarp();
+    if (elect_one()) {
+      bool ok = true;
+      const uint32_t bytes = (a.has_up ? 2 : 1) * kRows * kStageK + count * C * kStageK;
+      for (int i = 0; i < blocks; ++i, r.next(a.stages)) {
+        // Before its first use a stage counts as released.
+        if (!bar_wait(&pipe.empty[r.at], r.phase ^ 1)) { ok = false; break; }
+        uint8_t *stage = smem + r.at * kStageBytes;
+        const int k = (first + i) * kStep;
+        bar_expect(&pipe.full[r.at], bytes);
+        tma_load3(&gate, stage, &pipe.full[r.at], k, n0, expert);
+        if (a.has_up) tma_load3(&up, stage + kRows * kStageK, &pipe.full[r.at], k, n0, expert);
+        for (int t = 0; t < count; ++t) tma_load(&xmap, stage + (2 * kRows + t * C) * kStageK, &pipe.full[r.at], k, tokens[t] * C);
+      }
+      // The stages in flight are released (or, after a wait that gave up,
+      // have had their time) before the CTA ends.
+      for (int i = 0; i < a.stages; ++i, r.next(a.stages)) ok &= bar_wait(&pipe.empty[r.at], r.phase ^ 1);
+      if (!ok) pipe.failed = 1;
+    }
+  } else if (warp == kMmaWarp) {
+    if (elect_one()) {
+      Ring sum;
+      const uint32_t idesc = a.idesc | static_cast<uint32_t>(round16(count * C) / 8) << 17;
+      for (int i = 0; i < blocks; ++i, r.next(a.stages), sum.next(kBuffers)) {
+        if (!bar_wait(&pipe.taken[sum.at], sum.phase ^ 1) || !bar_wait(&pipe.full[r.at], r.phase)) { pipe.failed = 1; break; }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t gd = tile_desc(smem + r.at * kStageBytes), ud = gd + (kRows * kStageK >> 4), xd = ud + (kRows * kStageK >> 4);
+        const uint32_t d = tmem + sum.at * 2 * kN;
+#pragma unroll
+        for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(d, gd + 2 * j, xd + 2 * j, idesc, j > 0);
+        if (a.has_up) {
+#pragma unroll
+          for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(d + kN, ud + 2 * j, xd + 2 * j, idesc, j > 0);
+        }
+        mma_commit(&pipe.empty[r.at]);
+        mma_commit(&pipe.sums[sum.at]);
+      }
+    }
+  } else {
+    // The scales of a stage, one stage ahead: lane l has the tokens l, l + 32.
+    constexpr int kEach = (BT + 31) / 32;
+    const int block_row = n0 / kRun;
+    const float *const gs = a.scale[0] + expert * a.scale_expert[0] + block_row * a.scale_row[0];
+    const float *const us = a.scale[1] + expert * a.scale_expert[1] + block_row * a.scale_row[1];
+    int mine[kEach];
+    float x_next[kEach], g_next = 1.0f, u_next = 1.0f;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) mine[e] = lane + 32 * e < count ? a.list.token[slot0 + lane + 32 * e] : 0;
+    auto fetch = [&](int b) {
+      if (!kEight) return;
+      g_next = gs[b * a.scale_col[0]];
+      if (a.has_up) u_next = us[b * a.scale_col[1]];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) x_next[e] = lane + 32 * e < count ? a.xs[mine[e] * a.h_runs + b] : 0.0f;
+    };
+    if (blocks > 0) fetch(first);
+#pragma unroll
+    for (int t = 0; t < BT; ++t) g[t] = u[t] = 0.0f;
+    Ring sum;
+    for (int b = 0; b < blocks; ++b, sum.next(kBuffers)) {
+      float(*const sc)[BT] = scales[warp][b & 1];
+      if (kEight) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+          if (BT >= 32 || lane < BT) sc[0][lane + 32 * e] = x_next[e] * g_next, sc[1][lane + 32 * e] = x_next[e] * u_next;
+        if (b + 1 < blocks) fetch(first + b + 1);
+        __syncwarp();
+      }
+      if (!bar_wait(&pipe.sums[sum.at], sum.phase, sum_limit(a.h_blocks))) { pipe.failed = 1; break; }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16) + sum.at * 2 * kN;
+      auto add = [&](float(&to)[BT], uint32_t at, const float *s) {
+#pragma unroll
+        for (int t = 0; t < BT; t += 8) {
+          if (t >= count) continue;
+          uint32_t v[8 * C];
+          read_tokens<C>(at + t * C, v);
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+          if (kEight) {
+            *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(s + t);
+            *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(s + t + 4);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) to[t + j] = kEight ? fmaf(of_columns<C, kEight>(v, j), f[j], to[t + j]) : to[t + j] + of_columns<C, kEight>(v, j);
+        }
+      };
+      add(g, from, sc[0]);
+      if (a.has_up) add(u, from + kN, sc[1]);
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) local_arrive(&pipe.taken[sum.at]);
+    }
+  }
+  __syncwarp();
+
+  // h and its columns.  The CTAs of a cluster share the tokens out: CTA r joins
+  // and writes `share` of them from r * share on, whose partial sums every CTA
+  // puts into its shared memory, [splits][share][gate, up][kRows] over the
+  // stages.
+  const int share = (count + a.splits - 1) / a.splits;
+  const int begin = static_cast<int>(rank) * share, own = max(0, min(share, count - begin));
+  float *const joined = reinterpret_cast<float *>(smem);
+  const int row = threadIdx.x, n = n0 + row;
+  if (a.splits > 1) {
+    cluster_arrive();
+    cluster_wait();  // every CTA is done with its stages
+    if (warp < kSumWarps) {
+      uint32_t owner = 0, to = peer_addr(joined + rank * share * 2 * kRows + row, 0);
+      int left = share;
+#pragma unroll
+      for (int t = 0; t < BT; ++t) {
+        if (t >= count) continue;
+        if (left == 0) {
+          to = peer_addr(joined + rank * share * 2 * kRows + row, ++owner);
+          left = share;
+        }
+        peer_store(to, g[t]);
+        peer_store(to + kRows * 4, u[t]);
+        to += 2 * kRows * 4;
+        --left;
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (warp < kSumWarps) {
+    auto value = [&](float gv, float uv, int slot) {
+      float v[1] = {gv};
+      activate<false>(v, a.act);
+      return (a.has_up ? v[0] * uv : v[0]) * a.list.weight[slot];
+    };
+    auto emit = [&](float v, int t, int slot) {
+      float top = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kSumWarps; ++w) top = max_nan(top, tops[w][t]);
+      const float s = run_scale(top, kEight ? 8 : a.w_dtype == ST_BF16 ? 2 : 15);
+      if (row == 0) a.hs[int64_t(slot) * a.in_runs + n0 / kRun] = s;
+      if (n >= a.inter) return;
+      v *= exact_inverse(s);
+      uint8_t *const to = a.hq + int64_t(slot) * kOutColumns * a.h_pitch;
+      if constexpr (kEight) {
+        uint32_t c[kOutColumns];
+        columns8<kOutColumns>(v, c);
+#pragma unroll
+        for (int i = 0; i < kOutColumns; ++i) to[i * a.h_pitch + n] = static_cast<uint8_t>(c[i]);
+      } else {
+        const float hi[1] = {a.w_dtype == ST_BF16 ? to_float(__float2bfloat16_rn(v)) : to_float(__float2half_rn(v))}, lo[1] = {v - hi[0]};
+        store_any<1>(to, a.w_dtype, n, hi);
+        store_any<1>(to + a.h_pitch, a.w_dtype, n, lo);
+      }
+    };
+    if (a.splits > 1) {
+      for (int t = 0; t < own; ++t) {
+        float gv = 0.0f, uv = 0.0f;
+        for (int s = 0; s < a.splits; ++s) {
+          const float *from = joined + (s * share + t) * 2 * kRows + row;
+          gv += from[0], uv += from[kRows];
+        }
+        const float v = value(gv, uv, slot0 + begin + t), top = warp_top(fabsf(v));
+        joined[t * 2 * kRows + row] = v;
+        if (lane == 0) tops[warp][t] = top;
+      }
+      sum_warps_sync();
+      for (int t = 0; t < own; ++t) emit(joined[t * 2 * kRows + row], t, slot0 + begin + t);
+    } else {
+#pragma unroll
+      for (int t = 0; t < BT; ++t) {
+        if (t >= count) continue;
+        g[t] = value(g[t], u[t], slot0 + t);
+        const float top = warp_top(fabsf(g[t]));
+        if (lane == 0) tops[warp][t] = top;
+      }
+      sum_warps_sync();
+#pragma unroll
+      for (int t = 0; t < BT; ++t)
+        if (t < count) emit(g[t], t, slot0 + t);
+    }
+  }
+  pipe_end(pipe, warp, kColumns, a.err);
+}
+
+// 128 rows of y.  The stages of all chosen experts, one after the other, are
+// shared out over the cluster's CTAs; each keeps the tokens' sums of its part
+// in shared memory.
+template <int BT, bool kEight>
+__global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ CUtensorMap down, const __grid_constant__ CUtensorMap hmap,
+                                                        const __grid_constant__ MoeArgs a) {
+  constexpr int C = kEight ? 3 : 2, kN = round16(BT * C), kColumns = tmem_columns(2 * kN);
+  constexpr int kStageBytes = (kRows + kN) * kStageK, kStep = kEight ? kStageK : kStageK / 2;
+  constexpr int kPerRun = kRun / kStep;  // stages of a run of h
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  __shared__ Pipe pipe;
+  __shared__ __align__(16) float scales[kSumWarps][2][BT];
+  float *const total = reinterpret_cast<float *>(smem + a.stages * kStageBytes);  // [token][kRows]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x % a.splits;
+  const int n0 = static_cast<int>(blockIdx.x / a.splits) * kRows;
+  pipe_start(pipe, a.stages, warp, kColumns);
+  wait_for_previous();
+  let_next_start();
+  const int64_t all = int64_t(*a.list.count) * a.in_blocks;
+  const int64_t begin = all * rank / a.splits;
+  const int blocks = static_cast<int>(all * (rank + 1) / a.splits - begin);
+  const int which0 = static_cast<int>(begin / a.in_blocks), block0 = static_cast<int>(begin % a.in_blocks);
+  const uint32_t tmem = pipe.tmem;
+
+  // Walks over (chosen expert, stage of its sum).
+  struct Walk {
+    int which, block, expert, slot0, count;
+    __device__ __forceinline__ void look(const MoeArgs &a) {
+      expert = a.list.expert[which];
+      slot0 = a.list.first[which];
+      count = a.list.first[which + 1] - slot0;
+    }
+    __device__ __forceinline__ void next(const MoeArgs &a, bool more) {
+      if (++block == a.in_blocks) {
+        block = 0;
+        ++which;
+        if (more) look(a);
+      }
+    }
+  };
+  Walk at{which0, block0, 0, 0, 0};
+  if (blocks > 0) at.look(a);
+  Ring r;
+  if (warp == kCopyWarp) {
+    if (elect_one()) {
+      bool ok = true;
+      for (int i = 0; i < blocks; ++i, r.next(a.stages)) {
+        // Before its first use a stage counts as released.
+        if (!bar_wait(&pipe.empty[r.at], r.phase ^ 1)) { ok = false; break; }
+        uint8_t *stage = smem + r.at * kStageBytes;
+        const int columns = round16(at.count * C);
+        bar_expect(&pipe.full[r.at], (kRows + columns) * kStageK);
+        tma_load3(&down, stage, &pipe.full[r.at], at.block * kStep, n0, at.expert);
+        for (int c = 0; c < columns; c += 16)
+          tma_load(&hmap, stage + (kRows + c) * kStageK, &pipe.full[r.at], at.block * kStep, at.slot0 * C + c);
+        at.next(a, i + 1 < blocks);
+      }
+      // The stages in flight are released (or, after a wait that gave up,
+      // have had their time) before the CTA ends.
+      for (int i = 0; i < a.stages; ++i, r.next(a.stages)) ok &= bar_wait(&pipe.empty[r.at], r.phase ^ 1);
+      if (!ok) pipe.failed = 1;
+    }
+  } else if (warp == kMmaWarp) {
+    if (elect_one()) {
+      Ring sum;
+      for (int i = 0; i < blocks; ++i, r.next(a.stages), sum.next(2)) {
+        if (!bar_wait(&pipe.taken[sum.at], sum.phase ^ 1) || !bar_wait(&pipe.full[r.at], r.phase)) { pipe.failed = 1; break; }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t wd = tile_desc(smem + r.at * kStageBytes), hd = wd + (kRows * kStageK >> 4);
+        const uint32_t idesc = a.idesc | static_cast<uint32_t>(round16(at.count * C) / 8) << 17;
+#pragma unroll
+        for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(tmem + sum.at * kN, wd + 2 * j, hd + 2 * j, idesc, j > 0);
+        mma_commit(&pipe.empty[r.at]);
+        mma_commit(&pipe.sums[sum.at]);
+        at.next(a, i + 1 < blocks);
+      }
+    }
+  } else {
+    const int row = threadIdx.x;
+    for (int t = 0; t < a.tokens; ++t) total[t * kRows + row] = 0.0f;
+    // The scales of a stage, one stage ahead: lane l has the slots l, l + 32.
+    constexpr int kEach = (BT + 31) / 32;
+    Walk ahead = at;
+    float h_next[kEach], w_next = 1.0f;
+    auto fetch = [&]() {
+      const int run = ahead.block / kPerRun;
+      if (kEight) w_next = a.scale[2][ahead.expert * a.scale_expert[2] + n0 / kRun * a.scale_row[2] + run * a.scale_col[2]];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) h_next[e] = lane + 32 * e < ahead.count ? a.hs[int64_t(ahead.slot0 + lane + 32 * e) * a.in_runs + run] : 0.0f;
+    };
+    if (blocks > 0) fetch();
+    float acc[BT];
+#pragma unroll
+    for (int t = 0; t < BT; ++t) acc[t] = 0.0f;
+    Ring sum;
+    for (int b = 0; b < blocks; ++b, sum.next(2)) {
+      float *const sc = scales[warp][b & 1];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e)
+        if (BT >= 32 || lane < BT) sc[lane + 32 * e] = h_next[e] * w_next;
+      if (b + 1 < blocks) {
+        ahead.next(a, true);
+        fetch();
+      }
+      __syncwarp();
+      if (!bar_wait(&pipe.sums[sum.at], sum.phase, sum_limit(static_cast<int>(min(all, int64_t(0x7fffffff)))))) { pipe.failed = 1; break; }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16) + sum.at * kN;
+#pragma unroll
+      for (int t = 0; t < BT; t += 8) {
+        if (t >= at.count) continue;
+        uint32_t v[8 * C];
+        read_tokens<C>(from + t * C, v);
+        float f[8];
+        *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(sc + t);
+        *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(sc + t + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[t + j] = fmaf(of_columns<C, kEight>(v, j), f[j], acc[t + j]);
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) local_arrive(&pipe.taken[sum.at]);
+      if (at.block == a.in_blocks - 1 || b == blocks - 1) {
+        // The expert's part of its tokens' sums.  (Columns that are no token's
+        // have had anything added.)
+#pragma unroll
+        for (int t = 0; t < BT; ++t) {
+          if (t < at.count) total[a.list.token[at.slot0 + t] * kRows + row] += acc[t];
+          acc[t] = 0.0f;
+        }
+      }
+      at.next(a, b + 1 < blocks);
+    }
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  const int n = n0 + static_cast<int>(threadIdx.x);
+  if (warp < kSumWarps) {
+    const int share = (a.tokens + a.splits - 1) / a.splits, t0 = static_cast<int>(rank) * share, t1 = min(a.tokens, t0 + share);
+    for (int t = t0; t < t1; ++t) {
+      float v[1] = {0.0f}, old[1] = {0.0f};
+      if (a.residual && n < a.hidden) load_any<1>(a.residual, a.y_dtype, t * a.ldr + n, old);
+      for (int s = 0; s < a.splits; ++s) {
+        float part;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part) : "r"(peer_addr(total + t * kRows + threadIdx.x, s)) : "memory");
+        v[0] += part;
+      }
+      v[0] += old[0];
+      if (n < a.hidden) store_any<1>(a.y, a.y_dtype, t * a.ldy + n, v);
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  pipe_end(pipe, warp, kColumns, a.err);
+}
+
+// ------------------------------------------------------------------- host
+
+int item_of(const st_moe_args &p) { return p.w_dtype == ST_BF16 || p.w_dtype == ST_F16 ? 2 : 1; }
+int x_columns_of(const st_moe_args &p) { return item_of(p) == 2 ? 1 : p.x_dtype == ST_F16 ? 3 : 2; }
+int h_columns_of(const st_moe_args &p) { return item_of(p) == 2 ? 2 : 3; }
+
+// The workspace's parts, at multiples of 256 bytes.
+struct Space {
+  int64_t at = 0;
+  int64_t take(int64_t bytes) {
+    const int64_t from = at;
+    at += (bytes + 255) / 256 * 256;
+    return from;
+  }
+};
+int64_t lay_out(const st_moe_args &p, MoeArgs *a) {
+  const int item = item_of(p);
+  const int64_t slots = p.tokens * p.top_k, most = std::min(slots, p.experts);
+  const int64_t x_pitch = (p.hidden * item + 15) / 16 * 16, h_pitch = (p.inter * item + 15) / 16 * 16;
+  const int64_t h_runs = (p.hidden + kRun - 1) / kRun, in_runs = (p.inter + kRun - 1) / kRun;
+  Space s;
+  const int64_t logits = s.take(8 * p.tokens * p.experts), keys = s.take(p.router_bias && p.score == ST_MOE_SIGMOID ? 8 * p.tokens * p.experts : 0);
+  const int64_t xq = s.take(p.tokens * x_columns_of(p) * x_pitch), xs = s.take(item == 1 ? 4 * p.tokens * h_runs : 0);
+  const int64_t hq = s.take(slots * h_columns_of(p) * h_pitch), hs = s.take(4 * slots * in_runs);
+  const int64_t count = s.take(4), expert = s.take(4 * most), first = s.take(4 * (most + 1)), token = s.take(4 * slots), weight = s.take(4 * slots);
+  if (a) {
+    uint8_t *const base = static_cast<uint8_t *>(p.workspace);
+    a->logits = reinterpret_cast<double *>(base + logits);
+    a->keys = reinterpret_cast<double *>(base + keys);
+    a->xq = base + xq;
+    a->xs = reinterpret_cast<float *>(base + xs);
+    a->hq = base + hq;
+    a->hs = reinterpret_cast<float *>(base + hs);
+    a->x_pitch = x_pitch, a->h_pitch = h_pitch;
+    a->h_runs = static_cast<int>(h_runs), a->in_runs = static_cast<int>(in_runs);
+    a->list = {reinterpret_cast<int *>(base + count), reinterpret_cast<int *>(base + expert), reinterpret_cast<int *>(base + first),
+               reinterpret_cast<int *>(base + token), reinterpret_cast<float *>(base + weight)};
+  }
+  return s.at;
+}
+
+// All experts' [rows, k] matrices, read in boxes of 128 rows and 128 bytes of k.
+st_status encode_experts(CUtensorMap *map, const void *p, int64_t k, int64_t rows, int64_t experts, int64_t ld, int64_t step, int item, const char *op) {
+  EncodeFn fn = nullptr;
+  const st_status st = encoder(&fn, op);
+  if (st != ST_OK) return st;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(experts)};
+  const int64_t row = rows == 1 ? (k * item + 15) / 16 * 16 : ld * item;
+  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(experts == 1 ? (rows * row + 15) / 16 * 16 : step * item)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kStageK / item), kRows, 1}, each[3] = {1, 1, 1};
+  const CUresult r = fn(map, item == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(p), dims, stride, box,
+                        each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(ST_E_CUDA, "%s: tensor map of %lld x %lld x %lld refused (%d)", op, (long long)experts, (long long)rows, (long long)k, static_cast<int>(r));
+  return ST_OK;
+}
+
+struct Maps {
+  CUtensorMap gate, up, down, x, h;
+};
+
+template <class... P, class... A>
+st_status start(const char *what, void (*kernel)(P...), int64_t blocks, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st, const A &...args) {
+  const cudaError_t e = launch(kernel, dim3(static_cast<unsigned>(blocks)), threads, smem, cluster, st, args...);
+  return e == cudaSuccess ? ST_OK : set_error(ST_E_CUDA, "st_moe: %s launch: %s: %s", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+// Parts of the sum: as many as let all CTAs run at a time, each with at least
+// four stages.
+int parts(int64_t items, int64_t blocks, int most, int64_t room) {
+  int splits = 1;
+  while (splits < most && items * splits * 2 <= room && blocks / (splits * 2) >= 4) splits *= 2;
+  return splits;
+}
+constexpr int stages_in(int bytes, int stage) { return bytes / stage < kMaxStages ? bytes / stage : kMaxStages; }
+
+template <int BT, int C, bool kEight>
+st_status launch_up(MoeArgs a, const Maps &maps, int dev, int sms, cudaStream_t st) {
+  constexpr int kStageBytes = (2 * kRows + round16(BT * C)) * kStageK;
+  constexpr bool kHalf = 3 * kStageBytes <= kHalfSmem;
+  constexpr int kStages = stages_in(kHalf ? kHalfSmem : kSmem, kStageBytes), smem = kStages * kStageBytes + 1024;
+  // Sums to join, over the stages: [splits][share][2][kRows], for up to BT +
+  // splits - 1 tokens.
+  static_assert(kStages >= 3 && (BT + kMaxSplit) * 2 * kRows * 4 <= kStages * kStageBytes, "a ring of stages");
+  const int64_t most = std::min<int64_t>(int64_t(a.tokens) * a.top_k, a.experts);
+  a.tiles = (a.inter + kRows - 1) / kRows;
+  a.stages = kStages;
+  a.splits = parts(most * a.tiles, a.h_blocks, kMaxSplit, (kHalf ? 2 : 1) * sms);
+  constexpr auto kernel = up_kernel<BT, C, kEight>;
+  const cudaError_t e = allow_smem<kernel>(dev, smem);
+  if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_moe: %s", cudaGetErrorString(e));
+  return start("up", kernel, most * a.tiles * a.splits, kThreads, smem, a.splits, st, maps.gate, maps.up, maps.x, a);
+}
+
+template <int BT, bool kEight>
+st_status launch_down(MoeArgs a, const Maps &maps, int dev, int sms, cudaStream_t st) {
+  constexpr int kStageBytes = (kRows + round16(BT * (kEight ? 3 : 2))) * kStageK, kTotal = BT * kRows * 4;
+  constexpr bool kHalf = 3 * kStageBytes + kTotal <= kHalfSmem;
+  constexpr int kStages = stages_in((kHalf ? kHalfSmem : kSmem) - kTotal, kStageBytes), smem = kStages * kStageBytes + kTotal + 1024;
+  static_assert(kStages >= 3, "a ring of stages");
+  a.tiles = (a.hidden + kRows - 1) / kRows;
+  a.stages = kStages;
+  a.splits = parts(a.tiles, int64_t(a.top_k) * a.in_blocks, kMaxSplit, (kHalf ? 2 : 1) * sms);
+  constexpr auto kernel = down_kernel<BT, kEight>;
+  const cudaError_t e = allow_smem<kernel>(dev, smem);
+  if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_moe: %s", cudaGetErrorString(e));
+  return start("down", kernel, int64_t(a.tiles) * a.splits, kThreads, smem, a.splits, st, maps.down, maps.h, a);
+}
+
+template <int BT>
+st_status launch_products(const MoeArgs &a, const Maps &maps, int columns, int dev, int sms, cudaStream_t st) {
+  st_status s;
+  if (columns == 1) s = launch_up<BT, 1, false>(a, maps, dev, sms, st);
+  else if (columns == 2) s = launch_up<BT, 2, true>(a, maps, dev, sms, st);
+  else s = launch_up<BT, 3, true>(a, maps, dev, sms, st);
+  if (s != ST_OK) return s;
+  return columns == 1 ? launch_down<BT, false>(a, maps, dev, sms, st) : launch_down<BT, true>(a, maps, dev, sms, st);
+}
+
+}  // namespace
+
+int64_t moe_workspace(const st_moe_args &p) { return lay_out(p, nullptr); }
+
+st_status launch_moe(const st_moe_args &p, void *stream) {
+  const char *op = "st_moe";
+  MoeArgs a{};
+  a.x = p.x; a.router = p.router; a.residual = p.residual; a.bias = p.router_bias; a.y = p.y;
+  a.chosen = p.chosen; a.weights = p.weights;
+  a.ldx = p.ldx; a.ld_router = p.ld_router; a.ldr = p.ldr; a.ldy = p.ldy;
+  a.tokens = static_cast<int>(p.tokens); a.hidden = static_cast<int>(p.hidden); a.inter = static_cast<int>(p.inter);
+  a.experts = static_cast<int>(p.experts); a.top_k = static_cast<int>(p.top_k);
+  a.sigmoid = p.score == ST_MOE_SIGMOID; a.normalize = p.normalize != 0; a.factor = p.factor;
+  a.act = p.act; a.x_dtype = p.x_dtype; a.router_dtype = p.router_dtype; a.y_dtype = p.y_dtype; a.w_dtype = p.w_dtype;
+  a.has_up = p.up.w != nullptr;
+  const st_moe_weight *const weights[3] = {&p.gate, &p.up, &p.down};
+  for (int i = 0; i < 3; ++i) {
+    a.scale[i] = weights[i]->scale;
+    a.scale_expert[i] = weights[i]->scale_expert;
+    a.scale_row[i] = weights[i]->scale_row;
+    a.scale_col[i] = weights[i]->scale_col;
+  }
+  const int item = item_of(p), xc = x_columns_of(p), hc = h_columns_of(p), step = kStageK / item;
+  lay_out(p, &a);
+  a.h_blocks = (a.hidden + step - 1) / step;
+  a.in_blocks = (a.inter + step - 1) / step;
+  // Instruction descriptor: binary32 accumulators; formats of A (the weight)
+  // and B, both K-major; 128 rows.
+  const uint32_t fa = item == 2 ? p.w_dtype == ST_BF16 : p.w_dtype == ST_F8_E5M2, fb = item == 2 ? p.w_dtype == ST_BF16 : 0;
+  a.idesc = (1u << 4) | (fa << 7) | (fb << 10) | ((kRows / 16) << 24);
+  int dev = 0, sms = 0;
+  st_status s = product_device(&dev, &sms, &a.err);
+  Maps maps{};
+  if (s == ST_OK) s = encode_experts(&maps.gate, p.gate.w, p.hidden, p.inter, p.experts, p.gate.ld, p.gate.expert, item, op);
+  if (s == ST_OK && a.has_up) s = encode_experts(&maps.up, p.up.w, p.hidden, p.inter, p.experts, p.up.ld, p.up.expert, item, op);
+  if (s == ST_OK) s = encode_experts(&maps.down, p.down.w, p.inter, p.hidden, p.experts, p.down.ld, p.down.expert, item, op);
+  const int64_t slots = p.tokens * p.top_k;
+  if (s == ST_OK) s = encode(&maps.x, Side{a.xq, a.x_pitch, 0, p.tokens * xc}, p.hidden, item, xc, op);
+  if (s == ST_OK) s = encode(&maps.h, Side{a.hq, a.h_pitch, 0, slots * hc}, p.inter, item, 16, op);
+  if (s != ST_OK) return s;
+  const int64_t most = std::min<int64_t>(slots, p.experts) * ((p.inter + kRows - 1) / kRows);
+  if (most * kMaxSplit > 0x7fffffff) return set_error(ST_E_INVAL, "%s: more tiles than one launch has", op);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t items = p.experts * ((p.tokens + kLogitTokens - 1) / kLogitTokens);
+  s = start("router", logits_kernel, (items + kLogitWarps - 1) / kLogitWarps + p.tokens, 32 * kLogitWarps, 0, 1, st, a);
+  if (s != ST_OK) return s;
+  const unsigned ctas = p.tokens <= 8 ? 1 : p.tokens <= 16 ? 2 : p.tokens <= 32 ? 4 : 8;
+  auto route = p.experts <= 64 ? route_kernel<2> : p.experts <= 256 ? route_kernel<8> : route_kernel<32>;
+  s = start("route", route, ctas, 32 * kRouteWarps, 0, ctas, st, a);
+  if (s != ST_OK) return s;
+  return p.tokens <= 8    ? launch_products<8>(a, maps, xc, dev, sms, st)
+         : p.tokens <= 16 ? launch_products<16>(a, maps, xc, dev, sms, st)
+         : p.tokens <= 32 ? launch_products<32>(a, maps, xc, dev, sms, st)
+                          : launch_products<64>(a, maps, xc, dev, sms, st);
+}
+
+}  // namespace stmat

@@ -274,6 +274,101 @@ st_status run_linear(const st_linear_args *a, const st_linear_form *form, void *
   return launch_linear(*a, form, stream);
 }
 
+// An experts' matrix and its scales.
+st_status check_experts(const char *op, const char *name, const st_moe_weight &w, st_dtype dtype, int64_t experts, int64_t rows, int64_t k) {
+  const int64_t item = static_cast<int64_t>(st_dtype_size(dtype));
+  if (!w.w) return set_error(ST_E_INVAL, "%s: %s is NULL", op, name);
+  const int64_t row = rows > 1 ? w.ld : 0, step = experts > 1 ? w.expert : 0;
+  if ((rows > 1 && w.ld < k) || row < 0 || step < 0 || row > (int64_t(1) << 38) || step > (int64_t(1) << 38))
+    return set_error(ST_E_INVAL, "%s: %s has %lld elements between rows of %lld and %lld between experts", op, name, (long long)w.ld, (long long)k,
+                     (long long)w.expert);
+  if (experts > 1 && step < (rows - 1) * row + k)
+    return set_error(ST_E_INVAL, "%s: %s's experts of %lld x %lld are %lld elements apart", op, name, (long long)rows, (long long)k, (long long)step);
+  if (reinterpret_cast<uintptr_t>(w.w) % 16 || row * item % 16 || step * item % 16)
+    return set_error(ST_E_ALIGN, "%s: %s's address, rows and experts are not multiples of 16 bytes apart", op, name);
+  if (item == 2) return w.scale ? set_error(ST_E_INVAL, "%s: scales of a 16-bit %s", op, name) : ST_OK;
+  if (!w.scale) return set_error(ST_E_INVAL, "%s: %s has no scales", op, name);
+  ST_TRY(check_vector(op, "scales", w.scale, ST_F32));
+  const int64_t most = int64_t(1) << 40;
+  if (w.scale_expert < 0 || w.scale_row < 0 || w.scale_col < 0 || w.scale_expert > most || w.scale_row > most || w.scale_col > most)
+    return set_error(ST_E_INVAL, "%s: %s's scales have strides out of range", op, name);
+  return ST_OK;
+}
+
+st_status check_moe(const st_moe_args *a, bool *empty) {
+  const char *op = "st_moe";
+  constexpr int64_t kMost = int64_t(1) << 24;
+  if (a->tokens < 0 || a->tokens > ST_MOE_MAX_TOKENS)
+    return set_error(ST_E_INVAL, "%s: %lld tokens (0 .. %d: for more, group them by expert)", op, (long long)a->tokens, ST_MOE_MAX_TOKENS);
+  if (a->hidden < 1 || a->hidden > kMost || a->inter < 1 || a->inter > kMost)
+    return set_error(ST_E_INVAL, "%s: hidden %lld, inter %lld are out of range (1 .. 2^24)", op, (long long)a->hidden, (long long)a->inter);
+  if (a->experts < 1 || a->experts > 1024 || a->top_k < 1 || a->top_k > 32 || a->top_k > a->experts)
+    return set_error(ST_E_INVAL, "%s: %lld of %lld experts (1 .. 32 of up to 1024)", op, (long long)a->top_k, (long long)a->experts);
+  if (a->act < ST_ACT_NONE || a->act > ST_ACT_GELU_TANH) return set_error(ST_E_INVAL, "%s: unknown activation %d", op, (int)a->act);
+  if (a->score != ST_MOE_SOFTMAX && a->score != ST_MOE_SIGMOID) return set_error(ST_E_INVAL, "%s: unknown score %d", op, (int)a->score);
+  if (a->x_dtype != ST_BF16 && a->x_dtype != ST_F16) return set_error(ST_E_DTYPE, "%s: x is BF16 or F16, not %d", op, (int)a->x_dtype);
+  if (!is_float16or32(a->router_dtype)) return set_error(ST_E_DTYPE, "%s: router is BF16, F16 or F32, not %d", op, (int)a->router_dtype);
+  if (a->w_dtype != a->x_dtype && a->w_dtype != ST_F8_E4M3 && a->w_dtype != ST_F8_E5M2)
+    return set_error(ST_E_DTYPE, "%s: the experts are of x's dtype, F8_E4M3 or F8_E5M2, not %d", op, (int)a->w_dtype);
+  if (!is_float16or32(a->y_dtype)) return set_error(ST_E_DTYPE, "%s: the output is BF16, F16 or F32, not %d", op, (int)a->y_dtype);
+  *empty = a->tokens == 0;
+  if (*empty) return ST_OK;
+  ST_TRY(check_matrix(op, "x", a->x, a->ldx, a->x_dtype, a->tokens, a->hidden, true));
+  ST_TRY(check_matrix(op, "router", a->router, a->ld_router, a->router_dtype, a->experts, a->hidden, true));
+  ST_TRY(check_vector(op, "router_bias", a->router_bias, ST_F32));
+  ST_TRY(check_experts(op, "gate", a->gate, a->w_dtype, a->experts, a->inter, a->hidden));
+  if (a->up.w) ST_TRY(check_experts(op, "up", a->up, a->w_dtype, a->experts, a->inter, a->hidden));
+  ST_TRY(check_experts(op, "down", a->down, a->w_dtype, a->experts, a->hidden, a->inter));
+  if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->y_dtype, a->tokens, a->hidden, true));
+  ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->tokens, a->hidden, false));
+  ST_TRY(check_vector(op, "chosen", a->chosen, ST_F32));
+  ST_TRY(check_vector(op, "weights", a->weights, ST_F32));
+  return ST_OK;
+}
+
+// What a call writes overlaps nothing else, but y its residual.
+st_status check_moe_overlaps(const st_moe_args *a, int64_t space) {
+  const char *op = "st_moe";
+  struct Named {
+    const char *name;
+    Bytes bytes;
+  };
+  auto experts = [&](const st_moe_weight &w, int64_t rows, int64_t k) {
+    const int64_t item = static_cast<int64_t>(st_dtype_size(a->w_dtype));
+    return array_bytes(w.w, static_cast<uint64_t>(((a->experts - 1) * w.expert + (rows - 1) * w.ld + k) * item));
+  };
+  auto scales = [&](const st_moe_weight &w, int64_t rows, int64_t k) {
+    const int64_t last = (a->experts - 1) * w.scale_expert + (rows - 1) / 128 * w.scale_row + (k - 1) / 128 * w.scale_col;
+    return array_bytes(w.scale, static_cast<uint64_t>(4 * (last + 1)));
+  };
+  Named reads[12], writes[4];
+  int n = 0, m = 0;
+  reads[n++] = {"x", matrix_bytes(a->x, a->ldx, a->x_dtype, a->tokens, a->hidden)};
+  reads[n++] = {"router", matrix_bytes(a->router, a->ld_router, a->router_dtype, a->experts, a->hidden)};
+  if (a->router_bias) reads[n++] = {"router_bias", array_bytes(a->router_bias, 4 * a->experts)};
+  reads[n++] = {"gate", experts(a->gate, a->inter, a->hidden)};
+  if (a->up.w) reads[n++] = {"up", experts(a->up, a->inter, a->hidden)};
+  reads[n++] = {"down", experts(a->down, a->hidden, a->inter)};
+  if (a->gate.scale) reads[n++] = {"gate's scales", scales(a->gate, a->inter, a->hidden)};
+  if (a->up.w && a->up.scale) reads[n++] = {"up's scales", scales(a->up, a->inter, a->hidden)};
+  if (a->down.scale) reads[n++] = {"down's scales", scales(a->down, a->hidden, a->inter)};
+  if (a->residual) reads[n++] = {"the residual", matrix_bytes(a->residual, a->ldr, a->y_dtype, a->tokens, a->hidden)};
+  writes[m++] = {"y", matrix_bytes(a->y, a->ldy, a->y_dtype, a->tokens, a->hidden)};
+  writes[m++] = {"the workspace", array_bytes(a->workspace, static_cast<uint64_t>(space))};
+  if (a->chosen) writes[m++] = {"chosen", array_bytes(a->chosen, 4 * a->tokens * a->top_k)};
+  if (a->weights) writes[m++] = {"weights", array_bytes(a->weights, 4 * a->tokens * a->top_k)};
+  const bool in_place = a->residual == a->y && (a->tokens == 1 || a->ldr == a->ldy);
+  for (int i = 0; i < m; ++i) {
+    for (int j = 0; j < n; ++j) {
+      if (i == 0 && in_place && a->residual && j == n - 1) continue;
+      if (overlap(writes[i].bytes, reads[j].bytes)) return set_error(ST_E_INVAL, "%s: %s overlaps %s", op, writes[i].name, reads[j].name);
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(writes[i].bytes, writes[j].bytes)) return set_error(ST_E_INVAL, "%s: %s overlaps %s", op, writes[i].name, writes[j].name);
+  }
+  return ST_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -353,6 +448,29 @@ st_status st_block_linear(const st_block_linear_args *a, void *stream) { return 
 st_status st_block_linear_as(const st_block_linear_args *a, const st_linear_form *form, void *stream) {
   if (!form) return set_error(ST_E_INVAL, "st_block_linear_as: NULL form");
   return run_block_linear(a, form, stream);
+}
+
+st_status st_moe_workspace(const st_moe_args *a, uint64_t *bytes) {
+  if (!a || !bytes) return set_error(ST_E_INVAL, "st_moe_workspace: NULL argument");
+  bool empty = false;
+  ST_TRY(check_moe(a, &empty));
+  *bytes = empty ? 0 : static_cast<uint64_t>(moe_workspace(*a));
+  return ST_OK;
+}
+
+st_status st_moe(const st_moe_args *a, void *stream) {
+  const char *op = "st_moe";
+  if (!a) return set_error(ST_E_INVAL, "%s: NULL arguments", op);
+  bool empty = false;
+  ST_TRY(check_moe(a, &empty));
+  if (empty) return ST_OK;
+  const int64_t need = moe_workspace(*a);
+  if (!a->workspace || a->workspace_bytes < static_cast<uint64_t>(need))
+    return set_error(ST_E_INVAL, "%s: a workspace of %lld bytes is needed, %llu given", op, (long long)need,
+                     (unsigned long long)(a->workspace ? a->workspace_bytes : 0));
+  if (reinterpret_cast<uintptr_t>(a->workspace) % 256) return set_error(ST_E_ALIGN, "%s: the workspace is not 256-byte aligned", op);
+  ST_TRY(check_moe_overlaps(a, need));
+  return launch_moe(*a, stream);
 }
 
 }  // extern "C"

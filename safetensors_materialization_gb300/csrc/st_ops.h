@@ -32,5 +32,7 @@ st_status launch_block_linear(const st_block_linear_args &a, const st_linear_for
 st_status check_block_linear_form(const st_block_linear_args &a, const st_linear_form &form);
 st_linear_form choose_block_linear_form(const st_block_linear_args &a, int sms);
 int64_t block_linear_workspace(const st_block_linear_args &a);
+st_status launch_moe(const st_moe_args &a, void *stream);
+int64_t moe_workspace(const st_moe_args &a);
 
 }  // namespace stmat

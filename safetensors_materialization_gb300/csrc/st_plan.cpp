@@ -1549,7 +1549,7 @@ st_status st_static_check(void *stream, uint32_t *flags) {
     return set_error(ST_E_DEVICE, "static-scratch device flags 0x%x:%s%s%s", v,
                      (v & kErrBadDst) ? " a non-empty output had a NULL or misaligned destination;" : "",
                      (v & kErrTimeout) ? " a wait for a staged copy gave up;" : "",
-                     (v & kErrProduct) ? " a wait in st_linear gave up, its y is incomplete;" : "");
+                     (v & kErrProduct) ? " a wait in st_linear, st_block_linear or st_moe gave up, its y is incomplete;" : "");
   return ST_OK;
 }
 

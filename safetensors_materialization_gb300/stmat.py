@@ -133,7 +133,24 @@ class BlockLinearArgs(C.Structure):
                 ("ldy", C.c_int64), ("workspace", C.c_void_p), ("workspace_bytes", C.c_uint64)]
 
 
+class MoeWeight(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("expert", C.c_int64), ("ld", C.c_int64), ("scale", C.c_void_p),
+                ("scale_expert", C.c_int64), ("scale_row", C.c_int64), ("scale_col", C.c_int64)]
+
+
+class MoeArgs(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("hidden", C.c_int64), ("inter", C.c_int64), ("experts", C.c_int64),
+                ("top_k", C.c_int64), ("act", C.c_int), ("score", C.c_int), ("normalize", C.c_int32), ("factor", C.c_float),
+                ("x_dtype", C.c_int), ("router_dtype", C.c_int), ("w_dtype", C.c_int), ("y_dtype", C.c_int),
+                ("x", C.c_void_p), ("ldx", C.c_int64), ("router", C.c_void_p), ("ld_router", C.c_int64),
+                ("router_bias", C.c_void_p), ("gate", MoeWeight), ("up", MoeWeight), ("down", MoeWeight),
+                ("residual", C.c_void_p), ("ldr", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64),
+                ("chosen", C.c_void_p), ("weights", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_uint64)]
+
+
 LINEAR_KERNELS = ("split", "dense")
+SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_MAX_TOKENS = 64
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _lib = None
@@ -202,6 +219,8 @@ def lib():
             "st_block_linear_workspace": [C.POINTER(BlockLinearArgs), C.POINTER(U64)],
             "st_block_linear_choose": [C.POINTER(BlockLinearArgs), I, C.POINTER(LinearForm)],
             "st_block_linear_as": [C.POINTER(BlockLinearArgs), C.POINTER(LinearForm), P],
+            "st_moe": [C.POINTER(MoeArgs), P],
+            "st_moe_workspace": [C.POINTER(MoeArgs), C.POINTER(U64)],
             "st_linear": [C.POINTER(LinearArgs), P],
             "st_linear_workspace": [C.POINTER(LinearArgs), C.POINTER(U64)],
             "st_linear_choose": [C.POINTER(LinearArgs), I, I, I, C.POINTER(LinearForm)],
@@ -890,6 +909,7 @@ class Outputs:
 _NORM_ARGS = struct.Struct("@qqfiiiPqPqPPqPqPP")
 _ACT_ARGS = struct.Struct("@qqiiiPqPqPqPP")
 _LINEAR_ARGS = struct.Struct("@qqqiiiiiPqPqPqPqPPqPqPQ")
+_MOE_ARGS = struct.Struct("@qqqqqiiifiiiiPqPqPPqqPqqqPqqPqqqPqqPqqqPqPqPPPQ")
 
 _OPS = None
 
@@ -907,7 +927,7 @@ class _Ops:
         self.stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p)
         for n in ("rms_norm", "gated_act", "linear", "linear_workspace", "rms_norm_blocks", "gated_act_blocks",
-                  "block_linear", "block_linear_workspace"):
+                  "block_linear", "block_linear_workspace", "moe", "moe_workspace"):
             setattr(self, n, call(("st_" + n, lib())))
         call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p, C.c_void_p)
         self.linear_as, self.block_linear_as = call(("st_linear_as", lib())), call(("st_block_linear_as", lib()))
@@ -1254,3 +1274,89 @@ def block_linear_choice(m, n, k, sms=152):
     form = LinearForm()
     _check(lib().st_block_linear_choose(C.byref(args), sms, C.byref(form)))
     return LINEAR_KERNELS[form.kernel], form.width, form.splits
+
+
+def _experts(t, scale, name, gpu, experts, rows, k, dtype):
+    """The fields of st_moe_weight of an [experts, rows, k] tensor and its
+    scales."""
+    if tuple(t.shape) != (experts, rows, k) or t.dtype != dtype:
+        raise _invalid(f"{name}: {tuple(t.shape)} {t.dtype}, [{experts}, {rows}, {k}] {dtype} is needed")
+    if t.get_device() != gpu:
+        raise _elsewhere(t, name, gpu)
+    step, ld, inner = t.stride()
+    if inner != 1 and k > 1:
+        raise _invalid(f"{name}: the last dimension has stride {inner}, not 1")
+    if scale is None:
+        return t.data_ptr(), step, ld, 0, 0, 0, 0
+    shape = (experts, -(-rows // _BLOCK), -(-k // _BLOCK))
+    if tuple(scale.shape) != shape:
+        raise _invalid(f"{name}_scale: {tuple(scale.shape)}, {shape} is needed")
+    if str(scale.dtype) != "torch.float32":
+        raise StmatError(6, f"{name}_scale: {scale.dtype} is not F32")
+    if scale.get_device() != gpu:
+        raise _elsewhere(scale, name + "_scale", gpu)
+    return t.data_ptr(), step, ld, scale.data_ptr(), *scale.stride()
+
+
+def moe(x, router, gate, up, down, top_k, gate_scale=None, up_scale=None, down_scale=None, act="silu", score="softmax",
+        normalize=True, factor=1.0, router_bias=None, residual=None, dst=None, out=None, stream=None):
+    """st_moe: a mixture-of-experts layer for up to MOE_MAX_TOKENS tokens, the
+    rows of x (BF16 or F16, [..., hidden]).
+
+    router: [experts, hidden] BF16, F16 or F32; router_bias: [experts] F32, added
+    to the scores for the choice alone.  gate and up: [experts, inter, hidden],
+    down: [experts, hidden, inter], of x's dtype or, with their F32 scales for
+    128 x 128 blocks [experts, ceil(rows / 128), ceil(columns / 128)], F8_E4M3 or
+    F8_E5M2; rows and experts lie at multiples of 16 bytes.  up None: act(gate x)
+    alone.  score: "softmax" or "sigmoid"; the chosen experts' weights are factor
+    times their scores, divided by their sum with normalize.
+    dst, residual and out as for linear (dst: x's dtype by default).
+
+    Returns (y, chosen experts [..., top_k] int32, their weights F32).  No
+    gradient passes through; a wait that gave up shows in static_check()."""
+    ops = _OPS or _ops()
+    gpu = x.get_device()
+    if stream is not None or gpu < 0 or gpu != ops.device():
+        return _On(ops.torch, stream, gpu, "x").run(
+            lambda: moe(x, router, gate, up, down, top_k, gate_scale, up_scale, down_scale, act, score, normalize, factor,
+                        router_bias, residual, dst, out),
+            (x, router, gate, up, down, gate_scale, up_scale, down_scale, router_bias, residual, out))
+    codes, x_type, torch = ops.codes, x.dtype, ops.torch
+    px, ldx, tokens, hidden = _matrix(x, "x")
+    pr, ldr, experts, rh = _matrix(router, "router", gpu)
+    if rh != hidden or router.dim() != 2 or gate.dim() != 3:
+        raise _invalid(f"x has rows of {hidden}, router is {tuple(router.shape)}, gate {tuple(gate.shape)}")
+    inter, w_type = gate.shape[1], gate.dtype
+    weights = (*_experts(gate, gate_scale, "gate", gpu, experts, inter, hidden, w_type),
+               *((0,) * 7 if up is None else _experts(up, up_scale, "up", gpu, experts, inter, hidden, w_type)),
+               *_experts(down, down_scale, "down", gpu, experts, hidden, inter, w_type))
+    pb = 0 if router_bias is None else _vector(router_bias, "router_bias", gpu, experts, _F32, codes)[0]
+    if out is None:
+        y_type, y_code = _dst(dst, x_type, ops)
+        out = ops.empty(x.shape, dtype=y_type, device=x.device)
+        py, ldy = out.data_ptr(), hidden
+    else:
+        y_type = out.dtype
+        if out.shape != x.shape or (dst is not None and _dst(dst, None, ops)[0] != y_type):
+            raise _invalid(f"out: {tuple(out.shape)} {y_type}, the layer's is {tuple(x.shape)} {dst or ''}")
+        y_code = codes.get(y_type, -1)
+        py, ldy, _, _ = _matrix(out, "out", gpu)
+    ps = lds = 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != y_type:
+            raise _invalid(f"residual: {tuple(residual.shape)} {residual.dtype}, y: {tuple(x.shape)} {y_type}")
+        ps, lds, _, _ = _matrix(residual, "residual", gpu)
+    args = (tokens, hidden, inter, experts, top_k, ACTS.get(act, -1), SCORES.get(score, -1), bool(normalize), factor,
+            codes.get(x_type, -1), codes.get(router.dtype, -1), codes.get(w_type, -1), y_code, px, ldx, pr, ldr, pb,
+            *weights, ps, lds, py, ldy)
+    need = C.c_uint64()
+    code = ops.moe_workspace(_MOE_ARGS.pack(*args, 0, 0, 0, 0), C.addressof(need))
+    if code:
+        _check(code)
+    shape = x.shape[:-1] + (top_k,)
+    chosen, p = ops.empty(shape, dtype=torch.int32, device=x.device), ops.empty(shape, dtype=torch.float32, device=x.device)
+    space = ops.empty(need.value, dtype=torch.uint8, device=x.device)
+    code = ops.moe(_MOE_ARGS.pack(*args, chosen.data_ptr(), p.data_ptr(), space.data_ptr(), need.value), ops.stream(gpu))
+    if code:
+        _check(code)
+    return out, chosen, p
