@@ -45,17 +45,21 @@ constexpr int kMaxTop = 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSplit = 8;         // portable cluster size
 constexpr int kSumWarps = 4;         // one per 32 TMEM lanes
-constexpr int kMmaWarp = 4, kCopyWarp = 5, kThreads = 192;
+constexpr int kMmaWarp = 4, kCopyWarp = 5, kScaleWarp = 6, kThreads = 224;
+constexpr int kScaleSlots = 8, kScaleRun = 4;  // stages whose scales are ready, and brought in together
 constexpr int kLogitWarps = 8, kLogitTokens = 4;
 constexpr int kRouteWarps = 8;       // tokens of a CTA of route_kernel
-// Stages and sums to join: half of an SM's shared memory where three stages fit
-// in that, so that one CTA's start and end lie beside another's copies.
-constexpr int kHalfSmem = 108 * 1024, kSmem = 204 * 1024;
+constexpr int kGroup = 32;           // tokens of an expert that are multiplied at a time
+// Stages and sums: under half of an SM's shared memory, and at most half of its
+// TMEM, so that one CTA's start and end lie beside another's copies, and no CTA
+// of a cluster waits for TMEM that another cluster's holds.
+constexpr int kSmem = 106 * 1024;
 
 // What route_kernel finds.  Arrays of as many entries as can be needed.
 struct Lists {
-  int *count;         // chosen experts
-  int *expert;        // [i]: the i-th of them, ascending
+  int *count;         // groups: chosen experts with up to kGroup of their tokens
+  int *most;          // tokens of the largest group
+  int *expert;        // [i]: the i-th group's expert, ascending
   int *first;         // [i]: its first slot; [count]: the number of slots
   int *token;         // [slot]
   float *weight;      // [slot]
@@ -85,7 +89,7 @@ struct MoeArgs {
   int h_blocks, in_blocks, h_runs, in_runs;  // stages and runs of hidden and inter
   Lists list;
   uint32_t idesc;         // without the number of columns
-  int splits, stages, tiles;
+  int splits, tiles;
   uint32_t *err;
 };
 
@@ -133,13 +137,11 @@ struct Two {
   }
 };
 
-template <class T>
-__device__ __forceinline__ float element(const void *p, int64_t at) { return to_float(static_cast<const T *>(p)[at]); }
-
-// A warp has an expert and up to four tokens.
+// A block has an expert and up to four tokens; its warps share the sum.
 template <class X, class R>
-__device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0, int lane) {
-  const int live = min(kLogitTokens, a.tokens - t0);
+__device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {
+  __shared__ float part[kLogitWarps][kLogitTokens][2];
+  const int live = min(kLogitTokens, a.tokens - t0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const R *const w = static_cast<const R *>(a.router) + expert * a.ld_router;
   const X *const x = static_cast<const X *>(a.x) + t0 * a.ldx;
   Two sum[kLogitTokens];
@@ -153,20 +155,24 @@ __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0, int
   const bool wide = a.hidden % V == 0 && a.ldx % V == 0 && a.ld_router % V == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
   if (wide) {
-#pragma unroll 2
-    for (int c = lane * V; c < a.hidden; c += 32 * V) {
+    for (int c = threadIdx.x * V; c < a.hidden; c += 32 * kLogitWarps * V) {
+      const Raw<R, V> wr = *reinterpret_cast<const Raw<R, V> *>(w + c);
+      Raw<X, V> xr[kLogitTokens];
+#pragma unroll
+      for (int t = 0; t < kLogitTokens; ++t)
+        if (t < live) xr[t] = *reinterpret_cast<const Raw<X, V> *>(x + t * a.ldx + c);
       float wv[V], xv[V];
-      unpack(*reinterpret_cast<const Raw<R, V> *>(w + c), wv);
+      unpack(wr, wv);
 #pragma unroll
       for (int t = 0; t < kLogitTokens; ++t) {
         if (t >= live) continue;
-        unpack(*reinterpret_cast<const Raw<X, V> *>(x + t * a.ldx + c), xv);
+        unpack(xr[t], xv);
 #pragma unroll
         for (int i = 0; i < V; ++i) step(t, xv[i], wv[i]);
       }
     }
   } else {
-    for (int c = lane; c < a.hidden; c += 32) {
+    for (int c = threadIdx.x; c < a.hidden; c += 32 * kLogitWarps) {
       const float wv = to_float(w[c]);
 #pragma unroll
       for (int t = 0; t < kLogitTokens; ++t)
@@ -182,13 +188,22 @@ __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0, int
       sum[t].lo += lo;
       sum[t].add(hi);
     }
-    if (lane == 0) {
-      // Where the sum has left binary32's range its error has no meaning.
-      const double l = isfinite(sum[t].hi) ? static_cast<double>(sum[t].hi) + sum[t].lo : sum[t].hi;
-      const int64_t at = int64_t(t0 + t) * a.experts + expert;
-      a.logits[at] = l;
-      if (a.bias && a.sigmoid) a.keys[at] = 1.0 / (1.0 + exp(-l)) + a.bias[expert];
+    if (lane == 0) part[warp][t][0] = sum[t].hi, part[warp][t][1] = sum[t].lo;
+  }
+  __syncthreads();
+  if (threadIdx.x < live) {
+    const int t = threadIdx.x;
+    Two all;
+#pragma unroll
+    for (int i = 0; i < kLogitWarps; ++i) {
+      all.lo += part[i][t][1];
+      all.add(part[i][t][0]);
     }
+    // Where the sum has left binary32's range its error has no meaning.
+    const double l = isfinite(all.hi) ? static_cast<double>(all.hi) + all.lo : all.hi;
+    const int64_t at = int64_t(t0 + t) * a.experts + expert;
+    a.logits[at] = l;
+    if (a.bias && a.sigmoid) a.keys[at] = 1.0 / (1.0 + exp(-l)) + a.bias[expert];
   }
 }
 
@@ -232,94 +247,90 @@ __device__ __forceinline__ void x_columns(const MoeArgs &a, int token) {
 __global__ void __launch_bounds__(32 * kLogitWarps) logits_kernel(const __grid_constant__ MoeArgs a) {
   wait_for_previous();
   let_next_start();
-  const int groups = (a.tokens + kLogitTokens - 1) / kLogitTokens, items = a.experts * groups;
-  const int blocks = (items + kLogitWarps - 1) / kLogitWarps;
+  const int groups = (a.tokens + kLogitTokens - 1) / kLogitTokens;
   auto with_x = [&](auto &&f) {
     if (a.x_dtype == ST_BF16) f(__nv_bfloat16{});
     else f(__half{});
   };
-  if (blockIdx.x >= blocks) {
-    with_x([&](auto x) { x_columns<decltype(x)>(a, blockIdx.x - blocks); });
-    return;
-  }
-  const int item = blockIdx.x * kLogitWarps + (threadIdx.x >> 5);
-  if (item >= items) return;
-  with_x([&](auto x) {
-    with_type(a.router_dtype, [&](auto r) { logits<decltype(x), decltype(r)>(a, item / groups, item % groups * kLogitTokens, threadIdx.x & 31); });
-  });
+  const int item = blockIdx.x - a.tokens;
+  if (item < 0) with_x([&](auto x) { x_columns<decltype(x)>(a, blockIdx.x); });
+  else
+    with_x([&](auto x) {
+      with_type(a.router_dtype, [&](auto r) { logits<decltype(x), decltype(r)>(a, item / groups, item % groups * kLogitTokens); });
+    });
 }
 
 // -------------------------------------------------------- route_kernel
 
-// Order of the choice: NaN before all, then by size.
-__device__ __forceinline__ bool before(double k, int e, double best, int best_e) {
-  const bool kn = isnan(k), bn = isnan(best);
-  if (kn != bn) return kn;
-  if (!kn && k != best) return k > best;
-  return e < best_e;
+// A whole number in the order of the choice: by size, a NaN above all.  (The
+// SM compares 64 whole numbers in the time of one pair of binary64 ones: 1 of
+// 128 experts' choice of 8 took 19 us so.)
+__device__ __forceinline__ int64_t order(double v) {
+  int64_t b = __double_as_longlong(v);
+  if ((b & 0x7fffffffffffffffll) > 0x7ff0000000000000ll) return 0x7fffffffffffffffll;
+  if (b == static_cast<int64_t>(0x8000000000000000ull)) b = 0;  // -0
+  return b ^ ((b >> 63) & 0x7fffffffffffffffll);
 }
+__device__ __forceinline__ double ordered(int64_t k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffll)); }
 
 // A warp chooses for a token; kPer of the experts a lane (expert 32 j + lane).
 template <int kPer>
 __device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int lane, int *chosen, float *weight) {
+  constexpr int64_t kNone = static_cast<int64_t>(0x8000000000000000ull);  // below every number
   const double *const l = a.logits + int64_t(token) * a.experts;
-  double key[kPer];
+  int64_t key[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) key[j] = 32 * j + lane < a.experts ? l[32 * j + lane] : 0.0;
+  for (int j = 0; j < kPer; ++j) key[j] = 32 * j + lane < a.experts ? order(l[32 * j + lane]) : kNone;
   // Softmax: relative to the largest logit.
   double top = 0.0;
   float all = 0.0f;
   if (!a.sigmoid) {
-    top = __longlong_as_double(0xfff0000000000000ll);
-    bool none = true;
+    int64_t best = kNone;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (32 * j + lane < a.experts) top = none || key[j] > top || isnan(key[j]) ? key[j] : top, none = false;
+    for (int j = 0; j < kPer; ++j) best = max(best, key[j]);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      const double o = __shfl_xor_sync(~0u, top, d);
-      if (o > top || isnan(o)) top = o;
-    }
-    if (!a.normalize || a.bias) {
+    for (int d = 16; d; d >>= 1) best = max(best, static_cast<int64_t>(__shfl_xor_sync(~0u, best, d)));
+    top = ordered(best);
+    if (!a.normalize) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (32 * j + lane < a.experts) all += expf(static_cast<float>(key[j] - top));
+        if (32 * j + lane < a.experts) all += expf(static_cast<float>(ordered(key[j]) - top));
 #pragma unroll
       for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
     }
     if (a.bias) {
-      double sum = 0.0;
+      double sum = 0.0, s[kPer];
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (32 * j + lane < a.experts) key[j] = exp(key[j] - top), sum += key[j];
+        if (32 * j + lane < a.experts) s[j] = exp(ordered(key[j]) - top), sum += s[j];
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (32 * j + lane < a.experts) key[j] = key[j] / sum + a.bias[32 * j + lane];
+        if (32 * j + lane < a.experts) key[j] = order(s[j] / sum + a.bias[32 * j + lane]);
     }
   } else if (a.bias) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (32 * j + lane < a.experts) key[j] = a.keys[int64_t(token) * a.experts + 32 * j + lane];
+      if (32 * j + lane < a.experts) key[j] = order(a.keys[int64_t(token) * a.experts + 32 * j + lane]);
   }
-  uint32_t taken = 0;
+  // Taken experts leave with a key of none; an expert's own is above it.
   int mine = 0;
   for (int i = 0; i < a.top_k; ++i) {
-    double best = 0.0;
-    int best_e = 0x7fffffff;
+    int64_t best = kNone;
+    int best_e = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = 32 * j + lane;
-      if (e < a.experts && !(taken >> j & 1) && (best_e == 0x7fffffff || before(key[j], e, best, best_e))) best = key[j], best_e = e;
-    }
+    for (int j = 0; j < kPer; ++j)
+      if (key[j] > best) best = key[j], best_e = 32 * j + lane;
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
-      const double k = __shfl_xor_sync(~0u, best, d);
+      const int64_t k = __shfl_xor_sync(~0u, best, d);
       const int e = __shfl_xor_sync(~0u, best_e, d);
-      if (e != 0x7fffffff && (best_e == 0x7fffffff || before(k, e, best, best_e))) best = k, best_e = e;
+      if (k > best || (k == best && e < best_e)) best = k, best_e = e;
     }
-    if ((best_e & 31) == lane) taken |= 1u << (best_e >> 5);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (32 * j + lane == best_e) key[j] = kNone;
     if (lane == i) mine = best_e;
   }
   // Lane i has the i-th chosen expert.
@@ -345,7 +356,7 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int 
 template <int kPer>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ MoeArgs a) {
   __shared__ uint64_t mask[kMaxExperts];             // tokens of an expert
-  __shared__ int slots[kMaxExperts], totals[kRouteWarps][2];
+  __shared__ int slots[kMaxExperts], totals[kRouteWarps][3];
   __shared__ int chosen[kRouteWarps][kMaxTop];
   __shared__ float weight[kRouteWarps][kMaxTop];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = blockIdx.x * kRouteWarps + warp;
@@ -368,13 +379,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   // Slots, and places in the list: running counts over the experts, four (of up
   // to 1024) a thread.
   constexpr int kEach = kMaxExperts / kThreadsHere;
-  int n[kEach], used[kEach], all_n = 0, all_used = 0;
+  int n[kEach], all_n = 0, all_used = 0, most = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x * kEach + i;
     n[i] = e < a.experts ? __popcll(mask[e]) : 0;
-    used[i] = n[i] > 0;
-    all_n += n[i], all_used += used[i];
+    all_n += n[i], all_used += (n[i] + kGroup - 1) / kGroup;
+    most = max(most, min(n[i], kGroup));
   }
   int before_n = all_n, before_used = all_used;
 #pragma unroll
@@ -382,24 +393,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     const int o = __shfl_up_sync(~0u, before_n, d), u = __shfl_up_sync(~0u, before_used, d);
     if (lane >= d) before_n += o, before_used += u;
   }
-  if (lane == 31) totals[warp][0] = before_n, totals[warp][1] = before_used;
+  most = __reduce_max_sync(~0u, most);
+  if (lane == 31) totals[warp][0] = before_n, totals[warp][1] = before_used, totals[warp][2] = most;
   __syncthreads();
   before_n -= all_n, before_used -= all_used;
-  for (int w = 0; w < warp; ++w) before_n += totals[w][0], before_used += totals[w][1];
+  for (int w = 0; w < kRouteWarps; ++w) {
+    if (w < warp) before_n += totals[w][0], before_used += totals[w][1];
+    most = max(most, totals[w][2]);
+  }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x * kEach + i;
-    if (e < a.experts) {
-      slots[e] = before_n;
-      if (blockIdx.x == 0 && used[i]) {
-        a.list.expert[before_used] = e;
-        a.list.first[before_used] = before_n;
-      }
+    if (e < a.experts) slots[e] = before_n;
+    for (int g = 0; g < n[i]; g += kGroup, ++before_used) {
+      if (blockIdx.x > 0) continue;
+      a.list.expert[before_used] = e;
+      a.list.first[before_used] = before_n + g;
     }
-    before_n += n[i], before_used += used[i];
+    before_n += n[i];
   }
   if (blockIdx.x == 0 && threadIdx.x == kThreadsHere - 1) {
     *a.list.count = before_used;
+    *a.list.most = most;
     a.list.first[before_used] = before_n;
   }
   __syncthreads();
@@ -455,19 +470,23 @@ __host__ __device__ constexpr int tmem_columns(int n) { return n <= 32 ? 32 : n 
 
 // What both kernels' CTAs have.
 struct Pipe {
-  uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2], ready[kScaleSlots], used[kScaleSlots];
   uint32_t tmem;
   int failed;
 };
-__device__ __forceinline__ void pipe_start(Pipe &p, int stages, int warp, int columns) {
+__device__ __forceinline__ void pipe_start(Pipe &p, int warp, int columns) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       bar_init(&p.full[i], 1);
       bar_init(&p.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&p.sums[i], 1);
       bar_init(&p.taken[i], kSumWarps);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      bar_init(&p.ready[i], 1);
+      bar_init(&p.used[i], kSumWarps);
     }
     p.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -493,20 +512,35 @@ __device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, 128
 __device__ __forceinline__ void local_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// Adds eight tokens' sums of a stage, times their scales.
+template <int C, bool kEight, int BT>
+__device__ __forceinline__ void add_tokens(float (&to)[BT], int t, uint32_t from, const float *scale) {
+  uint32_t v[8 * C];
+  read_tokens<C>(from + t * C, v);
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+  if (scale) {
+    *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(scale + t);
+    *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(scale + t + 4);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) to[t + j] = fmaf(of_columns<C, kEight>(v, j), f[j], to[t + j]);
+}
 
-// h of 128 rows of one chosen expert.  BT: tokens an expert may have; C: columns
-// of an x.  Gate's and up's sums of a stage lie side by side in TMEM.
+// h of 128 rows of one group.  BT: tokens that a group may have; C: columns of
+// an x.  Gate's and up's sums of a stage lie side by side in TMEM.
 template <int BT, int C, bool kEight>
 __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CUtensorMap gate, const __grid_constant__ CUtensorMap up,
                                                       const __grid_constant__ CUtensorMap xmap, const __grid_constant__ MoeArgs a) {
-  constexpr int kN = round16(BT * C), kBuffers = 4 * kN <= 512 ? 2 : 1, kColumns = tmem_columns(kBuffers * 2 * kN);
-  constexpr int kStageBytes = (2 * kRows + kN) * kStageK, kStep = kEight ? kStageK : kStageK / 2;
-  constexpr int kOutColumns = kEight ? 3 : 2;
+  constexpr int kN = round16(BT * C), kBuffers = 4 * kN <= 256 ? 2 : 1, kColumns = tmem_columns(kBuffers * 2 * kN);
+  constexpr int kStep = kEight ? kStageK : kStageK / 2, kOutColumns = kEight ? 3 : 2;
+  static_assert(kColumns <= 256 && 2 * (2 * kRows + kN) * kStageK <= kSmem && (BT + kMaxSplit) * 2 * kRows * 4 <= kSmem, "half of an SM");
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   __shared__ Pipe pipe;
-  __shared__ __align__(16) float scales[kSumWarps][2][2][BT];
-  __shared__ float tops[kSumWarps][BT];
+  __shared__ __align__(16) float scales[kScaleSlots][2][BT];
+  __shared__ float tops[kSumWarps][BT], weights[BT];
   __shared__ int tokens[BT];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
   const int item = blockIdx.x / a.splits, which = item / a.tiles, n0 = item % a.tiles * kRows;
   const int first = static_cast<int>(int64_t(a.h_blocks) * rank / a.splits);
   const int blocks = static_cast<int>(int64_t(a.h_blocks) * (rank + 1) / a.splits) - first;
-  pipe_start(pipe, a.stages, warp, kColumns);
+  pipe_start(pipe, warp, kColumns);
   wait_for_previous();
   let_next_start();
   if (which >= *a.list.count) {  // every CTA of the cluster
@@ -522,20 +556,22 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
     return;
   }
   const int expert = a.list.expert[which], slot0 = a.list.first[which], count = a.list.first[which + 1] - slot0;
+  const int columns = round16(count * C), stage_bytes = (2 * kRows + columns) * kStageK;
+  const int stages = min(kMaxStages, kSmem / stage_bytes);
   const uint32_t tmem = pipe.tmem;
 
   Ring r;
   float g[BT], u[BT];
   if (warp == kCopyWarp) {
-    for (int i = lane; i < count; i += 32) tokens[i] = a.list.token[slot0 + i];
+    if (lane < count) tokens[lane] = a.list.token[slot0 + lane];
     __syncwarp();
     if (elect_one()) {
       bool ok = true;
       const uint32_t bytes = (a.has_up ? 2 : 1) * kRows * kStageK + count * C * kStageK;
-      for (int i = 0; i < blocks; ++i, r.next(a.stages)) {
+      for (int i = 0; i < blocks; ++i, r.next(stages)) {
         // Before its first use a stage counts as released.
         if (!bar_wait(&pipe.empty[r.at], r.phase ^ 1)) { ok = false; break; }
-        uint8_t *stage = smem + r.at * kStageBytes;
+        uint8_t *stage = smem + r.at * stage_bytes;
         const int k = (first + i) * kStep;
         bar_expect(&pipe.full[r.at], bytes);
         tma_load3(&gate, stage, &pipe.full[r.at], k, n0, expert);
@@ -544,17 +580,17 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
       }
       // The stages in flight are released (or, after a wait that gave up,
       // have had their time) before the CTA ends.
-      for (int i = 0; i < a.stages; ++i, r.next(a.stages)) ok &= bar_wait(&pipe.empty[r.at], r.phase ^ 1);
+      for (int i = 0; i < stages; ++i, r.next(stages)) ok &= bar_wait(&pipe.empty[r.at], r.phase ^ 1);
       if (!ok) pipe.failed = 1;
     }
   } else if (warp == kMmaWarp) {
     if (elect_one()) {
       Ring sum;
-      const uint32_t idesc = a.idesc | static_cast<uint32_t>(round16(count * C) / 8) << 17;
-      for (int i = 0; i < blocks; ++i, r.next(a.stages), sum.next(kBuffers)) {
+      const uint32_t idesc = a.idesc | static_cast<uint32_t>(columns / 8) << 17;
+      for (int i = 0; i < blocks; ++i, r.next(stages), sum.next(kBuffers)) {
         if (!bar_wait(&pipe.taken[sum.at], sum.phase ^ 1) || !bar_wait(&pipe.full[r.at], r.phase)) { pipe.failed = 1; break; }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t gd = tile_desc(smem + r.at * kStageBytes), ud = gd + (kRows * kStageK >> 4), xd = ud + (kRows * kStageK >> 4);
+        const uint64_t gd = tile_desc(smem + r.at * stage_bytes), ud = gd + (kRows * kStageK >> 4), xd = ud + (kRows * kStageK >> 4);
         const uint32_t d = tmem + sum.at * 2 * kN;
 #pragma unroll
         for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(d, gd + 2 * j, xd + 2 * j, idesc, j > 0);
@@ -566,61 +602,61 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
         mma_commit(&pipe.sums[sum.at]);
       }
     }
+  } else if (warp == kScaleWarp) {
+    // Scales of several stages at a time, well ahead: lane l has the token l.
+    // (Brought one stage ahead by the summing warps they took L2's latency a
+    // stage.)
+    if (kEight) {
+      const int block_row = n0 / kRun, token = lane < count ? a.list.token[slot0 + lane] : 0;
+      const float *const gs = a.scale[0] + expert * a.scale_expert[0] + block_row * a.scale_row[0];
+      const float *const us = a.scale[1] + expert * a.scale_expert[1] + block_row * a.scale_row[1];
+      const float *const xs = a.xs + token * a.h_runs;
+      bool ok = true;
+      for (int i0 = 0; i0 < blocks && ok; i0 += kScaleRun) {
+        float gv[kScaleRun], uv[kScaleRun], xv[kScaleRun];
+#pragma unroll
+        for (int i = 0; i < kScaleRun; ++i) {
+          const int b = first + min(i0 + i, blocks - 1);
+          gv[i] = gs[b * a.scale_col[0]];
+          uv[i] = a.has_up ? us[b * a.scale_col[1]] : 0.0f;
+          xv[i] = lane < count ? xs[b] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleRun; ++i) {
+          if (i0 + i >= blocks || !ok) continue;
+          if (!bar_wait(&pipe.used[r.at], r.phase ^ 1, sum_limit(a.h_blocks))) { ok = false; continue; }
+          if (lane < BT) scales[r.at][0][lane] = xv[i] * gv[i], scales[r.at][1][lane] = xv[i] * uv[i];
+          __syncwarp();
+          if (lane == 0) local_arrive(&pipe.ready[r.at]);
+          r.next(kScaleSlots);
+        }
+      }
+      if (!ok) pipe.failed = 1;
+    }
   } else {
-    // The scales of a stage, one stage ahead: lane l has the tokens l, l + 32.
-    constexpr int kEach = (BT + 31) / 32;
-    const int block_row = n0 / kRun;
-    const float *const gs = a.scale[0] + expert * a.scale_expert[0] + block_row * a.scale_row[0];
-    const float *const us = a.scale[1] + expert * a.scale_expert[1] + block_row * a.scale_row[1];
-    int mine[kEach];
-    float x_next[kEach], g_next = 1.0f, u_next = 1.0f;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) mine[e] = lane + 32 * e < count ? a.list.token[slot0 + lane + 32 * e] : 0;
-    auto fetch = [&](int b) {
-      if (!kEight) return;
-      g_next = gs[b * a.scale_col[0]];
-      if (a.has_up) u_next = us[b * a.scale_col[1]];
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) x_next[e] = lane + 32 * e < count ? a.xs[mine[e] * a.h_runs + b] : 0.0f;
-    };
-    if (blocks > 0) fetch(first);
+    if (threadIdx.x < count) weights[threadIdx.x] = a.list.weight[slot0 + threadIdx.x];
 #pragma unroll
     for (int t = 0; t < BT; ++t) g[t] = u[t] = 0.0f;
     Ring sum;
-    for (int b = 0; b < blocks; ++b, sum.next(kBuffers)) {
-      float(*const sc)[BT] = scales[warp][b & 1];
-      if (kEight) {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e)
-          if (BT >= 32 || lane < BT) sc[0][lane + 32 * e] = x_next[e] * g_next, sc[1][lane + 32 * e] = x_next[e] * u_next;
-        if (b + 1 < blocks) fetch(first + b + 1);
-        __syncwarp();
+    for (int b = 0; b < blocks; ++b, sum.next(kBuffers), r.next(kScaleSlots)) {
+      if ((kEight && !bar_wait(&pipe.ready[r.at], r.phase, sum_limit(a.h_blocks))) || !bar_wait(&pipe.sums[sum.at], sum.phase, sum_limit(a.h_blocks))) {
+        pipe.failed = 1;
+        break;
       }
-      if (!bar_wait(&pipe.sums[sum.at], sum.phase, sum_limit(a.h_blocks))) { pipe.failed = 1; break; }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16) + sum.at * 2 * kN;
-      auto add = [&](float(&to)[BT], uint32_t at, const float *s) {
 #pragma unroll
-        for (int t = 0; t < BT; t += 8) {
-          if (t >= count) continue;
-          uint32_t v[8 * C];
-          read_tokens<C>(at + t * C, v);
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = 1.0f;
-          if (kEight) {
-            *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(s + t);
-            *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(s + t + 4);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) to[t + j] = kEight ? fmaf(of_columns<C, kEight>(v, j), f[j], to[t + j]) : to[t + j] + of_columns<C, kEight>(v, j);
-        }
-      };
-      add(g, from, sc[0]);
-      if (a.has_up) add(u, from + kN, sc[1]);
+      for (int t = 0; t < BT; t += 8) {
+        if (t >= count) continue;
+        add_tokens<C, kEight>(g, t, from, kEight ? scales[r.at][0] : nullptr);
+        if (a.has_up) add_tokens<C, kEight>(u, t, from + kN, kEight ? scales[r.at][1] : nullptr);
+      }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) local_arrive(&pipe.taken[sum.at]);
+      if (lane == 0) {
+        local_arrive(&pipe.taken[sum.at]);
+        if (kEight) local_arrive(&pipe.used[r.at]);
+      }
     }
   }
   __syncwarp();
@@ -636,40 +672,54 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
   if (a.splits > 1) {
     cluster_arrive();
     cluster_wait();  // every CTA is done with its stages
-    if (warp < kSumWarps) {
-      uint32_t owner = 0, to = peer_addr(joined + rank * share * 2 * kRows + row, 0);
-      int left = share;
+  } else if (warp < kSumWarps) {
+    sum_warps_sync();  // the last MMAs are done, and with them the stages
+  }
+  if (warp < kSumWarps) {
+    uint32_t owner = 0, to = peer_addr(joined + rank * share * 2 * kRows + row, 0);
+    int left = share;
 #pragma unroll
-      for (int t = 0; t < BT; ++t) {
-        if (t >= count) continue;
-        if (left == 0) {
-          to = peer_addr(joined + rank * share * 2 * kRows + row, ++owner);
-          left = share;
-        }
-        peer_store(to, g[t]);
-        peer_store(to + kRows * 4, u[t]);
-        to += 2 * kRows * 4;
-        --left;
+    for (int t = 0; t < BT; ++t) {
+      if (t >= count) continue;
+      if (left == 0) {
+        to = peer_addr(joined + rank * share * 2 * kRows + row, ++owner);
+        left = share;
       }
+      peer_store(to, g[t]);
+      peer_store(to + kRows * 4, u[t]);
+      to += 2 * kRows * 4;
+      --left;
     }
+  }
+  if (a.splits > 1) {
     cluster_arrive();
     cluster_wait();
   }
   if (warp < kSumWarps) {
-    auto value = [&](float gv, float uv, int slot) {
-      float v[1] = {gv};
+    for (int t = 0; t < own; ++t) {
+      float v[1] = {0.0f}, uv = 0.0f;
+      for (int s = 0; s < a.splits; ++s) {
+        const float *from = joined + (s * share + t) * 2 * kRows + row;
+        v[0] += from[0], uv += from[kRows];
+      }
       activate<false>(v, a.act);
-      return (a.has_up ? v[0] * uv : v[0]) * a.list.weight[slot];
-    };
-    auto emit = [&](float v, int t, int slot) {
+      if (a.has_up) v[0] *= uv;
+      v[0] *= weights[begin + t];
+      joined[t * 2 * kRows + row] = v[0];
+      const float top = warp_top(fabsf(v[0]));
+      if (lane == 0) tops[warp][t] = top;
+    }
+    sum_warps_sync();
+#pragma unroll 2
+    for (int t = 0; t < own; ++t) {
+      const int64_t slot = slot0 + begin + t;
       float top = 0.0f;
 #pragma unroll
       for (int w = 0; w < kSumWarps; ++w) top = max_nan(top, tops[w][t]);
-      const float s = run_scale(top, kEight ? 8 : a.w_dtype == ST_BF16 ? 2 : 15);
-      if (row == 0) a.hs[int64_t(slot) * a.in_runs + n0 / kRun] = s;
-      if (n >= a.inter) return;
-      v *= exact_inverse(s);
-      uint8_t *const to = a.hq + int64_t(slot) * kOutColumns * a.h_pitch;
+      const float s = run_scale(top, kEight ? 8 : a.w_dtype == ST_BF16 ? 2 : 15), v = joined[t * 2 * kRows + row] * exact_inverse(s);
+      if (row == 0) a.hs[slot * a.in_runs + n0 / kRun] = s;
+      if (n >= a.inter) continue;
+      uint8_t *const to = a.hq + slot * kOutColumns * a.h_pitch;
       if constexpr (kEight) {
         uint32_t c[kOutColumns];
         columns8<kOutColumns>(v, c);
@@ -680,90 +730,69 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
         store_any<1>(to, a.w_dtype, n, hi);
         store_any<1>(to + a.h_pitch, a.w_dtype, n, lo);
       }
-    };
-    if (a.splits > 1) {
-      for (int t = 0; t < own; ++t) {
-        float gv = 0.0f, uv = 0.0f;
-        for (int s = 0; s < a.splits; ++s) {
-          const float *from = joined + (s * share + t) * 2 * kRows + row;
-          gv += from[0], uv += from[kRows];
-        }
-        const float v = value(gv, uv, slot0 + begin + t), top = warp_top(fabsf(v));
-        joined[t * 2 * kRows + row] = v;
-        if (lane == 0) tops[warp][t] = top;
-      }
-      sum_warps_sync();
-      for (int t = 0; t < own; ++t) emit(joined[t * 2 * kRows + row], t, slot0 + begin + t);
-    } else {
-#pragma unroll
-      for (int t = 0; t < BT; ++t) {
-        if (t >= count) continue;
-        g[t] = value(g[t], u[t], slot0 + t);
-        const float top = warp_top(fabsf(g[t]));
-        if (lane == 0) tops[warp][t] = top;
-      }
-      sum_warps_sync();
-#pragma unroll
-      for (int t = 0; t < BT; ++t)
-        if (t < count) emit(g[t], t, slot0 + t);
     }
   }
   pipe_end(pipe, warp, kColumns, a.err);
 }
 
-// 128 rows of y.  The stages of all chosen experts, one after the other, are
-// shared out over the cluster's CTAs; each keeps the tokens' sums of its part
-// in shared memory.
+// A walk over (group, stage of its sum).
+struct Walk {
+  int which, block, expert, slot0, count;
+  __device__ __forceinline__ void look(const MoeArgs &a) {
+    expert = a.list.expert[which];
+    slot0 = a.list.first[which];
+    count = a.list.first[which + 1] - slot0;
+  }
+  // more: there is a next one.
+  __device__ __forceinline__ bool next(const MoeArgs &a, bool more) {
+    if (++block < a.in_blocks) return false;
+    block = 0;
+    ++which;
+    if (more) look(a);
+    return true;
+  }
+};
+
+// 128 rows of y.  The stages of all groups, one after the other, are shared out
+// over the cluster's CTAs; each keeps the tokens' sums of its part in shared
+// memory.
 template <int BT, bool kEight>
 __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ CUtensorMap down, const __grid_constant__ CUtensorMap hmap,
                                                         const __grid_constant__ MoeArgs a) {
   constexpr int C = kEight ? 3 : 2, kN = round16(BT * C), kColumns = tmem_columns(2 * kN);
-  constexpr int kStageBytes = (kRows + kN) * kStageK, kStep = kEight ? kStageK : kStageK / 2;
+  constexpr int kStep = kEight ? kStageK : kStageK / 2;
   constexpr int kPerRun = kRun / kStep;  // stages of a run of h
+  static_assert(kColumns <= 256 && 2 * (kRows + kN) * kStageK + kMaxTokens * kRows * 4 <= kSmem, "half of an SM");
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   __shared__ Pipe pipe;
-  __shared__ __align__(16) float scales[kSumWarps][2][BT];
-  float *const total = reinterpret_cast<float *>(smem + a.stages * kStageBytes);  // [token][kRows]
+  __shared__ __align__(16) float scales[kScaleSlots][BT];
+  float *const total = reinterpret_cast<float *>(smem);  // [token][kRows]
+  uint8_t *const ring = smem + (a.tokens * kRows * 4 + 1023) / 1024 * 1024;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x % a.splits;
   const int n0 = static_cast<int>(blockIdx.x / a.splits) * kRows;
-  pipe_start(pipe, a.stages, warp, kColumns);
+  pipe_start(pipe, warp, kColumns);
   wait_for_previous();
   let_next_start();
   const int64_t all = int64_t(*a.list.count) * a.in_blocks;
   const int64_t begin = all * rank / a.splits;
   const int blocks = static_cast<int>(all * (rank + 1) / a.splits - begin);
-  const int which0 = static_cast<int>(begin / a.in_blocks), block0 = static_cast<int>(begin % a.in_blocks);
+  const uint32_t limit = sum_limit(static_cast<int>(min(all, int64_t(0x7fffffff))));
+  const int stage_bytes = (kRows + round16(*a.list.most * C)) * kStageK;
+  const int stages = min(kMaxStages, static_cast<int>(kSmem - (ring - smem)) / stage_bytes);
   const uint32_t tmem = pipe.tmem;
-
-  // Walks over (chosen expert, stage of its sum).
-  struct Walk {
-    int which, block, expert, slot0, count;
-    __device__ __forceinline__ void look(const MoeArgs &a) {
-      expert = a.list.expert[which];
-      slot0 = a.list.first[which];
-      count = a.list.first[which + 1] - slot0;
-    }
-    __device__ __forceinline__ void next(const MoeArgs &a, bool more) {
-      if (++block == a.in_blocks) {
-        block = 0;
-        ++which;
-        if (more) look(a);
-      }
-    }
-  };
-  Walk at{which0, block0, 0, 0, 0};
+  Walk at{static_cast<int>(begin / a.in_blocks), static_cast<int>(begin % a.in_blocks), 0, 0, 0};
   if (blocks > 0) at.look(a);
   Ring r;
   if (warp == kCopyWarp) {
     if (elect_one()) {
       bool ok = true;
-      for (int i = 0; i < blocks; ++i, r.next(a.stages)) {
+      for (int i = 0; i < blocks; ++i, r.next(stages)) {
         // Before its first use a stage counts as released.
         if (!bar_wait(&pipe.empty[r.at], r.phase ^ 1)) { ok = false; break; }
-        uint8_t *stage = smem + r.at * kStageBytes;
+        uint8_t *stage = ring + r.at * stage_bytes;
         const int columns = round16(at.count * C);
         bar_expect(&pipe.full[r.at], (kRows + columns) * kStageK);
         tma_load3(&down, stage, &pipe.full[r.at], at.block * kStep, n0, at.expert);
@@ -773,16 +802,16 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
       }
       // The stages in flight are released (or, after a wait that gave up,
       // have had their time) before the CTA ends.
-      for (int i = 0; i < a.stages; ++i, r.next(a.stages)) ok &= bar_wait(&pipe.empty[r.at], r.phase ^ 1);
+      for (int i = 0; i < stages; ++i, r.next(stages)) ok &= bar_wait(&pipe.empty[r.at], r.phase ^ 1);
       if (!ok) pipe.failed = 1;
     }
   } else if (warp == kMmaWarp) {
     if (elect_one()) {
       Ring sum;
-      for (int i = 0; i < blocks; ++i, r.next(a.stages), sum.next(2)) {
+      for (int i = 0; i < blocks; ++i, r.next(stages), sum.next(2)) {
         if (!bar_wait(&pipe.taken[sum.at], sum.phase ^ 1) || !bar_wait(&pipe.full[r.at], r.phase)) { pipe.failed = 1; break; }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t wd = tile_desc(smem + r.at * kStageBytes), hd = wd + (kRows * kStageK >> 4);
+        const uint64_t wd = tile_desc(ring + r.at * stage_bytes), hd = wd + (kRows * kStageK >> 4);
         const uint32_t idesc = a.idesc | static_cast<uint32_t>(round16(at.count * C) / 8) << 17;
 #pragma unroll
         for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(tmem + sum.at * kN, wd + 2 * j, hd + 2 * j, idesc, j > 0);
@@ -791,61 +820,67 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
         at.next(a, i + 1 < blocks);
       }
     }
+  } else if (warp == kScaleWarp) {
+    // As in up_kernel: lane l has the group's slot l.
+    bool ok = true;
+    for (int i0 = 0; i0 < blocks && ok; i0 += kScaleRun) {
+      float w[kScaleRun], h[kScaleRun];
+#pragma unroll
+      for (int i = 0; i < kScaleRun; ++i) {
+        if (i0 + i >= blocks) continue;
+        const int run = at.block / kPerRun;
+        w[i] = kEight ? a.scale[2][at.expert * a.scale_expert[2] + n0 / kRun * a.scale_row[2] + run * a.scale_col[2]] : 1.0f;
+        h[i] = lane < at.count ? a.hs[int64_t(at.slot0 + lane) * a.in_runs + run] : 0.0f;
+        at.next(a, i0 + i + 1 < blocks);
+      }
+#pragma unroll
+      for (int i = 0; i < kScaleRun; ++i) {
+        if (i0 + i >= blocks || !ok) continue;
+        if (!bar_wait(&pipe.used[r.at], r.phase ^ 1, limit)) { ok = false; continue; }
+        if (lane < BT) scales[r.at][lane] = w[i] * h[i];
+        __syncwarp();
+        if (lane == 0) local_arrive(&pipe.ready[r.at]);
+        r.next(kScaleSlots);
+      }
+    }
+    if (!ok) pipe.failed = 1;
   } else {
     const int row = threadIdx.x;
     for (int t = 0; t < a.tokens; ++t) total[t * kRows + row] = 0.0f;
-    // The scales of a stage, one stage ahead: lane l has the slots l, l + 32.
-    constexpr int kEach = (BT + 31) / 32;
-    Walk ahead = at;
-    float h_next[kEach], w_next = 1.0f;
-    auto fetch = [&]() {
-      const int run = ahead.block / kPerRun;
-      if (kEight) w_next = a.scale[2][ahead.expert * a.scale_expert[2] + n0 / kRun * a.scale_row[2] + run * a.scale_col[2]];
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) h_next[e] = lane + 32 * e < ahead.count ? a.hs[int64_t(ahead.slot0 + lane + 32 * e) * a.in_runs + run] : 0.0f;
-    };
-    if (blocks > 0) fetch();
+    // Lane l has the token of the group's slot l.
+    int token = blocks > 0 && lane < at.count ? a.list.token[at.slot0 + lane] : 0;
     float acc[BT];
 #pragma unroll
     for (int t = 0; t < BT; ++t) acc[t] = 0.0f;
     Ring sum;
-    for (int b = 0; b < blocks; ++b, sum.next(2)) {
-      float *const sc = scales[warp][b & 1];
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (BT >= 32 || lane < BT) sc[lane + 32 * e] = h_next[e] * w_next;
-      if (b + 1 < blocks) {
-        ahead.next(a, true);
-        fetch();
-      }
-      __syncwarp();
-      if (!bar_wait(&pipe.sums[sum.at], sum.phase, sum_limit(static_cast<int>(min(all, int64_t(0x7fffffff)))))) { pipe.failed = 1; break; }
+    for (int b = 0; b < blocks; ++b, sum.next(2), r.next(kScaleSlots)) {
+      if (!bar_wait(&pipe.ready[r.at], r.phase, limit) || !bar_wait(&pipe.sums[sum.at], sum.phase, limit)) { pipe.failed = 1; break; }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16) + sum.at * kN;
 #pragma unroll
-      for (int t = 0; t < BT; t += 8) {
-        if (t >= at.count) continue;
-        uint32_t v[8 * C];
-        read_tokens<C>(from + t * C, v);
-        float f[8];
-        *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(sc + t);
-        *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(sc + t + 4);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[t + j] = fmaf(of_columns<C, kEight>(v, j), f[j], acc[t + j]);
-      }
+      for (int t = 0; t < BT; t += 8)
+        if (t < at.count) add_tokens<C, kEight>(acc, t, from, scales[r.at]);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) local_arrive(&pipe.taken[sum.at]);
+      if (lane == 0) {
+        local_arrive(&pipe.taken[sum.at]);
+        local_arrive(&pipe.used[r.at]);
+      }
       if (at.block == a.in_blocks - 1 || b == blocks - 1) {
-        // The expert's part of its tokens' sums.  (Columns that are no token's
+        // The group's part of its tokens' sums.  (Columns that are no token's
         // have had anything added.)
 #pragma unroll
-        for (int t = 0; t < BT; ++t) {
-          if (t < at.count) total[a.list.token[at.slot0 + t] * kRows + row] += acc[t];
-          acc[t] = 0.0f;
+        for (int t = 0; t < BT; t += 8) {
+          if (t >= at.count) continue;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int to = __shfl_sync(~0u, token, t + j);
+            if (t + j < at.count) total[to * kRows + row] += acc[t + j];
+            acc[t + j] = 0.0f;
+          }
         }
       }
-      at.next(a, b + 1 < blocks);
+      if (at.next(a, b + 1 < blocks) && b + 1 < blocks) token = lane < at.count ? a.list.token[at.slot0 + lane] : 0;
     }
   }
   __syncwarp();
@@ -857,6 +892,7 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
     for (int t = t0; t < t1; ++t) {
       float v[1] = {0.0f}, old[1] = {0.0f};
       if (a.residual && n < a.hidden) load_any<1>(a.residual, a.y_dtype, t * a.ldr + n, old);
+#pragma unroll 4
       for (int s = 0; s < a.splits; ++s) {
         float part;
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part) : "r"(peer_addr(total + t * kRows + threadIdx.x, s)) : "memory");
@@ -886,16 +922,18 @@ struct Space {
     return from;
   }
 };
+// Groups at most: chosen experts, and those with more than kGroup tokens again.
+int64_t groups_of(const st_moe_args &p) { return std::min(p.tokens * p.top_k, p.experts + p.tokens * p.top_k / (kGroup + 1)); }
 int64_t lay_out(const st_moe_args &p, MoeArgs *a) {
   const int item = item_of(p);
-  const int64_t slots = p.tokens * p.top_k, most = std::min(slots, p.experts);
+  const int64_t slots = p.tokens * p.top_k, most = groups_of(p);
   const int64_t x_pitch = (p.hidden * item + 15) / 16 * 16, h_pitch = (p.inter * item + 15) / 16 * 16;
   const int64_t h_runs = (p.hidden + kRun - 1) / kRun, in_runs = (p.inter + kRun - 1) / kRun;
   Space s;
   const int64_t logits = s.take(8 * p.tokens * p.experts), keys = s.take(p.router_bias && p.score == ST_MOE_SIGMOID ? 8 * p.tokens * p.experts : 0);
   const int64_t xq = s.take(p.tokens * x_columns_of(p) * x_pitch), xs = s.take(item == 1 ? 4 * p.tokens * h_runs : 0);
   const int64_t hq = s.take(slots * h_columns_of(p) * h_pitch), hs = s.take(4 * slots * in_runs);
-  const int64_t count = s.take(4), expert = s.take(4 * most), first = s.take(4 * (most + 1)), token = s.take(4 * slots), weight = s.take(4 * slots);
+  const int64_t count = s.take(8), expert = s.take(4 * most), first = s.take(4 * (most + 1)), token = s.take(4 * slots), weight = s.take(4 * slots);
   if (a) {
     uint8_t *const base = static_cast<uint8_t *>(p.workspace);
     a->logits = reinterpret_cast<double *>(base + logits);
@@ -906,7 +944,7 @@ int64_t lay_out(const st_moe_args &p, MoeArgs *a) {
     a->hs = reinterpret_cast<float *>(base + hs);
     a->x_pitch = x_pitch, a->h_pitch = h_pitch;
     a->h_runs = static_cast<int>(h_runs), a->in_runs = static_cast<int>(in_runs);
-    a->list = {reinterpret_cast<int *>(base + count), reinterpret_cast<int *>(base + expert), reinterpret_cast<int *>(base + first),
+    a->list = {reinterpret_cast<int *>(base + count), reinterpret_cast<int *>(base + count) + 1, reinterpret_cast<int *>(base + expert), reinterpret_cast<int *>(base + first),
                reinterpret_cast<int *>(base + token), reinterpret_cast<float *>(base + weight)};
   }
   return s.at;
@@ -945,47 +983,33 @@ int parts(int64_t items, int64_t blocks, int most, int64_t room) {
   while (splits < most && items * splits * 2 <= room && blocks / (splits * 2) >= 4) splits *= 2;
   return splits;
 }
-constexpr int stages_in(int bytes, int stage) { return bytes / stage < kMaxStages ? bytes / stage : kMaxStages; }
 
 template <int BT, int C, bool kEight>
-st_status launch_up(MoeArgs a, const Maps &maps, int dev, int sms, cudaStream_t st) {
-  constexpr int kStageBytes = (2 * kRows + round16(BT * C)) * kStageK;
-  constexpr bool kHalf = 3 * kStageBytes <= kHalfSmem;
-  constexpr int kStages = stages_in(kHalf ? kHalfSmem : kSmem, kStageBytes), smem = kStages * kStageBytes + 1024;
-  // Sums to join, over the stages: [splits][share][2][kRows], for up to BT +
-  // splits - 1 tokens.
-  static_assert(kStages >= 3 && (BT + kMaxSplit) * 2 * kRows * 4 <= kStages * kStageBytes, "a ring of stages");
-  const int64_t most = std::min<int64_t>(int64_t(a.tokens) * a.top_k, a.experts);
+st_status launch_up(MoeArgs a, const Maps &maps, int64_t groups, int dev, int sms, cudaStream_t st) {
   a.tiles = (a.inter + kRows - 1) / kRows;
-  a.stages = kStages;
-  a.splits = parts(most * a.tiles, a.h_blocks, kMaxSplit, (kHalf ? 2 : 1) * sms);
+  a.splits = parts(groups * a.tiles, a.h_blocks, kMaxSplit, 2 * sms);
   constexpr auto kernel = up_kernel<BT, C, kEight>;
-  const cudaError_t e = allow_smem<kernel>(dev, smem);
+  const cudaError_t e = allow_smem<kernel>(dev, kSmem + 1024);
   if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_moe: %s", cudaGetErrorString(e));
-  return start("up", kernel, most * a.tiles * a.splits, kThreads, smem, a.splits, st, maps.gate, maps.up, maps.x, a);
+  return start("up", kernel, groups * a.tiles * a.splits, kThreads, kSmem + 1024, a.splits, st, maps.gate, maps.up, maps.x, a);
 }
 
 template <int BT, bool kEight>
 st_status launch_down(MoeArgs a, const Maps &maps, int dev, int sms, cudaStream_t st) {
-  constexpr int kStageBytes = (kRows + round16(BT * (kEight ? 3 : 2))) * kStageK, kTotal = BT * kRows * 4;
-  constexpr bool kHalf = 3 * kStageBytes + kTotal <= kHalfSmem;
-  constexpr int kStages = stages_in((kHalf ? kHalfSmem : kSmem) - kTotal, kStageBytes), smem = kStages * kStageBytes + kTotal + 1024;
-  static_assert(kStages >= 3, "a ring of stages");
   a.tiles = (a.hidden + kRows - 1) / kRows;
-  a.stages = kStages;
-  a.splits = parts(a.tiles, int64_t(a.top_k) * a.in_blocks, kMaxSplit, (kHalf ? 2 : 1) * sms);
+  a.splits = parts(a.tiles, int64_t(a.top_k) * a.in_blocks, kMaxSplit, 2 * sms);
   constexpr auto kernel = down_kernel<BT, kEight>;
-  const cudaError_t e = allow_smem<kernel>(dev, smem);
+  const cudaError_t e = allow_smem<kernel>(dev, kSmem + 1024);
   if (e != cudaSuccess) return set_error(ST_E_CUDA, "st_moe: %s", cudaGetErrorString(e));
-  return start("down", kernel, int64_t(a.tiles) * a.splits, kThreads, smem, a.splits, st, maps.down, maps.h, a);
+  return start("down", kernel, int64_t(a.tiles) * a.splits, kThreads, kSmem + 1024, a.splits, st, maps.down, maps.h, a);
 }
 
 template <int BT>
-st_status launch_products(const MoeArgs &a, const Maps &maps, int columns, int dev, int sms, cudaStream_t st) {
+st_status launch_products(const MoeArgs &a, const Maps &maps, int columns, int64_t groups, int dev, int sms, cudaStream_t st) {
   st_status s;
-  if (columns == 1) s = launch_up<BT, 1, false>(a, maps, dev, sms, st);
-  else if (columns == 2) s = launch_up<BT, 2, true>(a, maps, dev, sms, st);
-  else s = launch_up<BT, 3, true>(a, maps, dev, sms, st);
+  if (columns == 1) s = launch_up<BT, 1, false>(a, maps, groups, dev, sms, st);
+  else if (columns == 2) s = launch_up<BT, 2, true>(a, maps, groups, dev, sms, st);
+  else s = launch_up<BT, 3, true>(a, maps, groups, dev, sms, st);
   if (s != ST_OK) return s;
   return columns == 1 ? launch_down<BT, false>(a, maps, dev, sms, st) : launch_down<BT, true>(a, maps, dev, sms, st);
 }
@@ -1030,20 +1054,18 @@ st_status launch_moe(const st_moe_args &p, void *stream) {
   if (s == ST_OK) s = encode(&maps.x, Side{a.xq, a.x_pitch, 0, p.tokens * xc}, p.hidden, item, xc, op);
   if (s == ST_OK) s = encode(&maps.h, Side{a.hq, a.h_pitch, 0, slots * hc}, p.inter, item, 16, op);
   if (s != ST_OK) return s;
-  const int64_t most = std::min<int64_t>(slots, p.experts) * ((p.inter + kRows - 1) / kRows);
-  if (most * kMaxSplit > 0x7fffffff) return set_error(ST_E_INVAL, "%s: more tiles than one launch has", op);
+  const int64_t groups = groups_of(p);
+  if (groups * ((p.inter + kRows - 1) / kRows) * kMaxSplit > 0x7fffffff) return set_error(ST_E_INVAL, "%s: more tiles than one launch has", op);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t items = p.experts * ((p.tokens + kLogitTokens - 1) / kLogitTokens);
-  s = start("router", logits_kernel, (items + kLogitWarps - 1) / kLogitWarps + p.tokens, 32 * kLogitWarps, 0, 1, st, a);
+  s = start("router", logits_kernel, p.tokens + p.experts * ((p.tokens + kLogitTokens - 1) / kLogitTokens), 32 * kLogitWarps, 0, 1, st, a);
   if (s != ST_OK) return s;
   const unsigned ctas = p.tokens <= 8 ? 1 : p.tokens <= 16 ? 2 : p.tokens <= 32 ? 4 : 8;
   auto route = p.experts <= 64 ? route_kernel<2> : p.experts <= 256 ? route_kernel<8> : route_kernel<32>;
   s = start("route", route, ctas, 32 * kRouteWarps, 0, ctas, st, a);
   if (s != ST_OK) return s;
-  return p.tokens <= 8    ? launch_products<8>(a, maps, xc, dev, sms, st)
-         : p.tokens <= 16 ? launch_products<16>(a, maps, xc, dev, sms, st)
-         : p.tokens <= 32 ? launch_products<32>(a, maps, xc, dev, sms, st)
-                          : launch_products<64>(a, maps, xc, dev, sms, st);
+  return p.tokens <= 8    ? launch_products<8>(a, maps, xc, groups, dev, sms, st)
+         : p.tokens <= 16 ? launch_products<16>(a, maps, xc, groups, dev, sms, st)
+                          : launch_products<32>(a, maps, xc, groups, dev, sms, st);
 }
 
 }  // namespace stmat
