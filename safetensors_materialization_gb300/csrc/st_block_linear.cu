@@ -561,26 +561,35 @@ st_status check_block_linear_form(const st_block_linear_args &p, const st_linear
   return ST_OK;
 }
 
+// Either kernel's time in us, by what was measured of it, and the least of
+// them.  block_split_kernel: 4.5, and 0.33, 0.44 or 0.47 a block of its part of
+// the sum for tiles of 16, 32 and 64 tokens, 1.8 times as long for two CTAs an
+// SM, and again for each round of those.  (1 x 4096 x 14336 in 1, 2, 4, 8 parts: 39.8, 21.5, 13.7, 13.7; 64
+// tokens 53.7, 32.3, 19.2, 16.4; tiles of 128 tokens were slower than two of 64
+// or the other kernel.)  block_dense_kernel: 2.5, and a round of tiles 1 and 0.27,
+// 0.313, 0.452 or 0.522 a block by 64, 128, 192 and 256 weight rows (8192 x 14336
+// x 4096: 824, 481, 463, 401; 256 x 4096 x 4096 12.5, 13.6, 17.5, 19.6).
 st_linear_form choose_block_linear_form(const st_block_linear_args &p, int sms) {
   const int k_blocks = blocks_of(p);
-  if (p.m <= 128 || p.k == 0) {
-    const int width = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
-    const int64_t tiles = (p.m + width - 1) / width * ((p.n + kTileN - 1) / kTileN);
-    int splits = 1;
-    while (splits < kMaxSplit && tiles * splits <= sms && k_blocks / (splits * 2) >= 4) splits *= 2;
-    return {ST_LINEAR_SPLIT, width, splits};
+  const int tokens = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
+  const int64_t tiles = (p.m + tokens - 1) / tokens * ((p.n + kTileN - 1) / kTileN);
+  st_linear_form best{ST_LINEAR_SPLIT, tokens, 1};
+  double least = 0;
+  for (int splits = 1; splits <= kMaxSplit; splits *= 2) {
+    if (splits > 1 && k_blocks < 2 * splits) break;
+    const int64_t ctas = tiles * splits;
+    const double rounds = static_cast<double>((ctas + 2 * sms - 1) / (2 * sms)), block = tokens == 16 ? 0.33 : tokens == 32 ? 0.44 : 0.47;
+    const double us = rounds * (4.5 + (k_blocks + splits - 1) / splits * block * (ctas <= sms ? 1.0 : 1.8));
+    if (splits == 1 || us < least) best.splits = splits, least = us;
   }
-  // Rounds of tiles, each as long as its blocks (ns a block, 8192 x 14336 x
-  // 4096: tiles of 64 to 256 rows 824, 481, 463, 401 us).
-  static constexpr double kNs[] = {270, 313, 452, 522};
-  int width = 0;
-  double best = 0;
+  if (p.m <= 16 || p.k == 0) return best;
+  static constexpr double kBlock[] = {0.27, 0.313, 0.452, 0.522};
   for (int w = kPairMaxN; w >= 64; w -= 64) {
-    const int64_t tiles = (p.m + kPairM - 1) / kPairM * ((p.n + w - 1) / w);
-    const double all = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * kNs[w / 64 - 1];
-    if (width == 0 || all < best) width = w, best = all;
+    const int64_t dense = (p.m + kPairM - 1) / kPairM * ((p.n + w - 1) / w);
+    const double us = 2.5 + static_cast<double>((dense + sms / 2 - 1) / (sms / 2)) * (1 + k_blocks * kBlock[w / 64 - 1]);
+    if (us < least) best = {ST_LINEAR_DENSE, w, 1}, least = us;
   }
-  return {ST_LINEAR_DENSE, width, 1};
+  return best;
 }
 
 st_status launch_block_linear(const st_block_linear_args &p, const st_linear_form *form, void *stream) {

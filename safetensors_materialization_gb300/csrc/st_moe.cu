@@ -46,6 +46,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxSplit = 8;         // portable cluster size
 constexpr int kSumWarps = 4;         // one per 32 TMEM lanes
 constexpr int kMmaWarp = 4, kCopyWarp = 5, kScaleWarp = 6, kThreads = 224;
+constexpr int kMaxBuffers = 8;       // stages' sums that TMEM holds
 constexpr int kScaleSlots = 8, kScaleRun = 4;  // stages whose scales are ready, and brought in together
 constexpr int kLogitWarps = 8, kLogitTokens = 4;
 constexpr int kRouteWarps = 8;       // tokens of a CTA of route_kernel
@@ -142,6 +143,7 @@ template <class X, class R>
 __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {
   __shared__ float part[kLogitWarps][kLogitTokens][2];
   const int live = min(kLogitTokens, a.tokens - t0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kThreadsHere = 32 * kLogitWarps;
   const R *const w = static_cast<const R *>(a.router) + expert * a.ld_router;
   const X *const x = static_cast<const X *>(a.x) + t0 * a.ldx;
   Two sum[kLogitTokens];
@@ -155,7 +157,8 @@ __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {
   const bool wide = a.hidden % V == 0 && a.ldx % V == 0 && a.ld_router % V == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
   if (wide) {
-    for (int c = threadIdx.x * V; c < a.hidden; c += 32 * kLogitWarps * V) {
+#pragma unroll 2
+    for (int c = threadIdx.x * V; c < a.hidden; c += kThreadsHere * V) {
       const Raw<R, V> wr = *reinterpret_cast<const Raw<R, V> *>(w + c);
       Raw<X, V> xr[kLogitTokens];
 #pragma unroll
@@ -172,13 +175,14 @@ __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {
       }
     }
   } else {
-    for (int c = threadIdx.x; c < a.hidden; c += 32 * kLogitWarps) {
+    for (int c = threadIdx.x; c < a.hidden; c += kThreadsHere) {
       const float wv = to_float(w[c]);
 #pragma unroll
       for (int t = 0; t < kLogitTokens; ++t)
         if (t < live) step(t, to_float(x[t * a.ldx + c]), wv);
     }
   }
+  Two mine;  // lane t's: token t's
 #pragma unroll
   for (int t = 0; t < kLogitTokens; ++t) {
     if (t >= live) continue;
@@ -188,20 +192,20 @@ __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {
       sum[t].lo += lo;
       sum[t].add(hi);
     }
-    if (lane == 0) part[warp][t][0] = sum[t].hi, part[warp][t][1] = sum[t].lo;
+    if (lane == t) mine = sum[t];
   }
+  if (lane < live) part[warp][lane][0] = mine.hi, part[warp][lane][1] = mine.lo;
   __syncthreads();
   if (threadIdx.x < live) {
-    const int t = threadIdx.x;
-    Two all;
+    mine = Two{};
 #pragma unroll
     for (int i = 0; i < kLogitWarps; ++i) {
-      all.lo += part[i][t][1];
-      all.add(part[i][t][0]);
+      mine.lo += part[i][lane][1];
+      mine.add(part[i][lane][0]);
     }
     // Where the sum has left binary32's range its error has no meaning.
-    const double l = isfinite(all.hi) ? static_cast<double>(all.hi) + all.lo : all.hi;
-    const int64_t at = int64_t(t0 + t) * a.experts + expert;
+    const double l = isfinite(mine.hi) ? static_cast<double>(mine.hi) + mine.lo : mine.hi;
+    const int64_t at = int64_t(t0 + lane) * a.experts + expert;
     a.logits[at] = l;
     if (a.bias && a.sigmoid) a.keys[at] = 1.0 / (1.0 + exp(-l)) + a.bias[expert];
   }
@@ -244,20 +248,19 @@ __device__ __forceinline__ void x_columns(const MoeArgs &a, int token) {
   }
 }
 
+// A block for a token's columns, or an expert and four tokens.
 __global__ void __launch_bounds__(32 * kLogitWarps) logits_kernel(const __grid_constant__ MoeArgs a) {
   wait_for_previous();
   let_next_start();
-  const int groups = (a.tokens + kLogitTokens - 1) / kLogitTokens;
+  const int groups = (a.tokens + kLogitTokens - 1) / kLogitTokens, item = blockIdx.x - a.tokens;
   auto with_x = [&](auto &&f) {
     if (a.x_dtype == ST_BF16) f(__nv_bfloat16{});
     else f(__half{});
   };
-  const int item = blockIdx.x - a.tokens;
-  if (item < 0) with_x([&](auto x) { x_columns<decltype(x)>(a, blockIdx.x); });
-  else
-    with_x([&](auto x) {
-      with_type(a.router_dtype, [&](auto r) { logits<decltype(x), decltype(r)>(a, item / groups, item % groups * kLogitTokens); });
-    });
+  with_x([&](auto x) {
+    if (item < 0) x_columns<decltype(x)>(a, blockIdx.x);
+    else with_type(a.router_dtype, [&](auto r) { logits<decltype(x), decltype(r)>(a, item / groups, item % groups * kLogitTokens); });
+  });
 }
 
 // -------------------------------------------------------- route_kernel
@@ -274,7 +277,8 @@ __device__ __forceinline__ int64_t order(double v) {
 __device__ __forceinline__ double ordered(int64_t k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffll)); }
 
 // A warp chooses for a token; kPer of the experts a lane (expert 32 j + lane).
-template <int kPer>
+// kScores: what is compared is softmax's scores and a bias.
+template <int kPer, bool kScores>
 __device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int lane, int *chosen, float *weight) {
   constexpr int64_t kNone = static_cast<int64_t>(0x8000000000000000ull);  // below every number
   const double *const l = a.logits + int64_t(token) * a.experts;
@@ -298,7 +302,7 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int 
 #pragma unroll
       for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
     }
-    if (a.bias) {
+    if constexpr (kScores) {
       double sum = 0.0, s[kPer];
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
@@ -318,16 +322,14 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int 
   int mine = 0;
   for (int i = 0; i < a.top_k; ++i) {
     int64_t best = kNone;
-    int best_e = 0;
+    int best_e = 0x7fffffff;
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (key[j] > best) best = key[j], best_e = 32 * j + lane;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      const int64_t k = __shfl_xor_sync(~0u, best, d);
-      const int e = __shfl_xor_sync(~0u, best_e, d);
-      if (k > best || (k == best && e < best_e)) best = k, best_e = e;
-    }
+    // The warp's largest key by its two halves, then the lowest index.
+    const int high = static_cast<int>(best >> 32), top_high = __reduce_max_sync(~0u, high);
+    const uint32_t low = high == top_high ? static_cast<uint32_t>(best) : 0, top_low = __reduce_max_sync(~0u, low);
+    best_e = __reduce_min_sync(~0u, high == top_high && static_cast<uint32_t>(best) == top_low ? best_e : 0x7fffffff);
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (32 * j + lane == best_e) key[j] = kNone;
@@ -351,41 +353,42 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int 
   }
 }
 
-// The CTAs of one cluster have eight tokens each; the first then lists the
-// experts.
-template <int kPer>
+// The CTAs of one cluster have eight tokens each; each places its own in the
+// lists, and the first lists the groups.
+template <int kPer, bool kScores>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ MoeArgs a) {
-  __shared__ uint64_t mask[kMaxExperts];             // tokens of an expert
-  __shared__ int slots[kMaxExperts], totals[kRouteWarps][3];
-  __shared__ int chosen[kRouteWarps][kMaxTop];
-  __shared__ float weight[kRouteWarps][kMaxTop];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = blockIdx.x * kRouteWarps + warp;
+  __shared__ struct {
+    uint64_t mask[kMaxExperts];             // tokens of an expert
+    int slots[kMaxExperts], totals[kRouteWarps][3];
+    int chosen[kRouteWarps][kMaxTop];
+    float weight[kRouteWarps][kMaxTop];
+  } s;
+  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = cta * kRouteWarps + warp;
   constexpr int kThreadsHere = 32 * kRouteWarps;
-  for (int e = threadIdx.x; e < a.experts; e += kThreadsHere) mask[e] = 0;
+  for (int e = threadIdx.x; e < a.experts; e += kThreadsHere) s.mask[e] = 0;
   wait_for_previous();
   let_next_start();
-  if (token < a.tokens) choose_experts<kPer>(a, token, lane, chosen[warp], weight[warp]);
+  if (token < a.tokens) choose_experts<kPer, kScores>(a, token, lane, s.chosen[warp], s.weight[warp]);
   cluster_arrive();
+  __syncthreads();
   cluster_wait();
   // Every CTA reads all CTAs' choices, so that each can place its own.
   for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreadsHere) {
     const int t = i / a.top_k;
     int e;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(e) : "r"(peer_addr(&chosen[t % kRouteWarps][i % a.top_k], t / kRouteWarps)) : "memory");
-    atomicOr(reinterpret_cast<unsigned long long *>(&mask[e]), 1ull << t);
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(e) : "r"(peer_addr(&s.chosen[t % kRouteWarps][i % a.top_k], t / kRouteWarps)) : "memory");
+    atomicOr(reinterpret_cast<unsigned long long *>(&s.mask[e]), 1ull << t);
   }
   cluster_arrive();
   __syncthreads();
-  // Slots, and places in the list: running counts over the experts, four (of up
-  // to 1024) a thread.
-  constexpr int kEach = kMaxExperts / kThreadsHere;
-  int n[kEach], all_n = 0, all_used = 0, most = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int e = threadIdx.x * kEach + i;
-    n[i] = e < a.experts ? __popcll(mask[e]) : 0;
-    all_n += n[i], all_used += (n[i] + kGroup - 1) / kGroup;
-    most = max(most, min(n[i], kGroup));
+  // Slots, and places in the list: running counts over the experts, kEach a
+  // thread.
+  const int each = (a.experts + kThreadsHere - 1) / kThreadsHere;
+  int all_n = 0, all_used = 0, most = 0;
+  for (int i = 0; i < each; ++i) {
+    const int e = threadIdx.x * each + i, n = e < a.experts ? __popcll(s.mask[e]) : 0;
+    all_n += n, all_used += (n + kGroup - 1) / kGroup;
+    most = max(most, min(n, kGroup));
   }
   int before_n = all_n, before_used = all_used;
 #pragma unroll
@@ -394,34 +397,36 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     if (lane >= d) before_n += o, before_used += u;
   }
   most = __reduce_max_sync(~0u, most);
-  if (lane == 31) totals[warp][0] = before_n, totals[warp][1] = before_used, totals[warp][2] = most;
+  if (lane == 31) s.totals[warp][0] = before_n, s.totals[warp][1] = before_used, s.totals[warp][2] = most;
   __syncthreads();
   before_n -= all_n, before_used -= all_used;
-  for (int w = 0; w < kRouteWarps; ++w) {
-    if (w < warp) before_n += totals[w][0], before_used += totals[w][1];
-    most = max(most, totals[w][2]);
-  }
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int e = threadIdx.x * kEach + i;
-    if (e < a.experts) slots[e] = before_n;
-    for (int g = 0; g < n[i]; g += kGroup, ++before_used) {
-      if (blockIdx.x > 0) continue;
+  for (int w = 0; w < kRouteWarps; ++w) {
+    if (w < warp) before_n += s.totals[w][0], before_used += s.totals[w][1];
+    most = max(most, s.totals[w][2]);
+  }
+  for (int i = 0; i < each; ++i) {
+    const int e = threadIdx.x * each + i;
+    if (e >= a.experts) break;
+    const int n = __popcll(s.mask[e]);
+    s.slots[e] = before_n;
+    for (int g = 0; g < n; g += kGroup, ++before_used) {
+      if (cta > 0) continue;
       a.list.expert[before_used] = e;
       a.list.first[before_used] = before_n + g;
     }
-    before_n += n[i];
+    before_n += n;
   }
-  if (blockIdx.x == 0 && threadIdx.x == kThreadsHere - 1) {
+  if (cta == 0 && threadIdx.x == kThreadsHere - 1) {
     *a.list.count = before_used;
     *a.list.most = most;
     a.list.first[before_used] = before_n;
   }
   __syncthreads();
   if (token < a.tokens && lane < a.top_k) {
-    const int e = chosen[warp][lane], slot = slots[e] + __popcll(mask[e] & ((1ull << token) - 1));
+    const int e = s.chosen[warp][lane], slot = s.slots[e] + __popcll(s.mask[e] & ((1ull << token) - 1));
     a.list.token[slot] = token;
-    a.list.weight[slot] = weight[warp][lane];
+    a.list.weight[slot] = s.weight[warp][lane];
   }
   cluster_wait();  // no CTA ends while another reads its choices
 }
@@ -466,11 +471,12 @@ __device__ __forceinline__ float of_columns(const uint32_t (&v)[8 * C], int t) {
 }
 
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
+__host__ __device__ constexpr int buffers_of(int columns) { return 256 / columns < kMaxBuffers ? 256 / columns : kMaxBuffers; }
 __host__ __device__ constexpr int tmem_columns(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512; }
 
 // What both kernels' CTAs have.
 struct Pipe {
-  uint64_t full[kMaxStages], empty[kMaxStages], sums[2], taken[2], ready[kScaleSlots], used[kScaleSlots];
+  uint64_t full[kMaxStages], empty[kMaxStages], sums[kMaxBuffers], taken[kMaxBuffers], ready[kScaleSlots], used[kScaleSlots];
   uint32_t tmem;
   int failed;
 };
@@ -480,7 +486,7 @@ __device__ __forceinline__ void pipe_start(Pipe &p, int warp, int columns) {
       bar_init(&p.full[i], 1);
       bar_init(&p.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMaxBuffers; ++i) {
       bar_init(&p.sums[i], 1);
       bar_init(&p.taken[i], kSumWarps);
     }
@@ -509,9 +515,6 @@ __device__ __forceinline__ void pipe_end(Pipe &p, int warp, int columns, uint32_
 }
 // The four summing warps.
 __device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ void local_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
 // Adds eight tokens' sums of a stage, times their scales.
 template <int C, bool kEight, int BT>
 __device__ __forceinline__ void add_tokens(float (&to)[BT], int t, uint32_t from, const float *scale) {
@@ -533,7 +536,8 @@ __device__ __forceinline__ void add_tokens(float (&to)[BT], int t, uint32_t from
 template <int BT, int C, bool kEight>
 __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CUtensorMap gate, const __grid_constant__ CUtensorMap up,
                                                       const __grid_constant__ CUtensorMap xmap, const __grid_constant__ MoeArgs a) {
-  constexpr int kN = round16(BT * C), kBuffers = 4 * kN <= 256 ? 2 : 1, kColumns = tmem_columns(kBuffers * 2 * kN);
+  // Sixteen bits have no scales: their sums stay in TMEM to the end.
+  constexpr int kN = round16(BT * C), kBuffers = kEight ? buffers_of(2 * kN) : 1, kColumns = tmem_columns(kBuffers * 2 * kN);
   constexpr int kStep = kEight ? kStageK : kStageK / 2, kOutColumns = kEight ? 3 : 2;
   static_assert(kColumns <= 256 && 2 * (2 * kRows + kN) * kStageK <= kSmem && (BT + kMaxSplit) * 2 * kRows * 4 <= kSmem, "half of an SM");
   extern __shared__ uint8_t raw_smem[];
@@ -588,18 +592,19 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
       Ring sum;
       const uint32_t idesc = a.idesc | static_cast<uint32_t>(columns / 8) << 17;
       for (int i = 0; i < blocks; ++i, r.next(stages), sum.next(kBuffers)) {
-        if (!bar_wait(&pipe.taken[sum.at], sum.phase ^ 1) || !bar_wait(&pipe.full[r.at], r.phase)) { pipe.failed = 1; break; }
+        if ((kEight && !bar_wait(&pipe.taken[sum.at], sum.phase ^ 1)) || !bar_wait(&pipe.full[r.at], r.phase)) { pipe.failed = 1; break; }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint64_t gd = tile_desc(smem + r.at * stage_bytes), ud = gd + (kRows * kStageK >> 4), xd = ud + (kRows * kStageK >> 4);
         const uint32_t d = tmem + sum.at * 2 * kN;
+        const bool add = !kEight && i > 0;
 #pragma unroll
-        for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(d, gd + 2 * j, xd + 2 * j, idesc, j > 0);
+        for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(d, gd + 2 * j, xd + 2 * j, idesc, add || j > 0);
         if (a.has_up) {
 #pragma unroll
-          for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(d + kN, ud + 2 * j, xd + 2 * j, idesc, j > 0);
+          for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(d + kN, ud + 2 * j, xd + 2 * j, idesc, add || j > 0);
         }
         mma_commit(&pipe.empty[r.at]);
-        mma_commit(&pipe.sums[sum.at]);
+        if (kEight || i == blocks - 1) mma_commit(&pipe.sums[sum.at]);
       }
     }
   } else if (warp == kScaleWarp) {
@@ -612,24 +617,33 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
       const float *const us = a.scale[1] + expert * a.scale_expert[1] + block_row * a.scale_row[1];
       const float *const xs = a.xs + token * a.h_runs;
       bool ok = true;
-      for (int i0 = 0; i0 < blocks && ok; i0 += kScaleRun) {
-        float gv[kScaleRun], uv[kScaleRun], xv[kScaleRun];
+      float gv[2][kScaleRun], uv[2][kScaleRun], xv[2][kScaleRun];
+      auto fetch = [&](int at, int i0) {
 #pragma unroll
         for (int i = 0; i < kScaleRun; ++i) {
           const int b = first + min(i0 + i, blocks - 1);
-          gv[i] = gs[b * a.scale_col[0]];
-          uv[i] = a.has_up ? us[b * a.scale_col[1]] : 0.0f;
-          xv[i] = lane < count ? xs[b] : 0.0f;
+          gv[at][i] = gs[b * a.scale_col[0]];
+          uv[at][i] = a.has_up ? us[b * a.scale_col[1]] : 0.0f;
+          xv[at][i] = lane < count ? xs[b] : 0.0f;
         }
+      };
+      auto put = [&](int at, int i0) {
 #pragma unroll
         for (int i = 0; i < kScaleRun; ++i) {
           if (i0 + i >= blocks || !ok) continue;
           if (!bar_wait(&pipe.used[r.at], r.phase ^ 1, sum_limit(a.h_blocks))) { ok = false; continue; }
-          if (lane < BT) scales[r.at][0][lane] = xv[i] * gv[i], scales[r.at][1][lane] = xv[i] * uv[i];
+          if (lane < BT) scales[r.at][0][lane] = xv[at][i] * gv[at][i], scales[r.at][1][lane] = xv[at][i] * uv[at][i];
           __syncwarp();
           if (lane == 0) local_arrive(&pipe.ready[r.at]);
           r.next(kScaleSlots);
         }
+      };
+      fetch(0, 0);
+      for (int i0 = 0; i0 < blocks && ok; i0 += 2 * kScaleRun) {
+        fetch(1, i0 + kScaleRun);
+        put(0, i0);
+        fetch(0, i0 + 2 * kScaleRun);
+        put(1, i0 + kScaleRun);
       }
       if (!ok) pipe.failed = 1;
     }
@@ -638,7 +652,7 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
 #pragma unroll
     for (int t = 0; t < BT; ++t) g[t] = u[t] = 0.0f;
     Ring sum;
-    for (int b = 0; b < blocks; ++b, sum.next(kBuffers), r.next(kScaleSlots)) {
+    for (int b = 0; b < (kEight ? blocks : 1); ++b, sum.next(kBuffers), r.next(kScaleSlots)) {
       if ((kEight && !bar_wait(&pipe.ready[r.at], r.phase, sum_limit(a.h_blocks))) || !bar_wait(&pipe.sums[sum.at], sum.phase, sum_limit(a.h_blocks))) {
         pipe.failed = 1;
         break;
@@ -735,33 +749,46 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const __grid_constant__ CU
   pipe_end(pipe, warp, kColumns, a.err);
 }
 
-// A walk over (group, stage of its sum).
+// A walk over (group, run of its sum), with the next group's entries read ahead.
 struct Walk {
-  int which, block, expert, slot0, count;
-  __device__ __forceinline__ void look(const MoeArgs &a) {
-    expert = a.list.expert[which];
+  int groups, which, run, expert, slot0, count, next_expert, next_end;
+  __device__ __forceinline__ void begin(const MoeArgs &a, int n, int64_t at) {
+    groups = n;
+    which = static_cast<int>(at / a.in_runs);
+    run = static_cast<int>(at % a.in_runs);
+    expert = slot0 = count = next_expert = next_end = 0;
+    if (which >= groups) return;
+    next_expert = a.list.expert[which];
     slot0 = a.list.first[which];
-    count = a.list.first[which + 1] - slot0;
+    next_end = a.list.first[which + 1];
+    enter(a);
   }
-  // more: there is a next one.
-  __device__ __forceinline__ bool next(const MoeArgs &a, bool more) {
-    if (++block < a.in_blocks) return false;
-    block = 0;
-    ++which;
-    if (more) look(a);
+  __device__ __forceinline__ void enter(const MoeArgs &a) {
+    expert = next_expert;
+    slot0 += count;
+    count = next_end - slot0;
+    if (which + 1 >= groups) return;
+    next_expert = a.list.expert[which + 1];
+    next_end = a.list.first[which + 2];
+  }
+  // Whether the next run is another group's.
+  __device__ __forceinline__ bool next(const MoeArgs &a) {
+    if (++run < a.in_runs) return false;
+    run = 0;
+    if (++which < groups) enter(a);
     return true;
   }
 };
 
-// 128 rows of y.  The stages of all groups, one after the other, are shared out
+// 128 rows of y.  The runs of all groups, one after the other, are shared out
 // over the cluster's CTAs; each keeps the tokens' sums of its part in shared
-// memory.
+// memory.  A run is one stage of eight bits, two of sixteen (one, where a last
+// run is short), whose sums are read out together.
 template <int BT, bool kEight>
 __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ CUtensorMap down, const __grid_constant__ CUtensorMap hmap,
                                                         const __grid_constant__ MoeArgs a) {
-  constexpr int C = kEight ? 3 : 2, kN = round16(BT * C), kColumns = tmem_columns(2 * kN);
-  constexpr int kStep = kEight ? kStageK : kStageK / 2;
-  constexpr int kPerRun = kRun / kStep;  // stages of a run of h
+  constexpr int C = kEight ? 3 : 2, kN = round16(BT * C), kBuffers = buffers_of(kN), kColumns = tmem_columns(kBuffers * kN);
+  constexpr int kStep = kEight ? kStageK : kStageK / 2, kPerRun = kRun / kStep;
   static_assert(kColumns <= 256 && 2 * (kRows + kN) * kStageK + kMaxTokens * kRows * 4 <= kSmem, "half of an SM");
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -774,31 +801,48 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
   const uint32_t rank = blockIdx.x % a.splits;
   const int n0 = static_cast<int>(blockIdx.x / a.splits) * kRows;
   pipe_start(pipe, warp, kColumns);
-  wait_for_previous();
-  let_next_start();
-  const int64_t all = int64_t(*a.list.count) * a.in_blocks;
-  const int64_t begin = all * rank / a.splits;
-  const int blocks = static_cast<int>(all * (rank + 1) / a.splits - begin);
-  const uint32_t limit = sum_limit(static_cast<int>(min(all, int64_t(0x7fffffff))));
+  // The lists are the router's, which has ended: up_kernel's CTAs waited for
+  // that before any let this kernel start.  So the first stages' weights are
+  // under way before h is there.
+  const int groups = *a.list.count;
+  const int64_t all = int64_t(groups) * a.in_runs, begin = all * rank / a.splits, end = all * (rank + 1) / a.splits;
+  const int runs = static_cast<int>(end - begin);
+  // Stages before run r of all.
+  auto stages_before = [&](int64_t r) { return r / a.in_runs * a.in_blocks + r % a.in_runs * kPerRun; };
+  const int64_t blocks = stages_before(end) - stages_before(begin);
+  const uint32_t limit = sum_limit(static_cast<int>(min(all * kPerRun, int64_t(0x7fffffff))));
   const int stage_bytes = (kRows + round16(*a.list.most * C)) * kStageK;
   const int stages = min(kMaxStages, static_cast<int>(kSmem - (ring - smem)) / stage_bytes);
   const uint32_t tmem = pipe.tmem;
-  Walk at{static_cast<int>(begin / a.in_blocks), static_cast<int>(begin % a.in_blocks), 0, 0, 0};
-  if (blocks > 0) at.look(a);
+  auto stages_of = [&](const Walk &w) { return min(kPerRun, a.in_blocks - w.run * kPerRun); };
+  Walk at;
+  at.begin(a, groups, begin);
   Ring r;
   if (warp == kCopyWarp) {
     if (elect_one()) {
       bool ok = true;
-      for (int i = 0; i < blocks; ++i, r.next(stages)) {
-        // Before its first use a stage counts as released.
-        if (!bar_wait(&pipe.empty[r.at], r.phase ^ 1)) { ok = false; break; }
-        uint8_t *stage = ring + r.at * stage_bytes;
+      auto weights = [&](const Walk &w, int part, int slot) {
+        bar_expect(&pipe.full[slot], (kRows + round16(w.count * C)) * kStageK);
+        tma_load3(&down, ring + slot * stage_bytes, &pipe.full[slot], (w.run * kPerRun + part) * kStep, n0, w.expert);
+      };
+      Walk early = at;
+      for (int i = 0, part = 0; i < min(int64_t(stages), blocks); ++i) {
+        weights(early, part, i);
+        if (++part == stages_of(early)) part = 0, early.next(a);
+      }
+      wait_for_previous();
+      let_next_start();
+      int part = 0;
+      for (int64_t i = 0; i < blocks; ++i, r.next(stages)) {
+        if (i >= stages) {
+          if (!bar_wait(&pipe.empty[r.at], r.phase ^ 1)) { ok = false; break; }
+          weights(at, part, r.at);
+        }
+        uint8_t *const h = ring + r.at * stage_bytes + kRows * kStageK;
         const int columns = round16(at.count * C);
-        bar_expect(&pipe.full[r.at], (kRows + columns) * kStageK);
-        tma_load3(&down, stage, &pipe.full[r.at], at.block * kStep, n0, at.expert);
         for (int c = 0; c < columns; c += 16)
-          tma_load(&hmap, stage + (kRows + c) * kStageK, &pipe.full[r.at], at.block * kStep, at.slot0 * C + c);
-        at.next(a, i + 1 < blocks);
+          tma_load(&hmap, h + c * kStageK, &pipe.full[r.at], (at.run * kPerRun + part) * kStep, at.slot0 * C + c);
+        if (++part == stages_of(at)) part = 0, at.next(a);
       }
       // The stages in flight are released (or, after a wait that gave up,
       // have had their time) before the CTA ends.
@@ -808,52 +852,70 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
   } else if (warp == kMmaWarp) {
     if (elect_one()) {
       Ring sum;
-      for (int i = 0; i < blocks; ++i, r.next(stages), sum.next(2)) {
-        if (!bar_wait(&pipe.taken[sum.at], sum.phase ^ 1) || !bar_wait(&pipe.full[r.at], r.phase)) { pipe.failed = 1; break; }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t wd = tile_desc(ring + r.at * stage_bytes), hd = wd + (kRows * kStageK >> 4);
+      bool ok = true;
+      wait_for_previous();
+      for (int i = 0; i < runs && ok; ++i, sum.next(kBuffers), at.next(a)) {
+        if (!bar_wait(&pipe.taken[sum.at], sum.phase ^ 1)) { ok = false; break; }
         const uint32_t idesc = a.idesc | static_cast<uint32_t>(round16(at.count * C) / 8) << 17;
+        const int parts = stages_of(at);
+        for (int part = 0; part < parts; ++part, r.next(stages)) {
+          if (!bar_wait(&pipe.full[r.at], r.phase)) { ok = false; break; }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t wd = tile_desc(ring + r.at * stage_bytes), hd = wd + (kRows * kStageK >> 4);
 #pragma unroll
-        for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(tmem + sum.at * kN, wd + 2 * j, hd + 2 * j, idesc, j > 0);
-        mma_commit(&pipe.empty[r.at]);
+          for (int j = 0; j < kStageK / 32; ++j) mma<kEight>(tmem + sum.at * kN, wd + 2 * j, hd + 2 * j, idesc, part > 0 || j > 0);
+          mma_commit(&pipe.empty[r.at]);
+        }
         mma_commit(&pipe.sums[sum.at]);
-        at.next(a, i + 1 < blocks);
       }
+      if (!ok) pipe.failed = 1;
     }
   } else if (warp == kScaleWarp) {
     // As in up_kernel: lane l has the group's slot l.
+    wait_for_previous();
+    let_next_start();
     bool ok = true;
-    for (int i0 = 0; i0 < blocks && ok; i0 += kScaleRun) {
-      float w[kScaleRun], h[kScaleRun];
+    float w[2][kScaleRun], h[2][kScaleRun];
+    auto fetch = [&](float(&wv)[kScaleRun], float(&hv)[kScaleRun], int i0) {
 #pragma unroll
       for (int i = 0; i < kScaleRun; ++i) {
-        if (i0 + i >= blocks) continue;
-        const int run = at.block / kPerRun;
-        w[i] = kEight ? a.scale[2][at.expert * a.scale_expert[2] + n0 / kRun * a.scale_row[2] + run * a.scale_col[2]] : 1.0f;
-        h[i] = lane < at.count ? a.hs[int64_t(at.slot0 + lane) * a.in_runs + run] : 0.0f;
-        at.next(a, i0 + i + 1 < blocks);
+        if (i0 + i >= runs) continue;
+        wv[i] = kEight ? a.scale[2][at.expert * a.scale_expert[2] + n0 / kRun * a.scale_row[2] + at.run * a.scale_col[2]] : 1.0f;
+        hv[i] = lane < at.count ? a.hs[int64_t(at.slot0 + lane) * a.in_runs + at.run] : 0.0f;
+        at.next(a);
       }
+    };
+    auto put = [&](const float(&wv)[kScaleRun], const float(&hv)[kScaleRun], int i0) {
 #pragma unroll
       for (int i = 0; i < kScaleRun; ++i) {
-        if (i0 + i >= blocks || !ok) continue;
+        if (i0 + i >= runs || !ok) continue;
         if (!bar_wait(&pipe.used[r.at], r.phase ^ 1, limit)) { ok = false; continue; }
-        if (lane < BT) scales[r.at][lane] = w[i] * h[i];
+        if (lane < BT) scales[r.at][lane] = wv[i] * hv[i];
         __syncwarp();
         if (lane == 0) local_arrive(&pipe.ready[r.at]);
         r.next(kScaleSlots);
       }
+    };
+    fetch(w[0], h[0], 0);
+    for (int i0 = 0; i0 < runs && ok; i0 += 2 * kScaleRun) {
+      fetch(w[1], h[1], i0 + kScaleRun);
+      put(w[0], h[0], i0);
+      fetch(w[0], h[0], i0 + 2 * kScaleRun);
+      put(w[1], h[1], i0 + kScaleRun);
     }
     if (!ok) pipe.failed = 1;
   } else {
     const int row = threadIdx.x;
     for (int t = 0; t < a.tokens; ++t) total[t * kRows + row] = 0.0f;
+    wait_for_previous();
+    let_next_start();
     // Lane l has the token of the group's slot l.
-    int token = blocks > 0 && lane < at.count ? a.list.token[at.slot0 + lane] : 0;
+    int token = runs > 0 && lane < at.count ? a.list.token[at.slot0 + lane] : 0;
     float acc[BT];
 #pragma unroll
     for (int t = 0; t < BT; ++t) acc[t] = 0.0f;
     Ring sum;
-    for (int b = 0; b < blocks; ++b, sum.next(2), r.next(kScaleSlots)) {
+    for (int b = 0; b < runs; ++b, sum.next(kBuffers), r.next(kScaleSlots)) {
       if (!bar_wait(&pipe.ready[r.at], r.phase, limit) || !bar_wait(&pipe.sums[sum.at], sum.phase, limit)) { pipe.failed = 1; break; }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16) + sum.at * kN;
@@ -866,7 +928,7 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
         local_arrive(&pipe.taken[sum.at]);
         local_arrive(&pipe.used[r.at]);
       }
-      if (at.block == a.in_blocks - 1 || b == blocks - 1) {
+      if (at.run == a.in_runs - 1 || b == runs - 1) {
         // The group's part of its tokens' sums.  (Columns that are no token's
         // have had anything added.)
 #pragma unroll
@@ -880,7 +942,7 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
           }
         }
       }
-      if (at.next(a, b + 1 < blocks) && b + 1 < blocks) token = lane < at.count ? a.list.token[at.slot0 + lane] : 0;
+      if (at.next(a) && b + 1 < runs) token = lane < at.count ? a.list.token[at.slot0 + lane] : 0;
     }
   }
   __syncwarp();
@@ -889,16 +951,25 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
   const int n = n0 + static_cast<int>(threadIdx.x);
   if (warp < kSumWarps) {
     const int share = (a.tokens + a.splits - 1) / a.splits, t0 = static_cast<int>(rank) * share, t1 = min(a.tokens, t0 + share);
+    // A token's residual and parts are under way while the one before is summed.
+    float part[kMaxSplit], next[kMaxSplit], old[1] = {0.0f}, next_old[1] = {0.0f};
+    auto read = [&](int t, float(&to)[kMaxSplit], float(&res)[1]) {
+      if (a.residual && n < a.hidden) load_any<1>(a.residual, a.y_dtype, t * a.ldr + n, res);
+#pragma unroll
+      for (int s = 0; s < kMaxSplit; ++s)
+        if (s < a.splits) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(to[s]) : "r"(peer_addr(total + t * kRows + threadIdx.x, s)) : "memory");
+    };
+    if (t0 < t1) read(t0, part, old);
     for (int t = t0; t < t1; ++t) {
-      float v[1] = {0.0f}, old[1] = {0.0f};
-      if (a.residual && n < a.hidden) load_any<1>(a.residual, a.y_dtype, t * a.ldr + n, old);
-#pragma unroll 4
-      for (int s = 0; s < a.splits; ++s) {
-        float part;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part) : "r"(peer_addr(total + t * kRows + threadIdx.x, s)) : "memory");
-        v[0] += part;
+      if (t + 1 < t1) read(t + 1, next, next_old);
+      float v[1] = {0.0f};
+#pragma unroll
+      for (int s = 0; s < kMaxSplit; ++s) {
+        if (s < a.splits) v[0] += part[s];
+        part[s] = next[s];
       }
       v[0] += old[0];
+      old[0] = next_old[0];
       if (n < a.hidden) store_any<1>(a.y, a.y_dtype, t * a.ldy + n, v);
     }
   }
@@ -1057,11 +1128,19 @@ st_status launch_moe(const st_moe_args &p, void *stream) {
   const int64_t groups = groups_of(p);
   if (groups * ((p.inter + kRows - 1) / kRows) * kMaxSplit > 0x7fffffff) return set_error(ST_E_INVAL, "%s: more tiles than one launch has", op);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool scores = p.router_bias && !a.sigmoid;
+  auto pick = [&](auto of) {  // kernels by the experts a lane has, and what is compared
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    using std::integral_constant;
+    if (p.experts <= 64) return scores ? of(integral_constant<int, 2>{}, yes) : of(integral_constant<int, 2>{}, no);
+    if (p.experts <= 256) return scores ? of(integral_constant<int, 8>{}, yes) : of(integral_constant<int, 8>{}, no);
+    return scores ? of(integral_constant<int, 32>{}, yes) : of(integral_constant<int, 32>{}, no);
+  };
   s = start("router", logits_kernel, p.tokens + p.experts * ((p.tokens + kLogitTokens - 1) / kLogitTokens), 32 * kLogitWarps, 0, 1, st, a);
   if (s != ST_OK) return s;
   const unsigned ctas = p.tokens <= 8 ? 1 : p.tokens <= 16 ? 2 : p.tokens <= 32 ? 4 : 8;
-  auto route = p.experts <= 64 ? route_kernel<2> : p.experts <= 256 ? route_kernel<8> : route_kernel<32>;
-  s = start("route", route, ctas, 32 * kRouteWarps, 0, ctas, st, a);
+  s = start("route", pick([](auto per, auto sc) { return &route_kernel<decltype(per)::value, decltype(sc)::value>; }), ctas, 32 * kRouteWarps, 0, ctas, st, a);
   if (s != ST_OK) return s;
   return p.tokens <= 8    ? launch_products<8>(a, maps, xc, groups, dev, sms, st)
          : p.tokens <= 16 ? launch_products<16>(a, maps, xc, groups, dev, sms, st)

@@ -55,6 +55,9 @@ __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
 __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void local_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 // One thread of the (converged) warp, chosen so that the compiler knows that
 // it runs alone: the tensor core's and TMA's operands then stay in uniform
 // registers.

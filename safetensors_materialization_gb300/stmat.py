@@ -923,6 +923,7 @@ class _Ops:
         names = ("BF16", "F16", "F32", "F8_E4M3", "F8_E5M2")
         self.codes = {torch_dtype(n): DTYPES.index(n) for n in names}
         self.dsts = {n: (torch_dtype(n), DTYPES.index(n)) for n in names}
+        self.moe_spaces = {}
         # 0.1 us each; torch.cuda.current_stream() takes 11
         self.stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         call = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_void_p)
@@ -1276,10 +1277,10 @@ def block_linear_choice(m, n, k, sms=152):
     return LINEAR_KERNELS[form.kernel], form.width, form.splits
 
 
-def _experts(t, scale, name, gpu, experts, rows, k, dtype):
+def _experts(t, scale, name, gpu, experts, rows, k, dtype, f32):
     """The fields of st_moe_weight of an [experts, rows, k] tensor and its
     scales."""
-    if tuple(t.shape) != (experts, rows, k) or t.dtype != dtype:
+    if t.shape != (experts, rows, k) or t.dtype != dtype:
         raise _invalid(f"{name}: {tuple(t.shape)} {t.dtype}, [{experts}, {rows}, {k}] {dtype} is needed")
     if t.get_device() != gpu:
         raise _elsewhere(t, name, gpu)
@@ -1288,14 +1289,16 @@ def _experts(t, scale, name, gpu, experts, rows, k, dtype):
         raise _invalid(f"{name}: the last dimension has stride {inner}, not 1")
     if scale is None:
         return t.data_ptr(), step, ld, 0, 0, 0, 0
-    shape = (experts, -(-rows // _BLOCK), -(-k // _BLOCK))
-    if tuple(scale.shape) != shape:
-        raise _invalid(f"{name}_scale: {tuple(scale.shape)}, {shape} is needed")
-    if str(scale.dtype) != "torch.float32":
+    if scale.shape != (experts, -(-rows // _BLOCK), -(-k // _BLOCK)):
+        raise _invalid(f"{name}_scale: {tuple(scale.shape)}, [{experts}, {-(-rows // _BLOCK)}, {-(-k // _BLOCK)}] is needed")
+    if scale.dtype != f32:
         raise StmatError(6, f"{name}_scale: {scale.dtype} is not F32")
     if scale.get_device() != gpu:
         raise _elsewhere(scale, name + "_scale", gpu)
     return t.data_ptr(), step, ld, scale.data_ptr(), *scale.stride()
+
+
+_NO_EXPERTS = (0,) * 7
 
 
 def moe(x, router, gate, up, down, top_k, gate_scale=None, up_scale=None, down_scale=None, act="silu", score="softmax",
@@ -1327,9 +1330,10 @@ def moe(x, router, gate, up, down, top_k, gate_scale=None, up_scale=None, down_s
     if rh != hidden or router.dim() != 2 or gate.dim() != 3:
         raise _invalid(f"x has rows of {hidden}, router is {tuple(router.shape)}, gate {tuple(gate.shape)}")
     inter, w_type = gate.shape[1], gate.dtype
-    weights = (*_experts(gate, gate_scale, "gate", gpu, experts, inter, hidden, w_type),
-               *((0,) * 7 if up is None else _experts(up, up_scale, "up", gpu, experts, inter, hidden, w_type)),
-               *_experts(down, down_scale, "down", gpu, experts, hidden, inter, w_type))
+    f32 = torch.float32
+    gates = _experts(gate, gate_scale, "gate", gpu, experts, inter, hidden, w_type, f32)
+    ups = _NO_EXPERTS if up is None else _experts(up, up_scale, "up", gpu, experts, inter, hidden, w_type, f32)
+    downs = _experts(down, down_scale, "down", gpu, experts, hidden, inter, w_type, f32)
     pb = 0 if router_bias is None else _vector(router_bias, "router_bias", gpu, experts, _F32, codes)[0]
     if out is None:
         y_type, y_code = _dst(dst, x_type, ops)
@@ -1348,15 +1352,22 @@ def moe(x, router, gate, up, down, top_k, gate_scale=None, up_scale=None, down_s
         ps, lds, _, _ = _matrix(residual, "residual", gpu)
     args = (tokens, hidden, inter, experts, top_k, ACTS.get(act, -1), SCORES.get(score, -1), bool(normalize), factor,
             codes.get(x_type, -1), codes.get(router.dtype, -1), codes.get(w_type, -1), y_code, px, ldx, pr, ldr, pb,
-            *weights, ps, lds, py, ldy)
-    need = C.c_uint64()
-    code = ops.moe_workspace(_MOE_ARGS.pack(*args, 0, 0, 0, 0), C.addressof(need))
-    if code:
-        _check(code)
-    shape = x.shape[:-1] + (top_k,)
-    chosen, p = ops.empty(shape, dtype=torch.int32, device=x.device), ops.empty(shape, dtype=torch.float32, device=x.device)
-    space = ops.empty(need.value, dtype=torch.uint8, device=x.device)
-    code = ops.moe(_MOE_ARGS.pack(*args, chosen.data_ptr(), p.data_ptr(), space.data_ptr(), need.value), ops.stream(gpu))
+            *gates, *ups, *downs, ps, lds, py, ldy)
+    # The workspace's size goes by sizes and dtypes alone.
+    sizes = args[:5] + args[6:7] + args[9:12] + (not pb,)
+    need = ops.moe_spaces.get(sizes)
+    if need is None:
+        got = C.c_uint64()
+        code = ops.moe_workspace(_MOE_ARGS.pack(*args, 0, 0, 0, 0), C.addressof(got))
+        if code:
+            _check(code)
+        if len(ops.moe_spaces) >= 1024:
+            ops.moe_spaces.clear()
+        need = ops.moe_spaces[sizes] = got.value
+    shape, device = x.shape[:-1] + (top_k,), x.device
+    chosen, p = ops.empty(shape, dtype=torch.int32, device=device), ops.empty(shape, dtype=f32, device=device)
+    space = ops.empty(need, dtype=torch.uint8, device=device)
+    code = ops.moe(_MOE_ARGS.pack(*args, chosen.data_ptr(), p.data_ptr(), space.data_ptr(), need), ops.stream(gpu))
     if code:
         _check(code)
     return out, chosen, p
