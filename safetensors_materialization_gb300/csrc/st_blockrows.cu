@@ -31,112 +31,169 @@ struct BlockRowArgs {
   float *scales;
   int64_t ldx, ldr, ldh, ldy, blocks;
   int64_t rows;
-  int cols;
+  int cols, pieces;       // pieces of a row (gated activation)
   float eps;
   st_act act;
   st_dtype w_dtype;
 };
 
 // V elements from column c on of the row that starts at p, which may start at
-// any element: two aligned accesses, shifted.  Those that would leave the row,
-// and all of binary32's, go by element.  Zeros behind the row's end.
+// any element: two aligned accesses, shifted, where the row has neighbours to
+// both sides (`inside`: up to 8 elements before and 16 behind it belong to the
+// matrix), else single elements.  Zeros behind the row's end.
 template <class T, int V>
-__device__ __forceinline__ Raw<T, V> any_read(const T *p, int c, int cols) {
+__device__ __forceinline__ Raw<T, V> any_read(const T *p, int c, int cols, bool inside) {
   Raw<T, V> out;
-  if constexpr (sizeof(T) == 2) {
+  if (sizeof(T) == 2 && inside) {
     const uint32_t q = (reinterpret_cast<uintptr_t>(p) / 2) & 7;  // c is a multiple of 8
-    const int from = c - static_cast<int>(q);
-    if (from >= 0 && from + (q ? 16 : 8) <= cols) {
-      const uint4 lo = *reinterpret_cast<const uint4 *>(p + from);
-      const uint4 hi = q ? *reinterpret_cast<const uint4 *>(p + from + 8) : lo;
-      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, sh = 16 * (q & 1);
-      uint32_t a[6], b[5];
-#pragma unroll
-      for (int i = 0; i < 6; ++i) a[i] = q & 4 ? w[i + 2] : w[i];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) b[i] = q & 2 ? a[i + 1] : a[i];
-      uint32_t *u = reinterpret_cast<uint32_t *>(&out);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(b[i], b[i + 1], sh);
-      return out;
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (c < cols) {
+      lo = *reinterpret_cast<const uint4 *>(p + c - q);
+      if (q) hi = *reinterpret_cast<const uint4 *>(p + c - q + 8);
     }
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, sh = 16 * (q & 1);
+    uint32_t a[6], b[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) a[i] = q & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) b[i] = q & 2 ? a[i + 1] : a[i];
+    uint32_t *u = reinterpret_cast<uint32_t *>(&out);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) u[i] = __funnelshift_r(b[i], b[i + 1], sh);
+    if (c + V > cols) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c + i >= cols) out.e[i] = T(0.0f);
+    }
+    return out;
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) out.e[i] = c + i < cols ? p[c + i] : T(0.0f);
   return out;
 }
 
+// The n lowest bytes of `bytes` (fewer than 8) to any address, by the largest
+// aligned stores.
+__device__ __forceinline__ void put_bytes(uint8_t *p, uint64_t bytes, int n) {
+  auto put = [&](auto zero) {
+    using U = decltype(zero);
+    *reinterpret_cast<U *>(p) = static_cast<U>(bytes);
+    p += sizeof(U), bytes >>= 8 * sizeof(U), n -= sizeof(U);
+  };
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if ((at & 1) && n >= 1) put(uint8_t{});
+  if ((reinterpret_cast<uintptr_t>(p) & 2) && n >= 2) put(uint16_t{});
+  if (n >= 4) put(uint32_t{});
+  if (n >= 2) put(uint16_t{});
+  if (n >= 1) put(uint8_t{});
+}
+
 // Eight codes of every lane, from its column c on, in a row that starts at any
 // byte: a lane writes the aligned word that its first codes lie in, with the
 // last codes of the lane before.  The whole warp calls it, with consecutive
 // columns.
-__device__ __forceinline__ void put_codes8(uint8_t *row, int c, int cols, uint64_t codes, int lane) {
-  const int q = static_cast<int>(reinterpret_cast<uintptr_t>(row + c) & 7);
-  const uint64_t before = __shfl_up_sync(~0u, codes, 1);
-  if (q == 0) {
-    if (c + 8 <= cols) *reinterpret_cast<uint64_t *>(row + c) = codes;
-    else
-      for (int j = 0; c + j < cols && j < 8; ++j) row[c + j] = static_cast<uint8_t>(codes >> (8 * j));
-    return;
-  }
-  if (lane > 0 && c + 8 - q <= cols) {
-    *reinterpret_cast<uint64_t *>(row + c - q) = before >> (8 * (8 - q)) | codes << (8 * q);
-  } else {
-    if (lane > 0)
-      for (int j = 0; j < q && c - q + j < cols; ++j) row[c - q + j] = static_cast<uint8_t>(before >> (8 * (8 - q + j)));
-    for (int j = 0; j < 8 - q && c + j < cols; ++j) row[c + j] = static_cast<uint8_t>(codes >> (8 * j));
-  }
-  if (lane == 31)
-    for (int j = 8 - q; j < 8 && c + j < cols; ++j) row[c + j] = static_cast<uint8_t>(codes >> (8 * j));
+__device__ __forceinline__ void put_codes8(uint8_t *row, int c, int cols, uint32_t lo, uint32_t hi, int lane) {
+  const int q = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 7), left = cols - c;  // c is a multiple of 8
+  const uint32_t lo_before = __shfl_up_sync(~0u, lo, 1), hi_before = __shfl_up_sync(~0u, hi, 1);
+  // The word's bytes are those of the lane before's and this one's codes from
+  // byte 8 - q on.
+  const bool far = q > 4;
+  const uint32_t a = far ? lo_before : hi_before, b = far ? hi_before : lo, e = far ? lo : hi, sh = 8 * ((8 - q) & 3);
+  const uint32_t w0 = q ? __funnelshift_r(a, b, sh) : lo, w1 = q ? __funnelshift_r(b, e, sh) : hi;
+  // The first byte that is this lane's to write, and how many they are.
+  const int skip = lane > 0 ? 0 : q, n = min(8, left + q) - skip;
+  uint8_t *const to = row + c - q;
+  if (n == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w0, w1);
+  else if (n > 0) put_bytes(to + skip, (w0 | static_cast<uint64_t>(w1) << 32) >> (8 * skip), n);
+  if (lane == 31 && q && left > 8 - q) put_bytes(to + 8, (lo | static_cast<uint64_t>(hi) << 32) >> (8 * (8 - q)), min(q, left - (8 - q)));
 }
 
-// V values of h from column c on, by the widest accesses that its row's start
-// allows.
+// V values of h from column c on, likewise: words of two 16-bit values, shifted
+// by one where the row starts at an odd element.
 template <class T, int V>
-__device__ __forceinline__ void put_any(T *p, int c, int cols, const float (&v)[V]) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p + c);
-  if (c + V <= cols && at % (V * sizeof(T)) == 0) return store_any<V>(p, kDtype<T>, c, v);
-  if (sizeof(T) == 2 && c + V <= cols && at % 4 == 0) {
-    uint32_t *u = reinterpret_cast<uint32_t *>(p + c);
+__device__ __forceinline__ void put_any(T *row, int c, int cols, const float (&v)[V], int lane) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i < cols) row[c + i] = v[i];
+  } else {
+    uint32_t u[V / 2];
 #pragma unroll
     for (int i = 0; i < V / 2; ++i)
       u[i] = kDtype<T> == ST_BF16 ? pack_bf16(v[2 * i], v[2 * i + 1]) : pack_f16(v[2 * i], v[2 * i + 1]);
-    return;
-  }
+    const uint32_t before = __shfl_up_sync(~0u, u[V / 2 - 1], 1);
+    uint16_t *const p = reinterpret_cast<uint16_t *>(row + c);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (at % 16 == 0 && c + V <= cols) {
+      *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else if (at % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float one[1] = {v[i]};
-    if (c + i < cols) store_any<1>(p, kDtype<T>, c + i, one);
+      for (int i = 0; i < V / 2; ++i) {
+        if (c + 2 * i + 1 < cols) *reinterpret_cast<uint32_t *>(p + 2 * i) = u[i];
+        else if (c + 2 * i < cols) p[2 * i] = static_cast<uint16_t>(u[i]);
+      }
+    } else {
+      // Elements 2 i - 1 and 2 i.
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const uint32_t w = __funnelshift_r(i ? u[i - 1] : before, u[i], 16);
+        const bool first = (i > 0 || lane > 0) && c + 2 * i - 1 < cols, second = c + 2 * i < cols;
+        if (first && second) *reinterpret_cast<uint32_t *>(p + 2 * i - 1) = w;
+        else if (first) p[2 * i - 1] = static_cast<uint16_t>(w);
+        else if (second) p[2 * i] = static_cast<uint16_t>(w >> 16);
+      }
+      if (lane == 31 && c + V - 1 < cols) p[V - 1] = static_cast<uint16_t>(u[V / 2 - 1] >> 16);
+    }
   }
 }
 
+// A block's scale from its largest magnitude, and the scale's inverse.  Both
+// divisions in a few instructions, which every thread of the block takes: a
+// quotient by the rounded 1 / 448 and a reciprocal, each with one step that
+// takes its remainder in (within a unit of the last place).
+__device__ __forceinline__ float block_scale(float top, float *inv) {
+  constexpr float kInv = 1.0f / kE4M3Max;
+  const float q = top * kInv, exact = fmaf(fmaf(-kE4M3Max, q, top), kInv, q);
+  // (An infinite q has no remainder.)
+  const float s = max_nan(isinf(q) ? q : exact, kMinScale), r = fast_rcp(s);
+  *inv = isinf(s) ? 0.0f : fmaf(r, fmaf(-s, r, 1.0f), r);
+  return s;
+}
+
 // One row (kWarpRow: of a warp) in registers, NV accesses of V elements a
-// thread; the gated activation's block has columns from blockIdx.y on instead
-// of a whole row.  kAny: rows start anywhere, or end inside an access.
+// thread; the gated activation's block has a piece of a row.  kAny: rows start
+// anywhere, or end inside an access.
 template <class T, int V, int NV, bool kAny, Op kOp, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kWarps : kOp == kActOp ? kPieceThreads : NV >= 4 ? 512 : kMaxThreads)
 block_row_kernel(const BlockRowArgs a) {
-  const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+  const bool piece = kOp == kActOp && !kWarpRow;
+  const int64_t row = kWarpRow ? int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5) : piece ? blockIdx.x / a.pieces : blockIdx.x;
   const int t = kWarpRow ? (threadIdx.x & 31) : threadIdx.x, nt = kWarpRow ? 32 : blockDim.x, lane = threadIdx.x & 31;
-  const int first = kOp == kActOp && !kWarpRow ? blockIdx.y * nt * V * NV : 0;
+  const int first = piece ? static_cast<int>(blockIdx.x % a.pieces) * nt * V * NV : 0;
   wait_for_previous();
   let_next_start();
   if (kWarpRow && row >= a.rows) return;
-  if (kOp == kNormOp && !kWarpRow && !kAny && t == 0 && row + kAhead < a.rows) {
-    row_prefetch<T>(a.x, (row + kAhead) * a.ldx, a.cols);
-    if (a.r) row_prefetch<T>(a.r, (row + kAhead) * a.ldr, a.cols);
+  if (!kWarpRow && !kAny && t == 0 && row + kAhead < a.rows && first < a.cols) {
+    const int n = min(a.cols - first, piece ? nt * V * NV : a.cols);
+    row_prefetch<T>(a.x, (row + kAhead) * a.ldx + first, n);
+    if (a.r) row_prefetch<T>(a.r, (row + kAhead) * a.ldr + first, n);
   }
   auto column = [&](int i) { return first + (i * nt + t) * V; };
+  // Columns of the warp lie before the row's end or behind it: its lanes take
+  // the same way.
+  auto beyond = [&](int i) { return column(i) - lane * V >= a.cols; };
   const T *const px = static_cast<const T *>(a.x) + row * a.ldx, *const pr = static_cast<const T *>(a.r) + row * a.ldr;
   Raw<T, V> x[NV], r[NV];
+  auto inside = [&](int64_t ld) { return row * ld >= 8 && (a.rows - 1 - row) * ld >= 16; };
+  const bool x_inside = kAny && inside(a.ldx), r_inside = kAny && inside(a.ldr);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = column(i);
-    if (c >= a.cols) continue;
+    if (beyond(i)) continue;
     if constexpr (kAny) {
-      x[i] = any_read<T, V>(px, c, a.cols);
-      if (a.r) r[i] = any_read<T, V>(pr, c, a.cols);
-    } else {
+      x[i] = any_read<T, V>(px, c, a.cols, x_inside);
+      if (a.r) r[i] = any_read<T, V>(pr, c, a.cols, r_inside);
+    } else if (c < a.cols) {
       x[i] = row_read<T, V>(px, c);
       if (a.r) r[i] = row_read<T, V>(pr, c);
     }
@@ -149,7 +206,7 @@ block_row_kernel(const BlockRowArgs a) {
     top[i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
-    if (c >= a.cols) continue;
+    if (kAny ? beyond(i) : c >= a.cols) continue;
     float o[V];
     unpack(x[i], v[i]);
     if (a.r) unpack(r[i], o);
@@ -159,7 +216,7 @@ block_row_kernel(const BlockRowArgs a) {
         for (int j = 0; j < V; ++j) v[i][j] += o[j];
         if (a.h) {
           T *const ph = static_cast<T *>(a.h) + row * a.ldh;
-          if constexpr (kAny) put_any<T, V>(ph, c, a.cols, v[i]);
+          if constexpr (kAny) put_any<T, V>(ph, c, a.cols, v[i], lane);
           else store_any<V>(ph, kDtype<T>, c, v[i]);
         }
       }
@@ -169,11 +226,11 @@ block_row_kernel(const BlockRowArgs a) {
         with_type(a.w_dtype, [&](auto zero) {
           using W = decltype(zero);
           const W *w = static_cast<const W *>(a.w) + c;
-          if constexpr (kAny) {
+          if (!kAny || (c + V <= a.cols && reinterpret_cast<uintptr_t>(w) % alignof(Raw<W, V>) == 0)) {
+            unpack(*reinterpret_cast<const Raw<W, V> *>(w), o);
+          } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) o[j] = c + j < a.cols ? to_float(w[j]) : 0.0f;
-          } else {
-            unpack(*reinterpret_cast<const Raw<W, V> *>(w), o);
           }
         });
 #pragma unroll
@@ -198,23 +255,23 @@ block_row_kernel(const BlockRowArgs a) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = column(i);
-    // The columns of a warp lie before the row's end or behind it, with the
-    // shuffles' lanes all here.
-    if (c - lane * V >= a.cols) continue;
+    if (beyond(i)) continue;
 #pragma unroll
     for (int d = kBlock / V / 2; d; d >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(~0u, top[i], d));
-    const float scale = max_nan(top[i] * rstd / kE4M3Max, kMinScale), inv = 1.0f / scale;
+    float inv;
+    const float scale = block_scale(top[i] * rstd, &inv);
     if (lane % (kBlock / V) == 0 && c < a.cols) a.scales[row * a.blocks + c / kBlock] = scale;
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rstd * inv;
     uint32_t u[V / 4];
 #pragma unroll
-    for (int j = 0; j < V / 4; ++j)
-      u[j] = pack_e4m3(v[i][4 * j], v[i][4 * j + 1]) | pack_e4m3(v[i][4 * j + 2], v[i][4 * j + 3]) << 16;
+    for (int j = 0; j < V / 4; ++j) {
+      float2 lo = make_float2(v[i][4 * j], v[i][4 * j + 1]), hi = make_float2(v[i][4 * j + 2], v[i][4 * j + 3]);
+      if constexpr (kOp == kNormOp) lo = __fmul2_rn(lo, make_float2(rstd, rstd)), hi = __fmul2_rn(hi, make_float2(rstd, rstd));
+      lo = __fmul2_rn(lo, make_float2(inv, inv)), hi = __fmul2_rn(hi, make_float2(inv, inv));
+      u[j] = pack_e4m3(lo.x, lo.y) | pack_e4m3(hi.x, hi.y) << 16;
+    }
     if constexpr (V == 8) {
-      const uint64_t codes = u[0] | static_cast<uint64_t>(u[1]) << 32;
-      if constexpr (kAny) put_codes8(py, c, a.cols, codes, lane);
-      else if (c < a.cols) *reinterpret_cast<uint64_t *>(py + c) = codes;
+      if constexpr (kAny) put_codes8(py, c, a.cols, u[0], u[1], lane);
+      else if (c < a.cols) *reinterpret_cast<uint2 *>(py + c) = make_uint2(u[0], u[1]);
     } else if (c < a.cols) {
       if (!kAny || (c + V <= a.cols && reinterpret_cast<uintptr_t>(py + c) % V == 0)) *reinterpret_cast<uint32_t *>(py + c) = u[0];
       else
@@ -265,7 +322,8 @@ __global__ void __launch_bounds__(kMaxThreads) block_row_loop_kernel(const Block
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
-    const float scale = max_nan(top * rstd / kE4M3Max, kMinScale), inv = 1.0f / scale;
+    float inv;
+    const float scale = block_scale(top * rstd, &inv);
     if (lane == 0) a.scales[row * a.blocks + c0 / kBlock] = scale;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -297,11 +355,13 @@ cudaError_t launch_norm(const BlockRowArgs &a, cudaStream_t st) {
 }
 
 template <class T, int V, int NV, bool kAny>
-cudaError_t launch_pieces(const BlockRowArgs &a, int64_t accesses, cudaStream_t st) {
+cudaError_t launch_pieces(BlockRowArgs a, int64_t accesses, cudaStream_t st) {
   const int64_t pieces = (accesses + kPieceThreads * NV - 1) / (kPieceThreads * NV);
   // The pieces' threads, as even as whole warps allow.
   const unsigned nt = static_cast<unsigned>(((accesses + pieces * NV - 1) / (pieces * NV) + 31) / 32 * 32);
-  return launch(block_row_kernel<T, V, NV, kAny, kActOp, false>, dim3(static_cast<unsigned>(a.rows), static_cast<unsigned>(pieces)), nt, 0, 1, st, a);
+  if (a.rows * pieces > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  a.pieces = static_cast<int>(pieces);
+  return launch(block_row_kernel<T, V, NV, kAny, kActOp, false>, dim3(static_cast<unsigned>(a.rows * pieces)), nt, 0, 1, st, a);
 }
 
 // Pieces of 256 threads, two accesses a thread of each matrix; one where rows
