@@ -38,7 +38,10 @@ constexpr int kDenseMmaWarp = 8, kDenseCopyWarp = 9, kDenseThreads = 384;
 // Three warpgroups start with 168 registers a thread; the two that hold sums
 // take 240, the third gives the rest (2 x 240 + 24 = 3 x 168).
 constexpr int kSumRegisters = 240, kFeedRegisters = 24;
-constexpr int kDenseSmem = 192 * 1024;  // the ring of stages
+constexpr int kDenseSmem = 224 * 1024;  // the ring of stages, and y's tile
+// A readout warp's part of y's tile in 16 bits, or what rows at any place are
+// turned in.
+__host__ __device__ constexpr int part_bytes(int w) { return w * 32 > 3072 ? w * 32 : 3072; }
 
 struct BlockArgs : OutArgs {
   Side w, x;
@@ -46,6 +49,7 @@ struct BlockArgs : OutArgs {
   int k_blocks, splits, stages, m_tiles, n_tiles;
   int x_box;                         // token rows a TMA copy brings
   uint32_t idesc;
+  int tma_store;                     // y is written, and the residual read, by TMA
   const float *x_scale, *w_scale;
   int64_t ldxs, ldws;
   uint32_t *err;
@@ -312,11 +316,18 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
                :: "memory");
 }
 
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(smem_addr(src)) : "memory");
+}
+
 // W: weight rows of a tile.  kF32: y's type, with an activation (exact_act).
 template <int W, bool kF32>
 __global__ void __launch_bounds__(kDenseThreads, 1)
 block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                   const __grid_constant__ BlockArgs a) {
+                   const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap rmap, const __grid_constant__ BlockArgs a) {
+  // Narrow tiles' stores would hold up the copies of the next stages (8192 x
+  // 14336 x 4096 by tiles of 128: 567 us, 472 from registers).
+  const bool tma_y = W > 128 && a.tma_store;
   constexpr int kHalf = W / 2;       // columns of a thread; weight rows of a CTA's stage
   constexpr int kStageBytes = (128 + kHalf) * kStageK;
   // Blocks whose sums TMEM holds (8192 x 14336 x 4096 by tiles of 128: two 519
@@ -324,10 +335,11 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
   constexpr int kBuffers = W <= 128 ? 4 : 2, kBufferColumns = 512 / kBuffers;
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums[kBuffers], taken[kBuffers];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums[kBuffers], taken[kBuffers], residuals[kDenseSumWarps];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
-  __shared__ __align__(16) uint32_t turn[kDenseSumWarps][32][17];
+  __shared__ __align__(16) float biases[kDenseSumWarps][kChunk];
+  uint8_t *const tile = smem + a.stages * kStageBytes;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;
@@ -342,6 +354,7 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
       bar_init(&sums[i], 1);
       bar_init(&taken[i], 2 * kDenseSumWarps);
     }
+    for (int i = 0; i < kDenseSumWarps; ++i) bar_init(&residuals[i], 1);
     failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -363,19 +376,41 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
     const int quarter = warp & 3, left = (warp >> 2) * kHalf;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + left;
     const uint32_t taken_at = peer_addr(taken, 0);
+    // This warp's part of y's tile: chunks of 32 columns, rows of 64 bytes whose
+    // 16-byte parts are swizzled as TMA reads them.
+    uint8_t *const box = tile + warp * part_bytes(W);
+    uint32_t(&turn)[32][17] = *reinterpret_cast<uint32_t(*)[32][17]>(box);
+    bool stored = false;
+    uint32_t residual_phase = 0;
+    // The stores so far have left shared memory.
+    auto drain = [&]() {
+      if (lane == 0) asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    };
     Ring sum;
     bool ok = true;
+    // Whether the columns can lie in two of the weight's blocks.
+    constexpr bool kTwo = kHalf > kBlockK / 2 && kBlockK % kHalf != 0;
     for (int t = pair; t < tiles && ok; t += pairs) {
       const TileAt at = tile_at<W>(a, t);
       const int64_t mw = at.m0 + rank * 128 + quarter * 32, m = mw + lane, first = at.n0 + left;
       const bool row = m < a.m;
-      // The scales of a block, read one block ahead: the token's, and those of
-      // the one or two weight blocks that the columns lie in.  Columns from
-      // `edge` on have the second.
+      // The scales of a block, read one block ahead: the token's, and the weight
+      // block's (kTwo: and those of the next one, for the columns from `edge` on).
       const int edge = kBlockK - static_cast<int>(first % kBlockK);
-      const bool two = edge < kHalf && first + edge < a.n;
-      const float *xs = a.x_scale + (row ? m : 0) * a.ldxs, *ws = a.w_scale + (first < a.n ? first / kBlockK : 0) * a.ldws;
+      const bool two = kTwo && edge < kHalf && first + edge < a.n;
+      const float *const xs = a.x_scale + (row ? m : 0) * a.ldxs, *const ws = a.w_scale + (first < a.n ? first / kBlockK : 0) * a.ldws;
       float nx = xs[0], n0 = ws[0], n1 = two ? ws[a.ldws] : 0.0f;
+      // The residual's boxes take the place of y's while the sums are formed.
+      const int boxes = mw < a.m ? static_cast<int>(max(int64_t(0), min(int64_t(kHalf / kChunk), (a.n - first + kChunk - 1) / kChunk))) : 0;
+      if (tma_y && a.residual && boxes > 0) {
+        if (stored) drain();
+        if (lane == 0) {
+          bar_expect(&residuals[warp], boxes * 32 * 64);
+          for (int i = 0; i < boxes; ++i)
+            tma_load(&rmap, box + i * 32 * 64, &residuals[warp], static_cast<int32_t>(first + i * kChunk), static_cast<int32_t>(mw));
+        }
+      }
       float acc[kHalf];
 #pragma unroll
       for (int j = 0; j < kHalf; ++j) acc[j] = 0.0f;
@@ -399,19 +434,25 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
             __syncwarp();
             if (lane == 0) peer_arrive(taken_at + 8 * sum.at);
           }
-          const float s = kHalf > 32 && W % 256 != 0 && c >= edge ? s1 : s0;
+          const float s = kTwo && c >= edge ? s1 : s0;
 #pragma unroll
           for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[j]), s, acc[c + j]);
         }
       }
       if (!ok) break;
+      if (tma_y) {
+        if (boxes > 0 && a.residual) {
+          if (!bar_wait(&residuals[warp], residual_phase)) { ok = false; break; }
+          residual_phase ^= 1;
+        } else if (stored) drain();
+      }
 #pragma unroll
       for (int c = 0; c < kHalf; c += kChunk) {
         const int64_t n0c = first + c;
         if (n0c >= a.n) break;
         const bool wide = a.vec && n0c + kChunk <= a.n;
         uint32_t old[2][8];
-        if (a.residual && a.y_dtype != ST_F32) {
+        if (a.residual && !tma_y && a.y_dtype != ST_F32) {
           if (!wide) read_turned(a, mw, n0c, lane, old);
           else if (row) {
 #pragma unroll
@@ -424,18 +465,40 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
         if (a.bias) {
           float bl[1] = {0.0f};
           if (n0c + lane < a.n) load_any<1>(a.bias, a.bias_dtype, n0c + lane, bl);
-          float *const all = reinterpret_cast<float *>(turn[warp]);
           __syncwarp();
-          all[lane] = bl[0];
+          biases[warp][lane] = bl[0];
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < kChunk; j += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(all + j);
+            const float4 f = *reinterpret_cast<const float4 *>(biases[warp] + j);
             v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
           }
         }
         activate<kF32>(v, a.act);
-        if (wide) {
+        if (tma_y) {
+          uint8_t *const at_row = box + c * 64 + lane * 64;
+          auto part = [&](int i) { return reinterpret_cast<uint4 *>(at_row + ((i ^ (lane >> 1 & 3)) << 4)); };
+          if (a.residual) {
+            uint32_t o[2][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(&o[i / 2][i % 2 * 4]) = *part(i);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) add16(o[i], a.y_dtype == ST_BF16, v + 16 * i);
+          }
+          uint32_t u[16];
+          if (a.y_dtype == ST_BF16) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j] = pack_f16(v[2 * j], v[2 * j + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *part(i) = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && mw < a.m) tma_store(&ymap, box + c * 64, static_cast<int32_t>(n0c), static_cast<int32_t>(mw));
+        } else if (wide) {
           if (row) {
             if (a.residual && a.y_dtype != ST_F32) {
 #pragma unroll
@@ -443,12 +506,17 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
             } else if (a.residual) add_row32(a.residual, m * a.ldr + n0c, v);
             put_row(a.y, a.y_dtype, m * a.ldy + n0c, v);
           }
-        } else if (a.y_dtype == ST_BF16) put_turned<__nv_bfloat16>(turn[warp], a, mw, n0c, lane, old, v);
-        else if (a.y_dtype == ST_F16) put_turned<__half>(turn[warp], a, mw, n0c, lane, old, v);
-        else put_turned32(turn[warp], a, mw, n0c, lane, v);
+        } else if (a.y_dtype == ST_BF16) put_turned<__nv_bfloat16>(turn, a, mw, n0c, lane, old, v);
+        else if (a.y_dtype == ST_F16) put_turned<__half>(turn, a, mw, n0c, lane, old, v);
+        else put_turned32(turn, a, mw, n0c, lane, v);
       }
+      stored = tma_y;
     }
-    if (!ok) failed = 1;
+    if (stored && lane == 0) asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
+    if (!ok) {  // a residual under way lands before the CTA ends
+      if (tma_y && a.residual) bar_wait(&residuals[warp], residual_phase);
+      failed = 1;
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegisters));
     if (warp == kDenseCopyWarp) {
@@ -528,15 +596,31 @@ st_status launch_split(BlockArgs &a, const CUtensorMap &wmap, const CUtensorMap 
 }
 
 template <int W, bool kF32>
-st_status launch_dense(BlockArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, int dev, int sms, cudaStream_t st) {
-  constexpr int kStageBytes = (128 + W / 2) * kStageK, kStages = kDenseSmem / kStageBytes < kMaxStages ? kDenseSmem / kStageBytes : kMaxStages;
+st_status launch_dense(BlockArgs &a, const CUtensorMap &xmap, const CUtensorMap &wmap, const CUtensorMap &ymap, const CUtensorMap &rmap, int dev, int sms,
+                       cudaStream_t st) {
+  constexpr int kStageBytes = (128 + W / 2) * kStageK, kFit = (kDenseSmem - kDenseSumWarps * part_bytes(W)) / kStageBytes;
+  constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   a.stages = kStages;
-  constexpr int smem = kStages * kStageBytes + 1024;
+  constexpr int smem = kStages * kStageBytes + kDenseSumWarps * part_bytes(W) + 1024;
   constexpr auto kernel = block_dense_kernel<W, kF32>;
   cudaError_t e = allow_smem<kernel>(dev, smem);
   if (e == cudaSuccess)
-    e = launch(kernel, dim3(2u * static_cast<unsigned>(std::min(a.m_tiles * a.n_tiles, sms / 2))), kDenseThreads, smem, 2, st, xmap, wmap, a);
+    e = launch(kernel, dim3(2u * static_cast<unsigned>(std::min(a.m_tiles * a.n_tiles, sms / 2))), kDenseThreads, smem, 2, st, xmap, wmap, ymap, rmap, a);
   return e == cudaSuccess ? ST_OK : launch_error(a, e);
+}
+
+// Rows of 16-bit values, in boxes of 32 x 32.
+st_status encode_rows(CUtensorMap *map, const Side &s, int64_t n, const char *op) {
+  EncodeFn fn = nullptr;
+  const st_status st = encoder(&fn, op);
+  if (st != ST_OK) return st;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(s.rows)};
+  const cuuint64_t stride[1] = {s.rows == 1 ? static_cast<cuuint64_t>((n * 2 + 15) / 16 * 16) : static_cast<cuuint64_t>(s.pitch)};
+  const cuuint32_t box[2] = {kChunk, 32}, step[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint8_t *>(s.p), dims, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(ST_E_CUDA, "%s: tensor map of rows of %lld x %lld refused (%d)", op, (long long)s.rows, (long long)n, static_cast<int>(r));
+  return ST_OK;
 }
 
 int blocks_of(const st_block_linear_args &p) { return static_cast<int>((p.k + kBlockK - 1) / kBlockK); }
@@ -566,9 +650,10 @@ st_status check_block_linear_form(const st_block_linear_args &p, const st_linear
 // the sum for tiles of 16, 32 and 64 tokens, 1.8 times as long for two CTAs an
 // SM, and again for each round of those.  (1 x 4096 x 14336 in 1, 2, 4, 8 parts: 39.8, 21.5, 13.7, 13.7; 64
 // tokens 53.7, 32.3, 19.2, 16.4; tiles of 128 tokens were slower than two of 64
-// or the other kernel.)  block_dense_kernel: 2.5, and a round of tiles 1 and 0.27,
-// 0.313, 0.452 or 0.522 a block by 64, 128, 192 and 256 weight rows (8192 x 14336
-// x 4096: 824, 481, 463, 401; 256 x 4096 x 4096 12.5, 13.6, 17.5, 19.6).
+// or the other kernel.)  block_dense_kernel: 2.5, and a round of tiles 0.1 and
+// 0.008 a weight row of a tile to write it, and 0.265, 0.307, 0.43 or 0.487 a
+// block by 64, 128, 192 and 256 weight rows (8192 x 14336 x 4096: 814, 472, 441,
+// 374; 8192 x 4096 x 1024 76, 54, 53, 46; 256 x 4096 x 4096 12.5, 13.5, 16.9, 18.6).
 st_linear_form choose_block_linear_form(const st_block_linear_args &p, int sms) {
   const int k_blocks = blocks_of(p);
   const int tokens = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
@@ -583,10 +668,10 @@ st_linear_form choose_block_linear_form(const st_block_linear_args &p, int sms) 
     if (splits == 1 || us < least) best.splits = splits, least = us;
   }
   if (p.m <= 16 || p.k == 0) return best;
-  static constexpr double kBlock[] = {0.27, 0.313, 0.452, 0.522};
+  static constexpr double kBlock[] = {0.265, 0.307, 0.43, 0.487};
   for (int w = kPairMaxN; w >= 64; w -= 64) {
     const int64_t dense = (p.m + kPairM - 1) / kPairM * ((p.n + w - 1) / w);
-    const double us = 2.5 + static_cast<double>((dense + sms / 2 - 1) / (sms / 2)) * (1 + k_blocks * kBlock[w / 64 - 1]);
+    const double us = 2.5 + static_cast<double>((dense + sms / 2 - 1) / (sms / 2)) * (0.1 + 0.008 * w + k_blocks * kBlock[w / 64 - 1]);
     if (us < least) best = {ST_LINEAR_DENSE, w, 1}, least = us;
   }
   return best;
@@ -625,16 +710,21 @@ st_status launch_block_linear(const st_block_linear_args &p, const st_linear_for
   auto idesc = [](uint32_t fa, uint32_t fb, uint32_t r, uint32_t c) {
     return (1u << 4) | (fa << 7) | (fb << 10) | ((c / 8) << 17) | ((r / 16) << 24);
   };
-  CUtensorMap wmap{}, xmap{};
+  CUtensorMap wmap{}, xmap{}, ymap{}, rmap{};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dense) {
     a.idesc = idesc(0, e5m2, kPairM, f.width);
     s = encode(&xmap, a.x, p.k, 1, 128, op);
     if (s == ST_OK) s = encode(&wmap, a.w, p.k, 1, f.width / 2, op);
+    // y and the residual in boxes of a warp's 32 rows and 32 columns.
+    const Side y = side_of(p.y, p.ldy, p.m, p.n, 2), res = side_of(p.residual, p.ldr, p.m, p.n, 2);
+    a.tma_store = out == 2 && tma_ok(y) && (!p.residual || tma_ok(res));
+    if (s == ST_OK && a.tma_store) s = encode_rows(&ymap, y, p.n, op);
+    if (s == ST_OK && a.tma_store && p.residual) s = encode_rows(&rmap, res, p.n, op);
     if (s != ST_OK) return s;
     auto run = [&](auto w) {
       constexpr int W = decltype(w)::value;
-      return exact_act(a.act, a.y_dtype) ? launch_dense<W, true>(a, xmap, wmap, dev, sms, st) : launch_dense<W, false>(a, xmap, wmap, dev, sms, st);
+      return exact_act(a.act, a.y_dtype) ? launch_dense<W, true>(a, xmap, wmap, ymap, rmap, dev, sms, st) : launch_dense<W, false>(a, xmap, wmap, ymap, rmap, dev, sms, st);
     };
     switch (f.width) {
       case 64: return run(std::integral_constant<int, 64>{});
