@@ -41,7 +41,7 @@ constexpr int kSumRegisters = 240, kFeedRegisters = 24;
 constexpr int kDenseSmem = 224 * 1024;  // the ring of stages, and y's tile
 // A readout warp's part of y's tile in 16 bits, or what rows at any place are
 // turned in.
-__host__ __device__ constexpr int part_bytes(int w) { return w * 32 > 3072 ? w * 32 : 3072; }
+__host__ __device__ constexpr int part_bytes(int w) { return w * 32 > 3 * 1024 ? w * 32 : 3 * 1024; }
 
 struct BlockArgs : OutArgs {
   Side w, x;
