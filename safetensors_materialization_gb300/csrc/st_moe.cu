@@ -145,7 +145,10 @@ __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {
   const int live = min(kLogitTokens, a.tokens - t0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kThreadsHere = 32 * kLogitWarps;
   const R *const w = static_cast<const R *>(a.router) + expert * a.ld_router;
-  const X *const x = static_cast<const X *>(a.x) + t0 * a.ldx;
+  // Fewer than four: the last one again, so that all four's steps interleave.
+  const X *x[kLogitTokens];
+#pragma unroll
+  for (int t = 0; t < kLogitTokens; ++t) x[t] = static_cast<const X *>(a.x) + (t0 + min(t, live - 1)) * a.ldx;
   Two sum[kLogitTokens];
   auto step = [&](int t, float xv, float wv) {
     const float p = __fmul_rn(xv, wv);
@@ -157,43 +160,35 @@ __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {
   const bool wide = a.hidden % V == 0 && a.ldx % V == 0 && a.ld_router % V == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
   if (wide) {
-#pragma unroll 2
     for (int c = threadIdx.x * V; c < a.hidden; c += kThreadsHere * V) {
-      const Raw<R, V> wr = *reinterpret_cast<const Raw<R, V> *>(w + c);
-      Raw<X, V> xr[kLogitTokens];
+      float wv[V], xv[kLogitTokens][V];
+      unpack(*reinterpret_cast<const Raw<R, V> *>(w + c), wv);
 #pragma unroll
-      for (int t = 0; t < kLogitTokens; ++t)
-        if (t < live) xr[t] = *reinterpret_cast<const Raw<X, V> *>(x + t * a.ldx + c);
-      float wv[V], xv[V];
-      unpack(wr, wv);
+      for (int t = 0; t < kLogitTokens; ++t) unpack(*reinterpret_cast<const Raw<X, V> *>(x[t] + c), xv[t]);
 #pragma unroll
-      for (int t = 0; t < kLogitTokens; ++t) {
-        if (t >= live) continue;
-        unpack(xr[t], xv);
+      for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int i = 0; i < V; ++i) step(t, xv[i], wv[i]);
-      }
+        for (int t = 0; t < kLogitTokens; ++t) step(t, xv[t][i], wv[i]);
     }
   } else {
     for (int c = threadIdx.x; c < a.hidden; c += kThreadsHere) {
       const float wv = to_float(w[c]);
 #pragma unroll
-      for (int t = 0; t < kLogitTokens; ++t)
-        if (t < live) step(t, to_float(x[t * a.ldx + c]), wv);
+      for (int t = 0; t < kLogitTokens; ++t) step(t, to_float(x[t][c]), wv);
     }
   }
-  Two mine;  // lane t's: token t's
 #pragma unroll
-  for (int t = 0; t < kLogitTokens; ++t) {
-    if (t >= live) continue;
+  for (int d = 16; d; d >>= 1)
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
+    for (int t = 0; t < kLogitTokens; ++t) {
       const float hi = __shfl_xor_sync(~0u, sum[t].hi, d), lo = __shfl_xor_sync(~0u, sum[t].lo, d);
       sum[t].lo += lo;
       sum[t].add(hi);
     }
+  Two mine;  // lane t's: token t's
+#pragma unroll
+  for (int t = 0; t < kLogitTokens; ++t)
     if (lane == t) mine = sum[t];
-  }
   if (lane < live) part[warp][lane][0] = mine.hi, part[warp][lane][1] = mine.lo;
   __syncthreads();
   if (threadIdx.x < live) {
@@ -218,7 +213,13 @@ __device__ __forceinline__ void x_columns(const MoeArgs &a, int token) {
   const X *const x = static_cast<const X *>(a.x) + token * a.ldx;
   if (a.w_dtype == ST_BF16 || a.w_dtype == ST_F16) {
     X *const to = reinterpret_cast<X *>(a.xq + token * a.x_pitch);
-    for (int c = threadIdx.x; c < a.hidden; c += 32 * kLogitWarps) to[c] = x[c];
+    if (a.hidden % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0) {
+      for (int c = threadIdx.x * 8; c < a.hidden; c += 256 * kLogitWarps)
+        *reinterpret_cast<uint4 *>(to + c) = *reinterpret_cast<const uint4 *>(x + c);
+    } else {
+#pragma unroll 8
+      for (int c = threadIdx.x; c < a.hidden; c += 32 * kLogitWarps) to[c] = x[c];
+    }
     return;
   }
   constexpr int C = std::is_same<X, __half>::value ? 3 : 2;
