@@ -38,6 +38,8 @@ EXPORTS = [
     "st_cache_stats", "st_cache_clear", "st_load_tensors", "st_host_affinity", "st_device_reads_pageable",
     "st_files_prefetch", "st_rms_norm", "st_gated_act", "st_linear", "st_linear_workspace",
     "st_linear_choose", "st_linear_as",
+    "st_rms_norm_blocks", "st_gated_act_blocks", "st_block_linear", "st_block_linear_workspace",
+    "st_block_linear_choose", "st_block_linear_as", "st_moe", "st_moe_workspace",
     "st_last_error", "st_status_name", "st_dtype_size", "st_dtype_name", "st_version",
 ]
 
