@@ -20,6 +20,17 @@
 // 256 weight rows.  A thread of the eight readout warps has a token's sums for
 // half of the columns in registers (128 of them), so that its scale of a block
 // is one number, or two where its columns meet two of the weight's blocks.
+//
+// Bound, few tokens: HBM, behind a launch's chain of first copies, last MMAs
+// and join (1 x 14336 x 4096 13.1 us, 8.8 by the weight's bytes; 64 x 4096 x 14336
+// 17.1, 9.1).  Many: a block's chain.  Its four MMAs take 1100-1300 clocks from
+// their issue to their signal, their sums' way out of TMEM about 450, and TMEM
+// holds two blocks of 256 columns, so that a block is not done in less than
+// about 840, where the MMAs alone would take 512: 8192 x 14336 x 4096 374 us
+// (2.6 PFLOP/s; 244 at the tensor core's measured rate), the tensor pipe half
+// active.  With silu 417: its exponential and reciprocal, on the one unit that
+// has them, add 2400 clocks a tile to the 3800 that writes it.  Registers are
+// full: 64 bytes of spill in the loop over blocks cost 12 %.
 #include "st_tensor_device.h"
 
 namespace stmat {
@@ -330,8 +341,8 @@ block_dense_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
   const bool tma_y = W > 128 && a.tma_store;
   constexpr int kHalf = W / 2;       // columns of a thread; weight rows of a CTA's stage
   constexpr int kStageBytes = (128 + kHalf) * kStageK;
-  // Blocks whose sums TMEM holds (8192 x 14336 x 4096 by tiles of 128: two 519
-  // us, four 481).
+  // Blocks whose sums TMEM holds: as many as fit (8192 x 14336 x 4096 by tiles of
+  // 128: four instead of two 519 -> 481 us).
   constexpr int kBuffers = W <= 128 ? 4 : 2, kBufferColumns = 512 / kBuffers;
   extern __shared__ uint8_t raw_smem[];
   uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -652,8 +663,8 @@ st_status check_block_linear_form(const st_block_linear_args &p, const st_linear
 // tokens 53.7, 32.3, 19.2, 16.4; tiles of 128 tokens were slower than two of 64
 // or the other kernel.)  block_dense_kernel: 2.5, and a round of tiles 0.1 and
 // 0.008 a weight row of a tile to write it, and 0.265, 0.307, 0.43 or 0.487 a
-// block by 64, 128, 192 and 256 weight rows (8192 x 14336 x 4096: 814, 472, 441,
-// 374; 8192 x 4096 x 1024 76, 54, 53, 46; 256 x 4096 x 4096 12.5, 13.5, 16.9, 18.6).
+// block by 64, 128, 192 and 256 weight rows (8192 x 14336 x 4096: 828, 472, 440,
+// 374; 8192 x 4096 x 1024 77, 54, 53, 46; 256 x 4096 x 4096 12.7, 13.5, 16.8, 18.5).
 st_linear_form choose_block_linear_form(const st_block_linear_args &p, int sms) {
   const int k_blocks = blocks_of(p);
   const int tokens = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
