@@ -344,11 +344,20 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &a, int token, int 
       if (32 * j + lane == best_e) key[j] = kNone;
     if (lane == i) mine = best_e;
   }
-  // Lane i has the i-th chosen expert.
+  // Lane i has the i-th chosen expert.  Scores that their own sum divides are
+  // relative to the chosen ones' largest (a bias may have chosen experts, and
+  // sigmoid's scores may all lie, where exp leaves binary32's range).
+  const double v = lane < a.top_k ? l[mine] : __longlong_as_double(0xfff0000000000000ll);
+  if (a.normalize && (kScores || a.sigmoid)) {
+    float most = static_cast<float>(v);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+    top = a.sigmoid ? fminf(most, 0.0f) : most;
+  }
   float s = 0.0f;
   if (lane < a.top_k) {
-    const double v = l[mine];
-    s = a.sigmoid ? 1.0f / (1.0f + expf(static_cast<float>(-v))) : expf(static_cast<float>(v - top));
+    s = expf(static_cast<float>(v - top));
+    if (a.sigmoid) s = v < 0.0 ? s / (1.0f + expf(static_cast<float>(v))) : 1.0f / (1.0f + expf(static_cast<float>(-v)));
   }
   float sum = s;
 #pragma unroll

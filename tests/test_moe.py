@@ -200,6 +200,26 @@ def test_moe_choices(stmat, score, normalize, biased, t, e):
 
 
 @gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("t", [1, 5, 20])
+def test_chosen_scores_that_all_lie_below_binary32(stmat, score, t):
+    """A bias chooses experts whose logits are 200 below the largest, and all
+    of sigmoid's logits lie at -150: the chosen scores are 0 in binary32, their
+    shares of their sum are not.  (Logits differ by under 30, so P holds.)"""
+    args, weights = layer(t, t, 12, 256, 96, "BF16", "BF16")
+    args["x"][:, 0] = 1.0
+    bias = None
+    if score == "softmax":
+        args["router"][:, 0] = 200.0
+        args["router"][:5, 0] = 0.0
+        bias = torch.zeros(12, device="cuda")
+        bias[:5] = torch.tensor([5.0, 7.0, 6.0, 3.0, 4.0], device="cuda")
+    else:
+        args["router"][:, 0] = -150.0
+    check(stmat, args, weights, 4, score=score, bias=bias)
+
+
+@gpu
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("up", [False, True])
 @pytest.mark.parametrize("w_kind", ["F8_E4M3", "BF16"])
