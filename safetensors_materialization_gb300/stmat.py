@@ -1066,7 +1066,8 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, dst=None, scale=None, stre
     use instead; block=128: one scale for every 128 columns of a row, as
     block_linear takes them (st_rms_norm_blocks; scales has ceil(columns / 128)
     in place of the last dimension).  Returns (y, scales or None, h in x's dtype,
-    or None without a residual); y * scales[..., None] stands for the normed rows.
+    or None without a residual); y * scales[..., None], or the columns' blocks
+    times their scales, stand for the normed rows.
     No gradient passes through."""
     ops = _OPS or _ops()
     gpu = x.get_device()
