@@ -776,9 +776,9 @@ struct Walk {
     run = static_cast<int>(at % a.in_runs);
     expert = slot0 = count = next_expert = next_end = 0;
     if (which >= groups) return;
-    next_expert = a.list.expert[which];
-    slot0 = a.list.first[which];
-    next_end = a.list.first[which + 1];
+    next_expert = __ldcg(&a.list.expert[which]);
+    slot0 = __ldcg(&a.list.first[which]);
+    next_end = __ldcg(&a.list.first[which + 1]);
     enter(a);
   }
   __device__ __forceinline__ void enter(const MoeArgs &a) {
@@ -786,8 +786,8 @@ struct Walk {
     slot0 += count;
     count = next_end - slot0;
     if (which + 1 >= groups) return;
-    next_expert = a.list.expert[which + 1];
-    next_end = a.list.first[which + 2];
+    next_expert = __ldcg(&a.list.expert[which + 1]);
+    next_end = __ldcg(&a.list.first[which + 2]);
   }
   // Whether the next run is another group's.
   __device__ __forceinline__ bool next(const MoeArgs &a) {
@@ -821,15 +821,16 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const __grid_constant__ 
   pipe_start(pipe, warp, kColumns);
   // The lists are the router's, which has ended: up_kernel's CTAs waited for
   // that before any let this kernel start.  So the first stages' weights are
-  // under way before h is there.
-  const int groups = *a.list.count;
+  // under way before h is there.  (Read from L2: an L1 may hold an earlier
+  // call's lists until this kernel's own wait.)
+  const int groups = __ldcg(a.list.count);
   const int64_t all = int64_t(groups) * a.in_runs, begin = all * rank / a.splits, end = all * (rank + 1) / a.splits;
   const int runs = static_cast<int>(end - begin);
   // Stages before run r of all.
   auto stages_before = [&](int64_t r) { return r / a.in_runs * a.in_blocks + r % a.in_runs * kPerRun; };
   const int64_t blocks = stages_before(end) - stages_before(begin);
   const uint32_t limit = sum_limit(static_cast<int>(min(all * kPerRun, int64_t(0x7fffffff))));
-  const int stage_bytes = (kRows + round16(*a.list.most * C)) * kStageK;
+  const int stage_bytes = (kRows + round16(__ldcg(a.list.most) * C)) * kStageK;
   const int stages = min(kMaxStages, static_cast<int>(kSmem - (ring - smem)) / stage_bytes);
   const uint32_t tmem = pipe.tmem;
   auto stages_of = [&](const Walk &w) { return min(kPerRun, a.in_blocks - w.run * kPerRun); };
