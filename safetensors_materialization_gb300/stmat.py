@@ -1187,15 +1187,17 @@ def block_linear(x, weight, x_scale, w_scale, bias=None, act="none", residual=No
     return _product(ops, gpu, True, x, weight, x_scale, w_scale, bias, act, residual, dst, out, form)
 
 
-def _scales(t, name, gpu, rows, cols):
+def _scales(t, name, gpu, rows, cols, codes):
     """(address, elements between rows) of [rows, cols] F32 scales; an expanded
     matrix of one scale is no such rows, and is written out."""
+    if t is None:
+        raise _invalid(f"{name} is needed")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         t = t.contiguous()
     p, ld, n, c = _matrix(t, name, gpu)
     if n != rows or c != cols:
         raise _invalid(f"{name}: {tuple(t.shape)}, {rows} rows of {cols} are needed")
-    if str(t.dtype) != "torch.float32":
+    if codes.get(t.dtype) not in _F32:
         raise StmatError(6, f"{name}: {t.dtype} is not F32")
     return p, ld, t
 
@@ -1210,8 +1212,8 @@ def _product(ops, gpu, block, x, weight, x_scale, w_scale, bias, act, residual, 
     pxs = nxs = pws = nws = pb = pr = ldr = 0
     b_code = 11
     if block:
-        pxs, nxs, x_scale = _scales(x_scale, "x_scale", gpu, m, -(-k // _BLOCK))
-        pws, nws, w_scale = _scales(w_scale, "w_scale", gpu, -(-n // _BLOCK), -(-k // _BLOCK))
+        pxs, nxs, x_scale = _scales(x_scale, "x_scale", gpu, m, -(-k // _BLOCK), codes)
+        pws, nws, w_scale = _scales(w_scale, "w_scale", gpu, -(-n // _BLOCK), -(-k // _BLOCK), codes)
     else:
         if x_scale is not None:
             pxs, nxs, _ = _vector(x_scale, "x_scale", gpu, m, _F32, codes, True)

@@ -170,6 +170,8 @@ def test_binding_refusals(stmat):
             (lambda: stmat.gated_act(x, up, block=128, dst="BF16"), "ST_E_INVAL"),
             (lambda: stmat.block_linear(x8, w8, xs[:, :1], ws), "ST_E_INVAL"),
             (lambda: stmat.block_linear(x8, w8, xs[:3], ws), "ST_E_INVAL"),
+            (lambda: stmat.block_linear(x8, w8, None, ws), "ST_E_INVAL"),
+            (lambda: stmat.block_linear(x8, w8, xs, None), "ST_E_INVAL"),
             (lambda: stmat.block_linear(x8, w8, xs, ws[:1]), "ST_E_INVAL"),
             (lambda: stmat.block_linear(x8, w8, xs.half(), ws), "ST_E_DTYPE"),
             (lambda: stmat.block_linear(x8, w8, xs.cpu(), ws), "ST_E_INVAL"),
