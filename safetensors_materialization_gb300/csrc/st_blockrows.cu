@@ -343,13 +343,17 @@ __global__ void __launch_bounds__(kMaxThreads) block_row_loop_kernel(const Block
 
 // Threads and accesses of a row: as for st_rowops.cu's kernels, a warp for a
 // short row, else blocks of 256 threads so that several rows share an SM, or,
-// with few rows, the shortest way through one.
+// with few rows, the shortest way through one.  Many rows of 16 bits without a
+// residual are bound by instructions: half of the threads, with twice the
+// elements, spare some (16384 x 1536 BF16 25.1 -> 21.9 us, 13308 x 2752 34.7 ->
+// 31.5; with a residual 8192 x 4096 38.4 -> 39.0, F32 6095 x 1896 27.2 -> 28.7, and
+// 300 x 4096 3.3 -> 4.1, so not there).
 template <class T, int V, bool kAny>
 cudaError_t launch_norm(const BlockRowArgs &a, cudaStream_t st) {
   const int64_t accesses = (int64_t(a.cols) + V - 1) / V;
   const unsigned rows = static_cast<unsigned>(a.rows), groups = static_cast<unsigned>((a.rows + kWarps - 1) / kWarps);
   auto threads = [&](int nv) { return static_cast<unsigned>(((accesses + nv - 1) / nv + 31) / 32 * 32); };
-  const int64_t target = a.rows <= 256 ? kMaxThreads : 256;
+  const int64_t target = a.rows <= 256 ? kMaxThreads : a.rows <= 2048 || kAny || V == 4 || a.r ? 256 : 128;
   if (accesses <= 32) return launch(block_row_kernel<T, V, 1, kAny, kNormOp, true>, groups, 32 * kWarps, 0, 1, st, a);
   if (accesses <= 64 && a.rows > 256) return launch(block_row_kernel<T, V, 2, kAny, kNormOp, true>, groups, 32 * kWarps, 0, 1, st, a);
   if (accesses <= 128 && a.rows > 256) return launch(block_row_kernel<T, V, 4, kAny, kNormOp, true>, groups, 32 * kWarps, 0, 1, st, a);

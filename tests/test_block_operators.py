@@ -204,6 +204,18 @@ def test_norm_blocks(stmat, m, c, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("m", [2048, 2049])
+@pytest.mark.parametrize("c", [1000, 1032, 2048, 2056, 4104])
+@pytest.mark.parametrize("dtype", ["BF16", "F16", "F32"])
+def test_norm_blocks_of_many_rows(stmat, m, c, dtype):
+    """To both sides of the number of rows from which a row has fewer threads."""
+    x, w = normal(m + c, m, c, dtype=TYPES[dtype]), normal(3, c, dtype=TYPES[dtype])
+    for residual in (None, x):
+        y, scales, _ = stmat.rms_norm(x, w, residual=residual, dst="F8_E4M3", block=128)
+        check_block_codes(y, scales, norm64(x, residual, w, 1e-5)[1])
+
+
+@gpu
 @pytest.mark.parametrize("m,c", ROW_SIZES)
 @pytest.mark.parametrize("dtype", ["BF16", "F16", "F32"])
 def test_gated_act_blocks(stmat, m, c, dtype):
