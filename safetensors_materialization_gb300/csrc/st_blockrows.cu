@@ -6,15 +6,15 @@
 // columns 128 b .. 128 b + 127 of a row:
 //   scale[b] = max(max over b of |v| / 448, 2^-126),  code = e4m3(v / scale[b]).
 // A block is 16 (16-bit inputs) or 32 (binary32) neighbouring threads' vectors,
-// so its largest magnitude is a few shuffles.  The norm's rstd is one positive
-// number per row, known after the row's reduction: max|v| = max|h w| rstd as
-// computed, and the row stays in registers between the two.  The gated
+// so its largest magnitude is a reduction or two of a warp.  The norm's rstd is
+// one positive number per row, known after the row's reduction: max|v| = max|h w|
+// rstd as computed, and the row stays in registers between the two.  The gated
 // activation has no reduction over the row: its rows are cut into pieces.
 //
 // Bound: HBM (7 bytes an element for a 16-bit norm with residual and h, 5 for a
 // gated activation, and a scale's 4 bytes every 128).  A copy's rate is 6.7 TB/s:
-// norm 8192 x 4096 BF16 38.6 us (6.1 TB/s), gated 8192 x 14336 with silu 94.3
-// (6.3); a norm of one row is 1.9 us of latency.  Pieces instead of whole rows
+// norm 8192 x 4096 BF16 38.3 us (6.2 TB/s), gated 8192 x 14336 with silu 92.8
+// (6.4); a norm of one row is 1.9 us of latency.  Pieces instead of whole rows
 // took the gated activation from 108 to 101 us, the rest cheaper scales.  Rows
 // off 16-byte boundaries are bound by the instructions that shift them: gated
 // 8192 x 1111 22.8 us (6.8 by its bytes), norm 16384 x 1111 47 (19).  Norms of
@@ -167,6 +167,19 @@ __device__ __forceinline__ float block_scale(float top, float *inv) {
   return s;
 }
 
+// The largest of a block's magnitudes, in all of its threads: of numbers that
+// are not negative the bits are in order, a NaN's above all.  (Two reductions of whole warps, of each half's
+// block, for 16 bits; four shuffles took 1-4 % longer, five in binary32 5-10 %:
+// 8192 x 4096 F32 norm 47.5 -> 42.5 us.)
+template <int V>
+__device__ __forceinline__ float block_top(float top, int lane) {
+  const uint32_t u = __float_as_uint(top);
+  if constexpr (kBlock / V == 32) return __uint_as_float(__reduce_max_sync(~0u, u));
+  const bool low = lane < 16;
+  const uint32_t a = __reduce_max_sync(~0u, low ? u : 0), b = __reduce_max_sync(~0u, low ? 0 : u);
+  return __uint_as_float(low ? a : b);
+}
+
 // One row (kWarpRow: of a warp) in registers, NV accesses of V elements a
 // thread; the gated activation's block has a piece of a row.  kAny: rows start
 // anywhere, or end inside an access.
@@ -263,8 +276,7 @@ block_row_kernel(const BlockRowArgs a) {
   for (int i = 0; i < NV; ++i) {
     const int c = column(i);
     if (beyond(i)) continue;
-#pragma unroll
-    for (int d = kBlock / V / 2; d; d >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(~0u, top[i], d));
+    top[i] = block_top<V>(top[i], lane);
     float inv;
     const float scale = block_scale(top[i] * rstd, &inv);
     if (lane % (kBlock / V) == 0 && c < a.cols) a.scales[row * a.blocks + c / kBlock] = scale;
@@ -328,8 +340,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_row_loop_kernel(const Block
       v[j] *= w[0];
       top = max_nan(top, fabsf(v[j]));
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+    top = block_top<4>(top, lane);
     float inv;
     const float scale = block_scale(top * rstd, &inv);
     if (lane == 0) a.scales[row * a.blocks + c0 / kBlock] = scale;
