@@ -665,6 +665,13 @@ st_status check_block_linear_form(const st_block_linear_args &p, const st_linear
 // 0.008 a weight row of a tile to write it, and 0.265, 0.307, 0.43 or 0.487 a
 // block by 64, 128, 192 and 256 weight rows (8192 x 14336 x 4096: 828, 472, 440,
 // 374; 8192 x 4096 x 1024 77, 54, 53, 46; 256 x 4096 x 4096 12.7, 13.5, 16.8, 18.5).
+// Writing takes longer with an activation, and where rows off 32-byte boundaries
+// are turned in shared memory, and the longer the wider the tile: less of it lies
+// beside the next tile's sums (7178 x 1056 x 528 18.1, 14.8, 15.4, 13.6, with gelu
+// 21.8, 20.6, 23.9, 22.2; 7178 x 1053 x 528 26.1, 25.5, 28.7, 26.9, with gelu 31.2,
+// 31.4, 41.4, 41.1).  It counts among these widths alone: block_split_kernel's
+// own writing takes longer too, and is not in its time (5549 x 7887 x 99 with gelu
+// 122, and 285 by block_split_kernel).
 st_linear_form choose_block_linear_form(const st_block_linear_args &p, int sms) {
   const int k_blocks = blocks_of(p);
   const int tokens = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
@@ -680,11 +687,24 @@ st_linear_form choose_block_linear_form(const st_block_linear_args &p, int sms) 
   }
   if (p.m <= 16 || p.k == 0) return best;
   static constexpr double kBlock[] = {0.265, 0.307, 0.43, 0.487};
+  const int64_t item = static_cast<int64_t>(st_dtype_size(p.y_dtype));
+  auto off = [&](int64_t to) {
+    auto one = [&](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % to || (p.m > 1 && ld * item % to); };
+    return one(p.y, p.ldy) || (p.residual && one(p.residual, p.ldr));
+  };
+  const double act = p.act == ST_ACT_GELU ? 1.0 : p.act == ST_ACT_SILU || p.act == ST_ACT_GELU_TANH ? 0.4 : 0.0;
+  const bool tma = item == 2 && !off(16), turned = off(32);
+  double wide = 0;  // of block_dense_kernel's widths, what writing takes counted
+  int width = 0;
   for (int w = kPairMaxN; w >= 64; w -= 64) {
     const int64_t dense = (p.m + kPairM - 1) / kPairM * ((p.n + w - 1) / w);
-    const double us = 2.5 + static_cast<double>((dense + sms / 2 - 1) / (sms / 2)) * (0.1 + 0.008 * w + k_blocks * kBlock[w / 64 - 1]);
-    if (us < least) best = {ST_LINEAR_DENSE, w, 1}, least = us;
+    const double write = 0.008 + act * (0.006 + 0.00005 * w) + (turned && !(tma && w > 128) ? 0.015 + 0.00005 * w : 0.0);
+    const double rounds = static_cast<double>((dense + sms / 2 - 1) / (sms / 2)), us = 2.5 + rounds * (0.1 + 0.008 * w + k_blocks * kBlock[w / 64 - 1]);
+    const double whole = us + rounds * (write - 0.008) * w;
+    if (us < least) best.kernel = ST_LINEAR_DENSE, least = us;
+    if (!width || whole < wide) width = w, wide = whole;
   }
+  if (best.kernel == ST_LINEAR_DENSE) best.width = width, best.splits = 1;
   return best;
 }
 
