@@ -19,7 +19,7 @@
 // off 16-byte boundaries are bound by the instructions that shift them: gated
 // 8192 x 1111 22.8 us (6.8 by its bytes), norm 16384 x 1111 47 (19).  Norms of
 // more than 16384 columns read their row twice, an element a lane: 4096 x 20000
-// 240 us (86).
+// with a residual 252 us (86).
 #include "st_rows_device.h"
 
 namespace stmat {
@@ -303,7 +303,9 @@ block_row_kernel(const BlockRowArgs a) {
 // elements, one block of a binary32 or 16-bit row, and the second pass reads
 // the inputs again (each thread its own elements, so that an h in place of an
 // input is written after its last use).  Reads of 16 bytes a lane, with the
-// scales in groups of 16 lanes, were slower here.
+// scales in groups of 16 lanes, were slower here.  The squares are added in
+// chains of kChain (4096 x 20000 BF16 169 -> 161 us by the first pass's 32-bit
+// columns, 252 with a residual; 4 x 2^22 1091).
 template <class T>
 __global__ void __launch_bounds__(kMaxThreads) block_row_loop_kernel(const BlockRowArgs a) {
   const int64_t row = blockIdx.x;
@@ -313,17 +315,26 @@ __global__ void __launch_bounds__(kMaxThreads) block_row_loop_kernel(const Block
   const T *const px = static_cast<const T *>(a.x) + row * a.ldx, *const pr = static_cast<const T *>(a.r) + row * a.ldr;
   T *const ph = static_cast<T *>(a.h) + row * a.ldh;
   uint8_t *const py = a.y + row * a.ldy;
-  auto value = [&](int64_t c) {
+  auto value = [&](auto c) {
     return c < a.cols ? to_float(px[c]) + (a.r ? to_float(pr[c]) : 0.0f) : 0.0f;
   };
+  constexpr int kPass = kMaxThreads / 32 * kBlock;
   Stat s{0.0f, 0.0f};
-  for (int64_t c0 = threadIdx.x / 32 * kBlock; c0 < a.cols; c0 += kMaxThreads / 32 * kBlock) {
+  Two sum;
+  for (int c0 = threadIdx.x / 32 * kBlock; c0 < a.cols;) {
+    const int end = min(a.cols, c0 + kChain / 4 * kPass);
+    s.sum = 0.0f;
+#pragma unroll 2
+    for (; c0 < end; c0 += kPass) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float v = value(c0 + 32 * j + lane);
-      s.sum = fmaf(v, v, s.sum);
+      for (int j = 0; j < 4; ++j) {
+        const float v = value(c0 + 32 * j + lane);
+        s.sum = fmaf(v, v, s.sum);
+      }
     }
+    sum.add(s.sum);
   }
+  s.sum = sum.value();
   s = block_stat(s);
   const float rstd = rsqrtf(s.sum / static_cast<float>(a.cols) + a.eps);
   for (int64_t c0 = threadIdx.x / 32 * kBlock; c0 < a.cols; c0 += kMaxThreads / 32 * kBlock) {

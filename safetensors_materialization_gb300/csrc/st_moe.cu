@@ -136,16 +136,6 @@ __device__ __forceinline__ float warp_top(float v) {
 
 // ------------------------------------------------------- logits_kernel
 
-// A sum in two words: hi + lo, with the error of every addition to hi in lo.
-struct Two {
-  float hi = 0.0f, lo = 0.0f;
-  __device__ __forceinline__ void add(float v) {
-    const float s = hi + v, b = s - hi;
-    lo += (hi - (s - b)) + (v - b);
-    hi = s;
-  }
-};
-
 // A block has an expert and up to four tokens; its warps share the sum.
 template <class X, class R>
 __device__ __forceinline__ void logits(const MoeArgs &a, int expert, int t0) {

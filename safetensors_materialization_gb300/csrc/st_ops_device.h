@@ -194,6 +194,18 @@ __device__ __forceinline__ void activate(float (&v)[N], st_act act) {
   }
 }
 
+// A sum in two words: hi + lo, with the error of every addition to hi in lo
+// (Knuth's two-sum).  Where hi has left binary32's range lo has no meaning.
+struct Two {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float s = hi + v, b = s - hi;
+    lo += (hi - (s - b)) + (v - b);
+    hi = s;
+  }
+  __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+};
+
 // Whether a call's activation is one of those that differ for F32 outputs.
 inline bool exact_act(st_act act, st_dtype y_dtype) { return y_dtype == ST_F32 && act > ST_ACT_RELU; }
 
