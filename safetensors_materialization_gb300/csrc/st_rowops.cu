@@ -227,15 +227,31 @@ __global__ void __launch_bounds__(kMaxThreads) row_loop_kernel(const RowArgs a) 
   const int64_t row = blockIdx.x;
   wait_for_previous();
   let_next_start();
+  // (As the one loop over the row was unrolled, within 4 %: 4 x 2^22 BF16 583 ->
+  // 598 us; by 4 in binary32 too 256 x 100000 with a residual 91 -> 107.)
+  constexpr int kChainUnroll = V == 4 ? 2 : 4;
   Stat s{0.0f, 0.0f}, unused{0.0f, 0.0f};
   with_type(kOp == kNormOp ? a.w_dtype : kDtype<T>, [&](auto zero) {
     using W = decltype(zero);
     Raw<T, V> x, r;
     float v[V];
-    for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) {
+    auto add = [&](int64_t c) {
       x = row_read<T, V>(a.x, row * a.ldx + c);
       if (a.r) r = row_read<T, V>(a.r, row * a.ldr + c);
       row_values<T, W, V, false, kOp, false>(a, row, static_cast<int>(c), true, x, r, v, s);
+    };
+    if constexpr (kOp == kNormOp) {
+      Two sum;
+      for (int64_t c = threadIdx.x * V; c < a.cols;) {
+        const int64_t end = min(int64_t(a.cols), c + kChain * kMaxThreads);
+        s.sum = 0.0f;
+#pragma unroll kChainUnroll
+        for (; c < end; c += kMaxThreads * V) add(c);
+        sum.add(s.sum);
+      }
+      s.sum = sum.value();
+    } else {
+      for (int64_t c = threadIdx.x * V; c < a.cols; c += kMaxThreads * V) add(c);
     }
     s = block_stat(s);
     const Factor f = row_factor<kOp>(a, s, row, threadIdx.x == 0);
