@@ -812,7 +812,7 @@ typedef struct st_moe_args {
   const void *x;        int64_t ldx;
   const void *router;   int64_t ld_router; /* [experts, hidden] */
   const float *router_bias;         /* experts entries, or NULL: 0 */
-  st_moe_weight gate, up, down;     /* [inter, hidden] (up.w NULL: 1), [hidden, inter] */
+  st_moe_weight gate, up, down;     /* [inter, hidden] (up.w and up.scale NULL: 1), [hidden, inter] */
   const void *residual; int64_t ldr; /* or NULL */
   void *y;              int64_t ldy;
   int32_t *chosen;                  /* [tokens, top_k], written, or NULL */

@@ -318,6 +318,7 @@ st_status check_moe(const st_moe_args *a, bool *empty) {
   ST_TRY(check_vector(op, "router_bias", a->router_bias, ST_F32));
   ST_TRY(check_experts(op, "gate", a->gate, a->w_dtype, a->experts, a->inter, a->hidden));
   if (a->up.w) ST_TRY(check_experts(op, "up", a->up, a->w_dtype, a->experts, a->inter, a->hidden));
+  else if (a->up.scale) return set_error(ST_E_INVAL, "%s: scales of an up that is not given", op);
   ST_TRY(check_experts(op, "down", a->down, a->w_dtype, a->experts, a->hidden, a->inter));
   if (a->residual) ST_TRY(check_matrix(op, "residual", a->residual, a->ldr, a->y_dtype, a->tokens, a->hidden, true));
   ST_TRY(check_matrix(op, "y", a->y, a->ldy, a->y_dtype, a->tokens, a->hidden, false));

@@ -1337,6 +1337,8 @@ def moe(x, router, gate, up, down, top_k, gate_scale=None, up_scale=None, down_s
     inter, w_type = gate.shape[1], gate.dtype
     f32 = torch.float32
     gates = _experts(gate, gate_scale, "gate", gpu, experts, inter, hidden, w_type, f32)
+    if up is None and up_scale is not None:
+        raise _invalid("up_scale without up")
     ups = _NO_EXPERTS if up is None else _experts(up, up_scale, "up", gpu, experts, inter, hidden, w_type, f32)
     downs = _experts(down, down_scale, "down", gpu, experts, hidden, inter, w_type, f32)
     pb = 0 if router_bias is None else _vector(router_bias, "router_bias", gpu, experts, _F32, codes)[0]
