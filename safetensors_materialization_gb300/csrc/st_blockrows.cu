@@ -17,7 +17,7 @@
 // (6.4); a norm of one row is 1.9 us of latency.  Pieces instead of whole rows
 // took the gated activation from 108 to 101 us, the rest cheaper scales.  Rows
 // off 16-byte boundaries are bound by the instructions that shift them: gated
-// 8192 x 1111 22.8 us (6.8 by its bytes), norm 16384 x 1111 47 (19).  Norms of
+// 8192 x 1111 20.4 us (6.8 by its bytes), norm 16384 x 1111 47 (19).  Norms of
 // more than 16384 columns read their row twice, an element a lane: 4096 x 20000
 // with a residual 252 us (86).
 #include "st_rows_device.h"
@@ -398,20 +398,26 @@ cudaError_t launch_pieces(BlockRowArgs a, int64_t accesses, cudaStream_t st) {
   return launch(block_row_kernel<T, V, NV, kAny, kActOp, false>, dim3(static_cast<unsigned>(a.rows * pieces)), nt, 0, 1, st, a);
 }
 
-// Pieces of 256 threads, two accesses a thread of each matrix; one where rows
-// are too few to fill the SMs so.
+// Pieces of 256 threads with one access a thread of each matrix, or two where
+// there are more than 32 such blocks an SM (8192 x 14336 F32 without up 133 ->
+// 119 us, BF16 83.3 -> 82.9, gated 93.1 -> 92.8; 608 x 14336 9.4 -> 10.3, 1216 x
+// 2048 3.7 -> 4.4).  16-bit rows off 16-byte boundaries always have one: the
+// instructions that shift them take longer in pairs (8192 x 1111 F16 20.4, 25.6;
+// 60000 x 601 BF16 83, 114; F32 8192 x 2405 38.4, 35.7).
 template <class T, int V, bool kAny>
-cudaError_t launch_act(const BlockRowArgs &a, cudaStream_t st) {
+cudaError_t launch_act(const BlockRowArgs &a, int sms, cudaStream_t st) {
   const int64_t accesses = (int64_t(a.cols) + V - 1) / V;
   const unsigned groups = static_cast<unsigned>((a.rows + kWarps - 1) / kWarps);
   if (accesses <= 32) return launch(block_row_kernel<T, V, 1, kAny, kActOp, true>, groups, 32 * kWarps, 0, 1, st, a);
   if (accesses <= 64) return launch(block_row_kernel<T, V, 2, kAny, kActOp, true>, groups, 32 * kWarps, 0, 1, st, a);
-  if (a.rows * accesses <= 152 * 8 * kPieceThreads) return launch_pieces<T, V, 1, kAny>(a, accesses, st);
-  return launch_pieces<T, V, 2, kAny>(a, accesses, st);
+  if constexpr (!kAny || V == 4) {
+    if (a.rows * accesses > int64_t(sms) * 32 * kPieceThreads) return launch_pieces<T, V, 2, kAny>(a, accesses, st);
+  }
+  return launch_pieces<T, V, 1, kAny>(a, accesses, st);
 }
 
 template <Op kOp>
-st_status launch_blocks(const BlockRowArgs &a, st_dtype x_dtype, void *stream, const char *op) {
+st_status launch_blocks(const BlockRowArgs &a, st_dtype x_dtype, int sms, void *stream, const char *op) {
   const int v = x_dtype == ST_F32 ? 4 : 8;
   const bool aligned = a.cols % v == 0 && place(a.x, a.ldx, x_dtype, v).aligned() && place(a.y, a.ldy, ST_F8_E4M3, v).aligned() &&
                        (!a.r || place(a.r, a.ldr, x_dtype, v).aligned()) && (!a.h || place(a.h, a.ldh, x_dtype, v).aligned()) &&
@@ -421,7 +427,7 @@ st_status launch_blocks(const BlockRowArgs &a, st_dtype x_dtype, void *stream, c
     using T = decltype(zero);
     constexpr int V = sizeof(T) == 4 ? 4 : 8;
     if constexpr (kOp == kNormOp) return launch_norm<T, V, decltype(any)::value>(a, st);
-    else return launch_act<T, V, decltype(any)::value>(a, st);
+    else return launch_act<T, V, decltype(any)::value>(a, sms, st);
   };
   auto typed = [&](auto zero) { return aligned ? run(zero, std::false_type{}) : run(zero, std::true_type{}); };
   const cudaError_t e = x_dtype == ST_BF16 ? typed(__nv_bfloat16{}) : x_dtype == ST_F16 ? typed(__half{}) : typed(float{});
@@ -440,7 +446,7 @@ st_status launch_rms_norm_blocks(const st_rms_norm_args &p, void *stream) {
   a.ldx = p.ldx; a.ldr = p.ldr; a.ldh = p.ldh; a.ldy = p.ldy; a.blocks = (p.cols + kBlock - 1) / kBlock;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
   a.eps = p.eps; a.act = ST_ACT_NONE; a.w_dtype = p.weight ? p.w_dtype : p.x_dtype;
-  return launch_blocks<kNormOp>(a, p.x_dtype, stream, "st_rms_norm_blocks");
+  return launch_blocks<kNormOp>(a, p.x_dtype, 0, stream, "st_rms_norm_blocks");
 }
 
 st_status launch_gated_act_blocks(const st_gated_act_args &p, void *stream) {
@@ -451,7 +457,10 @@ st_status launch_gated_act_blocks(const st_gated_act_args &p, void *stream) {
   a.ldx = p.ldg; a.ldr = p.ldu; a.ldy = p.ldy; a.blocks = (p.cols + kBlock - 1) / kBlock;
   a.rows = p.rows; a.cols = static_cast<int>(p.cols);
   a.act = p.act; a.w_dtype = p.x_dtype;
-  return launch_blocks<kActOp>(a, p.x_dtype, stream, "st_gated_act_blocks");
+  int dev = 0, sms = 0;
+  uint32_t *err = nullptr;
+  const st_status s = product_device(&dev, &sms, &err);
+  return s == ST_OK ? launch_blocks<kActOp>(a, p.x_dtype, sms, stream, "st_gated_act_blocks") : s;
 }
 
 }  // namespace stmat

@@ -19,6 +19,8 @@ st_status launch_gated_act(const st_gated_act_args &a, void *stream);
 // The same with a scale for every 128 columns: F8_E4M3 output, scales of its own.
 st_status launch_rms_norm_blocks(const st_rms_norm_args &a, void *stream);
 st_status launch_gated_act_blocks(const st_gated_act_args &a, void *stream);
+// The current device, its SMs and its error word (kErrProduct).
+st_status product_device(int *dev, int *sms, uint32_t **err);
 // 2^-126 to the scales of rows without columns.
 st_status launch_empty_rows(float *scales, int64_t rows, void *stream, const char *op);
 // form: NULL, or a checked one.

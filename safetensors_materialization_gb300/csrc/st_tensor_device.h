@@ -27,9 +27,6 @@ inline Side side_of(const void *ptr, int64_t ld, int64_t rows, int64_t k, int it
 // in the workspace, the weight's first, and points the sides at them.
 st_status align_rows(Side *w, Side *x, int64_t row_bytes, void *workspace, void *stream, const char *op);
 
-// The current device, its SMs and its error word (kErrProduct).
-st_status product_device(int *dev, int *sms, uint32_t **err);
-
 namespace {
 
 constexpr int kStageK = 128;         // bytes of k per stage: one swizzle row
