@@ -785,7 +785,12 @@ st_status st_block_linear_as(const st_block_linear_args *args, const st_linear_f
  * Weights are 16-bit (x's dtype), or F8_E4M3 or F8_E5M2 with a scale for every
  * 128 x 128 block; x and the values between the products are not rounded to 8
  * bits for them (within 2^-12 of a value and 2^-21 of the largest of its run of
- * 128).  Values between the products that are not finite make the token's y NaN.
+ * 128).  For 16-bit weights x is taken as it is, and the values between the
+ * products within 2^-16 (BF16) or 2^-22 (F16) of a value and 2^-39 of the largest
+ * of its run.  So a binary32 y has these roundings of its terms.  p is within
+ * (2 d + 48) 2^-24 of its value, d being its logit's distance from the largest
+ * (sigmoid: from 0); the activation is that of 16-bit outputs.
+ * Values between the products that are not finite make the token's y NaN.
  * Logits are summed with their rounding errors (products that leave binary32's
  * range are not).  y may be the very matrix of the residual and overlap no other
  * operand.  Four launches; the same bits on every run. */

@@ -34,12 +34,13 @@
 // binary32 words with the rounding errors kept (Knuth's two-sum).
 //
 // Bound: HBM, behind the router.  64 tokens, 6 of 64 experts 4096 -> 1408 in 8
-// bits: 182 us, 165 by the chosen experts' bytes (logits 17, the choice 9, up and
-// down at 5.6 and 4.9 TB/s cold); 7 tokens, 2 of 8 experts 4096 -> 14336 BF16 388
-// (365).  One token, 8 of 128 experts 2048 -> 768 in 8 bits: 24.4 us (5.7), four
-// kernels' latencies of 4 to 6 each, overlapped.  Bringing the experts' weights
-// into L2 while the router runs was slower in all of seven cases (its reads wait
-// behind them: 8 tokens, 4 of 8 experts 2048 -> 1024 BF16 32.5 -> 37.8 us).
+// bits: 182 us, 135 by the bytes of the 52 experts chosen (logits 17, the choice
+// 9, up and down at 5.6 and 4.9 TB/s, each alone and cold); 7 tokens, 2 of 8
+// experts 4096 -> 14336 BF16 368 and 419 (7 and 8 experts: 368, 421).  One token,
+// 8 of 128 experts 2048 -> 768 in 8 bits: 24.4 us (5.7), four kernels' latencies
+// of 4 to 6 each, overlapped.  Bringing the experts' weights into L2 while the
+// router runs was slower in all of seven cases (its reads wait behind them: 8
+// tokens, 4 of 8 experts 2048 -> 1024 BF16 32.5 -> 37.8 us).
 #include "st_tensor_device.h"
 
 namespace stmat {

@@ -1,5 +1,6 @@
 // st_ops_device.h -- conversions, activations and vector accesses shared by
-// the operator kernels (st_rowops.cu, st_linear.cu).
+// the operator kernels (st_rowops.cu, st_blockrows.cu, st_linear.cu,
+// st_block_linear.cu, st_moe.cu).
 #pragma once
 
 #include <cuda_bf16.h>
